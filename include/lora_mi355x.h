@@ -304,6 +304,63 @@ int lora_shrink_expand_launches(int num_tokens, int max_loras, int hidden, int n
  * LORA_ERR_MAX_LORAS for arguments out of range.  A measurement aid. */
 int lora_prepare_meta_launches(int num_tokens, int max_loras);
 
+/*
+ * A projection that every request shares, with the adapters of many requests
+ * added in the same product (add_lora_linear on the "punica_gpu" page together
+ * with the base layer it is added to).  For every token t < num_tokens, m its id:
+ *     y[t] = w x[t] + w_bias                                   all out_features columns
+ *     y[t] += lora_b[i][m] s_i[t] + bias[i][m]                 slice i's columns, m not -1
+ *     s_i[t] = buf[i][t] = scale * lora_a[i][m] x[t]
+ * accumulated in float32 and rounded to bfloat16 once; slice i's columns start
+ * at offset_start plus the widths before it, as for lora_expand.  Unlike
+ * lora_expand every row and column of y is written (a token with id -1 gets
+ * the shared projection alone); rows of buf of such tokens are not touched.
+ * A value that is not finite reaches only what it belongs to: a token's row,
+ * an adapter's tokens, a column of w.
+ *   x       bf16 [num_tokens][ldx]; w bf16 [out_features][ldw] (ldw >= hidden);
+ *   w_bias  NULL or bf16 [out_features]; y bf16 [num_tokens][ldy]
+ *   bias    NULL, or host array [num_slices] of (NULL | device bf16 [max_loras][width])
+ *   buf     float32 [num_slices][num_tokens][rank], written as a fresh buffer
+ *   ldx, ldw, ldy, out_features, offset_start, hidden, rank: multiples of 8
+ *   workspace  device memory, 256-byte aligned, workspace_bytes of it: at least
+ *           what lora_linear_workspace_bytes gives for these sizes
+ * The workspace must be zeroed once before its first use; every call leaves
+ * its counters zero.  One workspace serves any number of calls that do not
+ * overlap, of any sizes that fit.  buf is deterministic where lora_shrink is;
+ * given buf, y is.
+ */
+int lora_linear(const void *x, int64_t ldx, int num_tokens, int hidden, const void *w, int64_t ldw, int out_features,
+                const void *w_bias, const void *const *lora_a, const void *const *lora_b, const void *const *bias,
+                const int *slice_widths, int num_slices, int rank, float *buf, void *y, int64_t ldy, int offset_start,
+                const lora_meta_t *meta, float scale, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The backward pass of lora_linear.  dy is the gradient of y, buf the buffer
+ * that the forward pass wrote (s_i[t]):
+ *     dbuf[i][t] = u_i[t] = scale * lora_b[i][m]^T dy_i[t]     (dy_i: slice i's columns of dy)
+ *     dx[t]    = w^T dy[t] + sum_i lora_a[i][m]^T u_i[t]
+ *     da[i][m] = sum over tokens t of id m of u_i[t] x[t]^T    bf16 [max_loras][rank][hidden]
+ *     db[i][m] = sum dy_i[t] s_i[t]^T                          bf16 [max_loras][width][rank]
+ *     dbias[i][m] = sum dy_i[t]                                bf16 [max_loras][width]
+ * Sums are float32, each result is rounded once.  Every id's gradients below
+ * max_loras are written: zeros for an id without tokens.  dx may be NULL (not
+ * needed), dbias NULL or hold NULLs.  The shared projection is frozen: it has
+ * no gradient.  Rows of dbuf of tokens with id -1 are not touched.  Results
+ * are deterministic.  dbuf float32 [num_slices][num_tokens][rank]; workspace
+ * as for lora_linear, with backward = 1.  An empty batch writes zero gradients.
+ */
+int lora_linear_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx, int num_tokens, int hidden,
+                         const void *w, int64_t ldw, int out_features, const void *const *lora_a,
+                         const void *const *lora_b, const int *slice_widths, int num_slices, int rank,
+                         const float *buf, float *dbuf, void *dx, int64_t lddx, void *const *da, void *const *db,
+                         void *const *dbias, int offset_start, const lora_meta_t *meta, float scale, void *workspace,
+                         size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace for batches of num_tokens tokens (backward != 0: for
+ * lora_linear_backward too).  0 if a size is out of range.  Host only. */
+size_t lora_linear_workspace_bytes(int num_tokens, int max_loras, int hidden, const int *slice_widths, int num_slices,
+                                   int rank, int backward);
+
 /* Static description of a status code. */
 const char *lora_status_string(int status);
 

@@ -6,7 +6,8 @@ mirror the C ABI in include/lora_mi355x.h:
 
     lora_meta_bytes, lora_meta_bind, lora_prepare_meta, lora_shrink,
     lora_expand, lora_shrink_expand, lora_prepare_shrink_expand,
-    lora_shrink_expand_noalloc, lora_status_string, and the measurement aids
+    lora_shrink_expand_noalloc, lora_linear, lora_linear_backward,
+    lora_linear_workspace_bytes, lora_status_string, and the measurement aids
     lora_shrink_expand_launches, lora_prepare_meta_launches, lora_probe_read,
     lora_probe_empty
 
@@ -46,7 +47,8 @@ LORA_MAX_RANK = 128
 EXPORTED = ("lora_meta_bytes", "lora_meta_bind", "lora_prepare_meta", "lora_shrink",
             "lora_expand", "lora_shrink_expand", "lora_prepare_shrink_expand", "lora_shrink_expand_launches",
             "lora_prepare_meta_launches",
-            "lora_status_string", "lora_probe_read", "lora_probe_empty", "lora_shrink_expand_noalloc")
+            "lora_status_string", "lora_probe_read", "lora_probe_empty", "lora_shrink_expand_noalloc",
+            "lora_linear", "lora_linear_backward", "lora_linear_workspace_bytes")
 
 
 class LoraError(RuntimeError):
@@ -103,6 +105,16 @@ def _load() -> ctypes.CDLL:
     lib.lora_shrink_expand_launches.argtypes = [i32, i32, i32, i32, i32, i32]
     lib.lora_prepare_meta_launches.restype = i32
     lib.lora_prepare_meta_launches.argtypes = [i32, i32]
+    Z = ctypes.c_size_t
+    META = ctypes.POINTER(lora_meta_t)
+    lib.lora_linear_workspace_bytes.restype = Z
+    lib.lora_linear_workspace_bytes.argtypes = [i32, i32, i32, P, i32, i32, i32]
+    lib.lora_linear.restype = i32
+    lib.lora_linear.argtypes = [P, i64, i32, i32, P, i64, i32, P, P, P, P, P, i32, i32, P, P, i64, i32, META,
+                                ctypes.c_float, P, Z, P]
+    lib.lora_linear_backward.restype = i32
+    lib.lora_linear_backward.argtypes = [P, i64, P, i64, i32, i32, P, i64, i32, P, P, P, i32, i32, P, P, P, i64, P, P,
+                                         P, i32, META, ctypes.c_float, P, Z, P]
     lib.lora_status_string.restype = ctypes.c_char_p
     lib.lora_status_string.argtypes = [i32]
     lib.lora_probe_read.restype = i32
@@ -420,3 +432,115 @@ def lora_prepare_shrink_expand(mapping, x, lora_a: Sequence, lora_b: Sequence, b
                                           buf.data_ptr(), y.data_ptr(), y.stride(0), int(offset_start),
                                           int(bool(add_inputs)), ctypes.byref(meta.struct), float(scale),
                                           _stream(stream)), "lora_prepare_shrink_expand")
+
+
+def _widths_array(widths) -> ctypes.Array:
+    return (ctypes.c_int * len(widths))(*[int(w) for w in widths])
+
+
+def lora_linear_workspace_bytes(num_tokens: int, max_loras: int, hidden: int, widths: Sequence, rank: int,
+                                backward: bool = False) -> int:
+    """Bytes of the workspace of lora_linear (backward: and of
+    lora_linear_backward) for batches of num_tokens tokens: a uint8 device
+    tensor, zeroed once."""
+    n = int(_lib().lora_linear_workspace_bytes(int(num_tokens), int(max_loras), int(hidden), _widths_array(widths),
+                                               len(widths), int(rank), 1 if backward else 0))
+    if n == 0:
+        raise LoraError(LORA_ERR_SHAPE, "lora_linear_workspace_bytes")
+    return n
+
+
+def _workspace(t, device, where: str) -> None:
+    import torch
+    if not (t.is_cuda and t.device == device):
+        raise TypeError("%s: workspace must be on %s (got %s)" % (where, device, t.device))
+    if t.dtype != torch.uint8:
+        raise TypeError("%s: workspace must be torch.uint8 (got %s)" % (where, t.dtype))
+    _need(t.dim() == 1 and t.is_contiguous(), LORA_ERR_BUFFER, where, "workspace must be a contiguous 1-d tensor")
+
+
+def _projection(where: str, meta, h: int, w, wide, name: str, offset_start: int, widths) -> None:
+    """The shared projection's matrix [out][hidden] and the activations of its
+    output side (y or dy) of at least its columns."""
+    import torch
+    _dev(w, torch.bfloat16, meta, where, "w")
+    _need(w.dim() == 2 and w.shape[1] == h, LORA_ERR_SHAPE, where, "w must be [out][%d]" % h)
+    _dev(wide, torch.bfloat16, meta, where, name)
+    _need(wide.dim() == 2 and wide.shape[0] == meta.num_tokens and wide.shape[1] == w.shape[0], LORA_ERR_SHAPE, where,
+          "%s must be [%d][%d]" % (name, meta.num_tokens, w.shape[0]))
+    _need(offset_start >= 0 and offset_start + sum(widths) <= w.shape[0], LORA_ERR_SHAPE, where,
+          "the slices end past w's rows")
+
+
+def lora_linear(x, w, w_bias, lora_a: Sequence, lora_b: Sequence, bias: Optional[Sequence], buf, y, meta: LoraMeta,
+                scale: float, workspace, offset_start: int = 0, stream=None) -> None:
+    """y = x @ w^T + w_bias, plus in slice i's columns buf[i][t] @ lora_b[i][id_t]^T
+    + bias[i][id_t] for tokens with an adapter, in one product (y is written,
+    rounded once); buf[i][t] = scale * x[t] @ lora_a[i][id_t]^T is written too.
+    x bf16 [N][H]; w bf16 [out][H]; w_bias None or bf16 [out]; lora_a, lora_b,
+    bias, buf as for lora_shrink_expand; y bf16 [N][out]; workspace uint8 of
+    lora_linear_workspace_bytes."""
+    import torch
+    where = "lora_linear"
+    n, h = x.shape
+    s, r = len(lora_a), lora_a[0].shape[1]
+    _layer_checks(where, meta, n, x=x, lora_a=lora_a, lora_b=lora_b, bias=bias, buf=buf, offset_start=offset_start)
+    _need(len(lora_b) == s and buf.shape[0] == s, LORA_ERR_SLICES, where, "one weight per buf slice")
+    widths = [int(t.shape[1]) for t in lora_b]
+    _projection(where, meta, h, w, y, "y", offset_start, widths)
+    if w_bias is not None:
+        _dev(w_bias, torch.bfloat16, meta, where, "w_bias")
+        _need(w_bias.dim() == 1 and w_bias.shape[0] == w.shape[0], LORA_ERR_SHAPE, where, "w_bias must be [%d]" % w.shape[0])
+    _workspace(workspace, meta.region.device, where)
+    _check(_lib().lora_linear(x.data_ptr(), x.stride(0), n, h, w.data_ptr(), w.stride(0), w.shape[0],
+                              None if w_bias is None else w_bias.data_ptr(), _ptr_array(lora_a), _ptr_array(lora_b),
+                              None if bias is None else _ptr_array(bias), _widths_array(widths), s, r, buf.data_ptr(),
+                              y.data_ptr(), y.stride(0), int(offset_start), ctypes.byref(meta.struct), float(scale),
+                              workspace.data_ptr(), workspace.numel(), _stream(stream)), where)
+
+
+def _grads(ts, like, meta, where: str, name: str) -> None:
+    import torch
+    _need(len(ts) == len(like), LORA_ERR_SLICES, where, "one %s per slice" % name)
+    for i, (t, shape) in enumerate(zip(ts, like)):
+        _dev(t, torch.bfloat16, meta, where, "%s[%d]" % (name, i))
+        _need(tuple(t.shape) == tuple(shape) and t.is_contiguous(), LORA_ERR_SHAPE, where,
+              "%s[%d] must be contiguous %s" % (name, i, tuple(shape)))
+
+
+def lora_linear_backward(dy, x, w, lora_a: Sequence, lora_b: Sequence, buf, dbuf, dx, da: Sequence, db: Sequence,
+                         dbias: Optional[Sequence], meta: LoraMeta, scale: float, workspace, offset_start: int = 0,
+                         stream=None) -> None:
+    """The gradients of lora_linear: dx = dy @ w + the adapters' part (dx may be
+    None), da[i], db[i] and dbias[i] (None: not wanted) like lora_a[i],
+    lora_b[i] and bias[i], zeros for ids without tokens.  buf is the forward
+    pass's; dbuf (like buf) is written: scale * dy_i[t] @ lora_b[i][id_t].
+    Matrices of ids from max_loras on are not touched."""
+    import torch
+    where = "lora_linear_backward"
+    n, h = x.shape
+    s, r = len(lora_a), lora_a[0].shape[1]
+    _layer_checks(where, meta, n, x=x, lora_a=lora_a, lora_b=lora_b, buf=buf)
+    _need(len(lora_b) == s and buf.shape[0] == s, LORA_ERR_SLICES, where, "one weight per buf slice")
+    widths = [int(t.shape[1]) for t in lora_b]
+    _projection(where, meta, h, w, dy, "dy", offset_start, widths)
+    _dev(dbuf, torch.float32, meta, where, "dbuf")
+    _need(dbuf.shape == buf.shape and dbuf.is_contiguous(), LORA_ERR_SHAPE, where, "dbuf must be contiguous like buf")
+    if dx is not None:
+        _dev(dx, torch.bfloat16, meta, where, "dx")
+        _need(tuple(dx.shape) == (n, h), LORA_ERR_SHAPE, where, "dx must be [%d][%d]" % (n, h))
+    _grads(da, [t.shape for t in lora_a], meta, where, "da")
+    _grads(db, [t.shape for t in lora_b], meta, where, "db")
+    if dbias is not None:
+        _need(len(dbias) == s, LORA_ERR_SLICES, where, "one dbias entry per slice")
+        for i, t in enumerate(dbias):
+            if t is not None:
+                _grads([t], [lora_b[i].shape[:2]], meta, where, "dbias")
+    _workspace(workspace, meta.region.device, where)
+    _check(_lib().lora_linear_backward(dy.data_ptr(), dy.stride(0), x.data_ptr(), x.stride(0), n, h, w.data_ptr(),
+                                       w.stride(0), w.shape[0], _ptr_array(lora_a), _ptr_array(lora_b),
+                                       _widths_array(widths), s, r, buf.data_ptr(), dbuf.data_ptr(),
+                                       None if dx is None else dx.data_ptr(), 0 if dx is None else dx.stride(0),
+                                       _ptr_array(da), _ptr_array(db), None if dbias is None else _ptr_array(dbias),
+                                       int(offset_start), ctypes.byref(meta.struct), float(scale),
+                                       workspace.data_ptr(), workspace.numel(), _stream(stream)), where)

@@ -73,7 +73,9 @@ int env_int(const char *name) {
     return e ? atoi(e) : 0;
 }
 
-MetaView view_of(const lora_meta_t *m) {
+}  // namespace
+
+MetaView lora::view_of(const lora_meta_t *m) {
     MetaView v;
     v.sorted = m->token_indices_sorted;
     v.active_ids = m->active_lora_ids;
@@ -85,7 +87,7 @@ MetaView view_of(const lora_meta_t *m) {
     return v;
 }
 
-int check_meta(const lora_meta_t *m) {
+int lora::check_meta(const lora_meta_t *m) {
     if (!m) return LORA_ERR_NULL;
     if (!m->token_lora_mapping || !m->token_indices_sorted || !m->active_lora_ids ||
         !m->num_tokens_per_lora || !m->lora_token_start_loc || !m->no_lora_flag || !m->status || !m->sync)
@@ -94,8 +96,6 @@ int check_meta(const lora_meta_t *m) {
     if (m->max_num_tokens < 0 || m->max_num_tokens > LORA_MAX_TOKENS) return LORA_ERR_NUM_TOKENS;
     return LORA_OK;
 }
-
-}  // namespace
 
 extern "C" {
 
@@ -273,6 +273,21 @@ ShrinkTuning shrink_tuning() {
     cfg.stream_k = env_int("LORA_SHRINK_SK");
     return cfg;
 }
+
+}  // namespace
+
+int lora::shrink_fresh(const void *x, int64_t ldx, int num_tokens, int hidden, const void *const *lora_a,
+                       int num_slices, int rank, float *buf, const lora_meta_t *meta, float scale,
+                       hipStream_t stream) {
+    ShrinkArgs a;
+    bool skip = false;
+    const int st = shrink_args(x, ldx, num_tokens, hidden, lora_a, num_slices, rank, buf, meta, scale, a, skip);
+    if (st || skip) return st;
+    a.overwrite = 1;
+    return launch_shrink(a, sk_args(meta), shrink_tuning(), stream) == hipSuccess ? LORA_OK : LORA_ERR_LAUNCH;
+}
+
+namespace {
 
 // Checks and kernel arguments of lora_expand.
 int expand_args(const float *buf, int num_tokens, int rank, const void *const *lora_b, const void *const *bias,

@@ -410,6 +410,13 @@ inline long persistent_grid(long units, long cap, const void *fn, int threads, s
     return g < kNumXcd ? kNumXcd : g;
 }
 
+// Host-side checks and calls of the API layer that other entry points use.
+int check_meta(const lora_meta_t *m);
+MetaView view_of(const lora_meta_t *m);
+// lora_shrink into a fresh buffer (buf written, not accumulated), with its checks.
+int shrink_fresh(const void *x, int64_t ldx, int num_tokens, int hidden, const void *const *lora_a, int num_slices,
+                 int rank, float *buf, const lora_meta_t *meta, float scale, hipStream_t stream);
+
 // Host-side launchers (defined next to their kernels).
 // Also zeroes the stream-K shrink's counters (sk_words words at sk_counters;
 // none when sk_words is 0).

@@ -1,0 +1,983 @@
+// lora_linear.hip -- a projection that every request shares with the adapters
+// of many requests added in the same product, and its backward pass:
+//
+//   y[t]   = W x[t] + b_w  + (slice i's columns)  B_i[m] s_i[t] + bias_i[m]     m = id_t
+//   u_i[t] = scale * B_i[m]^T dy_i[t]
+//   dx[t]  = W^T dy[t] + sum_i A_i[m]^T u_i[t]
+//   dA_i[m] = sum_{t of m} u_i[t] x[t]^T,  dB_i[m] = sum dy_i[t] s_i[t]^T,  dbias_i[m] = sum dy_i[t]
+//
+// with s_i[t] = scale * A_i[m] x[t] from the shrink kernels.
+//
+// The two large products run over the batch in the stable order sorted by id,
+// which the prepared metadata holds: a tile of tokens then meets few adapters
+// (its share of the batch plus one), and each of them is a continuation of the
+// tile's K walk: after W's columns come the ranks of every (adapter, slice)
+// the tile meets, with the rows of other adapters' tokens read as zeros.  The
+// sums stay in the MFMA accumulators, so y and dx are rounded once and are
+// written once; no pass over y adds the adapters afterwards.
+//
+// s and u are fp32.  They enter the products as two bf16 parts, hi = rne(v)
+// and lo = rne(v - hi) (about 16 mantissa bits together), side by side as 2 r
+// K elements; a single bf16 part would add an error as large as the result's
+// own rounding, and the ranks are a small share of the work.
+#include <string.h>
+
+#include <type_traits>
+
+#include "lora_gemm.h"
+
+namespace lora {
+namespace {
+
+extern __shared__ __attribute__((aligned(1024))) unsigned char g_lds[];
+
+// ---------------------------------------------------------------- workspace
+
+// Segment of each LoRA id, and the token tiles of the u product.
+struct SegEntry {
+    int32_t start, count;
+};
+struct UTile {
+    int32_t id, start, rows, pad;   // sorted positions [start, start + rows)
+};
+
+// ---------------------------------------------------------------- pack
+
+struct PackArgs {
+    MetaView meta;
+    const int32_t *ids;
+    const float *buf;
+    uint16_t *packed;
+    SegEntry *segs;       // NULL: no tables
+    UTile *tiles;
+    int32_t *num_tiles;
+    int32_t num_tokens, rank, slices, max_loras, tile_tokens, tiles_cap;
+};
+
+constexpr int kPackThreads = 256;
+
+__device__ __forceinline__ void split_hi_lo(float v, uint32_t &h, uint32_t &l) {
+    h = float_to_bf16_bits(v);
+    l = (h & 0x7f80u) == 0x7f80u ? 0u : float_to_bf16_bits(v - bf16_bits_to_float(h));   // inf and NaN: hi alone
+}
+
+// buf's rows in sorted order as bf16 hi | lo (one 2 r row per token and slice);
+// workgroup 0 also writes the tables when they are asked for.
+__global__ __launch_bounds__(kPackThreads) void pack_kernel(PackArgs a) {
+    const bool none = *a.meta.no_lora != 0;
+    const int tid = threadIdx.x;
+    if (a.segs && blockIdx.x == 0) {
+        __shared__ int s_wsum[kPackThreads / kWave];
+        for (int m = tid; m < a.max_loras; m += kPackThreads) a.segs[m] = SegEntry{0, 0};
+        __syncthreads();
+        constexpr int kPer = (LORA_MAX_LORAS + 1 + kPackThreads - 1) / kPackThreads;
+        int id[kPer], st[kPer], cnt[kPer], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int k = tid * kPer + i;
+            id[i] = -1;
+            st[i] = cnt[i] = 0;
+            if (!none && k < a.meta.nslots) {
+                id[i] = a.meta.active_ids[k];
+                st[i] = a.meta.start_loc[k];
+                cnt[i] = a.meta.counts[k];
+            }
+            const bool ok = id[i] >= 0 && id[i] < a.max_loras && st[i] >= 0 && cnt[i] > 0 && st[i] + cnt[i] <= a.num_tokens;
+            if (!ok) id[i] = -1, cnt[i] = 0;
+            if (ok) a.segs[id[i]] = SegEntry{st[i], cnt[i]};
+            sum += (cnt[i] + a.tile_tokens - 1) / a.tile_tokens;
+        }
+        const int incl = wave_inclusive_scan(sum);
+        if (lane_id() == kWave - 1) s_wsum[tid / kWave] = incl;
+        __syncthreads();
+        int at = incl - sum, total = 0;
+        for (int w = 0; w < kPackThreads / kWave; ++w) {
+            at += w < tid / kWave ? s_wsum[w] : 0;
+            total += s_wsum[w];
+        }
+        if (tid == 0) *a.num_tiles = total < a.tiles_cap ? total : a.tiles_cap;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            for (int o = 0; o < cnt[i]; o += a.tile_tokens, ++at)
+                if (at < a.tiles_cap) a.tiles[at] = UTile{id[i], st[i] + o, min(a.tile_tokens, cnt[i] - o), 0};
+    }
+    if (none) return;
+    const int per_row = a.rank / 4;
+    const int64_t work = (int64_t)a.slices * a.num_tokens * per_row;
+    for (int64_t w = (int64_t)blockIdx.x * kPackThreads + tid; w < work; w += (int64_t)gridDim.x * kPackThreads) {
+        const int q = (int)(w % per_row);
+        const int64_t row = w / per_row;              // slice * n + position
+        const int p = (int)(row % a.num_tokens);
+        const int64_t slice = row / a.num_tokens;
+        const int t = a.meta.sorted[p];
+        if ((unsigned)t >= (unsigned)a.num_tokens || a.ids[t] < 0) continue;
+        const floatx4 v = *reinterpret_cast<const floatx4 *>(a.buf + (slice * a.num_tokens + t) * a.rank + 4 * q);
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split_hi_lo(v[e], h[e], l[e]);
+        uint16_t *out = a.packed + row * 2 * a.rank + 4 * q;
+        *reinterpret_cast<u32x2g *>(out) = u32x2g{h[0] | h[1] << 16, h[2] | h[3] << 16};
+        *reinterpret_cast<u32x2g *>(out + a.rank) = u32x2g{l[0] | l[1] << 16, l[2] | l[3] << 16};
+    }
+}
+
+// ---------------------------------------------------------------- y and dx
+
+struct LinearArgs {
+    MetaView meta;
+    const int32_t *ids;
+    const uint16_t *in;                         // x (forward) or dy (backward), one row per token
+    int64_t ldin;
+    const uint16_t *w;                          // [out][hidden]
+    int64_t ldw;
+    const uint16_t *w_bias;
+    const uint16_t *lw[LORA_MAX_SLICES];        // B_i (forward) or A_i (backward)
+    const uint16_t *bias[LORA_MAX_SLICES];
+    int32_t width[LORA_MAX_SLICES], col[LORA_MAX_SLICES];
+    const uint16_t *packed;                     // s or u: [slices][n][2 r]
+    uint16_t *y;                                // y or dx
+    int64_t ldy;
+    float *slots;
+    int32_t *counters;
+    int32_t num_tokens, cols, k, rank, slices, max_loras;
+    int32_t mtiles, ntiles, group, splits, split_steps;
+};
+
+template <class T, bool BWD>
+struct LinearOp {
+    Walk<typename T::MSide> wm;
+    Walk<typename T::NSide> wn;
+    const LinearArgs &a;
+    const int (*seg)[4];       // LDS: lo, hi (sorted positions), id
+    int main_left, m0, p0;
+    int e, sl, kk, sl0, sl1, ksteps;
+
+    int main_steps, per_seg;
+    // an adapter's steps touch its own tokens' sums alone: one whose weights
+    // are not finite stays without effect on the others in the tile
+    __device__ __forceinline__ void mma(const typename T::Half &h, typename T::Acc &acc, int s) {
+        if (s < main_steps) {
+            T::mma(h, acc);
+            return;
+        }
+        const int x = (s - main_steps) / per_seg;
+        mma_rows<T>(h, acc, __builtin_amdgcn_readfirstlane(seg[x][0]) - p0,
+                    __builtin_amdgcn_readfirstlane(seg[x][1]) - p0);
+    }
+    __device__ __forceinline__ void issue(uint32_t at) {
+        if (main_left > 0) {
+            wm.issue(at);
+            wn.issue(at + T::MSide::kBytes);
+            --main_left;
+            return;
+        }
+        // one K step of adapter seg[e], slice sl: ranks 64 kk .. of [hi | lo]
+        const int lo = __builtin_amdgcn_readfirstlane(seg[e][0]), hi = __builtin_amdgcn_readfirstlane(seg[e][1]);
+        const int id = __builtin_amdgcn_readfirstlane(seg[e][2]);
+        const int r = a.rank, k0 = kk * kStepK;
+        const uint16_t *lw = select_slice(a.lw, sl);
+#pragma unroll
+        for (int j = 0; j < T::NSide::kInstr; ++j) {
+            const int pos = p0 + T::NSide::row(j), k = k0 + T::NSide::elem(j);
+            const bool ok = pos >= lo && pos < hi && k < 2 * r;
+            dma16(ok ? a.packed + ((int64_t)sl * a.num_tokens + pos) * 2 * r + k : zero_page,
+                  at + T::MSide::kBytes + T::NSide::dst(j));
+        }
+        const int width = select_slice(a.width, sl), col = select_slice(a.col, sl);
+#pragma unroll
+        for (int j = 0; j < T::MSide::kInstr; ++j) {
+            const uint16_t *src;
+            bool ok;
+            if (BWD) {      // A_i: ranks are rows, this side's index is the hidden column
+                const int k = k0 + T::MSide::row(j);
+                int c = m0 + T::MSide::elem(j);
+                c = c < a.cols ? c : a.cols - 8;
+                ok = k < 2 * r;
+                src = lw + ((int64_t)id * r + (k < r ? k : k - r)) * a.cols + c;
+            } else {        // B_i: rows are the slice's columns, ranks contiguous
+                const int c = m0 + T::MSide::row(j) - col, k = k0 + T::MSide::elem(j);
+                ok = c >= 0 && c < width && k < 2 * r;
+                src = lw + ((int64_t)id * width + c) * r + (k < r ? k : k - r);
+            }
+            dma16(ok ? src : zero_page, at + T::MSide::dst(j));
+        }
+        if (++kk == ksteps) {
+            kk = 0;
+            if (++sl == sl1) {
+                sl = sl0;
+                ++e;
+            }
+        }
+    }
+};
+
+template <class T, bool BWD>
+__global__ __launch_bounds__(T::kThreads) void linear_kernel(LinearArgs a) {
+    __shared__ int s_tok[T::BN], s_id[T::BN], s_seg[T::BN][4], s_count, s_flag;
+    const int tid = threadIdx.x;
+    const int split = blockIdx.x % a.splits;
+    TileAt at;
+    if (!tile_at(blockIdx.x / a.splits, a.mtiles, a.ntiles, a.group, at)) return;
+    const int m0 = at.m * T::BM, p0 = at.n * T::BN;
+    const int rows = min(T::BN, a.num_tokens - p0);
+    const bool none = *a.meta.no_lora != 0;
+
+    // the tile's tokens (a batch without adapters has no sorted order: batch order)
+    if (tid == 0) s_count = 0;
+    for (int r = tid; r < T::BN; r += T::kThreads) {
+        const int p = p0 + min(r, rows - 1);
+        int t = none ? p : a.meta.sorted[p];
+        t = (unsigned)t < (unsigned)a.num_tokens ? t : 0;
+        s_tok[r] = t;
+        s_id[r] = none ? -1 : a.ids[t];
+    }
+    __syncthreads();
+    // the adapters it meets (any order: each token takes part in one of them)
+    if (!none)
+        for (int k = tid; k < a.meta.nslots; k += T::kThreads) {
+            const int id = a.meta.active_ids[k], st = a.meta.start_loc[k], en = st + a.meta.counts[k];
+            const int lo = max(st, p0), hi = min(en, p0 + rows);
+            if (id >= 0 && id < a.max_loras && lo < hi) {
+                const int e = atomicAdd(&s_count, 1);
+                if (e < T::BN) {
+                    s_seg[e][0] = lo;
+                    s_seg[e][1] = hi;
+                    s_seg[e][2] = id;
+                }
+            }
+        }
+    __syncthreads();
+    const int nseg = __builtin_amdgcn_readfirstlane(min(s_count, T::BN));
+
+    LinearOp<T, BWD> op{{}, {}, a, s_seg, 0, m0, p0, 0, 0, 0, 0, a.slices, (2 * a.rank + kStepK - 1) / kStepK, 0, 1};
+    const int all = (a.k + kStepK - 1) / kStepK;
+    const int s0 = split * a.split_steps, s1 = min(all, s0 + a.split_steps);
+    op.main_left = op.main_steps = max(0, s1 - s0);
+    int ext = 0;
+    if (split == a.splits - 1 && nseg > 0) {
+        if (!BWD) {   // the slices that meet the tile's columns
+            op.sl0 = a.slices;
+            op.sl1 = 0;
+            for (int i = 0; i < a.slices; ++i) {
+                const int c = select_slice(a.col, i);
+                if (c < m0 + T::BM && c + select_slice(a.width, i) > m0) {
+                    op.sl0 = min(op.sl0, i);
+                    op.sl1 = i + 1;
+                }
+            }
+        }
+        op.sl = op.sl0;
+        op.per_seg = max(1, (op.sl1 - op.sl0) * op.ksteps);
+        ext = op.sl1 > op.sl0 ? nseg * (op.sl1 - op.sl0) * op.ksteps : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < T::NSide::kInstr; ++j)
+        op.wn.p[j] = a.in + (int64_t)s_tok[T::NSide::row(j)] * a.ldin + T::NSide::elem(j) + (int64_t)s0 * kStepK;
+    op.wn.step = kStepK;
+    op.wn.left = a.k - s0 * kStepK;
+#pragma unroll
+    for (int j = 0; j < T::MSide::kInstr; ++j) {
+        if (BWD) {
+            int c = m0 + T::MSide::elem(j);
+            c = c < a.cols ? c : a.cols - 8;
+            op.wm.p[j] = a.w + (int64_t)(s0 * kStepK + T::MSide::row(j)) * a.ldw + c;
+        } else {
+            const int c = min(m0 + T::MSide::row(j), a.cols - 1);
+            op.wm.p[j] = a.w + (int64_t)c * a.ldw + T::MSide::elem(j) + (int64_t)s0 * kStepK;
+        }
+    }
+    op.wm.step = BWD ? (int64_t)kStepK * a.ldw : kStepK;
+    op.wm.left = a.k - s0 * kStepK;
+
+    typename T::Acc acc;
+    clear<T>(acc);
+    mma_loop<T>(op, op.main_left + ext, acc, g_lds);
+
+    if constexpr (T::BM * T::BN <= 128 * 128) {
+        if (a.splits > 1) {
+            const int tile = at.n * a.mtiles + at.m;
+            if (!combine_splits<T>(acc, a.slots + (int64_t)tile * a.splits * (T::BM * T::BN), a.counters + tile, split,
+                                   a.splits, rows, &s_flag))
+                return;
+        }
+    }
+
+    // biases: of the projection for every token, of the adapter where there is one
+    if constexpr (T::QUADS) {
+        // groups of 8 consecutive columns (never across a slice's edge)
+#pragma unroll
+        for (int mt = 0; mt < T::MT; mt += 2) {
+            const int c = m0 + T::m_of(mt);
+            const bool cin = c < a.cols;
+            float wb[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) wb[x] = 0.f;
+            if (a.w_bias && cin) {
+                const u32x4 v = *reinterpret_cast<const u32x4 *>(a.w_bias + c);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) unpack_bf16(v[x], wb[2 * x], wb[2 * x + 1]);
+            }
+            const uint16_t *bp = nullptr;
+            int bw = 0;
+            for (int i = 0; i < a.slices; ++i) {
+                const int ci = select_slice(a.col, i), wi = select_slice(a.width, i);
+                const uint16_t *bi = select_slice(a.bias, i);
+                if (bi && c >= ci && c < ci + wi) {
+                    bp = bi + (c - ci);
+                    bw = wi;
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < T::NT; ++nt) {
+                const int r = T::n_of(nt);
+                if (r >= rows || !cin) continue;
+                const int id = s_id[r];
+                float v[8];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    v[x] = acc[mt][nt][x] + wb[x];
+                    v[4 + x] = acc[mt + 1][nt][x] + wb[4 + x];
+                }
+                if (bp && id >= 0) {
+                    const u32x4 b = *reinterpret_cast<const u32x4 *>(bp + (int64_t)id * bw);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        float p, q;
+                        unpack_bf16(b[x], p, q);
+                        v[2 * x] += p;
+                        v[2 * x + 1] += q;
+                    }
+                }
+                *reinterpret_cast<u32x4 *>(a.y + (int64_t)s_tok[r] * a.ldy + c) =
+                    u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+            }
+        }
+    } else {
+        // backward: no biases; 4 consecutive columns
+#pragma unroll
+        for (int nt = 0; nt < T::NT; ++nt) {
+            const int r = T::n_of(nt);
+            if (r >= rows) continue;
+            uint16_t *row = a.y + (int64_t)s_tok[r] * a.ldy;
+#pragma unroll
+            for (int mt = 0; mt < T::MT; ++mt) {
+                const int c = m0 + T::m_of(mt);
+                const floatx4 v = acc[mt][nt];
+                if (c < a.cols) *reinterpret_cast<u32x2g *>(row + c) = u32x2g{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- u
+
+struct UArgs {
+    const UTile *tiles;
+    const int32_t *num_tiles;
+    const int32_t *sorted;
+    const uint16_t *dy;
+    int64_t lddy;
+    const uint16_t *b[LORA_MAX_SLICES];
+    int32_t width[LORA_MAX_SLICES], col[LORA_MAX_SLICES];
+    float *dbuf;
+    uint16_t *packed;
+    float *slots;
+    int32_t *counters;
+    int32_t num_tokens, rank, slices, splits;
+    float scale;
+};
+
+template <class T>
+struct PlainOp {
+    Walk<typename T::MSide> wm;
+    Walk<typename T::NSide> wn;
+    __device__ __forceinline__ void mma(const typename T::Half &h, typename T::Acc &acc, int) { T::mma(h, acc); }
+    __device__ __forceinline__ void issue(uint32_t at) {
+        wm.issue(at);
+        wn.issue(at + T::MSide::kBytes);
+    }
+};
+
+// u_i[t] = scale * B_i[m]^T dy_i[t] for one tile of a segment's tokens and one
+// slice: K is the slice's width, all ranks are in the tile.
+template <class T>
+__global__ __launch_bounds__(T::kThreads) void u_kernel(UArgs a) {
+    __shared__ int s_tok[T::BN], s_flag;
+    const int split = blockIdx.x % a.splits, unit = blockIdx.x / a.splits;
+    const int tile = unit / a.slices, i = unit % a.slices;
+    if (tile >= *a.num_tiles) return;
+    const UTile ut = a.tiles[tile];
+    for (int r = threadIdx.x; r < T::BN; r += T::kThreads) {
+        const int t = a.sorted[ut.start + min(r, ut.rows - 1)];
+        s_tok[r] = (unsigned)t < (unsigned)a.num_tokens ? t : 0;
+    }
+    __syncthreads();
+    const int width = select_slice(a.width, i), col = select_slice(a.col, i);
+    const uint16_t *b = select_slice(a.b, i) + (int64_t)ut.id * width * a.rank;
+    const int all = (width + kStepK - 1) / kStepK, per = (all + a.splits - 1) / a.splits;
+    const int s0 = min(all, split * per), s1 = min(all, s0 + per);
+    PlainOp<T> op;
+#pragma unroll
+    for (int j = 0; j < T::NSide::kInstr; ++j)
+        op.wn.p[j] = a.dy + (int64_t)s_tok[T::NSide::row(j)] * a.lddy + col + s0 * kStepK + T::NSide::elem(j);
+    op.wn.step = kStepK;
+    op.wn.left = width - s0 * kStepK;
+#pragma unroll
+    for (int j = 0; j < T::MSide::kInstr; ++j) {
+        const int c = min(T::MSide::elem(j), a.rank - 8);
+        op.wm.p[j] = b + (int64_t)(s0 * kStepK + T::MSide::row(j)) * a.rank + c;
+    }
+    op.wm.step = (int64_t)kStepK * a.rank;
+    op.wm.left = width - s0 * kStepK;
+    typename T::Acc acc;
+    clear<T>(acc);
+    mma_loop<T>(op, s1 - s0, acc, g_lds);
+    if (a.splits > 1 && !combine_splits<T>(acc, a.slots + (int64_t)unit * a.splits * (T::BM * T::BN), a.counters + unit,
+                                           split, a.splits, ut.rows, &s_flag))
+        return;
+#pragma unroll
+    for (int nt = 0; nt < T::NT; ++nt) {
+        const int r = T::n_of(nt);
+        if (r >= ut.rows) continue;
+        float *out = a.dbuf + ((int64_t)i * a.num_tokens + s_tok[r]) * a.rank;
+        uint16_t *pk = a.packed + ((int64_t)i * a.num_tokens + ut.start + r) * 2 * a.rank;
+#pragma unroll
+        for (int mt = 0; mt < T::MT; ++mt) {
+            const int j = T::m_of(mt);
+            if (j >= a.rank) continue;
+            const floatx4 v = acc[mt][nt] * a.scale;
+            *reinterpret_cast<floatx4 *>(out + j) = v;
+            uint32_t h[4], l[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) split_hi_lo(v[x], h[x], l[x]);
+            *reinterpret_cast<u32x2g *>(pk + j) = u32x2g{h[0] | h[1] << 16, h[2] | h[3] << 16};
+            *reinterpret_cast<u32x2g *>(pk + a.rank + j) = u32x2g{l[0] | l[1] << 16, l[2] | l[3] << 16};
+        }
+    }
+}
+
+// ---------------------------------------------------------------- dA, dB, dbias
+
+struct GradArgs {
+    const SegEntry *segs;
+    const int32_t *sorted;
+    const uint16_t *act;                      // x (dA) or dy (dB), gathered token rows
+    int64_t ldact;
+    const uint16_t *packed;                   // u (dA) or s (dB): [slices][n][2 r]
+    uint16_t *out[LORA_MAX_SLICES];           // dA_i [id][r][hidden] or dB_i [id][width][r]
+    uint16_t *dbias[LORA_MAX_SLICES];
+    int32_t width[LORA_MAX_SLICES], col[LORA_MAX_SLICES];   // of act (dA: hidden, 0)
+    int32_t tiles_before[LORA_MAX_SLICES + 1];
+    int32_t num_tokens, rank, slices;
+};
+
+// dA_i[m] (DA: M side = x columns, N side = u's hi and lo parts) or dB_i[m]
+// (M side = s's hi and lo parts, N side = dy columns) over one segment's
+// tokens, one tile of the activation's columns.  An id without tokens gets
+// zeros: every adapter's gradient is written.
+template <class T, bool DA>
+struct GradOp {
+    using ASide = typename std::conditional<DA, typename T::MSide, typename T::NSide>::type;   // activations
+    using PSide = typename std::conditional<DA, typename T::NSide, typename T::MSide>::type;   // packed ranks
+    GatherWalk<ASide> wa;
+    Walk<PSide> wp;
+    floatx4 colsum[DA ? 1 : T::NT];
+    bool sums;
+    __device__ __forceinline__ void issue(uint32_t at) {
+        wa.issue(at + (DA ? 0 : T::MSide::kBytes));
+        wp.issue(at + (DA ? T::MSide::kBytes : 0));
+    }
+    // dB: the column sums of dy as one more MFMA row of ones
+    __device__ __forceinline__ void mma(const typename T::Half &h, typename T::Acc &acc, int) {
+        T::mma(h, acc);
+        if constexpr (!DA) {
+            if (sums) {
+                const bf16x8 ones = as_bf16x8(u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
+#pragma unroll
+                for (int nt = 0; nt < T::NT; ++nt) colsum[nt] = mfma16x16x32(ones, h.n[nt], colsum[nt]);
+            }
+        }
+    }
+};
+
+template <class T, bool DA>
+__global__ __launch_bounds__(T::kThreads) void grad_kernel(GradArgs a) {
+    using Op = GradOp<T, DA>;
+    using ASide = typename Op::ASide;
+    using PSide = typename Op::PSide;
+    constexpr int BA = DA ? T::BM : T::BN, BR = DA ? T::BN : T::BM;   // activation columns, ranks
+    const int per_id = a.tiles_before[a.slices];
+    const int m = blockIdx.x / per_id, tile = blockIdx.x % per_id;
+    int i = 0;
+    while (i + 1 < a.slices && tile >= a.tiles_before[i + 1]) ++i;
+    const int c0 = (tile - select_slice(a.tiles_before, i)) * BA;
+    const int width = select_slice(a.width, i), col = select_slice(a.col, i), r = a.rank;
+    const SegEntry sg = a.segs[m];
+    Op op;
+    op.sums = false;
+    typename T::Acc acc;
+    clear<T>(acc);
+    uint16_t *dbias = nullptr;
+    if constexpr (!DA) {
+        dbias = select_slice(a.dbias, i);
+        op.sums = dbias != nullptr && T::wave_m() == 0;
+#pragma unroll
+        for (int nt = 0; nt < T::NT; ++nt) op.colsum[nt] = floatx4{0.f, 0.f, 0.f, 0.f};
+    }
+    if (sg.count > 0) {
+        op.wa.base = a.act + col;
+        op.wa.sorted = a.sorted;
+        op.wa.ld = a.ldact;
+        op.wa.pos = sg.start;
+        op.wa.end = sg.start + sg.count;
+        op.wa.num_tokens = a.num_tokens;
+#pragma unroll
+        for (int j = 0; j < ASide::kInstr; ++j) op.wa.col[j] = min(c0 + ASide::elem(j), width - 8);
+        op.wa.fetch();
+#pragma unroll
+        for (int j = 0; j < PSide::kInstr; ++j) {
+            const int c = PSide::elem(j);
+            const int from = c < BR ? min(c, r - 8) : r + min(c - BR, r - 8);
+            op.wp.p[j] = a.packed + ((int64_t)i * a.num_tokens + sg.start + PSide::row(j)) * 2 * r + from;
+        }
+        op.wp.step = (int64_t)kStepK * 2 * r;
+        op.wp.left = sg.count;
+        mma_loop<T>(op, (sg.count + kStepK - 1) / kStepK, acc, g_lds);
+    }
+    uint16_t *out = select_slice(a.out, i);
+    if (out) {
+#pragma unroll
+        for (int nt = 0; nt < T::NT; ++nt)
+#pragma unroll
+            for (int mt = 0; mt < T::MT; ++mt) {
+                const floatx4 v = acc[mt][nt];
+                const int j = DA ? T::n_of(nt) : T::m_of(mt), c = c0 + (DA ? T::m_of(mt) : T::n_of(nt));
+                if (j >= r || c >= width) continue;
+                uint16_t *at = out + (DA ? ((int64_t)m * r + j) * width + c : ((int64_t)m * width + c) * r + j);
+                *reinterpret_cast<u32x2g *>(at) = u32x2g{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+            }
+    }
+    if constexpr (!DA) {
+        if (op.sums && lane_id() < 16)
+#pragma unroll
+            for (int nt = 0; nt < T::NT; ++nt) {
+                const int c = c0 + T::n_of(nt);
+                if (c < width) dbias[(int64_t)m * width + c] = (uint16_t)float_to_bf16_bits(op.colsum[nt][0]);
+            }
+    }
+}
+
+// ---------------------------------------------------------------- plans
+
+constexpr size_t kRound = 256;
+size_t up(size_t v) { return (v + kRound - 1) / kRound * kRound; }
+long ceil_div(long a, long b) { return (a + b - 1) / b; }
+
+enum LinearTile { kBig, kMid, kSmall };
+struct LinearPlan {
+    LinearTile tile;
+    int bm, bn, mtiles, ntiles, splits, split_steps;
+    size_t slot_bytes;
+};
+
+// The tile and K split of y or dx (n x cols over k): the 256 x 256 tile where
+// it fills the GPU's 256 CUs, else 128 x 128, or 128 x 32 for few tokens;
+// there K is split while the workgroups do not fill the CUs twice (each CU
+// holds at least two) and every part keeps at least 4 steps.
+LinearPlan plan_linear(long n, long cols, long k, bool allow_split) {
+    LinearPlan p;
+    const long steps = ceil_div(k, kStepK);
+    if (ceil_div(n, 256) * ceil_div(cols, 256) >= 192 && n > 128) {
+        p.tile = kBig;
+        p.bm = p.bn = 256;
+    } else if (n > 32) {
+        p.tile = kMid;
+        p.bm = p.bn = 128;
+    } else {
+        p.tile = kSmall;
+        p.bm = 128;
+        p.bn = 32;
+    }
+    p.mtiles = (int)ceil_div(cols, p.bm);
+    p.ntiles = (int)ceil_div(n, p.bn);
+    long splits = 1;
+    const long tiles = (long)p.mtiles * p.ntiles;
+    if (p.tile != kBig && allow_split && tiles > 0) {
+        splits = 512 / tiles;
+        if (splits > steps / 4) splits = steps / 4;
+        if (splits > 16) splits = 16;
+        if (splits < 1) splits = 1;
+    }
+    p.split_steps = (int)ceil_div(steps, splits);
+    p.splits = (int)ceil_div(steps, p.split_steps);
+    p.slot_bytes = p.splits > 1 ? sizeof(float) * (size_t)tiles * p.splits * p.bm * p.bn : 0;
+    return p;
+}
+
+constexpr int kCounterWords = 1024;   // tiles that may be split: at most 512 / 2, u units likewise
+
+struct UPlan {
+    int bm, tile_tokens, tiles_cap, splits;
+    size_t slot_bytes;
+};
+UPlan plan_u(long n, int max_loras, int slices, int rank, long widest) {
+    UPlan p;
+    p.bm = rank <= 32 ? 32 : rank <= 64 ? 64 : 128;
+    p.tile_tokens = 64;
+    const long segs = n < max_loras ? n : max_loras;
+    p.tiles_cap = (int)(ceil_div(n, p.tile_tokens) + segs);
+    const long units = (long)p.tiles_cap * slices;
+    long splits = 768 / (units > 0 ? units : 1);
+    const long steps = ceil_div(widest, kStepK);
+    if (splits > steps / 8) splits = steps / 8;
+    if (splits > 8) splits = 8;
+    if (splits < 1 || units > kCounterWords) splits = 1;
+    p.splits = (int)splits;
+    p.slot_bytes = splits > 1 ? sizeof(float) * (size_t)units * splits * p.bm * p.tile_tokens : 0;
+    return p;
+}
+
+struct Layout {
+    size_t counters, segs, num_tiles, tiles, s, u, slots, total;
+};
+Layout layout(long n, int max_loras, int slices, int rank, size_t slot_bytes, int tiles_cap, bool backward) {
+    Layout l;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = at;
+        at += up(bytes);
+        return o;
+    };
+    l.counters = take(sizeof(int32_t) * kCounterWords);
+    l.segs = take(backward ? sizeof(SegEntry) * (size_t)max_loras : 0);
+    l.num_tiles = take(backward ? sizeof(int32_t) : 0);
+    l.tiles = take(backward ? sizeof(UTile) * (size_t)tiles_cap : 0);
+    const size_t rows = sizeof(uint16_t) * 2 * (size_t)slices * (size_t)n * (size_t)rank;
+    l.s = take(rows);
+    l.u = take(backward ? rows : 0);
+    l.slots = take(slot_bytes);
+    l.total = at;
+    return l;
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+int check_sizes(int num_tokens, int max_loras, int hidden, const int *slice_widths, int num_slices, int rank) {
+    if (num_tokens < 0 || num_tokens > LORA_MAX_TOKENS) return LORA_ERR_NUM_TOKENS;
+    if (max_loras < 1 || max_loras > LORA_MAX_LORAS) return LORA_ERR_MAX_LORAS;
+    if (num_slices < 1 || num_slices > LORA_MAX_SLICES) return LORA_ERR_SLICES;
+    if (!slice_widths) return LORA_ERR_NULL;
+    if (hidden < 8 || hidden % 8) return LORA_ERR_SHAPE;
+    if (rank < 8 || rank > LORA_MAX_RANK || rank % 8) return LORA_ERR_SHAPE;
+    for (int i = 0; i < num_slices; ++i)
+        if (slice_widths[i] <= 0 || slice_widths[i] % 8) return LORA_ERR_SHAPE;
+    return LORA_OK;
+}
+
+// Everything the forward and the backward pass check alike.
+int check_call(int64_t ldx, int num_tokens, int hidden, const void *w, int64_t ldw, int out, const void *const *lora_a,
+               const void *const *lora_b, const int *slice_widths, int num_slices, int rank, int64_t ldy,
+               int offset_start, const lora_meta_t *meta, const void *workspace) {
+    int st = check_meta(meta);
+    if (st) return st;
+    if (meta->num_tokens < 0 || num_tokens != meta->num_tokens) return LORA_ERR_NUM_TOKENS;
+    if ((st = check_sizes(num_tokens, meta->max_loras, hidden, slice_widths, num_slices, rank))) return st;
+    if (!w || !lora_a || !lora_b || !workspace) return LORA_ERR_NULL;
+    if (ldx < hidden || ldx % 8 || ldw < hidden || ldw % 8 || out < 8 || out % 8 || ldy < out || ldy % 8)
+        return LORA_ERR_SHAPE;
+    if (offset_start < 0 || offset_start % 8) return LORA_ERR_SHAPE;
+    int64_t end = offset_start;
+    for (int i = 0; i < num_slices; ++i) {
+        end += slice_widths[i];
+        if (!lora_a[i] || !lora_b[i]) return LORA_ERR_NULL;
+        if (!aligned16(lora_a[i]) || !aligned16(lora_b[i])) return LORA_ERR_ALIGN;
+    }
+    if (end > out) return LORA_ERR_SHAPE;
+    if (!aligned16(w)) return LORA_ERR_ALIGN;
+    if ((reinterpret_cast<uintptr_t>(workspace) & (kRound - 1)) != 0) return LORA_ERR_BUFFER;
+    return LORA_OK;
+}
+
+long sum_widths(const int *w, int n) {
+    long s = 0;
+    for (int i = 0; i < n; ++i) s += w[i];
+    return s;
+}
+int widest(const int *w, int n) {
+    int s = 0;
+    for (int i = 0; i < n; ++i) s = w[i] > s ? w[i] : s;
+    return s;
+}
+
+hipError_t launch_pack(const lora_meta_t *meta, const MetaView &view, const float *buf, uint16_t *packed, int slices,
+                       int rank, char *ws, const Layout *l, const UPlan *u, hipStream_t s) {
+    PackArgs a;
+    memset(&a, 0, sizeof a);
+    a.meta = view;
+    a.ids = meta->token_lora_mapping;
+    a.buf = buf;
+    a.packed = packed;
+    if (l) {
+        a.segs = reinterpret_cast<SegEntry *>(ws + l->segs);
+        a.tiles = reinterpret_cast<UTile *>(ws + l->tiles);
+        a.num_tiles = reinterpret_cast<int32_t *>(ws + l->num_tiles);
+        a.tiles_cap = u->tiles_cap;
+        a.tile_tokens = u->tile_tokens;
+    }
+    a.num_tokens = meta->num_tokens;
+    a.rank = rank;
+    a.slices = slices;
+    a.max_loras = meta->max_loras;
+    const long work = (long)slices * meta->num_tokens * (rank / 4);
+    long grid = ceil_div(work, kPackThreads);
+    if (grid > 2048) grid = 2048;
+    if (grid < 1) grid = 1;
+    hipLaunchKernelGGL(pack_kernel, dim3((unsigned)grid), dim3(kPackThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+template <bool BWD>
+hipError_t launch_linear(LinearArgs &a, const LinearPlan &p, hipStream_t s) {
+    a.mtiles = p.mtiles;
+    a.ntiles = p.ntiles;
+    a.splits = p.splits;
+    a.split_steps = p.split_steps;
+    a.group = 8;
+    const unsigned grid = tile_grid((long)p.mtiles * p.ntiles) * (unsigned)p.splits;
+    switch (p.tile) {
+        case kBig: {
+            using T = Tile<256, 256, 4, 2, BWD, false>;
+            return launch_tiles<linear_kernel<T, BWD>>(grid, T::kThreads, T::kLds, s, a);
+        }
+        case kMid: {
+            using T = Tile<128, 128, 2, 2, BWD, false>;
+            return launch_tiles<linear_kernel<T, BWD>>(grid, T::kThreads, T::kLds, s, a);
+        }
+        default: {
+            using T = Tile<128, 32, 2, 2, BWD, false>;
+            return launch_tiles<linear_kernel<T, BWD>>(grid, T::kThreads, T::kLds, s, a);
+        }
+    }
+}
+
+template <int BR>
+hipError_t launch_u(const UArgs &a, const UPlan &p, hipStream_t s) {
+    using T = Tile<BR, 64, (BR == 32 ? 1 : 2), (BR == 32 ? 4 : 2), true, false>;
+    return launch_tiles<u_kernel<T>>((unsigned)((long)p.tiles_cap * a.slices * p.splits), T::kThreads, T::kLds, s, a);
+}
+
+template <int BR, bool DA>
+hipError_t launch_grad(GradArgs &a, int max_loras, hipStream_t s) {
+    using T = typename std::conditional<DA, Tile<128, BR, (BR == 16 ? 4 : 2), (BR == 16 ? 1 : 2), true, true, 2>,
+                                        Tile<BR, 128, (BR == 16 ? 1 : 2), (BR == 16 ? 4 : 2), true, true, 1>>::type;
+    a.tiles_before[0] = 0;
+    for (int i = 0; i < a.slices; ++i) a.tiles_before[i + 1] = a.tiles_before[i] + (int)ceil_div(a.width[i], 128);
+    const long grid = (long)max_loras * a.tiles_before[a.slices];
+    return launch_tiles<grad_kernel<T, DA>>((unsigned)grid, T::kThreads, T::kLds, s, a);
+}
+template <bool DA>
+hipError_t launch_grads(GradArgs &a, int max_loras, hipStream_t s) {
+    if (a.rank <= 16) return launch_grad<16, DA>(a, max_loras, s);
+    if (a.rank <= 32) return launch_grad<32, DA>(a, max_loras, s);
+    if (a.rank <= 64) return launch_grad<64, DA>(a, max_loras, s);
+    return launch_grad<128, DA>(a, max_loras, s);
+}
+
+}  // namespace
+}  // namespace lora
+
+using namespace lora;
+
+extern "C" {
+
+size_t lora_linear_workspace_bytes(int num_tokens, int max_loras, int hidden, const int *slice_widths, int num_slices,
+                                   int rank, int backward) {
+    if (check_sizes(num_tokens, max_loras, hidden, slice_widths, num_slices, rank)) return 0;
+    const long out = sum_widths(slice_widths, num_slices), n = num_tokens;
+    size_t slots = plan_linear(n, out, hidden, true).slot_bytes;
+    const UPlan u = plan_u(n, max_loras, num_slices, rank, widest(slice_widths, num_slices));
+    if (backward) {
+        const size_t d = plan_linear(n, hidden, out, true).slot_bytes;
+        slots = slots > d ? slots : d;
+        slots = slots > u.slot_bytes ? slots : u.slot_bytes;
+    }
+    return layout(n, max_loras, num_slices, rank, slots, u.tiles_cap, backward != 0).total;
+}
+
+int lora_linear(const void *x, int64_t ldx, int num_tokens, int hidden, const void *w, int64_t ldw, int out_features,
+                const void *w_bias, const void *const *lora_a, const void *const *lora_b, const void *const *bias,
+                const int *slice_widths, int num_slices, int rank, float *buf, void *y, int64_t ldy, int offset_start,
+                const lora_meta_t *meta, float scale, void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    int st = check_call(ldx, num_tokens, hidden, w, ldw, out_features, lora_a, lora_b, slice_widths, num_slices, rank,
+                        ldy, offset_start, meta, workspace);
+    if (st) return st;
+    if (w_bias && !aligned16(w_bias)) return LORA_ERR_ALIGN;
+    for (int i = 0; bias && i < num_slices; ++i)
+        if (bias[i] && !aligned16(bias[i])) return LORA_ERR_ALIGN;
+    if (num_tokens > 0 && (!x || !buf || !y)) return LORA_ERR_NULL;
+    if (num_tokens > 0 && (!aligned16(x) || !aligned16(buf) || !aligned16(y))) return LORA_ERR_ALIGN;
+    LinearPlan p = plan_linear(num_tokens, out_features, hidden, true);
+    Layout l = layout(num_tokens, meta->max_loras, num_slices, rank, p.slot_bytes, 0, false);
+    if (l.total > workspace_bytes) {   // sized for narrower outputs: no K split
+        p = plan_linear(num_tokens, out_features, hidden, false);
+        l = layout(num_tokens, meta->max_loras, num_slices, rank, 0, 0, false);
+        if (l.total > workspace_bytes) return LORA_ERR_BUFFER;
+    }
+    if (num_tokens == 0) return LORA_OK;
+    char *ws = static_cast<char *>(workspace);
+    if ((st = shrink_fresh(x, ldx, num_tokens, hidden, lora_a, num_slices, rank, buf, meta, scale, stream))) return st;
+    const MetaView view = view_of(meta);
+    uint16_t *packed = reinterpret_cast<uint16_t *>(ws + l.s);
+    if (launch_pack(meta, view, buf, packed, num_slices, rank, ws, nullptr, nullptr, stream) != hipSuccess)
+        return LORA_ERR_LAUNCH;
+    LinearArgs a;
+    memset(&a, 0, sizeof a);
+    a.meta = view;
+    a.ids = meta->token_lora_mapping;
+    a.in = static_cast<const uint16_t *>(x);
+    a.ldin = ldx;
+    a.w = static_cast<const uint16_t *>(w);
+    a.ldw = ldw;
+    a.w_bias = static_cast<const uint16_t *>(w_bias);
+    int off = offset_start;
+    for (int i = 0; i < num_slices; ++i) {
+        a.lw[i] = static_cast<const uint16_t *>(lora_b[i]);
+        a.bias[i] = bias ? static_cast<const uint16_t *>(bias[i]) : nullptr;
+        a.width[i] = slice_widths[i];
+        a.col[i] = off;
+        off += slice_widths[i];
+    }
+    a.packed = packed;
+    a.y = static_cast<uint16_t *>(y);
+    a.ldy = ldy;
+    a.slots = reinterpret_cast<float *>(ws + l.slots);
+    a.counters = reinterpret_cast<int32_t *>(ws + l.counters);
+    a.num_tokens = num_tokens;
+    a.cols = out_features;
+    a.k = hidden;
+    a.rank = rank;
+    a.slices = num_slices;
+    a.max_loras = meta->max_loras;
+    return launch_linear<false>(a, p, stream) == hipSuccess ? LORA_OK : LORA_ERR_LAUNCH;
+}
+
+int lora_linear_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx, int num_tokens, int hidden,
+                         const void *w, int64_t ldw, int out_features, const void *const *lora_a,
+                         const void *const *lora_b, const int *slice_widths, int num_slices, int rank,
+                         const float *buf, float *dbuf, void *dx, int64_t lddx, void *const *da, void *const *db,
+                         void *const *dbias, int offset_start, const lora_meta_t *meta, float scale, void *workspace,
+                         size_t workspace_bytes, hipStream_t stream) {
+    int st = check_call(ldx, num_tokens, hidden, w, ldw, out_features, lora_a, lora_b, slice_widths, num_slices, rank,
+                        lddy, offset_start, meta, workspace);
+    if (st) return st;
+    if (!da || !db) return LORA_ERR_NULL;
+    for (int i = 0; i < num_slices; ++i) {
+        if (!da[i] || !db[i]) return LORA_ERR_NULL;
+        if (!aligned16(da[i]) || !aligned16(db[i])) return LORA_ERR_ALIGN;
+        if (dbias && dbias[i] && !aligned16(dbias[i])) return LORA_ERR_ALIGN;
+    }
+    if (dx && (lddx < hidden || lddx % 8)) return LORA_ERR_SHAPE;
+    if (num_tokens > 0 && (!dy || !x || !buf || !dbuf)) return LORA_ERR_NULL;
+    if (num_tokens > 0 && (!aligned16(dy) || !aligned16(x) || !aligned16(buf) || !aligned16(dbuf) || !aligned16(dx)))
+        return LORA_ERR_ALIGN;
+    LinearPlan p = plan_linear(num_tokens, hidden, out_features, true);
+    UPlan u = plan_u(num_tokens, meta->max_loras, num_slices, rank, widest(slice_widths, num_slices));
+    auto make = [&] {
+        return layout(num_tokens, meta->max_loras, num_slices, rank, p.slot_bytes > u.slot_bytes ? p.slot_bytes : u.slot_bytes,
+                      u.tiles_cap, true);
+    };
+    Layout l = make();
+    if (l.total > workspace_bytes) {
+        p = plan_linear(num_tokens, hidden, out_features, false);
+        l = make();
+        if (l.total > workspace_bytes) return LORA_ERR_BUFFER;
+    }
+    char *ws = static_cast<char *>(workspace);
+    const MetaView view = view_of(meta);
+    uint16_t *s = reinterpret_cast<uint16_t *>(ws + l.s), *up = reinterpret_cast<uint16_t *>(ws + l.u);
+    float *slots = reinterpret_cast<float *>(ws + l.slots);
+    int32_t *counters = reinterpret_cast<int32_t *>(ws + l.counters);
+    const SegEntry *segs = reinterpret_cast<const SegEntry *>(ws + l.segs);
+    // (an empty batch still writes the adapters' gradients: zeros)
+    if (launch_pack(meta, view, buf, s, num_slices, rank, ws, &l, &u, stream) != hipSuccess) return LORA_ERR_LAUNCH;
+    int cols[LORA_MAX_SLICES], off = offset_start;
+    for (int i = 0; i < num_slices; ++i) {
+        cols[i] = off;
+        off += slice_widths[i];
+    }
+    if (num_tokens > 0) {
+        UArgs ua;
+        memset(&ua, 0, sizeof ua);
+        ua.tiles = reinterpret_cast<const UTile *>(ws + l.tiles);
+        ua.num_tiles = reinterpret_cast<const int32_t *>(ws + l.num_tiles);
+        ua.sorted = view.sorted;
+        ua.dy = static_cast<const uint16_t *>(dy);
+        ua.lddy = lddy;
+        for (int i = 0; i < num_slices; ++i) {
+            ua.b[i] = static_cast<const uint16_t *>(lora_b[i]);
+            ua.width[i] = slice_widths[i];
+            ua.col[i] = cols[i];
+        }
+        ua.dbuf = dbuf;
+        ua.packed = up;
+        ua.slots = slots;
+        ua.counters = counters;
+        ua.num_tokens = num_tokens;
+        ua.rank = rank;
+        ua.slices = num_slices;
+        ua.splits = u.splits;
+        ua.scale = scale;
+        const hipError_t e = u.bm == 32 ? launch_u<32>(ua, u, stream) : u.bm == 64 ? launch_u<64>(ua, u, stream) : launch_u<128>(ua, u, stream);
+        if (e != hipSuccess) return LORA_ERR_LAUNCH;
+    }
+    if (dx && num_tokens > 0) {
+        LinearArgs a;
+        memset(&a, 0, sizeof a);
+        a.meta = view;
+        a.ids = meta->token_lora_mapping;
+        a.in = static_cast<const uint16_t *>(dy);
+        a.ldin = lddy;
+        a.w = static_cast<const uint16_t *>(w);
+        a.ldw = ldw;
+        for (int i = 0; i < num_slices; ++i) a.lw[i] = static_cast<const uint16_t *>(lora_a[i]);
+        a.packed = up;
+        a.y = static_cast<uint16_t *>(dx);
+        a.ldy = lddx;
+        a.slots = slots;
+        a.counters = counters;
+        a.num_tokens = num_tokens;
+        a.cols = hidden;
+        a.k = out_features;
+        a.rank = rank;
+        a.slices = num_slices;
+        a.max_loras = meta->max_loras;
+        if (launch_linear<true>(a, p, stream) != hipSuccess) return LORA_ERR_LAUNCH;
+    }
+    GradArgs g;
+    memset(&g, 0, sizeof g);
+    g.segs = segs;
+    g.sorted = view.sorted;
+    g.num_tokens = num_tokens;
+    g.rank = rank;
+    g.slices = num_slices;
+    g.act = static_cast<const uint16_t *>(x);
+    g.ldact = ldx;
+    g.packed = up;
+    for (int i = 0; i < num_slices; ++i) {
+        g.out[i] = static_cast<uint16_t *>(da[i]);
+        g.width[i] = hidden;
+    }
+    if (launch_grads<true>(g, meta->max_loras, stream) != hipSuccess) return LORA_ERR_LAUNCH;
+    g.act = static_cast<const uint16_t *>(dy);
+    g.ldact = lddy;
+    g.packed = s;
+    for (int i = 0; i < num_slices; ++i) {
+        g.out[i] = static_cast<uint16_t *>(db[i]);
+        g.dbias[i] = dbias ? static_cast<uint16_t *>(dbias[i]) : nullptr;
+        g.width[i] = slice_widths[i];
+        g.col[i] = cols[i];
+    }
+    return launch_grads<false>(g, meta->max_loras, stream) == hipSuccess ? LORA_OK : LORA_ERR_LAUNCH;
+}
+
+}  // extern "C"
