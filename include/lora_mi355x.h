@@ -54,6 +54,7 @@ typedef enum lora_status {
 #define LORA_MAX_SLICES 8
 #define LORA_MAX_RANK 128
 #define LORA_MAX_TOKENS 2097152  /* tokens per batch */
+#define LORA_MAX_VOCAB 16777216  /* rows of a vocabulary matrix */
 
 /*
  * Per-batch kernel metadata (LoRAKernelMeta on the "lora_kernel_metadata"
@@ -360,6 +361,45 @@ int lora_linear_backward(const void *dy, int64_t lddy, const void *x, int64_t ld
  * lora_linear_backward too).  0 if a size is out of range.  Host only. */
 size_t lora_linear_workspace_bytes(int num_tokens, int max_loras, int hidden, const int *slice_widths, int num_slices,
                                    int rank, int backward);
+
+/*
+ * Softmax cross entropy of hidden states against a vocabulary matrix (the
+ * logits of add_lora_logits' base layer on the "punica_gpu" page and the loss
+ * taken of them), in pieces, without the logits in memory.  For every token t:
+ *     z[v] = sum_k x[t][k] w[v][k]                       (float32)
+ *     lse[t]  = log sum_v exp z[v]
+ *     loss[t] = lse[t] - z[targets[t]],  0 for an ignored token (target -1)
+ *   x bf16 [num_tokens][ldx]; w bf16 [vocab][ldw]; targets int32 [num_tokens]
+ *   loss, lse float32 [num_tokens]; any vocab from 1 to LORA_MAX_VOCAB;
+ *   hidden, ldx, ldw multiples of 8, operands 16-byte aligned
+ *   workspace  device memory, 256-byte aligned, of at least
+ *           lora_cross_entropy_workspace_bytes; its contents are ignored
+ * A target outside [-1, vocab) counts as ignored and is reported: the first
+ * int32 of the workspace is LORA_ERR_ID_RANGE after the call, else 0.
+ * Deterministic.
+ */
+int lora_cross_entropy(const void *x, int64_t ldx, int num_tokens, int hidden, const void *w, int64_t ldw, int vocab,
+                       const int32_t *targets, float *loss, float *lse, void *workspace, size_t workspace_bytes,
+                       hipStream_t stream);
+
+/*
+ * The gradients of lora_cross_entropy, from the lse that it wrote:
+ *     g[t][v]  = dloss[t] (exp(z[v] - lse[t]) - [v = targets[t]]), 0 for ignored tokens
+ *     dx[t]    = sum_v g[t][v] w[v]      bf16 [num_tokens][lddx], zeros for ignored tokens
+ *     dw[v]    = sum_t g[t][v] x[t]      bf16 [vocab][lddw]
+ * dx or dw may be NULL (not needed: a frozen vocabulary matrix has no dw).
+ * The logits are computed again piece by piece; g is held as bf16 for one
+ * piece.  Sums are float32 and each result is rounded once.  Ignored tokens'
+ * x, lse and dloss are not used.  Deterministic.
+ */
+int lora_cross_entropy_backward(const void *x, int64_t ldx, int num_tokens, int hidden, const void *w, int64_t ldw,
+                                int vocab, const int32_t *targets, const float *lse, const float *dloss, void *dx,
+                                int64_t lddx, void *dw, int64_t lddw, void *workspace, size_t workspace_bytes,
+                                hipStream_t stream);
+
+/* Bytes of workspace of lora_cross_entropy (backward != 0: of both calls) for
+ * these sizes.  0 if a size is out of range.  Host only. */
+size_t lora_cross_entropy_workspace_bytes(int num_tokens, int hidden, int vocab, int backward);
 
 /* Static description of a status code. */
 const char *lora_status_string(int status);

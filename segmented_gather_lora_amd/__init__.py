@@ -7,7 +7,9 @@ mirror the C ABI in include/lora_mi355x.h:
     lora_meta_bytes, lora_meta_bind, lora_prepare_meta, lora_shrink,
     lora_expand, lora_shrink_expand, lora_prepare_shrink_expand,
     lora_shrink_expand_noalloc, lora_linear, lora_linear_backward,
-    lora_linear_workspace_bytes, lora_status_string, and the measurement aids
+    lora_linear_workspace_bytes, lora_cross_entropy,
+    lora_cross_entropy_backward, lora_cross_entropy_workspace_bytes,
+    lora_status_string, and the measurement aids
     lora_shrink_expand_launches, lora_prepare_meta_launches, lora_probe_read,
     lora_probe_empty
 
@@ -48,7 +50,8 @@ EXPORTED = ("lora_meta_bytes", "lora_meta_bind", "lora_prepare_meta", "lora_shri
             "lora_expand", "lora_shrink_expand", "lora_prepare_shrink_expand", "lora_shrink_expand_launches",
             "lora_prepare_meta_launches",
             "lora_status_string", "lora_probe_read", "lora_probe_empty", "lora_shrink_expand_noalloc",
-            "lora_linear", "lora_linear_backward", "lora_linear_workspace_bytes")
+            "lora_linear", "lora_linear_backward", "lora_linear_workspace_bytes",
+            "lora_cross_entropy", "lora_cross_entropy_backward", "lora_cross_entropy_workspace_bytes")
 
 
 class LoraError(RuntimeError):
@@ -115,6 +118,12 @@ def _load() -> ctypes.CDLL:
     lib.lora_linear_backward.restype = i32
     lib.lora_linear_backward.argtypes = [P, i64, P, i64, i32, i32, P, i64, i32, P, P, P, i32, i32, P, P, P, i64, P, P,
                                          P, i32, META, ctypes.c_float, P, Z, P]
+    lib.lora_cross_entropy_workspace_bytes.restype = Z
+    lib.lora_cross_entropy_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    lib.lora_cross_entropy.restype = i32
+    lib.lora_cross_entropy.argtypes = [P, i64, i32, i32, P, i64, i32, P, P, P, P, Z, P]
+    lib.lora_cross_entropy_backward.restype = i32
+    lib.lora_cross_entropy_backward.argtypes = [P, i64, i32, i32, P, i64, i32, P, P, P, P, i64, P, i64, P, Z, P]
     lib.lora_status_string.restype = ctypes.c_char_p
     lib.lora_status_string.argtypes = [i32]
     lib.lora_probe_read.restype = i32
@@ -544,3 +553,71 @@ def lora_linear_backward(dy, x, w, lora_a: Sequence, lora_b: Sequence, buf, dbuf
                                        _ptr_array(da), _ptr_array(db), None if dbias is None else _ptr_array(dbias),
                                        int(offset_start), ctypes.byref(meta.struct), float(scale),
                                        workspace.data_ptr(), workspace.numel(), _stream(stream)), where)
+
+
+def lora_cross_entropy_workspace_bytes(num_tokens: int, hidden: int, vocab: int, backward: bool = False) -> int:
+    """Bytes of the workspace of lora_cross_entropy (backward: of both calls):
+    a uint8 device tensor."""
+    n = int(_lib().lora_cross_entropy_workspace_bytes(int(num_tokens), int(hidden), int(vocab), 1 if backward else 0))
+    if n == 0:
+        raise LoraError(LORA_ERR_SHAPE, "lora_cross_entropy_workspace_bytes")
+    return n
+
+
+def _on(t, dtype, device, shape, where: str, name: str, contiguous: bool = True) -> None:
+    """A tensor of this type and shape on `device`; rows of unit stride, or contiguous."""
+    if not (t.is_cuda and t.device == device):
+        raise TypeError("%s: %s must be on one GPU with w (got %s)" % (where, name, t.device))
+    if t.dtype != dtype:
+        raise TypeError("%s: %s must be %s (got %s)" % (where, name, dtype, t.dtype))
+    _need(tuple(t.shape) == tuple(shape), LORA_ERR_SHAPE, where, "%s must be %s" % (name, tuple(shape)))
+    _need(t.is_contiguous() if contiguous else t.stride(-1) == 1 or t.numel() <= 1, LORA_ERR_SHAPE, where,
+          "%s must be contiguous%s" % (name, "" if contiguous else " in its last dimension"))
+
+
+def _loss_checks(where: str, x, w, targets, workspace):
+    import torch
+    if not w.is_cuda:
+        raise TypeError("%s: w must be on a GPU (got %s)" % (where, w.device))
+    _need(x.dim() == 2 and w.dim() == 2, LORA_ERR_SHAPE, where, "x and w must be matrices")
+    n, h = x.shape
+    _on(w, torch.bfloat16, w.device, (w.shape[0], h), where, "w", False)
+    _on(x, torch.bfloat16, w.device, (n, h), where, "x", False)
+    _on(targets, torch.int32, w.device, (n,), where, "targets")
+    _workspace(workspace, w.device, where)
+    return n, h, w.shape[0]
+
+
+def lora_cross_entropy(x, w, targets, loss, lse, workspace, stream=None) -> None:
+    """loss[t] = lse[t] - (x @ w^T)[t][targets[t]] (0 where targets[t] is -1) and
+    lse[t] = logsumexp of x @ w^T, without the logits in memory.  x bf16
+    [N][H]; w bf16 [V][H]; targets int32 [N]; loss, lse float32 [N];
+    workspace uint8 of lora_cross_entropy_workspace_bytes, whose first int32
+    reports targets outside [-1, V) (LORA_ERR_ID_RANGE; they are ignored)."""
+    import torch
+    where = "lora_cross_entropy"
+    n, h, v = _loss_checks(where, x, w, targets, workspace)
+    _on(loss, torch.float32, w.device, (n,), where, "loss")
+    _on(lse, torch.float32, w.device, (n,), where, "lse")
+    _check(_lib().lora_cross_entropy(x.data_ptr(), x.stride(0), n, h, w.data_ptr(), w.stride(0), v, targets.data_ptr(),
+                                     loss.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                     _stream(stream)), where)
+
+
+def lora_cross_entropy_backward(x, w, targets, lse, dloss, dx, dw, workspace, stream=None) -> None:
+    """The gradients of lora_cross_entropy for dloss float32 [N], from its lse:
+    dx bf16 [N][H] and dw bf16 [V][H] are written (either may be None)."""
+    import torch
+    where = "lora_cross_entropy_backward"
+    n, h, v = _loss_checks(where, x, w, targets, workspace)
+    _on(lse, torch.float32, w.device, (n,), where, "lse")
+    _on(dloss, torch.float32, w.device, (n,), where, "dloss")
+    if dx is not None:
+        _on(dx, torch.bfloat16, w.device, (n, h), where, "dx", False)
+    if dw is not None:
+        _on(dw, torch.bfloat16, w.device, (v, h), where, "dw", False)
+    _check(_lib().lora_cross_entropy_backward(x.data_ptr(), x.stride(0), n, h, w.data_ptr(), w.stride(0), v,
+                                              targets.data_ptr(), lse.data_ptr(), dloss.data_ptr(),
+                                              None if dx is None else dx.data_ptr(), 0 if dx is None else dx.stride(0),
+                                              None if dw is None else dw.data_ptr(), 0 if dw is None else dw.stride(0),
+                                              workspace.data_ptr(), workspace.numel(), _stream(stream)), where)

@@ -1,0 +1,663 @@
+// lora_loss.hip -- softmax cross entropy of hidden states x against a
+// vocabulary matrix w, in pieces of the vocabulary, without the logits in
+// memory, and its gradients:
+//
+//   z[t] = w x[t],  lse[t] = log sum_v exp z[t][v],  loss[t] = lse[t] - z[t][target[t]]
+//   g[t][v] = dloss[t] (exp(z[t][v] - lse[t]) - [v = target[t]])
+//   dx[t] = w^T g[t],  dw = sum_t g[t] x[t]^T;  ignored tokens: loss 0, g 0
+//
+// Forward: every workgroup computes a tile of logits (vocabulary rows on the M
+// side, tokens on the N side, so that a token's logits lie in one lane and its
+// three neighbours 16 apart), reduces it to one (maximum, sum of exponentials)
+// pair per token in fp32 and forgets it; a second launch joins the pairs of a
+// token over the vocabulary tiles.  The target's logit is picked out by the
+// tile that holds it.
+//
+// Backward: the logits are computed again, a piece of the vocabulary at a time;
+// the epilogue turns them into g (bf16, the piece's buffer), from which two
+// products make the piece's part of dx (fp32 planes, added up in piece order)
+// and the piece's rows of dw.  Only the tokens that count take part: a first
+// launch lists them in order.  g is rounded to bf16 because the matrix
+// products take bf16; its fp32 value is formed from fp32 logits before that.
+#include <string.h>
+
+#include <type_traits>
+
+#include "lora_gemm.h"
+
+namespace lora {
+namespace {
+
+extern __shared__ __attribute__((aligned(1024))) unsigned char g_lds[];
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kNegInf = -__builtin_huge_valf();
+
+// exp(d): the hardware's 2^x of d log2(e).
+__device__ __forceinline__ float exp_of(float d) { return __builtin_amdgcn_exp2f(d * kLog2e); }
+
+struct Stat {
+    float max, sum;   // sum of exp(z - max)
+};
+__device__ __forceinline__ Stat join(const Stat &a, const Stat &b) {
+    const float m = fmaxf(a.max, b.max);
+    const float base = m == kNegInf ? 0.f : m;
+    return Stat{m, a.sum * exp_of(a.max - base) + b.sum * exp_of(b.max - base)};
+}
+
+struct LogitArgs {
+    const uint16_t *x;
+    int64_t ldx;
+    const uint16_t *w;          // the piece's first row
+    int64_t ldw;
+    const int32_t *targets;
+    // statistics
+    Stat *stats;                // [vocabulary tile][n]
+    float *target_logit;        // [n]
+    int32_t *status;
+    // gradient
+    const int32_t *list, *count;   // tokens that count
+    const float *lse, *dloss;
+    uint16_t *g;                // [listed token][ldg]
+    int64_t ldg;
+    int32_t num_tokens, hidden, first, rows, vocab;   // piece: vocabulary [first, first + rows)
+    int32_t mtiles, ntiles, group;
+};
+
+template <class T>
+struct PairOp {
+    Walk<typename T::MSide> wm;
+    Walk<typename T::NSide> wn;
+    __device__ __forceinline__ void mma(const typename T::Half &h, typename T::Acc &acc, int) { T::mma(h, acc); }
+    __device__ __forceinline__ void issue(uint32_t at) {
+        wm.issue(at);
+        wn.issue(at + T::MSide::kBytes);
+    }
+};
+
+template <class T, bool GRAD>
+__global__ __launch_bounds__(T::kThreads) void logit_kernel(LogitArgs a) {
+    __shared__ int s_tok[T::BN];
+    __shared__ Stat s_stat[GRAD ? 1 : T::WM][T::BN];
+    const int tid = threadIdx.x;
+    const int n = GRAD ? *a.count : a.num_tokens;
+    const int ntiles = GRAD ? (n + T::BN - 1) / T::BN : a.ntiles;
+    if (!GRAD && blockIdx.x == 0 && tid == 0) *a.status = 0;
+    TileAt at;
+    if (!tile_at(blockIdx.x, a.mtiles, ntiles, a.group, at)) return;
+    const int m0 = at.m * T::BM, p0 = at.n * T::BN, rows = min(T::BN, n - p0);
+    for (int r = tid; r < T::BN; r += T::kThreads) {
+        const int p = p0 + min(r, rows - 1);
+        s_tok[r] = GRAD ? a.list[p] : p;
+    }
+    __syncthreads();
+    PairOp<T> op;
+#pragma unroll
+    for (int j = 0; j < T::NSide::kInstr; ++j)
+        op.wn.p[j] = a.x + (int64_t)s_tok[T::NSide::row(j)] * a.ldx + T::NSide::elem(j);
+#pragma unroll
+    for (int j = 0; j < T::MSide::kInstr; ++j)
+        op.wm.p[j] = a.w + (int64_t)min(m0 + T::MSide::row(j), a.rows - 1) * a.ldw + T::MSide::elem(j);
+    op.wn.step = op.wm.step = kStepK;
+    op.wn.left = op.wm.left = a.hidden;
+    typename T::Acc acc;
+    clear<T>(acc);
+    mma_loop<T>(op, (a.hidden + kStepK - 1) / kStepK, acc, g_lds);
+
+    if constexpr (!GRAD) {
+#pragma unroll
+        for (int nt = 0; nt < T::NT; ++nt) {
+            const int r = T::n_of(nt);
+            const int target = r < rows ? a.targets[p0 + r] : -1;
+            Stat s{kNegInf, 0.f};
+#pragma unroll
+            for (int mt = 0; mt < T::MT; ++mt) {
+                const int v = m0 + T::m_of(mt);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (v + e >= a.rows) acc[mt][nt][e] = kNegInf;
+                    if (v + e == target && v + e < a.rows) a.target_logit[p0 + r] = acc[mt][nt][e];
+                    s.max = fmaxf(s.max, acc[mt][nt][e]);
+                }
+            }
+            const float base = s.max == kNegInf ? 0.f : s.max;
+#pragma unroll
+            for (int mt = 0; mt < T::MT; ++mt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s.sum += exp_of(acc[mt][nt][e] - base);
+            // the other three lanes of this token
+#pragma unroll
+            for (int d = 16; d < 64; d <<= 1) s = join(s, Stat{__shfl_xor(s.max, d), __shfl_xor(s.sum, d)});
+            if (lane_id() < 16) s_stat[T::wave_m()][r] = s;
+        }
+        __syncthreads();
+        for (int r = tid; r < rows; r += T::kThreads) {
+            Stat s = s_stat[0][r];
+#pragma unroll
+            for (int w = 1; w < T::WM; ++w) s = join(s, s_stat[w][r]);
+            a.stats[(int64_t)at.m * a.num_tokens + p0 + r] = s;
+        }
+    } else {
+#pragma unroll
+        for (int nt = 0; nt < T::NT; ++nt) {
+            const int r = T::n_of(nt);
+            if (r >= rows) continue;
+            const int t = s_tok[r], target = a.targets[t] - a.first;
+            const float lse = a.lse[t], dl = a.dloss[t];
+            uint16_t *row = a.g + (int64_t)(p0 + r) * a.ldg;
+            constexpr int kStep = T::QUADS ? 2 : 1;
+#pragma unroll
+            for (int mt = 0; mt < T::MT; mt += kStep) {
+                const int v = m0 + T::m_of(mt);
+                if (v >= a.ldg) continue;
+                float g[4 * kStep];
+#pragma unroll
+                for (int x = 0; x < 4 * kStep; ++x) {
+                    const float p = exp_of(acc[mt + x / 4][nt][x % 4] - lse);
+                    g[x] = v + x < a.rows ? (p - (v + x == target ? 1.f : 0.f)) * dl : 0.f;
+                }
+                if constexpr (kStep == 2)
+                    *reinterpret_cast<u32x4 *>(row + v) =
+                        u32x4{pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]), pack_bf16(g[4], g[5]), pack_bf16(g[6], g[7])};
+                else
+                    *reinterpret_cast<u32x2g *>(row + v) = u32x2g{pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3])};
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- joining the pieces' statistics
+
+struct JoinArgs {
+    const Stat *stats;
+    const float *target_logit;
+    const int32_t *targets;
+    float *loss, *lse;
+    int32_t *status;
+    int32_t num_tokens, mtiles, vocab;
+};
+
+// 16 tokens a workgroup, 16 threads each.
+__global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
+    __shared__ Stat s_part[16][16];
+    const int tok = threadIdx.x % 16, part = threadIdx.x / 16, t = blockIdx.x * 16 + tok;
+    Stat s{kNegInf, 0.f};
+    if (t < a.num_tokens)
+        for (int k = part; k < a.mtiles; k += 16) s = join(s, a.stats[(int64_t)k * a.num_tokens + t]);
+    s_part[part][tok] = s;
+    __syncthreads();
+    if (part == 0 && t < a.num_tokens) {
+        for (int k = 1; k < 16; ++k) s = join(s, s_part[k][tok]);
+        const float lse = s.max + logf(s.sum);
+        const int target = a.targets[t];
+        a.lse[t] = lse;
+        a.loss[t] = target >= 0 && target < a.vocab ? lse - a.target_logit[t] : 0.f;
+        if (target < -1 || target >= a.vocab)
+            __hip_atomic_store(a.status, (int)LORA_ERR_ID_RANGE, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+}
+
+// ---------------------------------------------------------------- the tokens that count
+
+struct ListArgs {
+    const int32_t *targets;
+    int32_t *list, *place, *count;   // listed tokens; each token's place in the list or -1
+    int32_t num_tokens, vocab;
+};
+constexpr int kListThreads = 1024;
+
+// One workgroup: the list is short against the products it shortens.
+__global__ __launch_bounds__(kListThreads) void list_kernel(ListArgs a) {
+    __shared__ int s_wsum[kListThreads / kWave];
+    int base = 0;
+    for (int t0 = 0; t0 < a.num_tokens; t0 += kListThreads) {
+        const int t = t0 + threadIdx.x;
+        const int target = t < a.num_tokens ? a.targets[t] : -1;
+        const bool counts = target >= 0 && target < a.vocab;
+        const uint64_t mask = ballot(counts);
+        if (lane_id() == 0) s_wsum[wave_id()] = __popcll(mask);
+        __syncthreads();
+        int before = base, all = 0;
+        for (int w = 0; w < kListThreads / kWave; ++w) {
+            before += w < wave_id() ? s_wsum[w] : 0;
+            all += s_wsum[w];
+        }
+        const int p = before + __popcll(mask & lanemask_lt());
+        if (counts) a.list[p] = t;
+        if (t < a.num_tokens) a.place[t] = counts ? p : -1;
+        base += all;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) *a.count = base;
+}
+
+// ---------------------------------------------------------------- dx and dw of a piece
+
+struct DxArgs {
+    const uint16_t *w;          // the piece's first row
+    int64_t ldw;
+    const uint16_t *g;
+    int64_t ldg;
+    float *planes;              // [split][n][hidden]
+    const int32_t *count;
+    int32_t num_tokens, hidden, rows, add;
+    int32_t mtiles, group, splits, split_steps;
+};
+
+// planes[split][p] (+)= sum over the split's vocabulary rows of g[p][v] w[v].
+template <class T>
+__global__ __launch_bounds__(T::kThreads) void dx_kernel(DxArgs a) {
+    const int n = *a.count, ntiles = (n + T::BN - 1) / T::BN;
+    const int split = blockIdx.x % a.splits;
+    TileAt at;
+    if (!tile_at(blockIdx.x / a.splits, a.mtiles, ntiles, a.group, at)) return;
+    const int m0 = at.m * T::BM, p0 = at.n * T::BN, rows = min(T::BN, n - p0);
+    const int all = (a.rows + kStepK - 1) / kStepK, s0 = min(all, split * a.split_steps), s1 = min(all, s0 + a.split_steps);
+    PairOp<T> op;
+#pragma unroll
+    for (int j = 0; j < T::NSide::kInstr; ++j)
+        op.wn.p[j] = a.g + (int64_t)(p0 + min(T::NSide::row(j), rows - 1)) * a.ldg + s0 * kStepK + T::NSide::elem(j);
+    op.wn.step = kStepK;
+#pragma unroll
+    for (int j = 0; j < T::MSide::kInstr; ++j)
+        op.wm.p[j] = a.w + (int64_t)(s0 * kStepK + T::MSide::row(j)) * a.ldw + min(m0 + T::MSide::elem(j), a.hidden - 8);
+    op.wm.step = (int64_t)kStepK * a.ldw;
+    op.wn.left = op.wm.left = a.rows - s0 * kStepK;
+    typename T::Acc acc;
+    clear<T>(acc);
+    mma_loop<T>(op, s1 - s0, acc, g_lds);
+#pragma unroll
+    for (int nt = 0; nt < T::NT; ++nt) {
+        const int r = T::n_of(nt);
+        if (r >= rows) continue;
+        float *row = a.planes + ((int64_t)split * a.num_tokens + p0 + r) * a.hidden;
+#pragma unroll
+        for (int mt = 0; mt < T::MT; ++mt) {
+            const int c = m0 + T::m_of(mt);
+            if (c >= a.hidden) continue;
+            floatx4 *at4 = reinterpret_cast<floatx4 *>(row + c);
+            *at4 = a.add ? *at4 + acc[mt][nt] : acc[mt][nt];
+        }
+    }
+}
+
+struct FinishArgs {
+    const float *planes;
+    const int32_t *place;
+    uint16_t *dx;
+    int64_t lddx;
+    int32_t num_tokens, hidden, splits;
+};
+__global__ __launch_bounds__(256) void finish_kernel(FinishArgs a) {
+    const int per = a.hidden / 8;
+    const int64_t work = (int64_t)a.num_tokens * per;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < work; i += (int64_t)gridDim.x * 256) {
+        const int64_t t = i / per;
+        const int c = (int)(i % per) * 8, p = a.place[t];
+        floatx4 v0 = {0.f, 0.f, 0.f, 0.f}, v1 = v0;
+        if (p >= 0)
+            for (int s = 0; s < a.splits; ++s) {
+                const floatx4 *q = reinterpret_cast<const floatx4 *>(a.planes + ((int64_t)s * a.num_tokens + p) * a.hidden + c);
+                v0 += q[0];
+                v1 += q[1];
+            }
+        *reinterpret_cast<u32x4 *>(a.dx + t * a.lddx + c) =
+            u32x4{pack_bf16(v0[0], v0[1]), pack_bf16(v0[2], v0[3]), pack_bf16(v1[0], v1[1]), pack_bf16(v1[2], v1[3])};
+    }
+}
+
+struct DwArgs {
+    const uint16_t *x;
+    int64_t ldx;
+    const uint16_t *g;
+    int64_t ldg;
+    uint16_t *dw;               // the piece's first row
+    int64_t lddw;
+    const int32_t *list, *count;
+    int32_t num_tokens, hidden, rows;
+    int32_t mtiles, ntiles, group;
+};
+template <class T>
+struct DwOp {
+    GatherWalk<typename T::MSide> wm;
+    Walk<typename T::NSide> wn;
+    __device__ __forceinline__ void mma(const typename T::Half &h, typename T::Acc &acc, int) { T::mma(h, acc); }
+    __device__ __forceinline__ void issue(uint32_t at) {
+        wm.issue(at);
+        wn.issue(at + T::MSide::kBytes);
+    }
+};
+
+// dw[v] = sum over the listed tokens of g[p][v] x[list[p]]: both sides have K
+// (the tokens) as their row index.
+template <class T>
+__global__ __launch_bounds__(T::kThreads) void dw_kernel(DwArgs a) {
+    TileAt at;
+    if (!tile_at(blockIdx.x, a.mtiles, a.ntiles, a.group, at)) return;
+    const int n = *a.count, m0 = at.m * T::BM, v0 = at.n * T::BN;
+    typename T::Acc acc;
+    clear<T>(acc);
+    if (n > 0) {
+        DwOp<T> op;
+        op.wm.base = a.x;
+        op.wm.sorted = a.list;
+        op.wm.ld = a.ldx;
+        op.wm.pos = 0;
+        op.wm.end = n;
+        op.wm.num_tokens = a.num_tokens;
+#pragma unroll
+        for (int j = 0; j < T::MSide::kInstr; ++j) op.wm.col[j] = min(m0 + T::MSide::elem(j), a.hidden - 8);
+        op.wm.fetch();
+#pragma unroll
+        for (int j = 0; j < T::NSide::kInstr; ++j)
+            op.wn.p[j] = a.g + (int64_t)T::NSide::row(j) * a.ldg + min(v0 + T::NSide::elem(j), (int)a.ldg - 8);
+        op.wn.step = (int64_t)kStepK * a.ldg;
+        op.wn.left = n;
+        mma_loop<T>(op, (n + kStepK - 1) / kStepK, acc, g_lds);
+    }
+#pragma unroll
+    for (int nt = 0; nt < T::NT; ++nt) {
+        const int v = v0 + T::n_of(nt);
+        if (v >= a.rows) continue;
+        uint16_t *row = a.dw + (int64_t)v * a.lddw;
+#pragma unroll
+        for (int mt = 0; mt < T::MT; ++mt) {
+            const int c = m0 + T::m_of(mt);
+            const floatx4 q = acc[mt][nt];
+            if (c < a.hidden) *reinterpret_cast<u32x2g *>(row + c) = u32x2g{pack_bf16(q[0], q[1]), pack_bf16(q[2], q[3])};
+        }
+    }
+}
+
+// ---------------------------------------------------------------- plans
+
+constexpr size_t kRound = 256;
+size_t up(size_t v) { return (v + kRound - 1) / kRound * kRound; }
+long ceil_div(long a, long b) { return (a + b - 1) / b; }
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+enum LossTile { kBig, kMid, kSmall };
+// The tile of a product of m by n outputs: 256 x 256 where that fills the CUs
+// (one workgroup each), else 128 x 128, 128 x 32 for few tokens.
+LossTile pick_tile(long m, long n, long splits = 1) {
+    if (n > 128 && ceil_div(m, 256) * ceil_div(n, 256) * splits >= 192) return kBig;
+    return n > 32 ? kMid : kSmall;
+}
+int tile_m(LossTile t) { return t == kBig ? 256 : 128; }
+int tile_n(LossTile t) { return t == kBig ? 256 : t == kMid ? 128 : 32; }
+
+struct LossPlan {
+    LossTile logits, grad, dx, dw;
+    long mtiles;         // vocabulary tiles of the statistics
+    long piece;          // vocabulary rows of a piece (a multiple of 256)
+    int splits, split_steps;
+};
+// g's buffer: 2^27 elements (256 MB, the size of the last-level cache), at
+// least 4096 vocabulary rows.
+constexpr long kPieceElems = 1L << 27, kPieceMin = 4096;
+
+LossPlan plan_loss(long n, long hidden, long vocab) {
+    LossPlan p;
+    p.logits = pick_tile(vocab, n);
+    p.mtiles = ceil_div(vocab, tile_m(p.logits));
+    const long whole = ceil_div(vocab, 256) * 256;
+    long piece = kPieceElems / (n > 0 ? n : 1) / 256 * 256;
+    if (piece < kPieceMin) piece = kPieceMin;
+    if (piece > whole) piece = whole;
+    piece = ceil_div(ceil_div(whole, ceil_div(whole, piece)), 256) * 256;   // pieces of equal size
+    p.piece = piece;
+    p.grad = pick_tile(piece, n);
+    const long steps = piece / kStepK;
+    // dx: K (the piece) is split until the CUs are full, into parts of at least 16 steps
+    auto splits_of = [&](LossTile t) {
+        const long tiles = ceil_div(hidden, tile_m(t)) * ceil_div(n > 0 ? n : 1, tile_n(t));
+        long s = (t == kBig ? 256 : 512) / tiles;
+        if (s > steps / 16) s = steps / 16;
+        if (s > 16) s = 16;
+        return s < 1 ? 1 : s;
+    };
+    p.dx = n > 128 && ceil_div(hidden, 256) * ceil_div(n, 256) * splits_of(kBig) >= 192 ? kBig : n > 32 ? kMid : kSmall;
+    const long s = splits_of(p.dx);
+    p.split_steps = (int)ceil_div(steps, s);
+    p.splits = (int)ceil_div(steps, p.split_steps);
+    p.dw = pick_tile(hidden, piece);
+    return p;
+}
+
+struct LossLayout {
+    size_t status, target_logit, stats, list, place, count, g, planes, total;
+};
+LossLayout loss_layout(const LossPlan &p, long n, long hidden, bool train) {
+    LossLayout l;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = at;
+        at += up(bytes);
+        return o;
+    };
+    l.status = take(sizeof(int32_t));
+    // the forward pass's areas and the backward pass's are not in use together
+    const size_t begin = at;
+    l.target_logit = take(sizeof(float) * (size_t)n);
+    l.stats = take(sizeof(Stat) * (size_t)p.mtiles * (size_t)n);
+    const size_t forward = at;
+    at = begin;
+    l.list = take(train ? sizeof(int32_t) * (size_t)n : 0);
+    l.place = take(train ? sizeof(int32_t) * (size_t)n : 0);
+    l.count = take(train ? sizeof(int32_t) : 0);
+    l.g = take(train ? sizeof(uint16_t) * (size_t)n * (size_t)p.piece : 0);
+    l.planes = take(train ? sizeof(float) * (size_t)p.splits * (size_t)n * (size_t)hidden : 0);
+    l.total = at > forward ? at : forward;
+    return l;
+}
+
+int check_sizes(int num_tokens, int hidden, int vocab) {
+    if (num_tokens < 0 || num_tokens > LORA_MAX_TOKENS) return LORA_ERR_NUM_TOKENS;
+    if (hidden < 8 || hidden % 8 || vocab < 1 || vocab > LORA_MAX_VOCAB) return LORA_ERR_SHAPE;
+    return LORA_OK;
+}
+int check_loss(const void *x, int64_t ldx, int num_tokens, int hidden, const void *w, int64_t ldw, int vocab,
+               const int32_t *targets, const void *workspace, size_t workspace_bytes, bool train) {
+    const int st = check_sizes(num_tokens, hidden, vocab);
+    if (st) return st;
+    if (ldx < hidden || ldx % 8 || ldw < hidden || ldw % 8) return LORA_ERR_SHAPE;
+    if (!w || !workspace || (num_tokens > 0 && (!x || !targets))) return LORA_ERR_NULL;
+    if (!aligned16(w) || (num_tokens > 0 && !aligned16(x))) return LORA_ERR_ALIGN;
+    if ((reinterpret_cast<uintptr_t>(workspace) & (kRound - 1)) != 0) return LORA_ERR_BUFFER;
+    const LossPlan p = plan_loss(num_tokens, hidden, vocab);
+    if (loss_layout(p, num_tokens, hidden, train).total > workspace_bytes) return LORA_ERR_BUFFER;
+    return LORA_OK;
+}
+
+// Runs F with the tile type of `t` (M side strided: MS, N side: NS).
+template <bool MS, bool NS, class F>
+hipError_t with_tile(LossTile t, F f) {
+    switch (t) {
+        case kBig: return f(Tile<256, 256, 4, 2, MS, NS>{});
+        case kMid: return f(Tile<128, 128, 2, 2, MS, NS>{});
+        default: return f(Tile<128, 32, 2, 2, MS, NS>{});
+    }
+}
+
+}  // namespace
+}  // namespace lora
+
+using namespace lora;
+
+extern "C" {
+
+size_t lora_cross_entropy_workspace_bytes(int num_tokens, int hidden, int vocab, int backward) {
+    if (check_sizes(num_tokens, hidden, vocab)) return 0;
+    return loss_layout(plan_loss(num_tokens, hidden, vocab), num_tokens, hidden, backward != 0).total;
+}
+
+int lora_cross_entropy(const void *x, int64_t ldx, int num_tokens, int hidden, const void *w, int64_t ldw, int vocab,
+                       const int32_t *targets, float *loss, float *lse, void *workspace, size_t workspace_bytes,
+                       hipStream_t stream) {
+    const int st = check_loss(x, ldx, num_tokens, hidden, w, ldw, vocab, targets, workspace, workspace_bytes, false);
+    if (st) return st;
+    if (num_tokens > 0 && (!loss || !lse)) return LORA_ERR_NULL;
+    if (num_tokens == 0) return LORA_OK;
+    const LossPlan p = plan_loss(num_tokens, hidden, vocab);
+    const LossLayout l = loss_layout(p, num_tokens, hidden, false);
+    char *ws = static_cast<char *>(workspace);
+    LogitArgs a;
+    memset(&a, 0, sizeof a);
+    a.x = static_cast<const uint16_t *>(x);
+    a.ldx = ldx;
+    a.w = static_cast<const uint16_t *>(w);
+    a.ldw = ldw;
+    a.targets = targets;
+    a.stats = reinterpret_cast<Stat *>(ws + l.stats);
+    a.target_logit = reinterpret_cast<float *>(ws + l.target_logit);
+    a.status = reinterpret_cast<int32_t *>(ws + l.status);
+    a.num_tokens = num_tokens;
+    a.hidden = hidden;
+    a.rows = a.vocab = vocab;
+    a.mtiles = (int)p.mtiles;
+    a.ntiles = (int)ceil_div(num_tokens, tile_n(p.logits));
+    a.group = 8;
+    const unsigned grid = tile_grid((long)a.mtiles * a.ntiles);
+    hipError_t e = with_tile<false, false>(p.logits, [&](auto tile) {
+        using T = decltype(tile);
+        return launch_tiles<logit_kernel<T, false>>(grid, T::kThreads, T::kLds, stream, a);
+    });
+    if (e != hipSuccess) return LORA_ERR_LAUNCH;
+    JoinArgs j;
+    j.stats = a.stats;
+    j.target_logit = a.target_logit;
+    j.targets = targets;
+    j.loss = loss;
+    j.lse = lse;
+    j.status = a.status;
+    j.num_tokens = num_tokens;
+    j.mtiles = a.mtiles;
+    j.vocab = vocab;
+    hipLaunchKernelGGL(join_kernel, dim3((unsigned)ceil_div(num_tokens, 16)), dim3(256), 0, stream, j);
+    return hipGetLastError() == hipSuccess ? LORA_OK : LORA_ERR_LAUNCH;
+}
+
+int lora_cross_entropy_backward(const void *x, int64_t ldx, int num_tokens, int hidden, const void *w, int64_t ldw,
+                                int vocab, const int32_t *targets, const float *lse, const float *dloss, void *dx,
+                                int64_t lddx, void *dw, int64_t lddw, void *workspace, size_t workspace_bytes,
+                                hipStream_t stream) {
+    const int st = check_loss(x, ldx, num_tokens, hidden, w, ldw, vocab, targets, workspace, workspace_bytes, true);
+    if (st) return st;
+    if ((dx && (lddx < hidden || lddx % 8)) || (dw && (lddw < hidden || lddw % 8))) return LORA_ERR_SHAPE;
+    if (num_tokens > 0 && (!lse || !dloss)) return LORA_ERR_NULL;
+    if (!aligned16(dx) || !aligned16(dw)) return LORA_ERR_ALIGN;
+    if (!dx && !dw) return LORA_OK;
+    const LossPlan p = plan_loss(num_tokens, hidden, vocab);
+    const LossLayout l = loss_layout(p, num_tokens, hidden, true);
+    char *ws = static_cast<char *>(workspace);
+    ListArgs la;
+    la.targets = targets;
+    la.list = reinterpret_cast<int32_t *>(ws + l.list);
+    la.place = reinterpret_cast<int32_t *>(ws + l.place);
+    la.count = reinterpret_cast<int32_t *>(ws + l.count);
+    la.num_tokens = num_tokens;
+    la.vocab = vocab;
+    hipLaunchKernelGGL(list_kernel, dim3(1), dim3(kListThreads), 0, stream, la);
+    if (hipGetLastError() != hipSuccess) return LORA_ERR_LAUNCH;
+    uint16_t *g = reinterpret_cast<uint16_t *>(ws + l.g);
+    float *planes = reinterpret_cast<float *>(ws + l.planes);
+    for (long first = 0; first < vocab; first += p.piece) {
+        const int rows = (int)(vocab - first < p.piece ? vocab - first : p.piece);
+        const uint16_t *wp = static_cast<const uint16_t *>(w) + first * ldw;
+        const long ldg = p.piece;
+        if (num_tokens > 0) {
+            LogitArgs a;
+            memset(&a, 0, sizeof a);
+            a.x = static_cast<const uint16_t *>(x);
+            a.ldx = ldx;
+            a.w = wp;
+            a.ldw = ldw;
+            a.targets = targets;
+            a.list = la.list;
+            a.count = la.count;
+            a.lse = lse;
+            a.dloss = dloss;
+            a.g = g;
+            a.ldg = ldg;
+            a.num_tokens = num_tokens;
+            a.hidden = hidden;
+            a.first = (int)first;
+            a.rows = rows;
+            a.vocab = vocab;
+            a.mtiles = (int)ceil_div(rows, tile_m(p.grad));
+            a.ntiles = (int)ceil_div(num_tokens, tile_n(p.grad));
+            a.group = 8;
+            const unsigned grid = tile_grid((long)a.mtiles * a.ntiles);
+            if (with_tile<false, false>(p.grad, [&](auto tile) {
+                    using T = decltype(tile);
+                    return launch_tiles<logit_kernel<T, true>>(grid, T::kThreads, T::kLds, stream, a);
+                }) != hipSuccess)
+                return LORA_ERR_LAUNCH;
+        }
+        if (dx && num_tokens > 0) {
+            DxArgs d;
+            memset(&d, 0, sizeof d);
+            d.w = wp;
+            d.ldw = ldw;
+            d.g = g;
+            d.ldg = ldg;
+            d.planes = planes;
+            d.count = la.count;
+            d.num_tokens = num_tokens;
+            d.hidden = hidden;
+            d.rows = rows;
+            d.add = first > 0;
+            d.mtiles = (int)ceil_div(hidden, tile_m(p.dx));
+            d.group = 8;
+            d.splits = p.splits;
+            d.split_steps = p.split_steps;
+            const unsigned grid = tile_grid((long)d.mtiles * ceil_div(num_tokens, tile_n(p.dx))) * (unsigned)p.splits;
+            if (with_tile<true, false>(p.dx, [&](auto tile) {
+                    using T = decltype(tile);
+                    return launch_tiles<dx_kernel<T>>(grid, T::kThreads, T::kLds, stream, d);
+                }) != hipSuccess)
+                return LORA_ERR_LAUNCH;
+        }
+        if (dw) {
+            DwArgs d;
+            memset(&d, 0, sizeof d);
+            d.x = static_cast<const uint16_t *>(x);
+            d.ldx = ldx;
+            d.g = g;
+            d.ldg = ldg;
+            d.dw = static_cast<uint16_t *>(dw) + first * lddw;
+            d.lddw = lddw;
+            d.list = la.list;
+            d.count = la.count;
+            d.num_tokens = num_tokens;
+            d.hidden = hidden;
+            d.rows = rows;
+            d.mtiles = (int)ceil_div(hidden, tile_m(p.dw));
+            d.ntiles = (int)ceil_div(rows, tile_n(p.dw));
+            d.group = 8;
+            const unsigned grid = tile_grid((long)d.mtiles * d.ntiles);
+            if (with_tile<true, true>(p.dw, [&](auto tile) {
+                    using T = decltype(tile);
+                    return launch_tiles<dw_kernel<T>>(grid, T::kThreads, T::kLds, stream, d);
+                }) != hipSuccess)
+                return LORA_ERR_LAUNCH;
+        }
+    }
+    if (dx && num_tokens > 0) {
+        FinishArgs f;
+        f.planes = planes;
+        f.place = la.place;
+        f.dx = static_cast<uint16_t *>(dx);
+        f.lddx = lddx;
+        f.num_tokens = num_tokens;
+        f.hidden = hidden;
+        f.splits = p.splits;
+        long grid = ceil_div((long)num_tokens * (hidden / 8), 256);
+        if (grid > 2048) grid = 2048;
+        hipLaunchKernelGGL(finish_kernel, dim3((unsigned)grid), dim3(256), 0, stream, f);
+        if (hipGetLastError() != hipSuccess) return LORA_ERR_LAUNCH;
+    }
+    return LORA_OK;
+}
+
+}  // extern "C"
