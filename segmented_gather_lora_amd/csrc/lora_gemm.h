@@ -27,12 +27,16 @@
 //
 // Per step a wave holds the operands of one 32-wide half in registers while
 // the other half is being read:
-//     read half 1 of step s          MFMA half 0
+//     phase 0   MFMA half 0 of step s, with the reads of half 1 between
 //     wait: step s + 1 has landed, own reads done; barrier
-//     issue the loads of step s + 2 into the stage of step s
-//     read half 0 of step s + 1      MFMA half 1
+//     phase 1   MFMA half 1, with the loads of step s + 2 into the stage of
+//               step s and the reads of half 0 of step s + 1 between
 // so there is one barrier a step and a step's loads have the MFMA time of a
-// whole step to land.
+// whole step to land.  The order inside a phase is pinned: left to itself the
+// compiler puts a phase's reads first, and the eight waves, just past a
+// barrier, then queue at the LDS for as long as the MFMAs of half a phase take.
+// Steps that need more than that (K tails, adapters' ranks) run after the
+// pinned loop in a plain one that holds one half at a time.
 //
 // The direct-to-LDS loads are written in assembly (they have no output
 // registers): the builtin makes the compiler wait for every load in flight
@@ -111,7 +115,7 @@ struct Side {
             return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
         }
         const int r = QUADS ? base + 64 * (t >> 2) + 16 * (l16 >> 2) + 4 * (t & 3) + (l16 & 3) : base + 16 * t + l16;
-        return *(const lds_bf16x8 *)(st + r * 128 + 16 * ((4 * h + g) ^ f_row(QUADS ? l16 & 3 | (l16 >> 2 & 1) << 4 : l16)));
+        return *(const lds_bf16x8 *)(st + r * 128 + 16 * ((4 * h + g) ^ f_row(QUADS ? (l16 & 3) | (l16 >> 2 & 1) << 4 : l16)));
     }
 };
 
@@ -144,27 +148,32 @@ struct Tile {
     struct Half {
         bf16x8 m[MT * (SPLIT == 1 ? 2 : 1)], n[NT * (SPLIT == 2 ? 2 : 1)];
     };
+    static constexpr int kMReads = MT * (SPLIT == 1 ? 2 : 1), kNReads = NT * (SPLIT == 2 ? 2 : 1);
+    static constexpr int kReads = kMReads + kNReads, kLoads = MSide::kInstr + NSide::kInstr;
+    // operand i of a half: the M side's, then the N side's
+    __device__ __forceinline__ static void read_one(Half &r, const lds_byte *st, int h, int i) {
+        if (i < kMReads)
+            r.m[i] = MSide::read(st, (i < MT ? 0 : BM) + wave_m() * (BM / WM), i % MT, h);
+        else
+            r.n[i - kMReads] = NSide::read(st + MSide::kBytes, (i - kMReads < NT ? 0 : BN) + wave_n() * (BN / WN),
+                                           (i - kMReads) % NT, h);
+    }
     __device__ __forceinline__ static void read(Half &r, const lds_byte *st, int h) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) r.n[t] = NSide::read(st + MSide::kBytes, wave_n() * (BN / WN), t, h);
-        if constexpr (SPLIT == 2)
+        for (int i = 0; i < kReads; ++i) read_one(r, st, h, i);
+    }
+    // the products of one 16-row tile of the N side
+    __device__ __forceinline__ static void mma_n(const Half &r, Acc &acc, int nt) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t) r.n[NT + t] = NSide::read(st + MSide::kBytes, BN + wave_n() * (BN / WN), t, h);
-#pragma unroll
-        for (int t = 0; t < MT; ++t) r.m[t] = MSide::read(st, wave_m() * (BM / WM), t, h);
-        if constexpr (SPLIT == 1)
-#pragma unroll
-            for (int t = 0; t < MT; ++t) r.m[MT + t] = MSide::read(st, BM + wave_m() * (BM / WM), t, h);
+        for (int mt = 0; mt < MT; ++mt) {
+            acc[mt][nt] = mfma16x16x32(r.m[mt], r.n[nt], acc[mt][nt]);
+            if constexpr (SPLIT == 1) acc[mt][nt] = mfma16x16x32(r.m[MT + mt], r.n[nt], acc[mt][nt]);
+            if constexpr (SPLIT == 2) acc[mt][nt] = mfma16x16x32(r.m[mt], r.n[NT + nt], acc[mt][nt]);
+        }
     }
     __device__ __forceinline__ static void mma(const Half &r, Acc &acc) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                acc[mt][nt] = mfma16x16x32(r.m[mt], r.n[nt], acc[mt][nt]);
-                if constexpr (SPLIT == 1) acc[mt][nt] = mfma16x16x32(r.m[MT + mt], r.n[nt], acc[mt][nt]);
-                if constexpr (SPLIT == 2) acc[mt][nt] = mfma16x16x32(r.m[mt], r.n[NT + nt], acc[mt][nt]);
-            }
+        for (int nt = 0; nt < NT; ++nt) mma_n(r, acc, nt);
     }
 };
 
@@ -196,34 +205,74 @@ __device__ __forceinline__ void clear(typename T::Acc &acc) {
         for (int nt = 0; nt < T::NT; ++nt) acc[mt][nt] = floatx4{0.f, 0.f, 0.f, 0.f};
 }
 
+template <int N>
+__device__ __forceinline__ void wait_loads_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
 // Runs `nsteps` steps.  op.issue(stage) copies the next step's operands to the
 // LDS byte address `stage` (called once per step, in order); op.mma(half, acc,
-// s) multiplies a half of step s into the sums.
+// s, h) multiplies half h of step s into the sums.  The first `fast` steps are
+// plain: op.load(stage, i), i < T::kLoads, are their copies one by one,
+// op.next() moves on to the next step, op.mma_n(half, acc, nt) multiplies.
 // All threads of the workgroup call it; LDS of T::kLds bytes at `lds`, which
 // no one else uses until it returns.
 template <class T, class Op>
-__device__ __forceinline__ void mma_loop(Op &op, int nsteps, typename T::Acc &acc, unsigned char *lds_generic) {
+__device__ __forceinline__ void mma_loop(Op &op, int fast, int nsteps, typename T::Acc &acc, unsigned char *lds_generic) {
     const lds_byte *lds = (const lds_byte *)lds_generic;
     const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
     if (nsteps <= 0) return;
     op.issue(base);
-    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-    if (nsteps > 1) op.issue(base + T::kStage);
-    typename T::Half r0, r1;
-    T::read(r0, lds, 0);
-    for (int s = 0; s < nsteps; ++s) {
-        const uint32_t cur = (uint32_t)(s & 1) * T::kStage, nxt = T::kStage - cur;
-        T::read(r1, lds + cur, 1);
-        __builtin_amdgcn_sched_barrier(0);
-        op.mma(r0, acc, s);
-        __builtin_amdgcn_sched_barrier(0);
-        // the own reads of this step's stage are done and the next step has landed, for every wave
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (s + 2 < nsteps) op.issue(base + cur);
-        if (s + 1 < nsteps) T::read(r0, lds + nxt, 0);
-        __builtin_amdgcn_sched_barrier(0);
-        op.mma(r1, acc, s);
-        __builtin_amdgcn_sched_barrier(0);
+    if (nsteps > 1) {
+        op.issue(base + T::kStage);
+        wait_loads_barrier<T::kLoads>();
+    } else {
+        wait_loads_barrier<0>();
+    }
+    int s = 0;
+    if (fast > 2) {
+        constexpr int G = T::NT, R = T::kReads, D = T::kLoads;
+        typename T::Half r0, r1;
+        T::read(r0, lds, 0);
+        for (; s + 2 < fast; ++s) {
+            const uint32_t cur = (uint32_t)(s & 1) * T::kStage, nxt = T::kStage - cur;
+            // half 1's reads end a group or two early: the wait below is for them too
+            constexpr int GA = G > 4 ? G - 2 : G > 1 ? G - 1 : 1;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+#pragma unroll
+                for (int i = g * R / GA; i < (g + 1) * R / GA && i < R; ++i) T::read_one(r1, lds + cur, 1, i);
+                op.mma_n(r0, acc, g);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            // the own reads of this step's stage are done and the next step has landed, for every wave
+            wait_loads_barrier<0>();
+            op.settle();
+            constexpr int GD = G > 1 ? G / 2 : 1;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+#pragma unroll
+                for (int i = g * D / GD; i < (g + 1) * D / GD && i < D; ++i) op.load(base + cur, i);
+#pragma unroll
+                for (int i = g * R / G; i < (g + 1) * R / G; ++i) T::read_one(r0, lds + nxt, 0, i);
+                op.mma_n(r1, acc, g);
+                if (g == G - 1) op.next();
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    }
+    for (; s < nsteps; ++s) {
+        const uint32_t cur = (uint32_t)(s & 1) * T::kStage;
+        typename T::Half r;
+        T::read(r, lds + cur, 0);
+        op.mma(r, acc, s, 0);
+        T::read(r, lds + cur, 1);
+        wait_loads_barrier<0>();
+        if (s + 2 < nsteps) {
+            op.settle();
+            op.issue(base + cur);
+        }
+        op.mma(r, acc, s, 1);
     }
 }
 
@@ -234,18 +283,18 @@ struct Walk {
     const uint16_t *p[S::kInstr];
     int64_t step;
     int left;      // K elements (rows) left from the next step on
-    __device__ __forceinline__ void issue(uint32_t at) {
-        if (left >= kStepK) {
-#pragma unroll
-            for (int j = 0; j < S::kInstr; ++j) dma16(p[j], at + S::dst(j));
-        } else {
-#pragma unroll
-            for (int j = 0; j < S::kInstr; ++j) dma16(S::koff(j) < left ? p[j] : zero_page, at + S::dst(j));
-        }
+    __device__ __forceinline__ void load(uint32_t at, int j) { dma16(p[j], at + S::dst(j)); }
+    __device__ __forceinline__ void next() {
 #pragma unroll
         for (int j = 0; j < S::kInstr; ++j) p[j] += step;
         left -= kStepK;
     }
+    __device__ __forceinline__ void issue(uint32_t at) {
+#pragma unroll
+        for (int j = 0; j < S::kInstr; ++j) dma16(S::koff(j) < left ? p[j] : zero_page, at + S::dst(j));
+        next();
+    }
+    __device__ __forceinline__ void settle() {}
 };
 
 // K rows gathered by the sorted token indices (weight gradients: K runs over a
@@ -264,16 +313,56 @@ struct GatherWalk {
             tok[j] = sorted[p < end ? p : end - 1];
         }
     }
-    __device__ __forceinline__ void issue(uint32_t at) {
+    // the indices are in (all of them now: a wait between the copies would be for the copies too)
+    __device__ __forceinline__ void settle() {
 #pragma unroll
-        for (int j = 0; j < S::kInstr; ++j) {
-            const bool ok = pos + S::koff(j) < end && (unsigned)tok[j] < (unsigned)num_tokens;
-            dma16(ok ? base + (int64_t)tok[j] * ld + col[j] : zero_page, at + S::dst(j));
-        }
+        for (int j = 0; j < S::kInstr; ++j) asm volatile("" : "+v"(tok[j]));
+    }
+    __device__ __forceinline__ const uint16_t *at_token(int j) const {
+        return (unsigned)tok[j] < (unsigned)num_tokens ? base + (int64_t)tok[j] * ld + col[j] : zero_page;
+    }
+    __device__ __forceinline__ void load(uint32_t at, int j) { dma16(at_token(j), at + S::dst(j)); }
+    __device__ __forceinline__ void next() {
         pos += kStepK;
         if (pos < end) fetch();
     }
+    __device__ __forceinline__ void issue(uint32_t at) {
+        settle();
+#pragma unroll
+        for (int j = 0; j < S::kInstr; ++j)
+            dma16(pos + S::koff(j) < end ? at_token(j) : zero_page, at + S::dst(j));
+        next();
+    }
 };
+
+// The two sides of a product whose steps are all plain but the last.
+template <class T, class WM, class WN>
+struct PairOp {
+    WM wm;
+    WN wn;
+    __device__ __forceinline__ void mma(const typename T::Half &h, typename T::Acc &acc, int, int) { T::mma(h, acc); }
+    __device__ __forceinline__ void mma_n(const typename T::Half &h, typename T::Acc &acc, int nt) { T::mma_n(h, acc, nt); }
+    __device__ __forceinline__ void load(uint32_t at, int i) {
+        if (i < T::MSide::kInstr)
+            wm.load(at, i);
+        else
+            wn.load(at + T::MSide::kBytes, i - T::MSide::kInstr);
+    }
+    __device__ __forceinline__ void next() {
+        wm.next();
+        wn.next();
+    }
+    __device__ __forceinline__ void settle() {
+        wm.settle();
+        wn.settle();
+    }
+    __device__ __forceinline__ void issue(uint32_t at) {
+        wm.issue(at);
+        wn.issue(at + T::MSide::kBytes);
+    }
+};
+template <class T>
+using PlainOp = PairOp<T, Walk<typename T::MSide>, Walk<typename T::NSide>>;
 
 // Adds up the partial sums of `splits` workgroups that share a tile, each over
 // its own K steps.  Every workgroup stores its sums in its slot and counts

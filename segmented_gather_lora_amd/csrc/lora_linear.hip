@@ -12,7 +12,7 @@
 // which the prepared metadata holds: a tile of tokens then meets few adapters
 // (its share of the batch plus one), and each of them is a continuation of the
 // tile's K walk: after W's columns come the ranks of every (adapter, slice)
-// the tile meets, with the rows of other adapters' tokens read as zeros.  The
+// the tile meets, each multiplied into its own tokens' rows alone.  The
 // sums stay in the MFMA accumulators, so y and dx are rounded once and are
 // written once; no pass over y adds the adapters afterwards.
 //
@@ -140,73 +140,108 @@ struct LinearArgs {
     float *slots;
     int32_t *counters;
     int32_t num_tokens, cols, k, rank, slices, max_loras;
-    int32_t mtiles, ntiles, group, splits, split_steps;
+    int32_t mtiles, ntiles, group, splits;
 };
 
+// The adapters' share of a tile's K walk is cut into units of 32 K elements,
+// one half of a step: unit (e, sl, kk) holds elements 32 kk .. of [hi | lo] of
+// adapter seg[e] and slice sl.  A step's two units may belong to two adapters,
+// so that a rank of 16 wastes nothing.
+constexpr int kUnitK = kStepK / 2;
+
 template <class T, bool BWD>
-struct LinearOp {
-    Walk<typename T::MSide> wm;
-    Walk<typename T::NSide> wn;
+struct LinearOp : PlainOp<T> {
     const LinearArgs &a;
     const int (*seg)[4];       // LDS: lo, hi (sorted positions), id
-    int main_left, m0, p0;
-    int e, sl, kk, sl0, sl1, ksteps;
+    int main_left, main_steps, m0, p0, nseg;
+    int sl0, sl1, ksteps;      // slices that meet the tile; units of one slice
+    int e, sl, kk;             // next unit to copy
+    int me, mleft;             // next unit to multiply: its adapter and the adapter's units left
 
-    int main_steps, per_seg;
-    // an adapter's steps touch its own tokens' sums alone: one whose weights
+    __device__ __forceinline__ LinearOp(const LinearArgs &args, const int (*segments)[4]) : a(args), seg(segments) {}
+    // the walk over the units starts at unit u
+    __device__ __forceinline__ void start(int u) {
+        const int per = (sl1 - sl0) * ksteps;
+        e = me = u / per;
+        const int in = u % per;
+        sl = sl0 + in / ksteps;
+        kk = in % ksteps;
+        mleft = per - in;
+    }
+    // an adapter's units touch its own tokens' sums alone: one whose weights
     // are not finite stays without effect on the others in the tile
-    __device__ __forceinline__ void mma(const typename T::Half &h, typename T::Acc &acc, int s) {
-        if (s < main_steps) {
-            T::mma(h, acc);
-            return;
+    // (W's last steps go the same way with all rows: a branch here would cost the
+    // registers of a second set of sums)
+    __device__ __forceinline__ void mma(const typename T::Half &h, typename T::Acc &acc, int s, int) {
+        const bool all = s < main_steps, some = all || me < nseg;
+        const int lo = all || !some ? 0 : __builtin_amdgcn_readfirstlane(seg[me][0]) - p0;
+        const int hi = all ? T::BN : !some ? 0 : __builtin_amdgcn_readfirstlane(seg[me][1]) - p0;
+        mma_rows<T>(h, acc, lo, hi);
+        if (!all && --mleft == 0) {
+            mleft = (sl1 - sl0) * ksteps;
+            ++me;
         }
-        const int x = (s - main_steps) / per_seg;
-        mma_rows<T>(h, acc, __builtin_amdgcn_readfirstlane(seg[x][0]) - p0,
-                    __builtin_amdgcn_readfirstlane(seg[x][1]) - p0);
+    }
+    struct Unit {
+        const uint16_t *rows, *weights;   // the slice's packed rows, the adapter's matrix
+        int lo, hi, k0, col, width;
+    };
+    __device__ __forceinline__ Unit unit() {
+        Unit u{a.packed, a.packed, 0, 0, 0, 0, 0};
+        if (e < nseg) {
+            u.lo = __builtin_amdgcn_readfirstlane(seg[e][0]);
+            u.hi = __builtin_amdgcn_readfirstlane(seg[e][1]);
+            u.k0 = kk * kUnitK;
+            u.width = BWD ? a.cols : select_slice(a.width, sl);
+            u.col = BWD ? 0 : select_slice(a.col, sl);
+            u.rows = a.packed + (int64_t)sl * a.num_tokens * 2 * a.rank;
+            u.weights = select_slice(a.lw, sl) + (int64_t)__builtin_amdgcn_readfirstlane(seg[e][2]) * a.rank * u.width;
+            if (++kk == ksteps) {
+                kk = 0;
+                if (++sl == sl1) {
+                    sl = sl0;
+                    ++e;
+                }
+            }
+        }
+        return u;
+    }
+    __device__ __forceinline__ void next() {
+        PlainOp<T>::next();
+        --main_left;
     }
     __device__ __forceinline__ void issue(uint32_t at) {
         if (main_left > 0) {
-            wm.issue(at);
-            wn.issue(at + T::MSide::kBytes);
+            PlainOp<T>::issue(at);
             --main_left;
             return;
         }
-        // one K step of adapter seg[e], slice sl: ranks 64 kk .. of [hi | lo]
-        const int lo = __builtin_amdgcn_readfirstlane(seg[e][0]), hi = __builtin_amdgcn_readfirstlane(seg[e][1]);
-        const int id = __builtin_amdgcn_readfirstlane(seg[e][2]);
-        const int r = a.rank, k0 = kk * kStepK;
-        const uint16_t *lw = select_slice(a.lw, sl);
+        const Unit u0 = unit(), u1 = unit();
+        const int r = a.rank;
 #pragma unroll
         for (int j = 0; j < T::NSide::kInstr; ++j) {
-            const int pos = p0 + T::NSide::row(j), k = k0 + T::NSide::elem(j);
-            const bool ok = pos >= lo && pos < hi && k < 2 * r;
-            dma16(ok ? a.packed + ((int64_t)sl * a.num_tokens + pos) * 2 * r + k : zero_page,
+            const int pos = p0 + T::NSide::row(j), ko = T::NSide::elem(j);
+            const Unit &u = ko < kUnitK ? u0 : u1;
+            const int k = u.k0 + (ko & (kUnitK - 1));
+            dma16(pos >= u.lo && pos < u.hi && k < 2 * r ? u.rows + (int64_t)pos * 2 * r + k : zero_page,
                   at + T::MSide::kBytes + T::NSide::dst(j));
         }
-        const int width = select_slice(a.width, sl), col = select_slice(a.col, sl);
 #pragma unroll
         for (int j = 0; j < T::MSide::kInstr; ++j) {
+            const int ko = T::MSide::koff(j);
+            const Unit &u = ko < kUnitK ? u0 : u1;
+            const int k = u.k0 + (ko & (kUnitK - 1)), kr = k < r ? k : k - r;
+            bool ok = u.hi > 0 && k < 2 * r;
             const uint16_t *src;
-            bool ok;
             if (BWD) {      // A_i: ranks are rows, this side's index is the hidden column
-                const int k = k0 + T::MSide::row(j);
-                int c = m0 + T::MSide::elem(j);
-                c = c < a.cols ? c : a.cols - 8;
-                ok = k < 2 * r;
-                src = lw + ((int64_t)id * r + (k < r ? k : k - r)) * a.cols + c;
+                const int c = m0 + T::MSide::elem(j);
+                src = u.weights + (int64_t)kr * a.cols + (c < a.cols ? c : a.cols - 8);
             } else {        // B_i: rows are the slice's columns, ranks contiguous
-                const int c = m0 + T::MSide::row(j) - col, k = k0 + T::MSide::elem(j);
-                ok = c >= 0 && c < width && k < 2 * r;
-                src = lw + ((int64_t)id * width + c) * r + (k < r ? k : k - r);
+                const int c = m0 + T::MSide::row(j) - u.col;
+                ok = ok && c >= 0 && c < u.width;
+                src = u.weights + (int64_t)c * r + kr;
             }
             dma16(ok ? src : zero_page, at + T::MSide::dst(j));
-        }
-        if (++kk == ksteps) {
-            kk = 0;
-            if (++sl == sl1) {
-                sl = sl0;
-                ++e;
-            }
         }
     }
 };
@@ -249,27 +284,31 @@ __global__ __launch_bounds__(T::kThreads) void linear_kernel(LinearArgs a) {
     __syncthreads();
     const int nseg = __builtin_amdgcn_readfirstlane(min(s_count, T::BN));
 
-    LinearOp<T, BWD> op{{}, {}, a, s_seg, 0, m0, p0, 0, 0, 0, 0, a.slices, (2 * a.rank + kStepK - 1) / kStepK, 0, 1};
-    const int all = (a.k + kStepK - 1) / kStepK;
-    const int s0 = split * a.split_steps, s1 = min(all, s0 + a.split_steps);
-    op.main_left = op.main_steps = max(0, s1 - s0);
-    int ext = 0;
-    if (split == a.splits - 1 && nseg > 0) {
-        if (!BWD) {   // the slices that meet the tile's columns
-            op.sl0 = a.slices;
-            op.sl1 = 0;
-            for (int i = 0; i < a.slices; ++i) {
-                const int c = select_slice(a.col, i);
-                if (c < m0 + T::BM && c + select_slice(a.width, i) > m0) {
-                    op.sl0 = min(op.sl0, i);
-                    op.sl1 = i + 1;
-                }
+    LinearOp<T, BWD> op(a, s_seg);
+    op.m0 = m0;
+    op.p0 = p0;
+    op.nseg = nseg;
+    op.ksteps = (2 * a.rank + kUnitK - 1) / kUnitK;
+    op.sl0 = 0;
+    op.sl1 = a.slices;
+    if (!BWD) {   // the slices that meet the tile's columns
+        op.sl0 = a.slices;
+        op.sl1 = 0;
+        for (int i = 0; i < a.slices; ++i) {
+            const int c = select_slice(a.col, i);
+            if (c < m0 + T::BM && c + select_slice(a.width, i) > m0) {
+                op.sl0 = min(op.sl0, i);
+                op.sl1 = i + 1;
             }
         }
-        op.sl = op.sl0;
-        op.per_seg = max(1, (op.sl1 - op.sl0) * op.ksteps);
-        ext = op.sl1 > op.sl0 ? nseg * (op.sl1 - op.sl0) * op.ksteps : 0;
     }
+    // the tile's steps, W's and then the adapters', are dealt to the splits in equal runs
+    const int units = op.sl1 > op.sl0 ? nseg * (op.sl1 - op.sl0) * op.ksteps : 0;
+    const int all = (a.k + kStepK - 1) / kStepK, total = all + (units + 1) / 2, per = (total + a.splits - 1) / a.splits;
+    const int t0 = min(total, split * per), t1 = min(total, t0 + per);
+    const int s0 = min(t0, all), s1 = min(t1, all);
+    op.main_left = op.main_steps = s1 - s0;
+    if (t1 > all) op.start(2 * (max(t0, all) - all));
 #pragma unroll
     for (int j = 0; j < T::NSide::kInstr; ++j)
         op.wn.p[j] = a.in + (int64_t)s_tok[T::NSide::row(j)] * a.ldin + T::NSide::elem(j) + (int64_t)s0 * kStepK;
@@ -291,7 +330,7 @@ __global__ __launch_bounds__(T::kThreads) void linear_kernel(LinearArgs a) {
 
     typename T::Acc acc;
     clear<T>(acc);
-    mma_loop<T>(op, op.main_left + ext, acc, g_lds);
+    mma_loop<T>(op, min(s1, a.k / kStepK) - s0, t1 - t0, acc, g_lds);
 
     if constexpr (T::BM * T::BN <= 128 * 128) {
         if (a.splits > 1) {
@@ -387,17 +426,6 @@ struct UArgs {
     float scale;
 };
 
-template <class T>
-struct PlainOp {
-    Walk<typename T::MSide> wm;
-    Walk<typename T::NSide> wn;
-    __device__ __forceinline__ void mma(const typename T::Half &h, typename T::Acc &acc, int) { T::mma(h, acc); }
-    __device__ __forceinline__ void issue(uint32_t at) {
-        wm.issue(at);
-        wn.issue(at + T::MSide::kBytes);
-    }
-};
-
 // u_i[t] = scale * B_i[m]^T dy_i[t] for one tile of a segment's tokens and one
 // slice: K is the slice's width, all ranks are in the tile.
 template <class T>
@@ -431,7 +459,7 @@ __global__ __launch_bounds__(T::kThreads) void u_kernel(UArgs a) {
     op.wm.left = width - s0 * kStepK;
     typename T::Acc acc;
     clear<T>(acc);
-    mma_loop<T>(op, s1 - s0, acc, g_lds);
+    mma_loop<T>(op, min(s1, width / kStepK) - s0, s1 - s0, acc, g_lds);
     if (a.splits > 1 && !combine_splits<T>(acc, a.slots + (int64_t)unit * a.splits * (T::BM * T::BN), a.counters + unit,
                                            split, a.splits, ut.rows, &s_flag))
         return;
@@ -487,16 +515,31 @@ struct GradOp {
         wa.issue(at + (DA ? 0 : T::MSide::kBytes));
         wp.issue(at + (DA ? T::MSide::kBytes : 0));
     }
+    __device__ __forceinline__ void load(uint32_t at, int i) {
+        constexpr int nm = T::MSide::kInstr;
+        const uint32_t to = i < nm ? at : at + T::MSide::kBytes;
+        const int j = i < nm ? i : i - nm;
+        if ((i < nm) == DA)
+            wa.load(to, j);
+        else
+            wp.load(to, j);
+    }
+    __device__ __forceinline__ void next() {
+        wa.next();
+        wp.next();
+    }
+    __device__ __forceinline__ void settle() { wa.settle(); }
     // dB: the column sums of dy as one more MFMA row of ones
-    __device__ __forceinline__ void mma(const typename T::Half &h, typename T::Acc &acc, int) {
-        T::mma(h, acc);
+    __device__ __forceinline__ void mma_n(const typename T::Half &h, typename T::Acc &acc, int nt) {
+        T::mma_n(h, acc, nt);
         if constexpr (!DA) {
-            if (sums) {
-                const bf16x8 ones = as_bf16x8(u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
-#pragma unroll
-                for (int nt = 0; nt < T::NT; ++nt) colsum[nt] = mfma16x16x32(ones, h.n[nt], colsum[nt]);
-            }
+            const bf16x8 ones = as_bf16x8(u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
+            if (sums) colsum[nt] = mfma16x16x32(ones, h.n[nt], colsum[nt]);
         }
+    }
+    __device__ __forceinline__ void mma(const typename T::Half &h, typename T::Acc &acc, int, int) {
+#pragma unroll
+        for (int nt = 0; nt < T::NT; ++nt) mma_n(h, acc, nt);
     }
 };
 
@@ -542,7 +585,7 @@ __global__ __launch_bounds__(T::kThreads) void grad_kernel(GradArgs a) {
         }
         op.wp.step = (int64_t)kStepK * 2 * r;
         op.wp.left = sg.count;
-        mma_loop<T>(op, (sg.count + kStepK - 1) / kStepK, acc, g_lds);
+        mma_loop<T>(op, sg.count / kStepK, (sg.count + kStepK - 1) / kStepK, acc, g_lds);
     }
     uint16_t *out = select_slice(a.out, i);
     if (out) {
@@ -576,7 +619,7 @@ long ceil_div(long a, long b) { return (a + b - 1) / b; }
 enum LinearTile { kBig, kMid, kSmall };
 struct LinearPlan {
     LinearTile tile;
-    int bm, bn, mtiles, ntiles, splits, split_steps;
+    int bm, bn, mtiles, ntiles, splits;
     size_t slot_bytes;
 };
 
@@ -608,8 +651,7 @@ LinearPlan plan_linear(long n, long cols, long k, bool allow_split) {
         if (splits > 16) splits = 16;
         if (splits < 1) splits = 1;
     }
-    p.split_steps = (int)ceil_div(steps, splits);
-    p.splits = (int)ceil_div(steps, p.split_steps);
+    p.splits = (int)splits;
     p.slot_bytes = p.splits > 1 ? sizeof(float) * (size_t)tiles * p.splits * p.bm * p.bn : 0;
     return p;
 }
@@ -741,7 +783,6 @@ hipError_t launch_linear(LinearArgs &a, const LinearPlan &p, hipStream_t s) {
     a.mtiles = p.mtiles;
     a.ntiles = p.ntiles;
     a.splits = p.splits;
-    a.split_steps = p.split_steps;
     a.group = 8;
     const unsigned grid = tile_grid((long)p.mtiles * p.ntiles) * (unsigned)p.splits;
     switch (p.tile) {

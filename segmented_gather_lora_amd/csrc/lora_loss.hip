@@ -64,17 +64,6 @@ struct LogitArgs {
     int32_t mtiles, ntiles, group;
 };
 
-template <class T>
-struct PairOp {
-    Walk<typename T::MSide> wm;
-    Walk<typename T::NSide> wn;
-    __device__ __forceinline__ void mma(const typename T::Half &h, typename T::Acc &acc, int) { T::mma(h, acc); }
-    __device__ __forceinline__ void issue(uint32_t at) {
-        wm.issue(at);
-        wn.issue(at + T::MSide::kBytes);
-    }
-};
-
 template <class T, bool GRAD>
 __global__ __launch_bounds__(T::kThreads) void logit_kernel(LogitArgs a) {
     __shared__ int s_tok[T::BN];
@@ -91,7 +80,7 @@ __global__ __launch_bounds__(T::kThreads) void logit_kernel(LogitArgs a) {
         s_tok[r] = GRAD ? a.list[p] : p;
     }
     __syncthreads();
-    PairOp<T> op;
+    PlainOp<T> op;
 #pragma unroll
     for (int j = 0; j < T::NSide::kInstr; ++j)
         op.wn.p[j] = a.x + (int64_t)s_tok[T::NSide::row(j)] * a.ldx + T::NSide::elem(j);
@@ -102,7 +91,7 @@ __global__ __launch_bounds__(T::kThreads) void logit_kernel(LogitArgs a) {
     op.wn.left = op.wm.left = a.hidden;
     typename T::Acc acc;
     clear<T>(acc);
-    mma_loop<T>(op, (a.hidden + kStepK - 1) / kStepK, acc, g_lds);
+    mma_loop<T>(op, a.hidden / kStepK, (a.hidden + kStepK - 1) / kStepK, acc, g_lds);
 
     if constexpr (!GRAD) {
 #pragma unroll
@@ -253,7 +242,7 @@ __global__ __launch_bounds__(T::kThreads) void dx_kernel(DxArgs a) {
     if (!tile_at(blockIdx.x / a.splits, a.mtiles, ntiles, a.group, at)) return;
     const int m0 = at.m * T::BM, p0 = at.n * T::BN, rows = min(T::BN, n - p0);
     const int all = (a.rows + kStepK - 1) / kStepK, s0 = min(all, split * a.split_steps), s1 = min(all, s0 + a.split_steps);
-    PairOp<T> op;
+    PlainOp<T> op;
 #pragma unroll
     for (int j = 0; j < T::NSide::kInstr; ++j)
         op.wn.p[j] = a.g + (int64_t)(p0 + min(T::NSide::row(j), rows - 1)) * a.ldg + s0 * kStepK + T::NSide::elem(j);
@@ -265,7 +254,7 @@ __global__ __launch_bounds__(T::kThreads) void dx_kernel(DxArgs a) {
     op.wn.left = op.wm.left = a.rows - s0 * kStepK;
     typename T::Acc acc;
     clear<T>(acc);
-    mma_loop<T>(op, s1 - s0, acc, g_lds);
+    mma_loop<T>(op, min(s1, a.rows / kStepK) - s0, s1 - s0, acc, g_lds);
 #pragma unroll
     for (int nt = 0; nt < T::NT; ++nt) {
         const int r = T::n_of(nt);
@@ -317,17 +306,6 @@ struct DwArgs {
     int32_t num_tokens, hidden, rows;
     int32_t mtiles, ntiles, group;
 };
-template <class T>
-struct DwOp {
-    GatherWalk<typename T::MSide> wm;
-    Walk<typename T::NSide> wn;
-    __device__ __forceinline__ void mma(const typename T::Half &h, typename T::Acc &acc, int) { T::mma(h, acc); }
-    __device__ __forceinline__ void issue(uint32_t at) {
-        wm.issue(at);
-        wn.issue(at + T::MSide::kBytes);
-    }
-};
-
 // dw[v] = sum over the listed tokens of g[p][v] x[list[p]]: both sides have K
 // (the tokens) as their row index.
 template <class T>
@@ -338,7 +316,7 @@ __global__ __launch_bounds__(T::kThreads) void dw_kernel(DwArgs a) {
     typename T::Acc acc;
     clear<T>(acc);
     if (n > 0) {
-        DwOp<T> op;
+        PairOp<T, GatherWalk<typename T::MSide>, Walk<typename T::NSide>> op;
         op.wm.base = a.x;
         op.wm.sorted = a.list;
         op.wm.ld = a.ldx;
@@ -353,7 +331,7 @@ __global__ __launch_bounds__(T::kThreads) void dw_kernel(DwArgs a) {
             op.wn.p[j] = a.g + (int64_t)T::NSide::row(j) * a.ldg + min(v0 + T::NSide::elem(j), (int)a.ldg - 8);
         op.wn.step = (int64_t)kStepK * a.ldg;
         op.wn.left = n;
-        mma_loop<T>(op, (n + kStepK - 1) / kStepK, acc, g_lds);
+        mma_loop<T>(op, n / kStepK, (n + kStepK - 1) / kStepK, acc, g_lds);
     }
 #pragma unroll
     for (int nt = 0; nt < T::NT; ++nt) {
