@@ -135,6 +135,7 @@ struct Tile {
     static constexpr int kStage = MSide::kBytes + NSide::kBytes;
     static constexpr int kLds = 2 * kStage;
     typedef floatx4 Acc[MT][NT];
+    static constexpr bool kEven = true;   // every wave makes the same copies
 
     __device__ __forceinline__ static int wave_m() { return wave_id() % WM; }
     __device__ __forceinline__ static int wave_n() { return wave_id() / WM; }
@@ -231,31 +232,36 @@ __device__ __forceinline__ void mma_loop(Op &op, int fast, int nsteps, typename 
     }
     int s = 0;
     if (fast > 2) {
-        constexpr int G = T::NT, R = T::kReads, D = T::kLoads;
+        // groups of a step: one 16-row tile of the N side, half 0 then half 1
+        constexpr int G = 2 * T::NT, R = T::kReads, D = T::kLoads;
+        constexpr int F = T::NT > 1 ? T::NT * 3 / 4 : 1, L = T::NT + T::NT / 4;
+        constexpr int kInFlight = T::kEven ? D * (L - F) / (G - F) : 0;
         typename T::Half r0, r1;
         T::read(r0, lds, 0);
         for (; s + 2 < fast; ++s) {
             const uint32_t cur = (uint32_t)(s & 1) * T::kStage, nxt = T::kStage - cur;
-            // half 1's reads end a group or two early: the wait below is for them too
-            constexpr int GA = G > 4 ? G - 2 : G > 1 ? G - 1 : 1;
 #pragma unroll
             for (int g = 0; g < G; ++g) {
+                if (g == F) {
+                    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                    op.settle();
+                }
+                if (g == L) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kInFlight) : "memory");
+                if (g < F) {
 #pragma unroll
-                for (int i = g * R / GA; i < (g + 1) * R / GA && i < R; ++i) T::read_one(r1, lds + cur, 1, i);
-                op.mma_n(r0, acc, g);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            // the own reads of this step's stage are done and the next step has landed, for every wave
-            wait_loads_barrier<0>();
-            op.settle();
-            constexpr int GD = G > 1 ? G / 2 : 1;
+                    for (int i = g * R / F; i < (g + 1) * R / F; ++i) T::read_one(r1, lds + cur, 1, i);
+                } else {
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
+                    for (int i = (g - F) * D / (G - F); i < (g - F + 1) * D / (G - F); ++i) op.load(base + cur, i);
+                }
+                if (g >= L) {
 #pragma unroll
-                for (int i = g * D / GD; i < (g + 1) * D / GD && i < D; ++i) op.load(base + cur, i);
-#pragma unroll
-                for (int i = g * R / G; i < (g + 1) * R / G; ++i) T::read_one(r0, lds + nxt, 0, i);
-                op.mma_n(r1, acc, g);
+                    for (int i = (g - L) * R / (G - L); i < (g - L + 1) * R / (G - L); ++i) T::read_one(r0, lds + nxt, 0, i);
+                }
+                if (g < T::NT)
+                    op.mma_n(r0, acc, g);
+                else
+                    op.mma_n(r1, acc, g - T::NT);
                 if (g == G - 1) op.next();
                 __builtin_amdgcn_sched_barrier(0);
             }
