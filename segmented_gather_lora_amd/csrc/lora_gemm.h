@@ -25,18 +25,22 @@
 // Both give lane (l16, g) of a wave the K elements 32 h + 8 g .. + 8 of half h
 // for row l16 of each 16-row tile, the layout the MFMA takes.
 //
-// Per step a wave holds the operands of one 32-wide half in registers while
-// the other half is being read:
-//     phase 0   MFMA half 0 of step s, with the reads of half 1 between
-//     wait: step s + 1 has landed, own reads done; barrier
-//     phase 1   MFMA half 1, with the loads of step s + 2 into the stage of
-//               step s and the reads of half 0 of step s + 1 between
-// so there is one barrier a step and a step's loads have the MFMA time of a
-// whole step to land.  The order inside a phase is pinned: left to itself the
-// compiler puts a phase's reads first, and the eight waves, just past a
-// barrier, then queue at the LDS for as long as the MFMAs of half a phase take.
-// Steps that need more than that (K tails, adapters' ranks) run after the
-// pinned loop in a plain one that holds one half at a time.
+// A step is 2 NT groups of MFMAs, one 16-row tile of the N side each, half 0 of
+// the step and then half 1; a wave holds both halves' operands in registers:
+//     groups 0 .. F    the reads of half 1 are between the MFMAs; barrier: every
+//                      wave has read the step's stage
+//     groups F ..      the copies of step s + 2 into that stage, evenly
+//     before group L   barrier: step s + 1 has landed (its copies had L + 2 NT - F
+//                      groups or more)
+//     groups L ..      the reads of half 0 of step s + 1
+// The copies of a step keep a CU's vector cache busy for 1200 of the 2048 cycles
+// that its MFMAs take (measured: 53 bytes a cycle where every row gives 128 bytes
+// or more, 27 where it gives 64, so that K steps of 32 in more stages are no
+// faster), hence the even spread; issued at once behind one barrier they made
+// the step 2900 cycles long.  The order is pinned: left to itself the compiler
+// puts the reads first, and eight waves, just past a barrier, queue at the LDS.
+// K tails and adapters' ranks run after the pinned loop in a plain one that
+// holds one half at a time and has two steps' copies in flight.
 //
 // The direct-to-LDS loads are written in assembly (they have no output
 // registers): the builtin makes the compiler wait for every load in flight
@@ -91,11 +95,13 @@ struct Side {
     }
     // copy: first element along the contiguous direction (K, or the side's own index)
     __device__ __forceinline__ static int elem(int j) {
-        if (STRIDED) {
-            const int slot = lane_id() % kLanesPerK;
-            return (((slot >> 1) ^ f_k(row(j))) * 2 + (slot & 1)) * 8;
-        }
+        if (STRIDED) return elem_of(row(j));
         return ((lane_id() & 7) ^ f_row(row(j))) * 8;
+    }
+    // strided: the same for K row k
+    __device__ __forceinline__ static int elem_of(int k) {
+        const int slot = lane_id() % kLanesPerK;
+        return (((slot >> 1) ^ f_k(k)) * 2 + (slot & 1)) * 8;
     }
     // K offset of the lane's 8 elements (contiguous) or its K row (strided)
     __device__ __forceinline__ static int koff(int j) { return STRIDED ? row(j) : elem(j); }
@@ -135,7 +141,7 @@ struct Tile {
     static constexpr int kStage = MSide::kBytes + NSide::kBytes;
     static constexpr int kLds = 2 * kStage;
     typedef floatx4 Acc[MT][NT];
-    static constexpr bool kEven = true;   // every wave makes the same copies
+    static constexpr bool kEven = true;           // every wave makes the same copies of a pinned step
 
     __device__ __forceinline__ static int wave_m() { return wave_id() % WM; }
     __device__ __forceinline__ static int wave_n() { return wave_id() / WM; }
@@ -162,6 +168,10 @@ struct Tile {
     __device__ __forceinline__ static void read(Half &r, const lds_byte *st, int h) {
 #pragma unroll
         for (int i = 0; i < kReads; ++i) read_one(r, st, h, i);
+    }
+    __device__ __forceinline__ static void read_n(Half &r, const lds_byte *st, int h) {
+#pragma unroll
+        for (int i = kMReads; i < kReads; ++i) read_one(r, st, h, i);
     }
     // the products of one 16-row tile of the N side
     __device__ __forceinline__ static void mma_n(const Half &r, Acc &acc, int nt) {
@@ -224,12 +234,7 @@ __device__ __forceinline__ void mma_loop(Op &op, int fast, int nsteps, typename 
     const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
     if (nsteps <= 0) return;
     op.issue(base);
-    if (nsteps > 1) {
-        op.issue(base + T::kStage);
-        wait_loads_barrier<T::kLoads>();
-    } else {
-        wait_loads_barrier<0>();
-    }
+    if (nsteps > 1) op.issue(base + T::kStage);
     int s = 0;
     if (fast > 2) {
         // groups of a step: one 16-row tile of the N side, half 0 then half 1
@@ -237,15 +242,13 @@ __device__ __forceinline__ void mma_loop(Op &op, int fast, int nsteps, typename 
         constexpr int F = T::NT > 1 ? T::NT * 3 / 4 : 1, L = T::NT + T::NT / 4;
         constexpr int kInFlight = T::kEven ? D * (L - F) / (G - F) : 0;
         typename T::Half r0, r1;
+        wait_loads_barrier<Op::kLast>();
         T::read(r0, lds, 0);
         for (; s + 2 < fast; ++s) {
             const uint32_t cur = (uint32_t)(s & 1) * T::kStage, nxt = T::kStage - cur;
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                if (g == F) {
-                    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-                    op.settle();
-                }
+                if (g == F) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
                 if (g == L) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kInFlight) : "memory");
                 if (g < F) {
 #pragma unroll
@@ -269,15 +272,17 @@ __device__ __forceinline__ void mma_loop(Op &op, int fast, int nsteps, typename 
     }
     for (; s < nsteps; ++s) {
         const uint32_t cur = (uint32_t)(s & 1) * T::kStage;
+        // step s has landed; of step s + 1 the copies that every wave makes last may be in flight
+        if (s + 1 < nsteps)
+            wait_loads_barrier<Op::kLast>();
+        else
+            wait_loads_barrier<0>();
         typename T::Half r;
-        T::read(r, lds + cur, 0);
+        op.read(r, lds + cur, s, 0);
         op.mma(r, acc, s, 0);
-        T::read(r, lds + cur, 1);
-        wait_loads_barrier<0>();
-        if (s + 2 < nsteps) {
-            op.settle();
-            op.issue(base + cur);
-        }
+        op.read(r, lds + cur, s, 1);
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (s + 2 < nsteps) op.issue(base + cur);
         op.mma(r, acc, s, 1);
     }
 }
@@ -300,32 +305,39 @@ struct Walk {
         for (int j = 0; j < S::kInstr; ++j) dma16(S::koff(j) < left ? p[j] : zero_page, at + S::dst(j));
         next();
     }
-    __device__ __forceinline__ void settle() {}
 };
 
 // K rows gathered by the sorted token indices (weight gradients: K runs over a
-// segment's tokens).  The indices of a step are loaded a step ahead.
+// segment's tokens) for a strided side.  An instruction copies few K rows, so
+// the indices of a step are loaded a step ahead as scalars: their wait does not
+// touch the count of the copies in flight.
+typedef const __attribute__((address_space(4))) int32_t *const_ints;
 template <class S>
 struct GatherWalk {
+    static constexpr int kRows = 64 / S::kLanesPerK;   // K rows of an instruction
     const uint16_t *base;
     const int32_t *sorted;
     int64_t ld;
-    int tok[S::kInstr], col[S::kInstr];
+    int tok[S::kInstr][kRows], col[S::kInstr];
     int pos, end, num_tokens;
     __device__ __forceinline__ void fetch() {
+        const_ints from = (const_ints)(uintptr_t)sorted;
 #pragma unroll
-        for (int j = 0; j < S::kInstr; ++j) {
-            const int p = pos + S::koff(j);
-            tok[j] = sorted[p < end ? p : end - 1];
-        }
-    }
-    // the indices are in (all of them now: a wait between the copies would be for the copies too)
-    __device__ __forceinline__ void settle() {
+        for (int j = 0; j < S::kInstr; ++j)
 #pragma unroll
-        for (int j = 0; j < S::kInstr; ++j) asm volatile("" : "+v"(tok[j]));
+            for (int q = 0; q < kRows; ++q) {
+                const int p = pos + (wave_id() * S::kInstr + j) * kRows + q;
+                tok[j][q] = from[__builtin_amdgcn_readfirstlane(p < end ? p : end - 1)];
+            }
     }
     __device__ __forceinline__ const uint16_t *at_token(int j) const {
-        return (unsigned)tok[j] < (unsigned)num_tokens ? base + (int64_t)tok[j] * ld + col[j] : zero_page;
+        int t = __builtin_amdgcn_readfirstlane(tok[j][0]);
+#pragma unroll
+        for (int q = 1; q < kRows; ++q) {   // (a plain select of the entries becomes an array in scratch memory)
+            const int u = __builtin_amdgcn_readfirstlane(tok[j][q]);
+            t = lane_id() / S::kLanesPerK == q ? u : t;
+        }
+        return (unsigned)t < (unsigned)num_tokens ? base + (int64_t)t * ld + col[j] : zero_page;
     }
     __device__ __forceinline__ void load(uint32_t at, int j) { dma16(at_token(j), at + S::dst(j)); }
     __device__ __forceinline__ void next() {
@@ -333,7 +345,6 @@ struct GatherWalk {
         if (pos < end) fetch();
     }
     __device__ __forceinline__ void issue(uint32_t at) {
-        settle();
 #pragma unroll
         for (int j = 0; j < S::kInstr; ++j)
             dma16(pos + S::koff(j) < end ? at_token(j) : zero_page, at + S::dst(j));
@@ -344,8 +355,10 @@ struct GatherWalk {
 // The two sides of a product whose steps are all plain but the last.
 template <class T, class WM, class WN>
 struct PairOp {
+    static constexpr int kLast = T::MSide::kInstr;
     WM wm;
     WN wn;
+    __device__ __forceinline__ void read(typename T::Half &r, const lds_byte *st, int, int h) { T::read(r, st, h); }
     __device__ __forceinline__ void mma(const typename T::Half &h, typename T::Acc &acc, int, int) { T::mma(h, acc); }
     __device__ __forceinline__ void mma_n(const typename T::Half &h, typename T::Acc &acc, int nt) { T::mma_n(h, acc, nt); }
     __device__ __forceinline__ void load(uint32_t at, int i) {
@@ -358,13 +371,9 @@ struct PairOp {
         wm.next();
         wn.next();
     }
-    __device__ __forceinline__ void settle() {
-        wm.settle();
-        wn.settle();
-    }
     __device__ __forceinline__ void issue(uint32_t at) {
-        wm.issue(at);
         wn.issue(at + T::MSide::kBytes);
+        wm.issue(at);
     }
 };
 template <class T>

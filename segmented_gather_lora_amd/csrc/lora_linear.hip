@@ -20,6 +20,10 @@
 // and lo = rne(v - hi) (about 16 mantissa bits together), side by side as 2 r
 // K elements; a single bf16 part would add an error as large as the result's
 // own rounding, and the ranks are a small share of the work.
+//
+// A packed row (one token, one slice) is made of blocks of 32 ranks, [32 hi |
+// 32 lo] each, or of a single block [16 hi | 16 lo] for ranks up to 16; ranks
+// past the last are zeros.
 #include <string.h>
 
 #include <type_traits>
@@ -43,6 +47,14 @@ struct UTile {
 
 // ---------------------------------------------------------------- pack
 
+__host__ __device__ __forceinline__ int packed_half(int rank) { return rank <= 16 ? 16 : 32; }
+__host__ __device__ __forceinline__ int packed_row(int rank) {
+    const int h = packed_half(rank);
+    return (rank + h - 1) / h * 2 * h;
+}
+// element of the hi part of rank j; its lo part is packed_half elements on
+__device__ __forceinline__ int packed_at(int j, int half) { return j / half * 2 * half + j % half; }
+
 struct PackArgs {
     MetaView meta;
     const int32_t *ids;
@@ -61,7 +73,7 @@ __device__ __forceinline__ void split_hi_lo(float v, uint32_t &h, uint32_t &l) {
     l = (h & 0x7f80u) == 0x7f80u ? 0u : float_to_bf16_bits(v - bf16_bits_to_float(h));   // inf and NaN: hi alone
 }
 
-// buf's rows in sorted order as bf16 hi | lo (one 2 r row per token and slice);
+// buf's rows in sorted order as packed rows;
 // workgroup 0 also writes the tables when they are asked for.
 __global__ __launch_bounds__(kPackThreads) void pack_kernel(PackArgs a) {
     const bool none = *a.meta.no_lora != 0;
@@ -102,22 +114,23 @@ __global__ __launch_bounds__(kPackThreads) void pack_kernel(PackArgs a) {
                 if (at < a.tiles_cap) a.tiles[at] = UTile{id[i], st[i] + o, min(a.tile_tokens, cnt[i] - o), 0};
     }
     if (none) return;
-    const int per_row = a.rank / 4;
+    const int half = packed_half(a.rank), row_len = packed_row(a.rank), per_row = row_len / 8;
     const int64_t work = (int64_t)a.slices * a.num_tokens * per_row;
     for (int64_t w = (int64_t)blockIdx.x * kPackThreads + tid; w < work; w += (int64_t)gridDim.x * kPackThreads) {
-        const int q = (int)(w % per_row);
+        const int q = (int)(w % per_row);             // 4 ranks
         const int64_t row = w / per_row;              // slice * n + position
         const int p = (int)(row % a.num_tokens);
         const int64_t slice = row / a.num_tokens;
         const int t = a.meta.sorted[p];
         if ((unsigned)t >= (unsigned)a.num_tokens || a.ids[t] < 0) continue;
-        const floatx4 v = *reinterpret_cast<const floatx4 *>(a.buf + (slice * a.num_tokens + t) * a.rank + 4 * q);
+        floatx4 v = {0.f, 0.f, 0.f, 0.f};
+        if (4 * q < a.rank) v = *reinterpret_cast<const floatx4 *>(a.buf + (slice * a.num_tokens + t) * a.rank + 4 * q);
         uint32_t h[4], l[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) split_hi_lo(v[e], h[e], l[e]);
-        uint16_t *out = a.packed + row * 2 * a.rank + 4 * q;
+        uint16_t *out = a.packed + row * row_len + packed_at(4 * q, half);
         *reinterpret_cast<u32x2g *>(out) = u32x2g{h[0] | h[1] << 16, h[2] | h[3] << 16};
-        *reinterpret_cast<u32x2g *>(out + a.rank) = u32x2g{l[0] | l[1] << 16, l[2] | l[3] << 16};
+        *reinterpret_cast<u32x2g *>(out + half) = u32x2g{l[0] | l[1] << 16, l[2] | l[3] << 16};
     }
 }
 
@@ -134,7 +147,7 @@ struct LinearArgs {
     const uint16_t *lw[LORA_MAX_SLICES];        // B_i (forward) or A_i (backward)
     const uint16_t *bias[LORA_MAX_SLICES];
     int32_t width[LORA_MAX_SLICES], col[LORA_MAX_SLICES];
-    const uint16_t *packed;                     // s or u: [slices][n][2 r]
+    const uint16_t *packed;                     // s or u: [slices][n][packed_row]
     uint16_t *y;                                // y or dx
     int64_t ldy;
     float *slots;
@@ -143,105 +156,143 @@ struct LinearArgs {
     int32_t mtiles, ntiles, group, splits;
 };
 
-// The adapters' share of a tile's K walk is cut into units of 32 K elements,
-// one half of a step: unit (e, sl, kk) holds elements 32 kk .. of [hi | lo] of
-// adapter seg[e] and slice sl.  A step's two units may belong to two adapters,
-// so that a rank of 16 wastes nothing.
-constexpr int kUnitK = kStepK / 2;
-
+// The adapters' share of a tile's K walk is made of units, for every slice that
+// meets the tile and every adapter (slices outermost: their arguments are read
+// once).  For ranks above 16 a unit is one step: a block of 32 ranks of the
+// packed rows, whose hi part is the step's first half and whose lo part the
+// second; both are multiplied with the same 32 ranks of the adapter's matrix,
+// staged once.  Up to 16 ranks a unit is half a step, [16 hi | 16 lo] against
+// the ranks twice, so that a step holds two adapters.
 template <class T, bool BWD>
 struct LinearOp : PlainOp<T> {
+    static constexpr int kLast = T::MSide::kInstr / 2;
     const LinearArgs &a;
     const int (*seg)[4];       // LDS: lo, hi (sorted positions), id
     int main_left, main_steps, m0, p0, nseg;
-    int sl0, sl1, ksteps;      // slices that meet the tile; units of one slice
-    int e, sl, kk;             // next unit to copy
-    int me, mleft;             // next unit to multiply: its adapter and the adapter's units left
+    int sl0, sl1, blocks;      // slices that meet the tile; blocks of 32 ranks (0: ranks up to 16)
+    int sl, e, kb;             // next unit to copy
+    int me, mleft, munits;     // next unit to multiply: its adapter, that adapter's units left, all units left
+    struct Slice {
+        const uint16_t *rows, *weights;   // the packed rows from the tile's first on, the adapters' matrices
+        int width, col;
+    } at_slice;
+    struct Seg {
+        int lo, hi;
+        const uint16_t *weights;
+    } at_seg;
+    int mlo, mhi;
 
     __device__ __forceinline__ LinearOp(const LinearArgs &args, const int (*segments)[4]) : a(args), seg(segments) {}
+    __device__ __forceinline__ int per_seg() const { return blocks ? blocks : 1; }
+    __device__ __forceinline__ void enter_slice() {
+        at_slice.width = BWD ? a.cols : select_slice(a.width, sl);
+        at_slice.col = BWD ? 0 : select_slice(a.col, sl);
+        at_slice.rows = a.packed + ((int64_t)sl * a.num_tokens + p0) * packed_row(a.rank);
+        at_slice.weights = select_slice(a.lw, sl);
+    }
+    __device__ __forceinline__ void enter_seg() {
+        at_seg.lo = __builtin_amdgcn_readfirstlane(seg[e][0]) - p0;
+        at_seg.hi = __builtin_amdgcn_readfirstlane(seg[e][1]) - p0;
+        at_seg.weights = at_slice.weights + (int64_t)__builtin_amdgcn_readfirstlane(seg[e][2]) * a.rank * at_slice.width;
+    }
+    __device__ __forceinline__ void enter_rows() {
+        mlo = __builtin_amdgcn_readfirstlane(seg[me][0]) - p0;
+        mhi = __builtin_amdgcn_readfirstlane(seg[me][1]) - p0;
+    }
     // the walk over the units starts at unit u
-    __device__ __forceinline__ void start(int u) {
-        const int per = (sl1 - sl0) * ksteps;
-        e = me = u / per;
+    __device__ __forceinline__ void start(int u, int count) {
+        munits = count;
+        const int per = nseg * per_seg();
+        sl = sl0 + u / per;
         const int in = u % per;
-        sl = sl0 + in / ksteps;
-        kk = in % ksteps;
-        mleft = per - in;
+        e = me = in / per_seg();
+        kb = in % per_seg();
+        mleft = per_seg() - kb;
+        enter_slice();
+        enter_seg();
+        enter_rows();
+    }
+    __device__ __forceinline__ void read(typename T::Half &r, const lds_byte *st, int s, int h) {
+        if (h == 0 || s < main_steps || blocks == 0)
+            T::read(r, st, h);
+        else
+            T::read_n(r, st, h);
     }
     // an adapter's units touch its own tokens' sums alone: one whose weights
     // are not finite stays without effect on the others in the tile
     // (W's last steps go the same way with all rows: a branch here would cost the
     // registers of a second set of sums)
-    __device__ __forceinline__ void mma(const typename T::Half &h, typename T::Acc &acc, int s, int) {
-        const bool all = s < main_steps, some = all || me < nseg;
-        const int lo = all || !some ? 0 : __builtin_amdgcn_readfirstlane(seg[me][0]) - p0;
-        const int hi = all ? T::BN : !some ? 0 : __builtin_amdgcn_readfirstlane(seg[me][1]) - p0;
-        mma_rows<T>(h, acc, lo, hi);
-        if (!all && --mleft == 0) {
-            mleft = (sl1 - sl0) * ksteps;
-            ++me;
-        }
-    }
-    struct Unit {
-        const uint16_t *rows, *weights;   // the slice's packed rows, the adapter's matrix
-        int lo, hi, k0, col, width;
-    };
-    __device__ __forceinline__ Unit unit() {
-        Unit u{a.packed, a.packed, 0, 0, 0, 0, 0};
-        if (e < nseg) {
-            u.lo = __builtin_amdgcn_readfirstlane(seg[e][0]);
-            u.hi = __builtin_amdgcn_readfirstlane(seg[e][1]);
-            u.k0 = kk * kUnitK;
-            u.width = BWD ? a.cols : select_slice(a.width, sl);
-            u.col = BWD ? 0 : select_slice(a.col, sl);
-            u.rows = a.packed + (int64_t)sl * a.num_tokens * 2 * a.rank;
-            u.weights = select_slice(a.lw, sl) + (int64_t)__builtin_amdgcn_readfirstlane(seg[e][2]) * a.rank * u.width;
-            if (++kk == ksteps) {
-                kk = 0;
-                if (++sl == sl1) {
-                    sl = sl0;
-                    ++e;
-                }
+    __device__ __forceinline__ void mma(const typename T::Half &h, typename T::Acc &acc, int s, int half) {
+        const bool all = s < main_steps;
+        mma_rows<T>(h, acc, all ? 0 : mlo, all ? T::BN : munits > 0 ? mhi : 0);
+        if (!all && (half == 1 || blocks == 0)) {
+            --munits;
+            if (--mleft == 0) {
+                mleft = per_seg();
+                if (++me == nseg) me = 0;
+                enter_rows();
             }
         }
-        return u;
     }
     __device__ __forceinline__ void next() {
         PlainOp<T>::next();
         --main_left;
     }
+    // copies of a unit: N rows of its adapter's tokens (other rows keep what the
+    // stage holds: their products are not added), then the ranks of its matrix.
+    // H: the half of the step that it fills, or -1 for both.
+    template <int H>
+    __device__ __forceinline__ void unit(uint32_t at) {
+        const int row_len = packed_row(a.rank), r = a.rank;
+        const bool live = sl < sl1;      // past the last unit: no rows, and ranks that are not used
+        const int lo = live ? at_seg.lo : 0, hi = live ? at_seg.hi : 0;
+        const uint16_t *rows = at_slice.rows + kb * 64;
+#pragma unroll
+        for (int j = 0; j < T::NSide::kInstr; ++j) {
+            const int row = T::NSide::row(j), ko = T::NSide::elem(j);
+            if (row >= lo && row < hi && (H < 0 || ko / 32 == H))
+                dma16(rows + row * row_len + (H < 0 ? ko : ko & 31), at + T::MSide::kBytes + T::NSide::dst(j));
+        }
+        const uint16_t *lw = at_seg.weights;
+        const int width = at_slice.width;
+        if (BWD) {      // A_i: ranks are K rows, this side's index is the hidden column
+            // half of the side's instructions hold the half's 32 K rows
+            constexpr int kHalf = T::MSide::kInstr / 2, kRows = 64 / T::MSide::kLanesPerK;
+#pragma unroll
+            for (int j = 0; j < kHalf; ++j) {
+                const int i = wave_id() * kHalf + j + (H > 0 ? T::kWaves * kHalf : 0);
+                const int k = i * kRows + lane_id() / T::MSide::kLanesPerK;
+                const int rank = H < 0 ? kb * 32 + k : k & 15;
+                const int c = m0 + T::MSide::elem_of(k);
+                dma16(lw + (int64_t)(rank < r ? rank : r - 1) * width + (c < width ? c : width - 8), at + i * 1024u);
+            }
+        } else {        // B_i: rows are the slice's columns, ranks contiguous
+#pragma unroll
+            for (int j = 0; j < T::MSide::kInstr; ++j) {
+                const int c = m0 + T::MSide::row(j) - at_slice.col, ko = T::MSide::elem(j);
+                const int rank = H < 0 ? kb * 32 + ko : ko & 15;
+                if (ko / 32 == (H > 0 ? 1 : 0))
+                    dma16(c >= 0 && c < width ? lw + (int64_t)c * r + (rank < r ? rank : r - 8) : zero_page, at + T::MSide::dst(j));
+            }
+        }
+        if (live && ++kb == per_seg()) {
+            kb = 0;
+            if (++e == nseg) {
+                e = 0;
+                if (++sl < sl1) enter_slice();
+            }
+            enter_seg();
+        }
+    }
     __device__ __forceinline__ void issue(uint32_t at) {
         if (main_left > 0) {
             PlainOp<T>::issue(at);
             --main_left;
-            return;
-        }
-        const Unit u0 = unit(), u1 = unit();
-        const int r = a.rank;
-#pragma unroll
-        for (int j = 0; j < T::NSide::kInstr; ++j) {
-            const int pos = p0 + T::NSide::row(j), ko = T::NSide::elem(j);
-            const Unit &u = ko < kUnitK ? u0 : u1;
-            const int k = u.k0 + (ko & (kUnitK - 1));
-            dma16(pos >= u.lo && pos < u.hi && k < 2 * r ? u.rows + (int64_t)pos * 2 * r + k : zero_page,
-                  at + T::MSide::kBytes + T::NSide::dst(j));
-        }
-#pragma unroll
-        for (int j = 0; j < T::MSide::kInstr; ++j) {
-            const int ko = T::MSide::koff(j);
-            const Unit &u = ko < kUnitK ? u0 : u1;
-            const int k = u.k0 + (ko & (kUnitK - 1)), kr = k < r ? k : k - r;
-            bool ok = u.hi > 0 && k < 2 * r;
-            const uint16_t *src;
-            if (BWD) {      // A_i: ranks are rows, this side's index is the hidden column
-                const int c = m0 + T::MSide::elem(j);
-                src = u.weights + (int64_t)kr * a.cols + (c < a.cols ? c : a.cols - 8);
-            } else {        // B_i: rows are the slice's columns, ranks contiguous
-                const int c = m0 + T::MSide::row(j) - u.col;
-                ok = ok && c >= 0 && c < u.width;
-                src = u.weights + (int64_t)c * r + kr;
-            }
-            dma16(ok ? src : zero_page, at + T::MSide::dst(j));
+        } else if (blocks) {
+            unit<-1>(at);
+        } else {
+            unit<0>(at);
+            unit<1>(at);
         }
     }
 };
@@ -288,7 +339,7 @@ __global__ __launch_bounds__(T::kThreads) void linear_kernel(LinearArgs a) {
     op.m0 = m0;
     op.p0 = p0;
     op.nseg = nseg;
-    op.ksteps = (2 * a.rank + kUnitK - 1) / kUnitK;
+    op.blocks = a.rank <= 16 ? 0 : (a.rank + 31) / 32;
     op.sl0 = 0;
     op.sl1 = a.slices;
     if (!BWD) {   // the slices that meet the tile's columns
@@ -303,12 +354,16 @@ __global__ __launch_bounds__(T::kThreads) void linear_kernel(LinearArgs a) {
         }
     }
     // the tile's steps, W's and then the adapters', are dealt to the splits in equal runs
-    const int units = op.sl1 > op.sl0 ? nseg * (op.sl1 - op.sl0) * op.ksteps : 0;
-    const int all = (a.k + kStepK - 1) / kStepK, total = all + (units + 1) / 2, per = (total + a.splits - 1) / a.splits;
+    const int units = op.sl1 > op.sl0 ? nseg * (op.sl1 - op.sl0) * op.per_seg() : 0;
+    const int ext = op.blocks ? units : (units + 1) / 2;
+    const int all = (a.k + kStepK - 1) / kStepK, total = all + ext, per = (total + a.splits - 1) / a.splits;
     const int t0 = min(total, split * per), t1 = min(total, t0 + per);
     const int s0 = min(t0, all), s1 = min(t1, all);
     op.main_left = op.main_steps = s1 - s0;
-    if (t1 > all) op.start(2 * (max(t0, all) - all));
+    if (t1 > all) {
+        const int of_step = op.blocks ? 1 : 2, first = (max(t0, all) - all) * of_step;
+        op.start(first, min(units, (t1 - all) * of_step) - first);
+    }
 #pragma unroll
     for (int j = 0; j < T::NSide::kInstr; ++j)
         op.wn.p[j] = a.in + (int64_t)s_tok[T::NSide::row(j)] * a.ldin + T::NSide::elem(j) + (int64_t)s0 * kStepK;
@@ -463,23 +518,25 @@ __global__ __launch_bounds__(T::kThreads) void u_kernel(UArgs a) {
     if (a.splits > 1 && !combine_splits<T>(acc, a.slots + (int64_t)unit * a.splits * (T::BM * T::BN), a.counters + unit,
                                            split, a.splits, ut.rows, &s_flag))
         return;
+    const int half = packed_half(a.rank), row_ranks = packed_row(a.rank) / 2;
 #pragma unroll
     for (int nt = 0; nt < T::NT; ++nt) {
         const int r = T::n_of(nt);
         if (r >= ut.rows) continue;
         float *out = a.dbuf + ((int64_t)i * a.num_tokens + s_tok[r]) * a.rank;
-        uint16_t *pk = a.packed + ((int64_t)i * a.num_tokens + ut.start + r) * 2 * a.rank;
+        uint16_t *pk = a.packed + ((int64_t)i * a.num_tokens + ut.start + r) * packed_row(a.rank);
 #pragma unroll
         for (int mt = 0; mt < T::MT; ++mt) {
             const int j = T::m_of(mt);
-            if (j >= a.rank) continue;
-            const floatx4 v = acc[mt][nt] * a.scale;
-            *reinterpret_cast<floatx4 *>(out + j) = v;
+            if (j >= row_ranks) continue;
+            const floatx4 v = j < a.rank ? acc[mt][nt] * a.scale : floatx4{0.f, 0.f, 0.f, 0.f};
+            if (j < a.rank) *reinterpret_cast<floatx4 *>(out + j) = v;
             uint32_t h[4], l[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) split_hi_lo(v[x], h[x], l[x]);
-            *reinterpret_cast<u32x2g *>(pk + j) = u32x2g{h[0] | h[1] << 16, h[2] | h[3] << 16};
-            *reinterpret_cast<u32x2g *>(pk + a.rank + j) = u32x2g{l[0] | l[1] << 16, l[2] | l[3] << 16};
+            uint16_t *at = pk + packed_at(j, half);
+            *reinterpret_cast<u32x2g *>(at) = u32x2g{h[0] | h[1] << 16, h[2] | h[3] << 16};
+            *reinterpret_cast<u32x2g *>(at + half) = u32x2g{l[0] | l[1] << 16, l[2] | l[3] << 16};
         }
     }
 }
@@ -491,7 +548,7 @@ struct GradArgs {
     const int32_t *sorted;
     const uint16_t *act;                      // x (dA) or dy (dB), gathered token rows
     int64_t ldact;
-    const uint16_t *packed;                   // u (dA) or s (dB): [slices][n][2 r]
+    const uint16_t *packed;                   // u (dA) or s (dB): [slices][n][packed_row]
     uint16_t *out[LORA_MAX_SLICES];           // dA_i [id][r][hidden] or dB_i [id][width][r]
     uint16_t *dbias[LORA_MAX_SLICES];
     int32_t width[LORA_MAX_SLICES], col[LORA_MAX_SLICES];   // of act (dA: hidden, 0)
@@ -507,13 +564,19 @@ template <class T, bool DA>
 struct GradOp {
     using ASide = typename std::conditional<DA, typename T::MSide, typename T::NSide>::type;   // activations
     using PSide = typename std::conditional<DA, typename T::NSide, typename T::MSide>::type;   // packed ranks
+    static constexpr int kLast = T::MSide::kInstr;
     GatherWalk<ASide> wa;
     Walk<PSide> wp;
     floatx4 colsum[DA ? 1 : T::NT];
     bool sums;
     __device__ __forceinline__ void issue(uint32_t at) {
-        wa.issue(at + (DA ? 0 : T::MSide::kBytes));
-        wp.issue(at + (DA ? T::MSide::kBytes : 0));
+        if (DA) {
+            wp.issue(at + T::MSide::kBytes);
+            wa.issue(at);
+        } else {
+            wa.issue(at + T::MSide::kBytes);
+            wp.issue(at);
+        }
     }
     __device__ __forceinline__ void load(uint32_t at, int i) {
         constexpr int nm = T::MSide::kInstr;
@@ -528,7 +591,7 @@ struct GradOp {
         wa.next();
         wp.next();
     }
-    __device__ __forceinline__ void settle() { wa.settle(); }
+    __device__ __forceinline__ void read(typename T::Half &r, const lds_byte *st, int, int h) { T::read(r, st, h); }
     // dB: the column sums of dy as one more MFMA row of ones
     __device__ __forceinline__ void mma_n(const typename T::Half &h, typename T::Acc &acc, int nt) {
         T::mma_n(h, acc, nt);
@@ -568,6 +631,7 @@ __global__ __launch_bounds__(T::kThreads) void grad_kernel(GradArgs a) {
         for (int nt = 0; nt < T::NT; ++nt) op.colsum[nt] = floatx4{0.f, 0.f, 0.f, 0.f};
     }
     if (sg.count > 0) {
+        const int half = packed_half(r), row_len = packed_row(r);
         op.wa.base = a.act + col;
         op.wa.sorted = a.sorted;
         op.wa.ld = a.ldact;
@@ -580,10 +644,10 @@ __global__ __launch_bounds__(T::kThreads) void grad_kernel(GradArgs a) {
 #pragma unroll
         for (int j = 0; j < PSide::kInstr; ++j) {
             const int c = PSide::elem(j);
-            const int from = c < BR ? min(c, r - 8) : r + min(c - BR, r - 8);
-            op.wp.p[j] = a.packed + ((int64_t)i * a.num_tokens + sg.start + PSide::row(j)) * 2 * r + from;
+            const int from = c < BR ? packed_at(min(c, r - 8), half) : packed_at(min(c - BR, r - 8), half) + half;
+            op.wp.p[j] = a.packed + ((int64_t)i * a.num_tokens + sg.start + PSide::row(j)) * row_len + from;
         }
-        op.wp.step = (int64_t)kStepK * 2 * r;
+        op.wp.step = (int64_t)kStepK * row_len;
         op.wp.left = sg.count;
         mma_loop<T>(op, sg.count / kStepK, (sg.count + kStepK - 1) / kStepK, acc, g_lds);
     }
@@ -694,7 +758,7 @@ Layout layout(long n, int max_loras, int slices, int rank, size_t slot_bytes, in
     l.segs = take(backward ? sizeof(SegEntry) * (size_t)max_loras : 0);
     l.num_tiles = take(backward ? sizeof(int32_t) : 0);
     l.tiles = take(backward ? sizeof(UTile) * (size_t)tiles_cap : 0);
-    const size_t rows = sizeof(uint16_t) * 2 * (size_t)slices * (size_t)n * (size_t)rank;
+    const size_t rows = sizeof(uint16_t) * (size_t)slices * (size_t)n * (size_t)packed_row(rank);
     l.s = take(rows);
     l.u = take(backward ? rows : 0);
     l.slots = take(slot_bytes);
@@ -770,7 +834,7 @@ hipError_t launch_pack(const lora_meta_t *meta, const MetaView &view, const floa
     a.rank = rank;
     a.slices = slices;
     a.max_loras = meta->max_loras;
-    const long work = (long)slices * meta->num_tokens * (rank / 4);
+    const long work = (long)slices * meta->num_tokens * (packed_row(rank) / 8);
     long grid = ceil_div(work, kPackThreads);
     if (grid > 2048) grid = 2048;
     if (grid < 1) grid = 1;
