@@ -42,10 +42,13 @@
 // K tails and adapters' ranks run after the pinned loop in a plain one that
 // holds one half at a time and has two steps' copies in flight.
 //
+// Tiles too small to be bound by the MFMA have more stages and a plain loop:
+// what counts there is the bytes in flight.
+//
 // The direct-to-LDS loads are written in assembly (they have no output
 // registers): the builtin makes the compiler wait for every load in flight
 // before each LDS read, since it cannot tell the stages apart.  The waits that
-// order them are the explicit ones in mma_loop.
+// order them are the explicit ones of the loops.
 #pragma once
 
 #include "lora_internal.h"
@@ -128,9 +131,9 @@ struct Side {
 // Tile of BM x BN by WM x WN waves.  SPLIT: 0 plain; 1: the M side's stage
 // holds 2 * BM rows, the low parts after the high parts, and both are
 // multiplied into the same sums; 2: the same on the N side.
-template <int BM_, int BN_, int WM_, int WN_, bool MS_, bool NS_, int SPLIT_ = 0>
+template <int BM_, int BN_, int WM_, int WN_, bool MS_, bool NS_, int SPLIT_ = 0, int STAGES_ = 2>
 struct Tile {
-    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, SPLIT = SPLIT_;
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, SPLIT = SPLIT_, kStages = STAGES_;
     static constexpr bool MS = MS_, NS = NS_;
     static constexpr int kWaves = WM * WN, kThreads = kWaves * kWave;
     static constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
@@ -139,7 +142,7 @@ struct Tile {
     using MSide = Side<MROWS, kWaves, MS, QUADS>;
     using NSide = Side<NROWS, kWaves, NS, false>;
     static constexpr int kStage = MSide::kBytes + NSide::kBytes;
-    static constexpr int kLds = 2 * kStage;
+    static constexpr int kLds = kStages * kStage;
     typedef floatx4 Acc[MT][NT];
     static constexpr bool kEven = true;           // every wave makes the same copies of a pinned step
 
@@ -221,22 +224,83 @@ __device__ __forceinline__ void wait_loads_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// Runs `nsteps` steps.  op.issue(stage) copies the next step's operands to the
-// LDS byte address `stage` (called once per step, in order); op.mma(half, acc,
-// s, h) multiplies half h of step s into the sums.  The first `fast` steps are
-// plain: op.load(stage, i), i < T::kLoads, are their copies one by one,
-// op.next() moves on to the next step, op.mma_n(half, acc, nt) multiplies.
-// All threads of the workgroup call it; LDS of T::kLds bytes at `lds`, which
-// no one else uses until it returns.
+__device__ __forceinline__ void own_reads_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// A product of `nsteps` steps: mma_begin, then mma_loop with the same
+// arguments; between them a workgroup may do what does not touch `lds`.
+// op.issue(stage) copies the next step's operands to the LDS byte address
+// `stage` (called once per step, in order; every wave makes at least Op::kLast
+// copies after the last of the N side); op.read(half, stage, s, h) and
+// op.mma(half, acc, s, h) read a half of step s and multiply it into the sums.
+// The first `plain` steps make T::kLoads copies in every wave: op.load(stage, i)
+// are these one by one, op.next() moves on to the next step, op.mma_n(half, acc,
+// nt) multiplies.  All threads of the workgroup call it; LDS of T::kLds bytes at
+// `lds`, which no one else uses until it returns.
+__device__ __forceinline__ uint32_t lds_address(unsigned char *lds) {
+    return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_byte *)lds);
+}
+template <class T>
+constexpr int kAhead = T::kStages == 2 ? 2 : T::kStages - 1;   // steps copied before the first is multiplied
+
 template <class T, class Op>
-__device__ __forceinline__ void mma_loop(Op &op, int fast, int nsteps, typename T::Acc &acc, unsigned char *lds_generic) {
+__device__ __forceinline__ void mma_begin(Op &op, int nsteps, unsigned char *lds) {
+    const uint32_t base = lds_address(lds);
+    for (int i = 0; i < kAhead<T> && i < nsteps; ++i) op.issue(base + i * T::kStage);
+}
+
+// Small tiles: one barrier a step, kStages - 2 steps' copies in flight across it.
+template <class T, class Op>
+__device__ __forceinline__ void ring_loop(Op &op, int plain, int nsteps, typename T::Acc &acc, const lds_byte *lds,
+                                          uint32_t base) {
+    constexpr int S = T::kStages;
+    int cur = 0, to = (S - 1) * T::kStage, s = 0;
+    auto turn = [&] {
+        to = cur;
+        cur = cur + T::kStage == T::kLds ? 0 : cur + T::kStage;
+    };
+    // at the barrier step s has landed, for every wave, and step s - 1 is read
+    for (; s + S - 1 < plain; ++s) {
+        wait_loads_barrier<(S - 2) * T::kLoads>();
+#pragma unroll
+        for (int i = 0; i < T::kLoads; ++i) op.load(base + to, i);
+        op.next();
+        typename T::Half r0, r1;
+        T::read(r0, lds + cur, 0);
+        T::read(r1, lds + cur, 1);
+#pragma unroll
+        for (int nt = 0; nt < T::NT; ++nt) op.mma_n(r0, acc, nt);
+#pragma unroll
+        for (int nt = 0; nt < T::NT; ++nt) op.mma_n(r1, acc, nt);
+        turn();
+    }
+    for (; s < nsteps; ++s) {
+        if (s + S - 1 <= plain)
+            wait_loads_barrier<(S - 2) * T::kLoads>();
+        else if (s + S - 1 <= nsteps)
+            wait_loads_barrier<(S - 2) * Op::kLast>();
+        else
+            wait_loads_barrier<0>();
+        if (s + S - 1 < nsteps) op.issue(base + to);
+        typename T::Half r;
+        op.read(r, lds + cur, s, 0);
+        op.mma(r, acc, s, 0);
+        op.read(r, lds + cur, s, 1);
+        op.mma(r, acc, s, 1);
+        turn();
+    }
+}
+
+template <class T, class Op>
+__device__ __forceinline__ void mma_loop(Op &op, int plain, int nsteps, typename T::Acc &acc, unsigned char *lds_generic) {
     const lds_byte *lds = (const lds_byte *)lds_generic;
-    const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
+    const uint32_t base = lds_address(lds_generic);
     if (nsteps <= 0) return;
-    op.issue(base);
-    if (nsteps > 1) op.issue(base + T::kStage);
+    if constexpr (T::kStages > 2) {
+        ring_loop<T>(op, plain, nsteps, acc, lds, base);
+        return;
+    }
     int s = 0;
-    if (fast > 2) {
+    if (plain > 2) {
         // groups of a step: one 16-row tile of the N side, half 0 then half 1
         constexpr int G = 2 * T::NT, R = T::kReads, D = T::kLoads;
         constexpr int F = T::NT > 1 ? T::NT * 3 / 4 : 1, L = T::NT + T::NT / 4;
@@ -244,11 +308,11 @@ __device__ __forceinline__ void mma_loop(Op &op, int fast, int nsteps, typename 
         typename T::Half r0, r1;
         wait_loads_barrier<Op::kLast>();
         T::read(r0, lds, 0);
-        for (; s + 2 < fast; ++s) {
+        for (; s + 2 < plain; ++s) {
             const uint32_t cur = (uint32_t)(s & 1) * T::kStage, nxt = T::kStage - cur;
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                if (g == F) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                if (g == F) own_reads_barrier();
                 if (g == L) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kInFlight) : "memory");
                 if (g < F) {
 #pragma unroll
@@ -281,7 +345,7 @@ __device__ __forceinline__ void mma_loop(Op &op, int fast, int nsteps, typename 
         op.read(r, lds + cur, s, 0);
         op.mma(r, acc, s, 0);
         op.read(r, lds + cur, s, 1);
-        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        own_reads_barrier();
         if (s + 2 < nsteps) op.issue(base + cur);
         op.mma(r, acc, s, 1);
     }

@@ -150,10 +150,8 @@ struct LinearArgs {
     const uint16_t *packed;                     // s or u: [slices][n][packed_row]
     uint16_t *y;                                // y or dx
     int64_t ldy;
-    float *slots;
-    int32_t *counters;
     int32_t num_tokens, cols, k, rank, slices, max_loras;
-    int32_t mtiles, ntiles, group, splits;
+    int32_t mtiles, ntiles, group, has_bias;
 };
 
 // The adapters' share of a tile's K walk is made of units, for every slice that
@@ -199,15 +197,11 @@ struct LinearOp : PlainOp<T> {
         mlo = __builtin_amdgcn_readfirstlane(seg[me][0]) - p0;
         mhi = __builtin_amdgcn_readfirstlane(seg[me][1]) - p0;
     }
-    // the walk over the units starts at unit u
-    __device__ __forceinline__ void start(int u, int count) {
-        munits = count;
-        const int per = nseg * per_seg();
-        sl = sl0 + u / per;
-        const int in = u % per;
-        e = me = in / per_seg();
-        kb = in % per_seg();
-        mleft = per_seg() - kb;
+    __device__ __forceinline__ void start(int units) {
+        munits = units;
+        sl = sl0;
+        e = me = kb = 0;
+        mleft = per_seg();
         enter_slice();
         enter_seg();
         enter_rows();
@@ -298,31 +292,71 @@ struct LinearOp : PlainOp<T> {
 };
 
 template <class T, bool BWD>
-__global__ __launch_bounds__(T::kThreads) void linear_kernel(LinearArgs a) {
-    __shared__ int s_tok[T::BN], s_id[T::BN], s_seg[T::BN][4], s_count, s_flag;
+__global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(LinearArgs a) {
+    __shared__ int s_tok[T::BN], s_id[T::BN], s_seg[T::BN][4], s_count;
+    static_assert(T::BN <= T::kThreads, "a thread a token row");
     const int tid = threadIdx.x;
-    const int split = blockIdx.x % a.splits;
     TileAt at;
-    if (!tile_at(blockIdx.x / a.splits, a.mtiles, a.ntiles, a.group, at)) return;
+    if (!tile_at(blockIdx.x, a.mtiles, a.ntiles, a.group, at)) return;
     const int m0 = at.m * T::BM, p0 = at.n * T::BN;
     const int rows = min(T::BN, a.num_tokens - p0);
-    const bool none = *a.meta.no_lora != 0;
-
-    // the tile's tokens (a batch without adapters has no sorted order: batch order)
     if (tid == 0) s_count = 0;
-    for (int r = tid; r < T::BN; r += T::kThreads) {
+
+    // one memory round trip: the flag, the tile's tokens, the first segments
+    // (a batch without adapters has no sorted order: batch order)
+    const bool none = *a.meta.no_lora != 0;
+    auto token = [&](int r) {
         const int p = p0 + min(r, rows - 1);
-        int t = none ? p : a.meta.sorted[p];
-        t = (unsigned)t < (unsigned)a.num_tokens ? t : 0;
-        s_tok[r] = t;
-        s_id[r] = none ? -1 : a.ids[t];
+        const int t = none ? p : a.meta.sorted[p];
+        return (unsigned)t < (unsigned)a.num_tokens ? t : 0;
+    };
+    const int own = token(min(tid, T::BN - 1));
+    int id = -1, st = 0, count = 0;
+    if (tid < a.meta.nslots) {
+        id = a.meta.active_ids[tid];
+        st = a.meta.start_loc[tid];
+        count = a.meta.counts[tid];
     }
+    LinearOp<T, BWD> op(a, s_seg);
+    op.m0 = m0;
+    op.p0 = p0;
+    op.blocks = a.rank <= 16 ? 0 : (a.rank + 31) / 32;
+#pragma unroll
+    for (int j = 0; j < T::NSide::kInstr; ++j)
+        op.wn.p[j] = a.in + (int64_t)token(T::NSide::row(j)) * a.ldin + T::NSide::elem(j);
+    op.wn.step = kStepK;
+    op.wn.left = a.k;
+#pragma unroll
+    for (int j = 0; j < T::MSide::kInstr; ++j) {
+        if (BWD) {
+            const int c = m0 + T::MSide::elem(j);
+            op.wm.p[j] = a.w + (int64_t)T::MSide::row(j) * a.ldw + (c < a.cols ? c : a.cols - 8);
+        } else {
+            op.wm.p[j] = a.w + (int64_t)min(m0 + T::MSide::row(j), a.cols - 1) * a.ldw + T::MSide::elem(j);
+        }
+    }
+    op.wm.step = BWD ? (int64_t)kStepK * a.ldw : kStepK;
+    op.wm.left = a.k;
+    const int main = (a.k + kStepK - 1) / kStepK;
+    op.main_left = op.main_steps = main;
+    const bool early = main >= kAhead<T>;
+    if (early) mma_begin<T>(op, main, g_lds);
+
+    // while they land: the tile's tokens and ids, and the adapters it meets
+    // (any order: each token takes part in one of them)
     __syncthreads();
-    // the adapters it meets (any order: each token takes part in one of them)
+    if (tid < T::BN) {
+        s_tok[tid] = own;
+        s_id[tid] = none || (BWD || !a.has_bias) ? -1 : a.ids[own];
+    }
     if (!none)
         for (int k = tid; k < a.meta.nslots; k += T::kThreads) {
-            const int id = a.meta.active_ids[k], st = a.meta.start_loc[k], en = st + a.meta.counts[k];
-            const int lo = max(st, p0), hi = min(en, p0 + rows);
+            if (k != tid) {
+                id = a.meta.active_ids[k];
+                st = a.meta.start_loc[k];
+                count = a.meta.counts[k];
+            }
+            const int lo = max(st, p0), hi = min(st + count, p0 + rows);
             if (id >= 0 && id < a.max_loras && lo < hi) {
                 const int e = atomicAdd(&s_count, 1);
                 if (e < T::BN) {
@@ -334,12 +368,7 @@ __global__ __launch_bounds__(T::kThreads) void linear_kernel(LinearArgs a) {
         }
     __syncthreads();
     const int nseg = __builtin_amdgcn_readfirstlane(min(s_count, T::BN));
-
-    LinearOp<T, BWD> op(a, s_seg);
-    op.m0 = m0;
-    op.p0 = p0;
     op.nseg = nseg;
-    op.blocks = a.rank <= 16 ? 0 : (a.rank + 31) / 32;
     op.sl0 = 0;
     op.sl1 = a.slices;
     if (!BWD) {   // the slices that meet the tile's columns
@@ -353,97 +382,68 @@ __global__ __launch_bounds__(T::kThreads) void linear_kernel(LinearArgs a) {
             }
         }
     }
-    // the tile's steps, W's and then the adapters', are dealt to the splits in equal runs
     const int units = op.sl1 > op.sl0 ? nseg * (op.sl1 - op.sl0) * op.per_seg() : 0;
-    const int ext = op.blocks ? units : (units + 1) / 2;
-    const int all = (a.k + kStepK - 1) / kStepK, total = all + ext, per = (total + a.splits - 1) / a.splits;
-    const int t0 = min(total, split * per), t1 = min(total, t0 + per);
-    const int s0 = min(t0, all), s1 = min(t1, all);
-    op.main_left = op.main_steps = s1 - s0;
-    if (t1 > all) {
-        const int of_step = op.blocks ? 1 : 2, first = (max(t0, all) - all) * of_step;
-        op.start(first, min(units, (t1 - all) * of_step) - first);
-    }
-#pragma unroll
-    for (int j = 0; j < T::NSide::kInstr; ++j)
-        op.wn.p[j] = a.in + (int64_t)s_tok[T::NSide::row(j)] * a.ldin + T::NSide::elem(j) + (int64_t)s0 * kStepK;
-    op.wn.step = kStepK;
-    op.wn.left = a.k - s0 * kStepK;
-#pragma unroll
-    for (int j = 0; j < T::MSide::kInstr; ++j) {
-        if (BWD) {
-            int c = m0 + T::MSide::elem(j);
-            c = c < a.cols ? c : a.cols - 8;
-            op.wm.p[j] = a.w + (int64_t)(s0 * kStepK + T::MSide::row(j)) * a.ldw + c;
-        } else {
-            const int c = min(m0 + T::MSide::row(j), a.cols - 1);
-            op.wm.p[j] = a.w + (int64_t)c * a.ldw + T::MSide::elem(j) + (int64_t)s0 * kStepK;
-        }
-    }
-    op.wm.step = BWD ? (int64_t)kStepK * a.ldw : kStepK;
-    op.wm.left = a.k - s0 * kStepK;
-
+    const int steps = main + (op.blocks ? units : (units + 1) / 2);
+    if (units > 0) op.start(units);
+    if (!early) mma_begin<T>(op, steps, g_lds);
     typename T::Acc acc;
     clear<T>(acc);
-    mma_loop<T>(op, min(s1, a.k / kStepK) - s0, t1 - t0, acc, g_lds);
-
-    if constexpr (T::BM * T::BN <= 128 * 128) {
-        if (a.splits > 1) {
-            const int tile = at.n * a.mtiles + at.m;
-            if (!combine_splits<T>(acc, a.slots + (int64_t)tile * a.splits * (T::BM * T::BN), a.counters + tile, split,
-                                   a.splits, rows, &s_flag))
-                return;
-        }
-    }
+    mma_loop<T>(op, a.k / kStepK, steps, acc, g_lds);
 
     // biases: of the projection for every token, of the adapter where there is one
     if constexpr (T::QUADS) {
-        // groups of 8 consecutive columns (never across a slice's edge)
+        // groups of 8 consecutive columns (never across a slice's edge); a group's loads are issued together
 #pragma unroll
         for (int mt = 0; mt < T::MT; mt += 2) {
             const int c = m0 + T::m_of(mt);
-            const bool cin = c < a.cols;
+            if (c >= a.cols) continue;
             float wb[8];
 #pragma unroll
             for (int x = 0; x < 8; ++x) wb[x] = 0.f;
-            if (a.w_bias && cin) {
+            if (a.w_bias) {
                 const u32x4 v = *reinterpret_cast<const u32x4 *>(a.w_bias + c);
 #pragma unroll
                 for (int x = 0; x < 4; ++x) unpack_bf16(v[x], wb[2 * x], wb[2 * x + 1]);
             }
             const uint16_t *bp = nullptr;
             int bw = 0;
-            for (int i = 0; i < a.slices; ++i) {
-                const int ci = select_slice(a.col, i), wi = select_slice(a.width, i);
-                const uint16_t *bi = select_slice(a.bias, i);
-                if (bi && c >= ci && c < ci + wi) {
-                    bp = bi + (c - ci);
-                    bw = wi;
+            if (a.has_bias)
+                for (int i = op.sl0; i < op.sl1; ++i) {
+                    const int ci = select_slice(a.col, i), wi = select_slice(a.width, i);
+                    const uint16_t *bi = select_slice(a.bias, i);
+                    if (bi && c >= ci && c < ci + wi) {
+                        bp = bi + (c - ci);
+                        bw = wi;
+                    }
                 }
-            }
+            u32x4 b[T::NT];
+            if (a.has_bias)
+#pragma unroll
+                for (int nt = 0; nt < T::NT; ++nt) {
+                    const int m = s_id[T::n_of(nt)];
+                    b[nt] = u32x4{0u, 0u, 0u, 0u};
+                    if (bp && m >= 0) b[nt] = *reinterpret_cast<const u32x4 *>(bp + (int64_t)m * bw);
+                }
 #pragma unroll
             for (int nt = 0; nt < T::NT; ++nt) {
                 const int r = T::n_of(nt);
-                if (r >= rows || !cin) continue;
-                const int id = s_id[r];
                 float v[8];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     v[x] = acc[mt][nt][x] + wb[x];
                     v[4 + x] = acc[mt + 1][nt][x] + wb[4 + x];
                 }
-                if (bp && id >= 0) {
-                    const u32x4 b = *reinterpret_cast<const u32x4 *>(bp + (int64_t)id * bw);
+                if (a.has_bias)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         float p, q;
-                        unpack_bf16(b[x], p, q);
+                        unpack_bf16(b[nt][x], p, q);
                         v[2 * x] += p;
                         v[2 * x + 1] += q;
                     }
-                }
-                *reinterpret_cast<u32x4 *>(a.y + (int64_t)s_tok[r] * a.ldy + c) =
-                    u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+                if (r < rows)
+                    *reinterpret_cast<u32x4 *>(a.y + (int64_t)s_tok[r] * a.ldy + c) =
+                        u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
             }
         }
     } else {
@@ -460,6 +460,163 @@ __global__ __launch_bounds__(T::kThreads) void linear_kernel(LinearArgs a) {
                 if (c < a.cols) *reinterpret_cast<u32x2g *>(row + c) = u32x2g{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
             }
         }
+    }
+}
+
+// ---------------------------------------------------------------- few tokens
+
+// Up to 32 tokens: a call is one pass over W and the adapters, bound by their
+// bytes and by latency, so it is two launches without a sort or a split over
+// workgroups.  s: 16 ranks of one token and slice a workgroup, 4 lanes a rank.
+struct RowsArgs {
+    const int32_t *ids, *no_lora;   // a batch without adapters has no ids
+    const uint16_t *x;
+    int64_t ldx;
+    const uint16_t *w;
+    int64_t ldw;
+    const uint16_t *w_bias;
+    const uint16_t *la[LORA_MAX_SLICES], *lb[LORA_MAX_SLICES], *bias[LORA_MAX_SLICES];
+    int32_t width[LORA_MAX_SLICES], col[LORA_MAX_SLICES];
+    float *buf;
+    uint16_t *y;
+    int64_t ldy;
+    int32_t num_tokens, cols, k, rank, slices, max_loras;
+    float scale;
+};
+constexpr int kRowsTokens = 32, kRowsWaves = 16, kRowsCols = 32, kRowsThreads = kRowsWaves * kWave;
+constexpr int kRowsRanks = 16, kRowsShrinkWaves = 8;
+
+__device__ __forceinline__ void fma_bf16x8(const u32x4 &a, const u32x4 &b, float &sum) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        float a0, a1, b0, b1;
+        unpack_bf16(a[x], a0, a1);
+        unpack_bf16(b[x], b0, b1);
+        sum = fmaf(a0, b0, sum);
+        sum = fmaf(a1, b1, sum);
+    }
+}
+
+__global__ __launch_bounds__(kRowsShrinkWaves *kWave) void rows_shrink_kernel(RowsArgs a) {
+    __shared__ float s_part[kRowsShrinkWaves][kRowsRanks];
+    const int per = (a.rank + kRowsRanks - 1) / kRowsRanks;
+    const int t = blockIdx.x / (per * a.slices), i = blockIdx.x / per % a.slices, r0 = blockIdx.x % per * kRowsRanks;
+    const int none = *a.no_lora, id = a.ids[t];
+    if (none || id < 0 || id >= a.max_loras) return;
+    const int rank = min(r0 + (lane_id() >> 2), a.rank - 1), first = (wave_id() * 4 + (lane_id() & 3)) * 8;
+    const uint16_t *row = select_slice(a.la, i) + ((int64_t)id * a.rank + rank) * a.k, *x = a.x + t * a.ldx;
+    constexpr int kStride = kRowsShrinkWaves * 32;
+    float sum = 0.f;
+#pragma unroll 8
+    for (int k = first; k < a.k; k += kStride)
+        fma_bf16x8(*reinterpret_cast<const u32x4 *>(row + k), *reinterpret_cast<const u32x4 *>(x + k), sum);
+    sum += __shfl_xor(sum, 1);
+    sum += __shfl_xor(sum, 2);
+    if ((lane_id() & 3) == 0) s_part[wave_id()][lane_id() >> 2] = sum;
+    __syncthreads();
+    if (threadIdx.x < kRowsRanks && r0 + (int)threadIdx.x < a.rank) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kRowsShrinkWaves; ++w) v += s_part[w][threadIdx.x];
+        a.buf[((int64_t)i * a.num_tokens + t) * a.rank + r0 + threadIdx.x] = a.scale * v;
+    }
+}
+
+// y: 32 columns a workgroup; its 16 waves share K, every operand goes from
+// memory straight into the registers of the MFMA, and the waves' sums are added
+// in wave order through LDS.  A thread adds its column's and token's adapter as
+// a float32 dot product, whose loads travel with the first of W's.
+template <int NT>
+__global__ __launch_bounds__(kRowsThreads) void rows_kernel(RowsArgs a) {
+    constexpr int kOut = kRowsCols * 16 * NT, kPer = kOut > kRowsThreads ? kOut / kRowsThreads : 1;
+    __shared__ float s_sum[kRowsWaves][16 * NT][kRowsCols];   // column c of token t in slot c ^ t: 64 banks
+    const int tid = threadIdx.x, l16 = lane_id() & 15, g = lane_id() >> 4, c0 = blockIdx.x * kRowsCols;
+    const uint16_t *wp[2], *xp[NT];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) wp[m] = a.w + (int64_t)min(c0 + 16 * m + l16, a.cols - 1) * a.ldw;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) xp[t] = a.x + (int64_t)min(16 * t + l16, a.num_tokens - 1) * a.ldx;
+    floatx4 acc[2][NT];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[m][t] = floatx4{0.f, 0.f, 0.f, 0.f};
+
+    // the wave's K: chunks of 32 elements wave, wave + 16, ..., four at a time
+    constexpr int kChunk = 4, kStride = kRowsWaves * 32;
+    u32x4 wv[kChunk][2], xv[kChunk][NT];
+    auto load = [&](int k0) {
+#pragma unroll
+        for (int q = 0; q < kChunk; ++q) {
+            const int k = k0 + q * kStride + 8 * g;
+            const bool in = k < a.k;
+#pragma unroll
+            for (int m = 0; m < 2; ++m) wv[q][m] = in ? *reinterpret_cast<const u32x4 *>(wp[m] + k) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int t = 0; t < NT; ++t) xv[q][t] = in ? *reinterpret_cast<const u32x4 *>(xp[t] + k) : u32x4{0u, 0u, 0u, 0u};
+        }
+    };
+    int k0 = wave_id() * 32;
+    load(k0);
+
+    float add[kPer];
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+        const int o = tid + q * kRowsThreads, c = c0 + o % kRowsCols, t = o / kRowsCols;
+        add[q] = 0.f;
+        if (t >= a.num_tokens || c >= a.cols) continue;
+        const int none = *a.no_lora, id = a.ids[t];
+        if (a.w_bias) add[q] = bf16_bits_to_float(a.w_bias[c]);
+        if (none || id < 0 || id >= a.max_loras) continue;
+        for (int i = 0; i < a.slices; ++i) {
+            const int in = c - select_slice(a.col, i), width = select_slice(a.width, i);
+            if (in < 0 || in >= width) continue;
+            const uint16_t *b = select_slice(a.lb, i) + ((int64_t)id * width + in) * a.rank;
+            const float *s = a.buf + ((int64_t)i * a.num_tokens + t) * a.rank;
+            float dot = 0.f;
+            for (int j = 0; j < a.rank; j += 8) {
+                const u32x4 v = *reinterpret_cast<const u32x4 *>(b + j);
+                const floatx4 s0 = *reinterpret_cast<const floatx4 *>(s + j), s1 = *reinterpret_cast<const floatx4 *>(s + j + 4);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    float b0, b1;
+                    unpack_bf16(v[x], b0, b1);
+                    dot = fmaf(b0, x < 2 ? s0[2 * x] : s1[2 * x - 4], dot);
+                    dot = fmaf(b1, x < 2 ? s0[2 * x + 1] : s1[2 * x - 3], dot);
+                }
+            }
+            const uint16_t *bias = select_slice(a.bias, i);
+            if (bias) dot += bf16_bits_to_float(bias[(int64_t)id * width + in]);
+            add[q] += dot;
+        }
+    }
+
+    for (;;) {
+#pragma unroll
+        for (int q = 0; q < kChunk; ++q)
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) acc[m][t] = mfma16x16x32(as_bf16x8(wv[q][m]), as_bf16x8(xv[q][t]), acc[m][t]);
+        k0 += kChunk * kStride;
+        if (k0 >= a.k) break;
+        load(k0);
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) s_sum[wave_id()][16 * t + l16][(16 * m + 4 * g + x) ^ (16 * t + l16)] = acc[m][t][x];
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+        const int o = tid + q * kRowsThreads, c = o % kRowsCols, t = o / kRowsCols;
+        if (o >= kOut || t >= a.num_tokens || c0 + c >= a.cols) continue;
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kRowsWaves; ++w) v += s_sum[w][t][c ^ t];
+        a.y[t * a.ldy + c0 + c] = (uint16_t)float_to_bf16_bits(v + add[q]);
     }
 }
 
@@ -514,6 +671,7 @@ __global__ __launch_bounds__(T::kThreads) void u_kernel(UArgs a) {
     op.wm.left = width - s0 * kStepK;
     typename T::Acc acc;
     clear<T>(acc);
+    mma_begin<T>(op, s1 - s0, g_lds);
     mma_loop<T>(op, min(s1, width / kStepK) - s0, s1 - s0, acc, g_lds);
     if (a.splits > 1 && !combine_splits<T>(acc, a.slots + (int64_t)unit * a.splits * (T::BM * T::BN), a.counters + unit,
                                            split, a.splits, ut.rows, &s_flag))
@@ -649,6 +807,7 @@ __global__ __launch_bounds__(T::kThreads) void grad_kernel(GradArgs a) {
         }
         op.wp.step = (int64_t)kStepK * row_len;
         op.wp.left = sg.count;
+        mma_begin<T>(op, (sg.count + kStepK - 1) / kStepK, g_lds);
         mma_loop<T>(op, sg.count / kStepK, (sg.count + kStepK - 1) / kStepK, acc, g_lds);
     }
     uint16_t *out = select_slice(a.out, i);
@@ -680,47 +839,38 @@ constexpr size_t kRound = 256;
 size_t up(size_t v) { return (v + kRound - 1) / kRound * kRound; }
 long ceil_div(long a, long b) { return (a + b - 1) / b; }
 
-enum LinearTile { kBig, kMid, kSmall };
+enum LinearTile { kBig, kMid, kFlat, kSmall };
 struct LinearPlan {
     LinearTile tile;
-    int bm, bn, mtiles, ntiles, splits;
-    size_t slot_bytes;
+    int mtiles, ntiles;
 };
 
-// The tile and K split of y or dx (n x cols over k): the 256 x 256 tile where
-// it fills the GPU's 256 CUs, else 128 x 128, or 128 x 32 for few tokens;
-// there K is split while the workgroups do not fill the CUs twice (each CU
-// holds at least two) and every part keeps at least 4 steps.
-LinearPlan plan_linear(long n, long cols, long k, bool allow_split) {
+// The tile of y or dx (n x cols): the largest of 256 x 256, 128 x 128, 64
+// columns x 128 tokens and 64 x 64 of which there are enough for the GPU's 256
+// CUs (one of the first a CU at a time, two of the second and the last).  K is
+// not split: joining fp32 partial tiles across XCDs took 22 of the 70 us of a
+// product of 256 tokens by 6144 columns over 4096.
+LinearPlan plan_linear(long n, long cols) {
+    auto tiles = [&](long bm, long bn) { return ceil_div(cols, bm) * ceil_div(n, bn); };
     LinearPlan p;
-    const long steps = ceil_div(k, kStepK);
-    if (ceil_div(n, 256) * ceil_div(cols, 256) >= 192 && n > 128) {
+    long bm = 64, bn = 64;
+    p.tile = kSmall;
+    if (n > 128 && tiles(256, 256) >= 192) {
         p.tile = kBig;
-        p.bm = p.bn = 256;
-    } else if (n > 32) {
+        bm = bn = 256;
+    } else if (tiles(128, 128) >= 256) {
         p.tile = kMid;
-        p.bm = p.bn = 128;
-    } else {
-        p.tile = kSmall;
-        p.bm = 128;
-        p.bn = 32;
+        bm = bn = 128;
+    } else if (tiles(64, 128) >= 160) {
+        p.tile = kFlat;
+        bn = 128;
     }
-    p.mtiles = (int)ceil_div(cols, p.bm);
-    p.ntiles = (int)ceil_div(n, p.bn);
-    long splits = 1;
-    const long tiles = (long)p.mtiles * p.ntiles;
-    if (p.tile != kBig && allow_split && tiles > 0) {
-        splits = 512 / tiles;
-        if (splits > steps / 4) splits = steps / 4;
-        if (splits > 16) splits = 16;
-        if (splits < 1) splits = 1;
-    }
-    p.splits = (int)splits;
-    p.slot_bytes = p.splits > 1 ? sizeof(float) * (size_t)tiles * p.splits * p.bm * p.bn : 0;
+    p.mtiles = (int)ceil_div(cols, bm);
+    p.ntiles = (int)ceil_div(n, bn);
     return p;
 }
 
-constexpr int kCounterWords = 1024;   // tiles that may be split: at most 512 / 2, u units likewise
+constexpr int kCounterWords = 1024;   // units of the u product whose K may be split
 
 struct UPlan {
     int bm, tile_tokens, tiles_cap, splits;
@@ -746,7 +896,7 @@ UPlan plan_u(long n, int max_loras, int slices, int rank, long widest) {
 struct Layout {
     size_t counters, segs, num_tiles, tiles, s, u, slots, total;
 };
-Layout layout(long n, int max_loras, int slices, int rank, size_t slot_bytes, int tiles_cap, bool backward) {
+Layout layout(long n, int max_loras, int slices, int rank, const UPlan &u, bool backward) {
     Layout l;
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -757,11 +907,11 @@ Layout layout(long n, int max_loras, int slices, int rank, size_t slot_bytes, in
     l.counters = take(sizeof(int32_t) * kCounterWords);
     l.segs = take(backward ? sizeof(SegEntry) * (size_t)max_loras : 0);
     l.num_tiles = take(backward ? sizeof(int32_t) : 0);
-    l.tiles = take(backward ? sizeof(UTile) * (size_t)tiles_cap : 0);
+    l.tiles = take(backward ? sizeof(UTile) * (size_t)u.tiles_cap : 0);
     const size_t rows = sizeof(uint16_t) * (size_t)slices * (size_t)n * (size_t)packed_row(rank);
     l.s = take(rows);
     l.u = take(backward ? rows : 0);
-    l.slots = take(slot_bytes);
+    l.slots = take(backward ? u.slot_bytes : 0);
     l.total = at;
     return l;
 }
@@ -804,11 +954,6 @@ int check_call(int64_t ldx, int num_tokens, int hidden, const void *w, int64_t l
     return LORA_OK;
 }
 
-long sum_widths(const int *w, int n) {
-    long s = 0;
-    for (int i = 0; i < n; ++i) s += w[i];
-    return s;
-}
 int widest(const int *w, int n) {
     int s = 0;
     for (int i = 0; i < n; ++i) s = w[i] > s ? w[i] : s;
@@ -843,25 +988,21 @@ hipError_t launch_pack(const lora_meta_t *meta, const MetaView &view, const floa
 }
 
 template <bool BWD>
-hipError_t launch_linear(LinearArgs &a, const LinearPlan &p, hipStream_t s) {
+hipError_t launch_linear(LinearArgs &a, hipStream_t s) {
+    const LinearPlan p = plan_linear(a.num_tokens, a.cols);
     a.mtiles = p.mtiles;
     a.ntiles = p.ntiles;
-    a.splits = p.splits;
     a.group = 8;
-    const unsigned grid = tile_grid((long)p.mtiles * p.ntiles) * (unsigned)p.splits;
+    const unsigned grid = tile_grid((long)p.mtiles * p.ntiles);
+    auto launch = [&](auto tile) {
+        using T = decltype(tile);
+        return launch_tiles<linear_kernel<T, BWD>>(grid, T::kThreads, T::kLds, s, a);
+    };
     switch (p.tile) {
-        case kBig: {
-            using T = Tile<256, 256, 4, 2, BWD, false>;
-            return launch_tiles<linear_kernel<T, BWD>>(grid, T::kThreads, T::kLds, s, a);
-        }
-        case kMid: {
-            using T = Tile<128, 128, 2, 2, BWD, false>;
-            return launch_tiles<linear_kernel<T, BWD>>(grid, T::kThreads, T::kLds, s, a);
-        }
-        default: {
-            using T = Tile<128, 32, 2, 2, BWD, false>;
-            return launch_tiles<linear_kernel<T, BWD>>(grid, T::kThreads, T::kLds, s, a);
-        }
+        case kBig: return launch(Tile<256, 256, 4, 2, BWD, false>{});
+        case kMid: return launch(Tile<128, 128, 2, 2, BWD, false>{});
+        case kFlat: return launch(Tile<64, 128, 1, 4, BWD, false, 0, 5>{});
+        default: return launch(Tile<64, 64, 1, 4, BWD, false, 0, 4>{});
     }
 }
 
@@ -898,15 +1039,9 @@ extern "C" {
 size_t lora_linear_workspace_bytes(int num_tokens, int max_loras, int hidden, const int *slice_widths, int num_slices,
                                    int rank, int backward) {
     if (check_sizes(num_tokens, max_loras, hidden, slice_widths, num_slices, rank)) return 0;
-    const long out = sum_widths(slice_widths, num_slices), n = num_tokens;
-    size_t slots = plan_linear(n, out, hidden, true).slot_bytes;
+    const long n = num_tokens;
     const UPlan u = plan_u(n, max_loras, num_slices, rank, widest(slice_widths, num_slices));
-    if (backward) {
-        const size_t d = plan_linear(n, hidden, out, true).slot_bytes;
-        slots = slots > d ? slots : d;
-        slots = slots > u.slot_bytes ? slots : u.slot_bytes;
-    }
-    return layout(n, max_loras, num_slices, rank, slots, u.tiles_cap, backward != 0).total;
+    return layout(n, max_loras, num_slices, rank, u, backward != 0).total;
 }
 
 int lora_linear(const void *x, int64_t ldx, int num_tokens, int hidden, const void *w, int64_t ldw, int out_features,
@@ -921,14 +1056,47 @@ int lora_linear(const void *x, int64_t ldx, int num_tokens, int hidden, const vo
         if (bias[i] && !aligned16(bias[i])) return LORA_ERR_ALIGN;
     if (num_tokens > 0 && (!x || !buf || !y)) return LORA_ERR_NULL;
     if (num_tokens > 0 && (!aligned16(x) || !aligned16(buf) || !aligned16(y))) return LORA_ERR_ALIGN;
-    LinearPlan p = plan_linear(num_tokens, out_features, hidden, true);
-    Layout l = layout(num_tokens, meta->max_loras, num_slices, rank, p.slot_bytes, 0, false);
-    if (l.total > workspace_bytes) {   // sized for narrower outputs: no K split
-        p = plan_linear(num_tokens, out_features, hidden, false);
-        l = layout(num_tokens, meta->max_loras, num_slices, rank, 0, 0, false);
-        if (l.total > workspace_bytes) return LORA_ERR_BUFFER;
-    }
+    const UPlan u = plan_u(num_tokens, meta->max_loras, num_slices, rank, widest(slice_widths, num_slices));
+    const Layout l = layout(num_tokens, meta->max_loras, num_slices, rank, u, false);
+    if (l.total > workspace_bytes) return LORA_ERR_BUFFER;
     if (num_tokens == 0) return LORA_OK;
+    if (num_tokens <= kRowsTokens) {
+        RowsArgs r;
+        memset(&r, 0, sizeof r);
+        r.ids = meta->token_lora_mapping;
+        r.no_lora = view_of(meta).no_lora;
+        r.x = static_cast<const uint16_t *>(x);
+        r.ldx = ldx;
+        r.w = static_cast<const uint16_t *>(w);
+        r.ldw = ldw;
+        r.w_bias = static_cast<const uint16_t *>(w_bias);
+        for (int i = 0, off = offset_start; i < num_slices; off += slice_widths[i++]) {
+            r.la[i] = static_cast<const uint16_t *>(lora_a[i]);
+            r.lb[i] = static_cast<const uint16_t *>(lora_b[i]);
+            r.bias[i] = bias ? static_cast<const uint16_t *>(bias[i]) : nullptr;
+            r.width[i] = slice_widths[i];
+            r.col[i] = off;
+        }
+        r.buf = buf;
+        r.y = static_cast<uint16_t *>(y);
+        r.ldy = ldy;
+        r.num_tokens = num_tokens;
+        r.cols = out_features;
+        r.k = hidden;
+        r.rank = rank;
+        r.slices = num_slices;
+        r.max_loras = meta->max_loras;
+        r.scale = scale;
+        const unsigned shrinks = (unsigned)(num_tokens * num_slices * (int)ceil_div(rank, kRowsRanks));
+        hipLaunchKernelGGL(rows_shrink_kernel, dim3(shrinks), dim3(kRowsShrinkWaves * kWave), 0, stream, r);
+        if (hipGetLastError() != hipSuccess) return LORA_ERR_LAUNCH;
+        const dim3 grid((unsigned)ceil_div(out_features, kRowsCols)), block(kRowsThreads);
+        if (num_tokens <= 16)
+            hipLaunchKernelGGL(rows_kernel<1>, grid, block, 0, stream, r);
+        else
+            hipLaunchKernelGGL(rows_kernel<2>, grid, block, 0, stream, r);
+        return hipGetLastError() == hipSuccess ? LORA_OK : LORA_ERR_LAUNCH;
+    }
     char *ws = static_cast<char *>(workspace);
     if ((st = shrink_fresh(x, ldx, num_tokens, hidden, lora_a, num_slices, rank, buf, meta, scale, stream))) return st;
     const MetaView view = view_of(meta);
@@ -948,6 +1116,7 @@ int lora_linear(const void *x, int64_t ldx, int num_tokens, int hidden, const vo
     for (int i = 0; i < num_slices; ++i) {
         a.lw[i] = static_cast<const uint16_t *>(lora_b[i]);
         a.bias[i] = bias ? static_cast<const uint16_t *>(bias[i]) : nullptr;
+        a.has_bias |= a.bias[i] != nullptr;
         a.width[i] = slice_widths[i];
         a.col[i] = off;
         off += slice_widths[i];
@@ -955,15 +1124,13 @@ int lora_linear(const void *x, int64_t ldx, int num_tokens, int hidden, const vo
     a.packed = packed;
     a.y = static_cast<uint16_t *>(y);
     a.ldy = ldy;
-    a.slots = reinterpret_cast<float *>(ws + l.slots);
-    a.counters = reinterpret_cast<int32_t *>(ws + l.counters);
     a.num_tokens = num_tokens;
     a.cols = out_features;
     a.k = hidden;
     a.rank = rank;
     a.slices = num_slices;
     a.max_loras = meta->max_loras;
-    return launch_linear<false>(a, p, stream) == hipSuccess ? LORA_OK : LORA_ERR_LAUNCH;
+    return launch_linear<false>(a, stream) == hipSuccess ? LORA_OK : LORA_ERR_LAUNCH;
 }
 
 int lora_linear_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx, int num_tokens, int hidden,
@@ -985,18 +1152,9 @@ int lora_linear_backward(const void *dy, int64_t lddy, const void *x, int64_t ld
     if (num_tokens > 0 && (!dy || !x || !buf || !dbuf)) return LORA_ERR_NULL;
     if (num_tokens > 0 && (!aligned16(dy) || !aligned16(x) || !aligned16(buf) || !aligned16(dbuf) || !aligned16(dx)))
         return LORA_ERR_ALIGN;
-    LinearPlan p = plan_linear(num_tokens, hidden, out_features, true);
-    UPlan u = plan_u(num_tokens, meta->max_loras, num_slices, rank, widest(slice_widths, num_slices));
-    auto make = [&] {
-        return layout(num_tokens, meta->max_loras, num_slices, rank, p.slot_bytes > u.slot_bytes ? p.slot_bytes : u.slot_bytes,
-                      u.tiles_cap, true);
-    };
-    Layout l = make();
-    if (l.total > workspace_bytes) {
-        p = plan_linear(num_tokens, hidden, out_features, false);
-        l = make();
-        if (l.total > workspace_bytes) return LORA_ERR_BUFFER;
-    }
+    const UPlan u = plan_u(num_tokens, meta->max_loras, num_slices, rank, widest(slice_widths, num_slices));
+    const Layout l = layout(num_tokens, meta->max_loras, num_slices, rank, u, true);
+    if (l.total > workspace_bytes) return LORA_ERR_BUFFER;
     char *ws = static_cast<char *>(workspace);
     const MetaView view = view_of(meta);
     uint16_t *s = reinterpret_cast<uint16_t *>(ws + l.s), *up = reinterpret_cast<uint16_t *>(ws + l.u);
@@ -1048,15 +1206,13 @@ int lora_linear_backward(const void *dy, int64_t lddy, const void *x, int64_t ld
         a.packed = up;
         a.y = static_cast<uint16_t *>(dx);
         a.ldy = lddx;
-        a.slots = slots;
-        a.counters = counters;
         a.num_tokens = num_tokens;
         a.cols = hidden;
         a.k = out_features;
         a.rank = rank;
         a.slices = num_slices;
         a.max_loras = meta->max_loras;
-        if (launch_linear<true>(a, p, stream) != hipSuccess) return LORA_ERR_LAUNCH;
+        if (launch_linear<true>(a, stream) != hipSuccess) return LORA_ERR_LAUNCH;
     }
     GradArgs g;
     memset(&g, 0, sizeof g);

@@ -91,6 +91,7 @@ __global__ __launch_bounds__(T::kThreads) void logit_kernel(LogitArgs a) {
     op.wn.left = op.wm.left = a.hidden;
     typename T::Acc acc;
     clear<T>(acc);
+    mma_begin<T>(op, (a.hidden + kStepK - 1) / kStepK, g_lds);
     mma_loop<T>(op, a.hidden / kStepK, (a.hidden + kStepK - 1) / kStepK, acc, g_lds);
 
     if constexpr (!GRAD) {
@@ -254,6 +255,7 @@ __global__ __launch_bounds__(T::kThreads) void dx_kernel(DxArgs a) {
     op.wn.left = op.wm.left = a.rows - s0 * kStepK;
     typename T::Acc acc;
     clear<T>(acc);
+    mma_begin<T>(op, s1 - s0, g_lds);
     mma_loop<T>(op, min(s1, a.rows / kStepK) - s0, s1 - s0, acc, g_lds);
 #pragma unroll
     for (int nt = 0; nt < T::NT; ++nt) {
@@ -331,6 +333,7 @@ __global__ __launch_bounds__(T::kThreads) void dw_kernel(DwArgs a) {
             op.wn.p[j] = a.g + (int64_t)T::NSide::row(j) * a.ldg + min(v0 + T::NSide::elem(j), (int)a.ldg - 8);
         op.wn.step = (int64_t)kStepK * a.ldg;
         op.wn.left = n;
+        mma_begin<T>(op, (n + kStepK - 1) / kStepK, g_lds);
         mma_loop<T>(op, n / kStepK, (n + kStepK - 1) / kStepK, acc, g_lds);
     }
 #pragma unroll
@@ -453,7 +456,7 @@ hipError_t with_tile(LossTile t, F f) {
     switch (t) {
         case kBig: return f(Tile<256, 256, 4, 2, MS, NS>{});
         case kMid: return f(Tile<128, 128, 2, 2, MS, NS>{});
-        default: return f(Tile<128, 32, 2, 2, MS, NS>{});
+        default: return f(Tile<128, 32, 2, 2, MS, NS, 0, 4>{});
     }
 }
 
