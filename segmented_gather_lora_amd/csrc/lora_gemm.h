@@ -72,6 +72,11 @@ __device__ __forceinline__ void dma16(const uint16_t *src, uint32_t dst) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(dst), "v"(src) : "memory");
 }
 
+// The same from a scalar base and a lane's byte offset.
+__device__ __forceinline__ void dma16(const uint16_t *base, uint32_t offset, uint32_t dst) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst), "v"(offset), "s"(base) : "memory");
+}
+
 // Which rows (or K rows) and chunks of a side's stage a lane copies, and where
 // it reads its operands.  ROWS: rows of the tile's side; WAVES: waves that
 // share the copy.  QUADS (contiguous sides): rows of a 64-row group are dealt
@@ -172,6 +177,10 @@ struct Tile {
 #pragma unroll
         for (int i = 0; i < kReads; ++i) read_one(r, st, h, i);
     }
+    __device__ __forceinline__ static void read_m(Half &r, const lds_byte *st, int h) {
+#pragma unroll
+        for (int i = 0; i < kMReads; ++i) read_one(r, st, h, i);
+    }
     __device__ __forceinline__ static void read_n(Half &r, const lds_byte *st, int h) {
 #pragma unroll
         for (int i = kMReads; i < kReads; ++i) read_one(r, st, h, i);
@@ -231,7 +240,8 @@ __device__ __forceinline__ void own_reads_barrier() { asm volatile("s_waitcnt lg
 // op.issue(stage) copies the next step's operands to the LDS byte address
 // `stage` (called once per step, in order; every wave makes at least Op::kLast
 // copies after the last of the N side); op.read(half, stage, s, h) and
-// op.mma(half, acc, s, h) read a half of step s and multiply it into the sums.
+// op.mma(half, acc, s, h) read a half of step s (half 1 with half 0's operands at
+// hand) and multiply it into the sums.
 // The first `plain` steps make T::kLoads copies in every wave: op.load(stage, i)
 // are these one by one, op.next() moves on to the next step, op.mma_n(half, acc,
 // nt) multiplies.  All threads of the workgroup call it; LDS of T::kLds bytes at
@@ -261,16 +271,21 @@ __device__ __forceinline__ void ring_loop(Op &op, int plain, int nsteps, typenam
     // at the barrier step s has landed, for every wave, and step s - 1 is read
     for (; s + S - 1 < plain; ++s) {
         wait_loads_barrier<(S - 2) * T::kLoads>();
-#pragma unroll
-        for (int i = 0; i < T::kLoads; ++i) op.load(base + to, i);
-        op.next();
         typename T::Half r0, r1;
         T::read(r0, lds + cur, 0);
         T::read(r1, lds + cur, 1);
+        __builtin_amdgcn_sched_barrier(0);
+        // the copies go between the MFMAs: a wave that issues them first waits for
+        // the whole workgroup's before it reads its operands
 #pragma unroll
-        for (int nt = 0; nt < T::NT; ++nt) op.mma_n(r0, acc, nt);
+        for (int g = 0; g < 2 * T::NT; ++g) {
+            constexpr int G = 2 * T::NT, D = T::kLoads;
+            op.mma_n(g < T::NT ? r0 : r1, acc, g % T::NT);
 #pragma unroll
-        for (int nt = 0; nt < T::NT; ++nt) op.mma_n(r1, acc, nt);
+            for (int i = g * D / G; i < (g + 1) * D / G; ++i) op.load(base + to, i);
+            if (g == G - 1) op.next();
+            __builtin_amdgcn_sched_barrier(0);
+        }
         turn();
     }
     for (; s < nsteps; ++s) {
@@ -281,11 +296,11 @@ __device__ __forceinline__ void ring_loop(Op &op, int plain, int nsteps, typenam
         else
             wait_loads_barrier<0>();
         if (s + S - 1 < nsteps) op.issue(base + to);
-        typename T::Half r;
-        op.read(r, lds + cur, s, 0);
-        op.mma(r, acc, s, 0);
-        op.read(r, lds + cur, s, 1);
-        op.mma(r, acc, s, 1);
+        typename T::Half r0, r1;
+        op.read(r0, lds + cur, s, 0);
+        op.read(r1, lds + cur, s, 1, r0);
+        op.mma(r0, acc, s, 0);
+        op.mma(r1, acc, s, 1);
         turn();
     }
 }
@@ -344,7 +359,7 @@ __device__ __forceinline__ void mma_loop(Op &op, int plain, int nsteps, typename
         typename T::Half r;
         op.read(r, lds + cur, s, 0);
         op.mma(r, acc, s, 0);
-        op.read(r, lds + cur, s, 1);
+        op.read(r, lds + cur, s, 1, r);
         own_reads_barrier();
         if (s + 2 < nsteps) op.issue(base + cur);
         op.mma(r, acc, s, 1);
@@ -423,6 +438,9 @@ struct PairOp {
     WM wm;
     WN wn;
     __device__ __forceinline__ void read(typename T::Half &r, const lds_byte *st, int, int h) { T::read(r, st, h); }
+    __device__ __forceinline__ void read(typename T::Half &r, const lds_byte *st, int, int h, const typename T::Half &) {
+        T::read(r, st, h);
+    }
     __device__ __forceinline__ void mma(const typename T::Half &h, typename T::Acc &acc, int, int) { T::mma(h, acc); }
     __device__ __forceinline__ void mma_n(const typename T::Half &h, typename T::Acc &acc, int nt) { T::mma_n(h, acc, nt); }
     __device__ __forceinline__ void load(uint32_t at, int i) {

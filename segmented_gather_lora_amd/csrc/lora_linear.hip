@@ -151,7 +151,7 @@ struct LinearArgs {
     uint16_t *y;                                // y or dx
     int64_t ldy;
     int32_t num_tokens, cols, k, rank, slices, max_loras;
-    int32_t mtiles, ntiles, group, has_bias;
+    int32_t mtiles, ntiles, group, has_bias, row_len;   // row_len: packed_row(rank)
 };
 
 // The adapters' share of a tile's K walk is made of units, for every slice that
@@ -161,56 +161,51 @@ struct LinearArgs {
 // second; both are multiplied with the same 32 ranks of the adapter's matrix,
 // staged once.  Up to 16 ranks a unit is half a step, [16 hi | 16 lo] against
 // the ranks twice, so that a step holds two adapters.
+//
+// What a unit needs of the two tables in LDS is read a unit ahead and made
+// scalar where it is used, so that a unit does not wait for it.
+struct SliceEntry {
+    uint32_t weights[2];   // the adapters' matrices of the slice
+    int32_t width, col;
+};
+struct SegRow {
+    int32_t lo, hi, id;    // rows of the tile, LoRA id
+};
+__device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 template <class T, bool BWD>
 struct LinearOp : PlainOp<T> {
     static constexpr int kLast = T::MSide::kInstr / 2;
     const LinearArgs &a;
-    const int (*seg)[4];       // LDS: lo, hi (sorted positions), id
+    const SegRow *segs;        // LDS
+    const SliceEntry *slices;  // LDS
     int main_left, main_steps, m0, p0, nseg;
     int sl0, sl1, blocks;      // slices that meet the tile; blocks of 32 ranks (0: ranks up to 16)
     int sl, e, kb;             // next unit to copy
     int me, mleft, munits;     // next unit to multiply: its adapter, that adapter's units left, all units left
-    struct Slice {
-        const uint16_t *rows, *weights;   // the packed rows from the tile's first on, the adapters' matrices
-        int width, col;
-    } at_slice;
-    struct Seg {
-        int lo, hi;
-        const uint16_t *weights;
-    } at_seg;
-    int mlo, mhi;
+    SliceEntry slice;          // of the next unit to copy
+    SegRow seg;
+    int mlo, mhi;              // rows of the next unit to multiply
 
-    __device__ __forceinline__ LinearOp(const LinearArgs &args, const int (*segments)[4]) : a(args), seg(segments) {}
+    __device__ __forceinline__ LinearOp(const LinearArgs &args, const SegRow *g, const SliceEntry *s)
+        : a(args), segs(g), slices(s) {}
     __device__ __forceinline__ int per_seg() const { return blocks ? blocks : 1; }
-    __device__ __forceinline__ void enter_slice() {
-        at_slice.width = BWD ? a.cols : select_slice(a.width, sl);
-        at_slice.col = BWD ? 0 : select_slice(a.col, sl);
-        at_slice.rows = a.packed + ((int64_t)sl * a.num_tokens + p0) * packed_row(a.rank);
-        at_slice.weights = select_slice(a.lw, sl);
-    }
-    __device__ __forceinline__ void enter_seg() {
-        at_seg.lo = __builtin_amdgcn_readfirstlane(seg[e][0]) - p0;
-        at_seg.hi = __builtin_amdgcn_readfirstlane(seg[e][1]) - p0;
-        at_seg.weights = at_slice.weights + (int64_t)__builtin_amdgcn_readfirstlane(seg[e][2]) * a.rank * at_slice.width;
-    }
-    __device__ __forceinline__ void enter_rows() {
-        mlo = __builtin_amdgcn_readfirstlane(seg[me][0]) - p0;
-        mhi = __builtin_amdgcn_readfirstlane(seg[me][1]) - p0;
-    }
     __device__ __forceinline__ void start(int units) {
         munits = units;
         sl = sl0;
         e = me = kb = 0;
         mleft = per_seg();
-        enter_slice();
-        enter_seg();
-        enter_rows();
+        slice = slices[sl];
+        seg = segs[0];
+        mlo = seg.lo;
+        mhi = seg.hi;
     }
-    __device__ __forceinline__ void read(typename T::Half &r, const lds_byte *st, int s, int h) {
-        if (h == 0 || s < main_steps || blocks == 0)
-            T::read(r, st, h);
-        else
-            T::read_n(r, st, h);
+    __device__ __forceinline__ void read(typename T::Half &r, const lds_byte *st, int, int h) { T::read(r, st, h); }
+    __device__ __forceinline__ void read(typename T::Half &r, const lds_byte *st, int s, int h, const typename T::Half &first) {
+        T::read_n(r, st, h);
+        // a block's lo part meets the same ranks as its hi part
+        const int hm = s < main_steps || blocks == 0 ? h : 0;
+        if (&r != &first || hm == h) T::read_m(r, st, hm);
     }
     // an adapter's units touch its own tokens' sums alone: one whose weights
     // are not finite stays without effect on the others in the tile
@@ -218,13 +213,14 @@ struct LinearOp : PlainOp<T> {
     // registers of a second set of sums)
     __device__ __forceinline__ void mma(const typename T::Half &h, typename T::Acc &acc, int s, int half) {
         const bool all = s < main_steps;
-        mma_rows<T>(h, acc, all ? 0 : mlo, all ? T::BN : munits > 0 ? mhi : 0);
+        mma_rows<T>(h, acc, all ? 0 : scalar(mlo), all ? T::BN : munits > 0 ? scalar(mhi) : 0);
         if (!all && (half == 1 || blocks == 0)) {
             --munits;
             if (--mleft == 0) {
                 mleft = per_seg();
                 if (++me == nseg) me = 0;
-                enter_rows();
+                mlo = segs[me].lo;
+                mhi = segs[me].hi;
             }
         }
     }
@@ -234,48 +230,64 @@ struct LinearOp : PlainOp<T> {
     }
     // copies of a unit: N rows of its adapter's tokens (other rows keep what the
     // stage holds: their products are not added), then the ranks of its matrix.
-    // H: the half of the step that it fills, or -1 for both.
+    // H: the half of the step that it fills, or -1 for both.  Lane offsets are 32
+    // bits from scalar bases; only a tile across a slice's edge and a block with
+    // ranks past the last take the checked way.
     template <int H>
     __device__ __forceinline__ void unit(uint32_t at) {
-        const int row_len = packed_row(a.rank), r = a.rank;
+        const int r = a.rank, row_len = a.row_len;
         const bool live = sl < sl1;      // past the last unit: no rows, and ranks that are not used
-        const int lo = live ? at_seg.lo : 0, hi = live ? at_seg.hi : 0;
-        const uint16_t *rows = at_slice.rows + kb * 64;
+        const int lo = scalar(seg.lo), count = live ? scalar(seg.hi) - lo : 0;
+        const int width = scalar(slice.width), col = scalar(slice.col);
+        const uint64_t base = (uint32_t)scalar((int)slice.weights[0]) | (uint64_t)(uint32_t)scalar((int)slice.weights[1]) << 32;
+        const uint16_t *lw =
+            reinterpret_cast<const uint16_t *>(base) + (uint64_t)(uint32_t)(scalar(seg.id) * r) * (uint32_t)width;
+        const uint16_t *rows = a.packed + (uint64_t)(uint32_t)((live ? sl : sl0) * a.num_tokens + p0) * (uint32_t)row_len + kb * 64;
 #pragma unroll
         for (int j = 0; j < T::NSide::kInstr; ++j) {
             const int row = T::NSide::row(j), ko = T::NSide::elem(j);
-            if (row >= lo && row < hi && (H < 0 || ko / 32 == H))
-                dma16(rows + row * row_len + (H < 0 ? ko : ko & 31), at + T::MSide::kBytes + T::NSide::dst(j));
+            if ((unsigned)(row - lo) < (unsigned)count && (H < 0 || ko / 32 == H))
+                dma16(rows, 2u * (uint32_t)(__umul24(row, row_len) + (H < 0 ? ko : ko & 31)),
+                      at + T::MSide::kBytes + T::NSide::dst(j));
         }
-        const uint16_t *lw = at_seg.weights;
-        const int width = at_slice.width;
+        const bool full = H < 0 ? kb * 32 + 32 <= r : r == 16;
         if (BWD) {      // A_i: ranks are K rows, this side's index is the hidden column
             // half of the side's instructions hold the half's 32 K rows
             constexpr int kHalf = T::MSide::kInstr / 2, kRows = 64 / T::MSide::kLanesPerK;
+            const uint16_t *block = lw + (uint64_t)(uint32_t)(H < 0 ? kb * 32 : 0) * (uint32_t)width;
 #pragma unroll
             for (int j = 0; j < kHalf; ++j) {
                 const int i = wave_id() * kHalf + j + (H > 0 ? T::kWaves * kHalf : 0);
                 const int k = i * kRows + lane_id() / T::MSide::kLanesPerK;
-                const int rank = H < 0 ? kb * 32 + k : k & 15;
-                const int c = m0 + T::MSide::elem_of(k);
-                dma16(lw + (int64_t)(rank < r ? rank : r - 1) * width + (c < width ? c : width - 8), at + i * 1024u);
+                int rank = H < 0 ? k : k & 15;
+                if (!full) rank = min(rank, r - 1 - (H < 0 ? kb * 32 : 0));
+                const int c = min(m0 + T::MSide::elem_of(k), width - 8);
+                dma16(block, 2u * (uint32_t)(rank * width + c), at + i * 1024u);
             }
         } else {        // B_i: rows are the slice's columns, ranks contiguous
+            const bool inside = full && m0 >= col && m0 + T::BM <= col + width;
+            const uint16_t *block = lw + (int64_t)(m0 - col) * r + (H < 0 ? kb * 32 : 0);
 #pragma unroll
             for (int j = 0; j < T::MSide::kInstr; ++j) {
-                const int c = m0 + T::MSide::row(j) - at_slice.col, ko = T::MSide::elem(j);
-                const int rank = H < 0 ? kb * 32 + ko : ko & 15;
-                if (ko / 32 == (H > 0 ? 1 : 0))
-                    dma16(c >= 0 && c < width ? lw + (int64_t)c * r + (rank < r ? rank : r - 8) : zero_page, at + T::MSide::dst(j));
+                const int row = T::MSide::row(j), ko = T::MSide::elem(j);
+                const int rank = H < 0 ? ko : ko & 15;
+                if (ko / 32 == (H > 0 ? 1 : 0)) {
+                    if (inside) {
+                        dma16(block, 2u * (uint32_t)(__umul24(row, r) + rank), at + T::MSide::dst(j));
+                    } else {
+                        const int c = m0 + row - col, last = r - 8 - (H < 0 ? kb * 32 : 0);
+                        dma16(c >= 0 && c < width ? block + row * r + min(rank, last) : zero_page, at + T::MSide::dst(j));
+                    }
+                }
             }
         }
         if (live && ++kb == per_seg()) {
             kb = 0;
             if (++e == nseg) {
                 e = 0;
-                if (++sl < sl1) enter_slice();
+                if (++sl < sl1) slice = slices[sl];
             }
-            enter_seg();
+            seg = segs[e];
         }
     }
     __device__ __forceinline__ void issue(uint32_t at) {
@@ -293,7 +305,9 @@ struct LinearOp : PlainOp<T> {
 
 template <class T, bool BWD>
 __global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(LinearArgs a) {
-    __shared__ int s_tok[T::BN], s_id[T::BN], s_seg[T::BN][4], s_count;
+    __shared__ int s_tok[T::BN], s_id[T::BN], s_count;
+    __shared__ SegRow s_seg[T::BN];
+    __shared__ SliceEntry s_slice[LORA_MAX_SLICES];
     static_assert(T::BN <= T::kThreads, "a thread a token row");
     const int tid = threadIdx.x;
     TileAt at;
@@ -306,8 +320,8 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(LinearArgs a) {
     // (a batch without adapters has no sorted order: batch order)
     const bool none = *a.meta.no_lora != 0;
     auto token = [&](int r) {
-        const int p = p0 + min(r, rows - 1);
-        const int t = none ? p : a.meta.sorted[p];
+        const int p = p0 + min(r, rows - 1), at = a.meta.sorted[p];   // (read whatever the flag says: no second trip)
+        const int t = none ? p : at;
         return (unsigned)t < (unsigned)a.num_tokens ? t : 0;
     };
     const int own = token(min(tid, T::BN - 1));
@@ -317,7 +331,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(LinearArgs a) {
         st = a.meta.start_loc[tid];
         count = a.meta.counts[tid];
     }
-    LinearOp<T, BWD> op(a, s_seg);
+    LinearOp<T, BWD> op(a, s_seg, s_slice);
     op.m0 = m0;
     op.p0 = p0;
     op.blocks = a.rank <= 16 ? 0 : (a.rank + 31) / 32;
@@ -345,6 +359,12 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(LinearArgs a) {
     // while they land: the tile's tokens and ids, and the adapters it meets
     // (any order: each token takes part in one of them)
     __syncthreads();
+#pragma unroll
+    for (int i = 0; i < LORA_MAX_SLICES; ++i)
+        if (tid == i) {
+            const uint64_t w = reinterpret_cast<uint64_t>(a.lw[i]);
+            s_slice[i] = SliceEntry{{(uint32_t)w, (uint32_t)(w >> 32)}, BWD ? a.cols : a.width[i], BWD ? 0 : a.col[i]};
+        }
     if (tid < T::BN) {
         s_tok[tid] = own;
         s_id[tid] = none || (BWD || !a.has_bias) ? -1 : a.ids[own];
@@ -359,11 +379,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(LinearArgs a) {
             const int lo = max(st, p0), hi = min(st + count, p0 + rows);
             if (id >= 0 && id < a.max_loras && lo < hi) {
                 const int e = atomicAdd(&s_count, 1);
-                if (e < T::BN) {
-                    s_seg[e][0] = lo;
-                    s_seg[e][1] = hi;
-                    s_seg[e][2] = id;
-                }
+                if (e < T::BN) s_seg[e] = SegRow{lo - p0, hi - p0, id};
             }
         }
     __syncthreads();
@@ -374,13 +390,12 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(LinearArgs a) {
     if (!BWD) {   // the slices that meet the tile's columns
         op.sl0 = a.slices;
         op.sl1 = 0;
-        for (int i = 0; i < a.slices; ++i) {
-            const int c = select_slice(a.col, i);
-            if (c < m0 + T::BM && c + select_slice(a.width, i) > m0) {
+#pragma unroll
+        for (int i = 0; i < LORA_MAX_SLICES; ++i)
+            if (i < a.slices && a.col[i] < m0 + T::BM && a.col[i] + a.width[i] > m0) {
                 op.sl0 = min(op.sl0, i);
                 op.sl1 = i + 1;
             }
-        }
     }
     const int units = op.sl1 > op.sl0 ? nseg * (op.sl1 - op.sl0) * op.per_seg() : 0;
     const int steps = main + (op.blocks ? units : (units + 1) / 2);
@@ -750,6 +765,9 @@ struct GradOp {
         wp.next();
     }
     __device__ __forceinline__ void read(typename T::Half &r, const lds_byte *st, int, int h) { T::read(r, st, h); }
+    __device__ __forceinline__ void read(typename T::Half &r, const lds_byte *st, int, int h, const typename T::Half &) {
+        T::read(r, st, h);
+    }
     // dB: the column sums of dy as one more MFMA row of ones
     __device__ __forceinline__ void mma_n(const typename T::Half &h, typename T::Acc &acc, int nt) {
         T::mma_n(h, acc, nt);
@@ -847,8 +865,8 @@ struct LinearPlan {
 
 // The tile of y or dx (n x cols): the largest of 256 x 256, 128 x 128, 64
 // columns x 128 tokens and 64 x 64 of which there are enough for the GPU's 256
-// CUs (one of the first a CU at a time, two of the second and the last).  K is
-// not split: joining fp32 partial tiles across XCDs took 22 of the 70 us of a
+// CUs (one of the first and third a CU at a time, two of the others; 256 tokens
+// by 6144 columns: 192 of 64 x 128 60 us, 384 of 64 x 64 53 us).  K is not split: joining fp32 partial tiles across XCDs took 22 of the 70 us of a
 // product of 256 tokens by 6144 columns over 4096.
 LinearPlan plan_linear(long n, long cols) {
     auto tiles = [&](long bm, long bn) { return ceil_div(cols, bm) * ceil_div(n, bn); };
@@ -861,7 +879,7 @@ LinearPlan plan_linear(long n, long cols) {
     } else if (tiles(128, 128) >= 256) {
         p.tile = kMid;
         bm = bn = 128;
-    } else if (tiles(64, 128) >= 160) {
+    } else if (tiles(64, 128) >= 384) {
         p.tile = kFlat;
         bn = 128;
     }
@@ -993,6 +1011,7 @@ hipError_t launch_linear(LinearArgs &a, hipStream_t s) {
     a.mtiles = p.mtiles;
     a.ntiles = p.ntiles;
     a.group = 8;
+    a.row_len = packed_row(a.rank);
     const unsigned grid = tile_grid((long)p.mtiles * p.ntiles);
     auto launch = [&](auto tile) {
         using T = decltype(tile);

@@ -95,30 +95,47 @@ __global__ __launch_bounds__(T::kThreads) void logit_kernel(LogitArgs a) {
     mma_loop<T>(op, a.hidden / kStepK, (a.hidden + kStepK - 1) / kStepK, acc, g_lds);
 
     if constexpr (!GRAD) {
-#pragma unroll
-        for (int nt = 0; nt < T::NT; ++nt) {
-            const int r = T::n_of(nt);
-            const int target = r < rows ? a.targets[p0 + r] : -1;
-            Stat s{kNegInf, 0.f};
-#pragma unroll
-            for (int mt = 0; mt < T::MT; ++mt) {
-                const int v = m0 + T::m_of(mt);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (v + e >= a.rows) acc[mt][nt][e] = kNegInf;
-                    if (v + e == target && v + e < a.rows) a.target_logit[p0 + r] = acc[mt][nt][e];
-                    s.max = fmaxf(s.max, acc[mt][nt][e]);
-                }
-            }
-            const float base = s.max == kNegInf ? 0.f : s.max;
+        // vocabulary entries past the last (the last tile alone)
+        if (m0 + T::BM > a.rows)
 #pragma unroll
             for (int mt = 0; mt < T::MT; ++mt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s.sum += exp_of(acc[mt][nt][e] - base);
-            // the other three lanes of this token
+                for (int e = 0; e < 4; ++e)
+                    if (m0 + T::m_of(mt) + e >= a.rows)
 #pragma unroll
-            for (int d = 16; d < 64; d <<= 1) s = join(s, Stat{__shfl_xor(s.max, d), __shfl_xor(s.sum, d)});
-            if (lane_id() < 16) s_stat[T::wave_m()][r] = s;
+                        for (int nt = 0; nt < T::NT; ++nt) acc[mt][nt][e] = kNegInf;
+        int target[T::NT];
+#pragma unroll
+        for (int nt = 0; nt < T::NT; ++nt) {
+            const int r = T::n_of(nt);
+            target[nt] = (r < rows ? a.targets[p0 + r] : -1) - m0;
+        }
+#pragma unroll
+        for (int nt = 0; nt < T::NT; ++nt) {
+            const int r = T::n_of(nt);
+            // few tiles hold a token's target
+            if ((unsigned)target[nt] < (unsigned)min(T::BM, a.rows - m0))
+#pragma unroll
+                for (int mt = 0; mt < T::MT; ++mt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (T::m_of(mt) + e == target[nt]) a.target_logit[p0 + r] = acc[mt][nt][e];
+            float top = kNegInf;
+#pragma unroll
+            for (int mt = 0; mt < T::MT; ++mt)
+                top = fmaxf(fmaxf(top, fmaxf(acc[mt][nt][0], acc[mt][nt][1])), fmaxf(acc[mt][nt][2], acc[mt][nt][3]));
+            // the maximum of this token's four lanes first: one scale for all of their terms
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float base = top == kNegInf ? 0.f : top;
+            float sum = 0.f;
+#pragma unroll
+            for (int mt = 0; mt < T::MT; ++mt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum += exp_of(acc[mt][nt][e] - base);
+            sum += __shfl_xor(sum, 16);
+            sum += __shfl_xor(sum, 32);
+            if (lane_id() < 16) s_stat[T::wave_m()][r] = Stat{top, sum};
         }
         __syncthreads();
         for (int r = tid; r < rows; r += T::kThreads) {
@@ -167,17 +184,33 @@ struct JoinArgs {
     int32_t num_tokens, mtiles, vocab;
 };
 
-// 16 tokens a workgroup, 16 threads each.
-__global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
-    __shared__ Stat s_part[16][16];
-    const int tok = threadIdx.x % 16, part = threadIdx.x / 16, t = blockIdx.x * 16 + tok;
+// 16 tokens a workgroup, 64 threads each, eight pairs at a time.
+constexpr int kJoinParts = 64, kJoinTokens = 16, kJoinChunk = 8;
+__global__ __launch_bounds__(kJoinParts *kJoinTokens) void join_kernel(JoinArgs a) {
+    __shared__ Stat s_part[kJoinParts][kJoinTokens];
+    const int tok = threadIdx.x % kJoinTokens, part = threadIdx.x / kJoinTokens, t = blockIdx.x * kJoinTokens + tok;
     Stat s{kNegInf, 0.f};
     if (t < a.num_tokens)
-        for (int k = part; k < a.mtiles; k += 16) s = join(s, a.stats[(int64_t)k * a.num_tokens + t]);
+        for (int k = part; k < a.mtiles; k += kJoinParts * kJoinChunk) {
+            Stat v[kJoinChunk];
+#pragma unroll
+            for (int i = 0; i < kJoinChunk; ++i) {
+                const int q = k + i * kJoinParts;
+                v[i] = q < a.mtiles ? a.stats[(int64_t)q * a.num_tokens + t] : Stat{kNegInf, 0.f};
+            }
+#pragma unroll
+            for (int w = kJoinChunk / 2; w; w /= 2)
+#pragma unroll
+                for (int i = 0; i < w; ++i) v[i] = join(v[i], v[i + w]);
+            s = join(s, v[0]);
+        }
     s_part[part][tok] = s;
-    __syncthreads();
+#pragma unroll
+    for (int w = kJoinParts / 2; w; w /= 2) {
+        __syncthreads();
+        if (part < w) s_part[part][tok] = s = join(s, s_part[part + w][tok]);
+    }
     if (part == 0 && t < a.num_tokens) {
-        for (int k = 1; k < 16; ++k) s = join(s, s_part[k][tok]);
         const float lse = s.max + logf(s.sum);
         const int target = a.targets[t];
         a.lse[t] = lse;
@@ -514,7 +547,7 @@ int lora_cross_entropy(const void *x, int64_t ldx, int num_tokens, int hidden, c
     j.num_tokens = num_tokens;
     j.mtiles = a.mtiles;
     j.vocab = vocab;
-    hipLaunchKernelGGL(join_kernel, dim3((unsigned)ceil_div(num_tokens, 16)), dim3(256), 0, stream, j);
+    hipLaunchKernelGGL(join_kernel, dim3((unsigned)ceil_div(num_tokens, kJoinTokens)), dim3(kJoinParts * kJoinTokens), 0, stream, j);
     return hipGetLastError() == hipSuccess ? LORA_OK : LORA_ERR_LAUNCH;
 }
 
