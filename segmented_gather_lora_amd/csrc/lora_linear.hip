@@ -725,7 +725,7 @@ struct GradArgs {
     uint16_t *out[LORA_MAX_SLICES];           // dA_i [id][r][hidden] or dB_i [id][width][r]
     uint16_t *dbias[LORA_MAX_SLICES];
     int32_t width[LORA_MAX_SLICES], col[LORA_MAX_SLICES];   // of act (dA: hidden, 0)
-    int32_t tiles_before[LORA_MAX_SLICES + 1];
+    int32_t runs_before[LORA_MAX_SLICES + 1], run_tiles;
     int32_t num_tokens, rank, slices;
 };
 
@@ -783,71 +783,72 @@ struct GradOp {
 };
 
 template <class T, bool DA>
-__global__ __launch_bounds__(T::kThreads) void grad_kernel(GradArgs a) {
+__global__ __launch_bounds__(T::kThreads, 2) void grad_kernel(GradArgs a) {
     using Op = GradOp<T, DA>;
     using ASide = typename Op::ASide;
     using PSide = typename Op::PSide;
+    static_assert(T::kStages == 2, "mma_loop ends with every wave's reads done");
     constexpr int BA = DA ? T::BM : T::BN, BR = DA ? T::BN : T::BM;   // activation columns, ranks
-    const int per_id = a.tiles_before[a.slices];
-    const int m = blockIdx.x / per_id, tile = blockIdx.x % per_id;
+    const int per_id = a.runs_before[a.slices];
+    const int m = blockIdx.x / per_id, run = blockIdx.x % per_id;
     int i = 0;
-    while (i + 1 < a.slices && tile >= a.tiles_before[i + 1]) ++i;
-    const int c0 = (tile - select_slice(a.tiles_before, i)) * BA;
+    while (i + 1 < a.slices && run >= a.runs_before[i + 1]) ++i;
     const int width = select_slice(a.width, i), col = select_slice(a.col, i), r = a.rank;
+    const int begin = (run - select_slice(a.runs_before, i)) * a.run_tiles * BA, end = min(width, begin + a.run_tiles * BA);
     const SegEntry sg = a.segs[m];
-    Op op;
-    op.sums = false;
-    typename T::Acc acc;
-    clear<T>(acc);
-    uint16_t *dbias = nullptr;
-    if constexpr (!DA) {
-        dbias = select_slice(a.dbias, i);
-        op.sums = dbias != nullptr && T::wave_m() == 0;
+    const int steps = (sg.count + kStepK - 1) / kStepK;
+    uint16_t *out = select_slice(a.out, i), *dbias = DA ? nullptr : select_slice(a.dbias, i);
+    const int half = packed_half(r), row_len = packed_row(r);
+    // the tiles of a run one after the other: an adapter of few tokens is a step
+    // or two a tile, and a workgroup a tile would be all latency
+    for (int c0 = begin; c0 < end; c0 += BA) {
+        Op op;
+        typename T::Acc acc;
+        clear<T>(acc);
+        op.sums = !DA && dbias && T::wave_m() == 0;
 #pragma unroll
-        for (int nt = 0; nt < T::NT; ++nt) op.colsum[nt] = floatx4{0.f, 0.f, 0.f, 0.f};
-    }
-    if (sg.count > 0) {
-        const int half = packed_half(r), row_len = packed_row(r);
-        op.wa.base = a.act + col;
-        op.wa.sorted = a.sorted;
-        op.wa.ld = a.ldact;
-        op.wa.pos = sg.start;
-        op.wa.end = sg.start + sg.count;
-        op.wa.num_tokens = a.num_tokens;
+        for (int nt = 0; nt < (DA ? 1 : T::NT); ++nt) op.colsum[nt] = floatx4{0.f, 0.f, 0.f, 0.f};
+        if (sg.count > 0) {
+            op.wa.base = a.act + col;
+            op.wa.sorted = a.sorted;
+            op.wa.ld = a.ldact;
+            op.wa.pos = sg.start;
+            op.wa.end = sg.start + sg.count;
+            op.wa.num_tokens = a.num_tokens;
 #pragma unroll
-        for (int j = 0; j < ASide::kInstr; ++j) op.wa.col[j] = min(c0 + ASide::elem(j), width - 8);
-        op.wa.fetch();
+            for (int j = 0; j < ASide::kInstr; ++j) op.wa.col[j] = min(c0 + ASide::elem(j), width - 8);
+            op.wa.fetch();
 #pragma unroll
-        for (int j = 0; j < PSide::kInstr; ++j) {
-            const int c = PSide::elem(j);
-            const int from = c < BR ? packed_at(min(c, r - 8), half) : packed_at(min(c - BR, r - 8), half) + half;
-            op.wp.p[j] = a.packed + ((int64_t)i * a.num_tokens + sg.start + PSide::row(j)) * row_len + from;
+            for (int j = 0; j < PSide::kInstr; ++j) {
+                const int c = PSide::elem(j);
+                const int from = c < BR ? packed_at(min(c, r - 8), half) : packed_at(min(c - BR, r - 8), half) + half;
+                op.wp.p[j] = a.packed + ((int64_t)i * a.num_tokens + sg.start + PSide::row(j)) * row_len + from;
+            }
+            op.wp.step = (int64_t)kStepK * row_len;
+            op.wp.left = sg.count;
+            mma_begin<T>(op, steps, g_lds);
+            mma_loop<T>(op, sg.count / kStepK, steps, acc, g_lds);
         }
-        op.wp.step = (int64_t)kStepK * row_len;
-        op.wp.left = sg.count;
-        mma_begin<T>(op, (sg.count + kStepK - 1) / kStepK, g_lds);
-        mma_loop<T>(op, sg.count / kStepK, (sg.count + kStepK - 1) / kStepK, acc, g_lds);
-    }
-    uint16_t *out = select_slice(a.out, i);
-    if (out) {
+        if (out) {
 #pragma unroll
-        for (int nt = 0; nt < T::NT; ++nt)
+            for (int nt = 0; nt < T::NT; ++nt)
 #pragma unroll
-            for (int mt = 0; mt < T::MT; ++mt) {
-                const floatx4 v = acc[mt][nt];
-                const int j = DA ? T::n_of(nt) : T::m_of(mt), c = c0 + (DA ? T::m_of(mt) : T::n_of(nt));
-                if (j >= r || c >= width) continue;
-                uint16_t *at = out + (DA ? ((int64_t)m * r + j) * width + c : ((int64_t)m * width + c) * r + j);
-                *reinterpret_cast<u32x2g *>(at) = u32x2g{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-            }
-    }
-    if constexpr (!DA) {
-        if (op.sums && lane_id() < 16)
+                for (int mt = 0; mt < T::MT; ++mt) {
+                    const floatx4 v = acc[mt][nt];
+                    const int j = DA ? T::n_of(nt) : T::m_of(mt), c = c0 + (DA ? T::m_of(mt) : T::n_of(nt));
+                    if (j >= r || c >= width) continue;
+                    uint16_t *at = out + (DA ? ((int64_t)m * r + j) * width + c : ((int64_t)m * width + c) * r + j);
+                    *reinterpret_cast<u32x2g *>(at) = u32x2g{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+                }
+        }
+        if constexpr (!DA) {
+            if (op.sums && lane_id() < 16)
 #pragma unroll
-            for (int nt = 0; nt < T::NT; ++nt) {
-                const int c = c0 + T::n_of(nt);
-                if (c < width) dbias[(int64_t)m * width + c] = (uint16_t)float_to_bf16_bits(op.colsum[nt][0]);
-            }
+                for (int nt = 0; nt < T::NT; ++nt) {
+                    const int c = c0 + T::n_of(nt);
+                    if (c < width) dbias[(int64_t)m * width + c] = (uint16_t)float_to_bf16_bits(op.colsum[nt][0]);
+                }
+        }
     }
 }
 
@@ -1033,11 +1034,19 @@ hipError_t launch_u(const UArgs &a, const UPlan &p, hipStream_t s) {
 
 template <int BR, bool DA>
 hipError_t launch_grad(GradArgs &a, int max_loras, hipStream_t s) {
-    using T = typename std::conditional<DA, Tile<128, BR, (BR == 16 ? 4 : 2), (BR == 16 ? 1 : 2), true, true, 2>,
-                                        Tile<BR, 128, (BR == 16 ? 1 : 2), (BR == 16 ? 4 : 2), true, true, 1>>::type;
-    a.tiles_before[0] = 0;
-    for (int i = 0; i < a.slices; ++i) a.tiles_before[i + 1] = a.tiles_before[i] + (int)ceil_div(a.width[i], 128);
-    const long grid = (long)max_loras * a.tiles_before[a.slices];
+    // 128 columns of the activations; 64 where more would leave room for one workgroup a CU
+    constexpr int BA = BR == 128 ? 64 : 128;
+    using T = typename std::conditional<DA, Tile<BA, BR, (BR == 16 ? 4 : 2), (BR == 16 ? 1 : 2), true, true, 2>,
+                                        Tile<BR, BA, (BR == 16 ? 1 : 2), (BR == 16 ? 4 : 2), true, true, 1>>::type;
+    long tiles = 0;
+    for (int i = 0; i < a.slices; ++i) tiles += ceil_div(a.width[i], BA);
+    // runs of up to 16 tiles while eight workgroups a CU remain
+    const long run = tiles * max_loras / 2048;
+    a.run_tiles = (int)(run < 1 ? 1 : run > 16 ? 16 : run);
+    a.runs_before[0] = 0;
+    for (int i = 0; i < a.slices; ++i)
+        a.runs_before[i + 1] = a.runs_before[i] + (int)ceil_div(a.width[i], (long)BA * a.run_tiles);
+    const long grid = (long)max_loras * a.runs_before[a.slices];
     return launch_tiles<grad_kernel<T, DA>>((unsigned)grid, T::kThreads, T::kLds, s, a);
 }
 template <bool DA>
