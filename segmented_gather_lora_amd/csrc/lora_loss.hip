@@ -46,7 +46,7 @@ __device__ __forceinline__ Stat join(const Stat &a, const Stat &b) {
 }
 
 struct LogitArgs {
-    const uint16_t *x;
+    const uint16_t *x;          // gradient: the listed tokens' rows
     int64_t ldx;
     const uint16_t *w;          // the piece's first row
     int64_t ldw;
@@ -66,8 +66,7 @@ struct LogitArgs {
 
 template <class T, bool GRAD>
 __global__ __launch_bounds__(T::kThreads) void logit_kernel(LogitArgs a) {
-    __shared__ int s_tok[T::BN];
-    __shared__ Stat s_stat[GRAD ? 1 : T::WM][T::BN];
+    __shared__ Stat s_stat[GRAD ? 1 : T::WM][GRAD ? 1 : T::BN];
     const int tid = threadIdx.x;
     const int n = GRAD ? *a.count : a.num_tokens;
     const int ntiles = GRAD ? (n + T::BN - 1) / T::BN : a.ntiles;
@@ -75,15 +74,10 @@ __global__ __launch_bounds__(T::kThreads) void logit_kernel(LogitArgs a) {
     TileAt at;
     if (!tile_at(blockIdx.x, a.mtiles, ntiles, a.group, at)) return;
     const int m0 = at.m * T::BM, p0 = at.n * T::BN, rows = min(T::BN, n - p0);
-    for (int r = tid; r < T::BN; r += T::kThreads) {
-        const int p = p0 + min(r, rows - 1);
-        s_tok[r] = GRAD ? a.list[p] : p;
-    }
-    __syncthreads();
     PlainOp<T> op;
 #pragma unroll
     for (int j = 0; j < T::NSide::kInstr; ++j)
-        op.wn.p[j] = a.x + (int64_t)s_tok[T::NSide::row(j)] * a.ldx + T::NSide::elem(j);
+        op.wn.p[j] = a.x + (int64_t)(p0 + min(T::NSide::row(j), rows - 1)) * a.ldx + T::NSide::elem(j);
 #pragma unroll
     for (int j = 0; j < T::MSide::kInstr; ++j)
         op.wm.p[j] = a.w + (int64_t)min(m0 + T::MSide::row(j), a.rows - 1) * a.ldw + T::MSide::elem(j);
@@ -145,12 +139,22 @@ __global__ __launch_bounds__(T::kThreads) void logit_kernel(LogitArgs a) {
             a.stats[(int64_t)at.m * a.num_tokens + p0 + r] = s;
         }
     } else {
+        // all the tokens' values in two round trips
+        int target[T::NT];
+        float lse[T::NT], dl[T::NT];
+#pragma unroll
+        for (int nt = 0; nt < T::NT; ++nt) target[nt] = a.list[p0 + min(T::n_of(nt), rows - 1)];
+#pragma unroll
+        for (int nt = 0; nt < T::NT; ++nt) {
+            const int t = target[nt];
+            lse[nt] = a.lse[t];
+            dl[nt] = a.dloss[t];
+            target[nt] = a.targets[t] - a.first;
+        }
 #pragma unroll
         for (int nt = 0; nt < T::NT; ++nt) {
             const int r = T::n_of(nt);
             if (r >= rows) continue;
-            const int t = s_tok[r], target = a.targets[t] - a.first;
-            const float lse = a.lse[t], dl = a.dloss[t];
             uint16_t *row = a.g + (int64_t)(p0 + r) * a.ldg;
             constexpr int kStep = T::QUADS ? 2 : 1;
 #pragma unroll
@@ -160,8 +164,8 @@ __global__ __launch_bounds__(T::kThreads) void logit_kernel(LogitArgs a) {
                 float g[4 * kStep];
 #pragma unroll
                 for (int x = 0; x < 4 * kStep; ++x) {
-                    const float p = exp_of(acc[mt + x / 4][nt][x % 4] - lse);
-                    g[x] = v + x < a.rows ? (p - (v + x == target ? 1.f : 0.f)) * dl : 0.f;
+                    const float p = exp_of(acc[mt + x / 4][nt][x % 4] - lse[nt]);
+                    g[x] = v + x < a.rows ? (p - (v + x == target[nt] ? 1.f : 0.f)) * dl[nt] : 0.f;
                 }
                 if constexpr (kStep == 2)
                     *reinterpret_cast<u32x4 *>(row + v) =
@@ -254,6 +258,24 @@ __global__ __launch_bounds__(kListThreads) void list_kernel(ListArgs a) {
     if (threadIdx.x == 0) *a.count = base;
 }
 
+// The listed tokens' rows of x one after the other: read through the list
+// instead, as K rows of dw, they cost dw 15 % (4096 tokens by 4096 by 32000).
+struct RowsOfArgs {
+    const uint16_t *x;
+    int64_t ldx;
+    const int32_t *list, *count;
+    uint16_t *out;
+    int32_t hidden;
+};
+__global__ __launch_bounds__(256) void rows_of_kernel(RowsOfArgs a) {
+    const int per = a.hidden / 8;
+    const int64_t work = (int64_t)*a.count * per;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < work; i += (int64_t)gridDim.x * 256) {
+        const int p = (int)(i / per), c = (int)(i % per) * 8;
+        *reinterpret_cast<u32x4 *>(a.out + i * 8) = *reinterpret_cast<const u32x4 *>(a.x + (int64_t)a.list[p] * a.ldx + c);
+    }
+}
+
 // ---------------------------------------------------------------- dx and dw of a piece
 
 struct DxArgs {
@@ -331,17 +353,17 @@ __global__ __launch_bounds__(256) void finish_kernel(FinishArgs a) {
 }
 
 struct DwArgs {
-    const uint16_t *x;
+    const uint16_t *x;          // the listed tokens' rows
     int64_t ldx;
     const uint16_t *g;
     int64_t ldg;
     uint16_t *dw;               // the piece's first row
     int64_t lddw;
-    const int32_t *list, *count;
-    int32_t num_tokens, hidden, rows;
+    const int32_t *count;
+    int32_t hidden, rows;
     int32_t mtiles, ntiles, group;
 };
-// dw[v] = sum over the listed tokens of g[p][v] x[list[p]]: both sides have K
+// dw[v] = sum over the listed tokens of g[p][v] x[p]: both sides have K
 // (the tokens) as their row index.
 template <class T>
 __global__ __launch_bounds__(T::kThreads) void dw_kernel(DwArgs a) {
@@ -351,16 +373,12 @@ __global__ __launch_bounds__(T::kThreads) void dw_kernel(DwArgs a) {
     typename T::Acc acc;
     clear<T>(acc);
     if (n > 0) {
-        PairOp<T, GatherWalk<typename T::MSide>, Walk<typename T::NSide>> op;
-        op.wm.base = a.x;
-        op.wm.sorted = a.list;
-        op.wm.ld = a.ldx;
-        op.wm.pos = 0;
-        op.wm.end = n;
-        op.wm.num_tokens = a.num_tokens;
+        PlainOp<T> op;
 #pragma unroll
-        for (int j = 0; j < T::MSide::kInstr; ++j) op.wm.col[j] = min(m0 + T::MSide::elem(j), a.hidden - 8);
-        op.wm.fetch();
+        for (int j = 0; j < T::MSide::kInstr; ++j)
+            op.wm.p[j] = a.x + (int64_t)T::MSide::row(j) * a.ldx + min(m0 + T::MSide::elem(j), a.hidden - 8);
+        op.wm.step = (int64_t)kStepK * a.ldx;
+        op.wm.left = n;
 #pragma unroll
         for (int j = 0; j < T::NSide::kInstr; ++j)
             op.wn.p[j] = a.g + (int64_t)T::NSide::row(j) * a.ldg + min(v0 + T::NSide::elem(j), (int)a.ldg - 8);
@@ -439,7 +457,7 @@ LossPlan plan_loss(long n, long hidden, long vocab) {
 }
 
 struct LossLayout {
-    size_t status, target_logit, stats, list, place, count, g, planes, total;
+    size_t status, target_logit, stats, list, place, count, x, g, planes, total;
 };
 LossLayout loss_layout(const LossPlan &p, long n, long hidden, bool train) {
     LossLayout l;
@@ -459,6 +477,7 @@ LossLayout loss_layout(const LossPlan &p, long n, long hidden, bool train) {
     l.list = take(train ? sizeof(int32_t) * (size_t)n : 0);
     l.place = take(train ? sizeof(int32_t) * (size_t)n : 0);
     l.count = take(train ? sizeof(int32_t) : 0);
+    l.x = take(train ? sizeof(uint16_t) * (size_t)n * (size_t)hidden : 0);
     l.g = take(train ? sizeof(uint16_t) * (size_t)n * (size_t)p.piece : 0);
     l.planes = take(train ? sizeof(float) * (size_t)p.splits * (size_t)n * (size_t)hidden : 0);
     l.total = at > forward ? at : forward;
@@ -573,6 +592,19 @@ int lora_cross_entropy_backward(const void *x, int64_t ldx, int num_tokens, int 
     la.vocab = vocab;
     hipLaunchKernelGGL(list_kernel, dim3(1), dim3(kListThreads), 0, stream, la);
     if (hipGetLastError() != hipSuccess) return LORA_ERR_LAUNCH;
+    RowsOfArgs ra;
+    ra.x = static_cast<const uint16_t *>(x);
+    ra.ldx = ldx;
+    ra.list = la.list;
+    ra.count = la.count;
+    ra.out = reinterpret_cast<uint16_t *>(ws + l.x);
+    ra.hidden = hidden;
+    if (num_tokens > 0) {
+        long grid = ceil_div((long)num_tokens * (hidden / 8), 256);
+        if (grid > 2048) grid = 2048;
+        hipLaunchKernelGGL(rows_of_kernel, dim3((unsigned)grid), dim3(256), 0, stream, ra);
+        if (hipGetLastError() != hipSuccess) return LORA_ERR_LAUNCH;
+    }
     uint16_t *g = reinterpret_cast<uint16_t *>(ws + l.g);
     float *planes = reinterpret_cast<float *>(ws + l.planes);
     for (long first = 0; first < vocab; first += p.piece) {
@@ -582,8 +614,8 @@ int lora_cross_entropy_backward(const void *x, int64_t ldx, int num_tokens, int 
         if (num_tokens > 0) {
             LogitArgs a;
             memset(&a, 0, sizeof a);
-            a.x = static_cast<const uint16_t *>(x);
-            a.ldx = ldx;
+            a.x = ra.out;
+            a.ldx = hidden;
             a.w = wp;
             a.ldw = ldw;
             a.targets = targets;
@@ -635,15 +667,13 @@ int lora_cross_entropy_backward(const void *x, int64_t ldx, int num_tokens, int 
         if (dw) {
             DwArgs d;
             memset(&d, 0, sizeof d);
-            d.x = static_cast<const uint16_t *>(x);
-            d.ldx = ldx;
+            d.x = ra.out;
+            d.ldx = hidden;
             d.g = g;
             d.ldg = ldg;
             d.dw = static_cast<uint16_t *>(dw) + first * lddw;
             d.lddw = lddw;
-            d.list = la.list;
             d.count = la.count;
-            d.num_tokens = num_tokens;
             d.hidden = hidden;
             d.rows = rows;
             d.mtiles = (int)ceil_div(hidden, tile_m(p.dw));
