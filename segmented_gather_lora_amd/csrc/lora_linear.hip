@@ -499,7 +499,7 @@ struct RowsArgs {
     float scale;
 };
 constexpr int kRowsTokens = 32, kRowsWaves = 16, kRowsCols = 32, kRowsThreads = kRowsWaves * kWave;
-constexpr int kRowsRanks = 16, kRowsShrinkWaves = 8;
+constexpr int kRowsRanks = 16, kRowsShrinkWaves = 16;
 
 __device__ __forceinline__ void fma_bf16x8(const u32x4 &a, const u32x4 &b, float &sum) {
 #pragma unroll

@@ -408,15 +408,18 @@ size_t up(size_t v) { return (v + kRound - 1) / kRound * kRound; }
 long ceil_div(long a, long b) { return (a + b - 1) / b; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-enum LossTile { kBig, kMid, kSmall };
+enum LossTile { kBig, kMid, kSmall, kRow };
 // The tile of a product of m by n outputs: 256 x 256 where that fills the CUs
-// (one workgroup each), else 128 x 128, 128 x 32 for few tokens.
+// (one workgroup each), else 128 x 128 where there are two a CU, else 64 x 64,
+// whose workgroups are short enough for the smallest sizes (a step
+// of 301 tokens by 5003 entries over 264: 59 us with 128 x 128, 47 us); 128 x 32 for few tokens.
 LossTile pick_tile(long m, long n, long splits = 1) {
     if (n > 128 && ceil_div(m, 256) * ceil_div(n, 256) * splits >= 192) return kBig;
-    return n > 32 ? kMid : kSmall;
+    if (n <= 32) return kRow;
+    return ceil_div(m, 128) * ceil_div(n, 128) * splits >= 384 ? kMid : kSmall;
 }
-int tile_m(LossTile t) { return t == kBig ? 256 : 128; }
-int tile_n(LossTile t) { return t == kBig ? 256 : t == kMid ? 128 : 32; }
+int tile_m(LossTile t) { return t == kBig ? 256 : t == kSmall ? 64 : 128; }
+int tile_n(LossTile t) { return t == kBig ? 256 : t == kMid ? 128 : t == kSmall ? 64 : 32; }
 
 struct LossPlan {
     LossTile logits, grad, dx, dw;
@@ -448,7 +451,10 @@ LossPlan plan_loss(long n, long hidden, long vocab) {
         if (s > 16) s = 16;
         return s < 1 ? 1 : s;
     };
-    p.dx = n > 128 && ceil_div(hidden, 256) * ceil_div(n, 256) * splits_of(kBig) >= 192 ? kBig : n > 32 ? kMid : kSmall;
+    p.dx = kRow;
+    if (n > 32) p.dx = kSmall;
+    if (n > 128 && ceil_div(hidden, 256) * ceil_div(n, 256) * splits_of(kBig) >= 192) p.dx = kBig;
+    else if (n > 32 && ceil_div(hidden, 128) * ceil_div(n, 128) * splits_of(kMid) >= 384) p.dx = kMid;
     const long s = splits_of(p.dx);
     p.split_steps = (int)ceil_div(steps, s);
     p.splits = (int)ceil_div(steps, p.split_steps);
@@ -508,6 +514,7 @@ hipError_t with_tile(LossTile t, F f) {
     switch (t) {
         case kBig: return f(Tile<256, 256, 4, 2, MS, NS>{});
         case kMid: return f(Tile<128, 128, 2, 2, MS, NS>{});
+        case kSmall: return f(Tile<64, 64, 1, 4, MS, NS, 0, 4>{});
         default: return f(Tile<128, 32, 2, 2, MS, NS, 0, 4>{});
     }
 }
