@@ -468,6 +468,38 @@ def _workspace(t, device, where: str) -> None:
     _need(t.dim() == 1 and t.is_contiguous(), LORA_ERR_BUFFER, where, "workspace must be a contiguous 1-d tensor")
 
 
+# The calls on the products accept what is plainly right in one look and go
+# through the checks that name the fault only otherwise: for a few tokens the
+# checks, spelled out, take longer than the kernels.
+
+def _whole(t, dtype, device: int, shape) -> bool:
+    return t.dtype is dtype and t.get_device() == device and t.shape == shape and t.is_contiguous()
+
+
+def _matrix(t, dtype, device: int, shape) -> bool:
+    """Rows of unit stride, any distance apart."""
+    return t.dtype is dtype and t.get_device() == device and t.shape == shape and t.stride(1) == 1
+
+
+def _linear_plain(meta, x, w, wide, lora_a, lora_b, bufs, widths, r: int, workspace, offset_start: int) -> bool:
+    import torch
+    n, h = x.shape
+    out, device, loras, bf16 = w.shape[0], meta.region.get_device(), lora_a[0].shape[0], torch.bfloat16
+    if not (device >= 0 and n == meta.num_tokens and loras >= meta.max_loras and len(lora_a) == len(lora_b)
+            and 0 <= offset_start and offset_start + sum(widths) <= out
+            and _matrix(x, bf16, device, (n, h)) and _matrix(w, bf16, device, (out, h))
+            and _matrix(wide, bf16, device, (n, out)) and workspace.dtype is torch.uint8
+            and workspace.get_device() == device and workspace.dim() == 1 and workspace.is_contiguous()):
+        return False
+    for t in bufs:
+        if not _whole(t, torch.float32, device, (len(lora_a), n, r)):
+            return False
+    for a, b, width in zip(lora_a, lora_b, widths):
+        if not (_whole(a, bf16, device, (loras, r, h)) and _whole(b, bf16, device, (loras, width, r))):
+            return False
+    return True
+
+
 def _projection(where: str, meta, h: int, w, wide, name: str, offset_start: int, widths) -> None:
     """The shared projection's matrix [out][hidden] and the activations of its
     output side (y or dy) of at least its columns."""
@@ -493,14 +525,16 @@ def lora_linear(x, w, w_bias, lora_a: Sequence, lora_b: Sequence, bias: Optional
     where = "lora_linear"
     n, h = x.shape
     s, r = len(lora_a), lora_a[0].shape[1]
-    _layer_checks(where, meta, n, x=x, lora_a=lora_a, lora_b=lora_b, bias=bias, buf=buf, offset_start=offset_start)
-    _need(len(lora_b) == s and buf.shape[0] == s, LORA_ERR_SLICES, where, "one weight per buf slice")
-    widths = [int(t.shape[1]) for t in lora_b]
-    _projection(where, meta, h, w, y, "y", offset_start, widths)
+    widths = [t.shape[1] for t in lora_b]
+    if not _linear_plain(meta, x, w, y, lora_a, lora_b, (buf,), widths, r, workspace, offset_start):
+        _layer_checks(where, meta, n, x=x, lora_a=lora_a, lora_b=lora_b, buf=buf, offset_start=offset_start)
+        _need(len(lora_b) == s and buf.shape[0] == s, LORA_ERR_SLICES, where, "one weight per buf slice")
+        _projection(where, meta, h, w, y, "y", offset_start, widths)
+        _workspace(workspace, meta.region.device, where)
+    _bias(bias, widths, meta, where)
     if w_bias is not None:
         _dev(w_bias, torch.bfloat16, meta, where, "w_bias")
         _need(w_bias.dim() == 1 and w_bias.shape[0] == w.shape[0], LORA_ERR_SHAPE, where, "w_bias must be [%d]" % w.shape[0])
-    _workspace(workspace, meta.region.device, where)
     _check(_lib().lora_linear(x.data_ptr(), x.stride(0), n, h, w.data_ptr(), w.stride(0), w.shape[0],
                               None if w_bias is None else w_bias.data_ptr(), _ptr_array(lora_a), _ptr_array(lora_b),
                               None if bias is None else _ptr_array(bias), _widths_array(widths), s, r, buf.data_ptr(),
@@ -511,7 +545,10 @@ def lora_linear(x, w, w_bias, lora_a: Sequence, lora_b: Sequence, bias: Optional
 def _grads(ts, like, meta, where: str, name: str) -> None:
     import torch
     _need(len(ts) == len(like), LORA_ERR_SLICES, where, "one %s per slice" % name)
+    device = meta.region.get_device()
     for i, (t, shape) in enumerate(zip(ts, like)):
+        if device >= 0 and _whole(t, torch.bfloat16, device, shape):
+            continue
         _dev(t, torch.bfloat16, meta, where, "%s[%d]" % (name, i))
         _need(tuple(t.shape) == tuple(shape) and t.is_contiguous(), LORA_ERR_SHAPE, where,
               "%s[%d] must be contiguous %s" % (name, i, tuple(shape)))
@@ -529,12 +566,14 @@ def lora_linear_backward(dy, x, w, lora_a: Sequence, lora_b: Sequence, buf, dbuf
     where = "lora_linear_backward"
     n, h = x.shape
     s, r = len(lora_a), lora_a[0].shape[1]
-    _layer_checks(where, meta, n, x=x, lora_a=lora_a, lora_b=lora_b, buf=buf)
-    _need(len(lora_b) == s and buf.shape[0] == s, LORA_ERR_SLICES, where, "one weight per buf slice")
-    widths = [int(t.shape[1]) for t in lora_b]
-    _projection(where, meta, h, w, dy, "dy", offset_start, widths)
-    _dev(dbuf, torch.float32, meta, where, "dbuf")
-    _need(dbuf.shape == buf.shape and dbuf.is_contiguous(), LORA_ERR_SHAPE, where, "dbuf must be contiguous like buf")
+    widths = [t.shape[1] for t in lora_b]
+    if not _linear_plain(meta, x, w, dy, lora_a, lora_b, (buf, dbuf), widths, r, workspace, offset_start):
+        _layer_checks(where, meta, n, x=x, lora_a=lora_a, lora_b=lora_b, buf=buf)
+        _need(len(lora_b) == s and buf.shape[0] == s, LORA_ERR_SLICES, where, "one weight per buf slice")
+        _projection(where, meta, h, w, dy, "dy", offset_start, widths)
+        _dev(dbuf, torch.float32, meta, where, "dbuf")
+        _need(dbuf.shape == buf.shape and dbuf.is_contiguous(), LORA_ERR_SHAPE, where, "dbuf must be contiguous like buf")
+        _workspace(workspace, meta.region.device, where)
     if dx is not None:
         _dev(dx, torch.bfloat16, meta, where, "dx")
         _need(tuple(dx.shape) == (n, h), LORA_ERR_SHAPE, where, "dx must be [%d][%d]" % (n, h))
@@ -545,7 +584,6 @@ def lora_linear_backward(dy, x, w, lora_a: Sequence, lora_b: Sequence, buf, dbuf
         for i, t in enumerate(dbias):
             if t is not None:
                 _grads([t], [lora_b[i].shape[:2]], meta, where, "dbias")
-    _workspace(workspace, meta.region.device, where)
     _check(_lib().lora_linear_backward(dy.data_ptr(), dy.stride(0), x.data_ptr(), x.stride(0), n, h, w.data_ptr(),
                                        w.stride(0), w.shape[0], _ptr_array(lora_a), _ptr_array(lora_b),
                                        _widths_array(widths), s, r, buf.data_ptr(), dbuf.data_ptr(),
@@ -566,6 +604,8 @@ def lora_cross_entropy_workspace_bytes(num_tokens: int, hidden: int, vocab: int,
 
 def _on(t, dtype, device, shape, where: str, name: str, contiguous: bool = True) -> None:
     """A tensor of this type and shape on `device`; rows of unit stride, or contiguous."""
+    if t.is_cuda and t.device == device and (_whole if contiguous else _matrix)(t, dtype, t.get_device(), shape):
+        return
     if not (t.is_cuda and t.device == device):
         raise TypeError("%s: %s must be on one GPU with w (got %s)" % (where, name, t.device))
     if t.dtype != dtype:
