@@ -782,6 +782,100 @@ struct GradOp {
     }
 };
 
+// The tile's results (and dbias) to memory.
+template <class T, bool DA>
+__device__ __forceinline__ void grad_store(const typename T::Acc &acc, const floatx4 *colsum, uint16_t *out, uint16_t *dbias,
+                                           int m, int c0, int width, int r) {
+#pragma unroll
+    for (int nt = 0; nt < T::NT; ++nt)
+#pragma unroll
+        for (int mt = 0; mt < T::MT; ++mt) {
+            const floatx4 v = acc[mt][nt];
+            const int j = DA ? T::n_of(nt) : T::m_of(mt), c = c0 + (DA ? T::m_of(mt) : T::n_of(nt));
+            if (j >= r || c >= width) continue;
+            uint16_t *at = out + (DA ? ((int64_t)m * r + j) * width + c : ((int64_t)m * width + c) * r + j);
+            *reinterpret_cast<u32x2g *>(at) = u32x2g{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+        }
+    if constexpr (!DA) {
+        if (dbias && T::wave_m() == 0 && lane_id() < 16)
+#pragma unroll
+            for (int nt = 0; nt < T::NT; ++nt) {
+                const int c = c0 + T::n_of(nt);
+                if (c < width) dbias[(int64_t)m * width + c] = (uint16_t)float_to_bf16_bits(colsum[nt][0]);
+            }
+    }
+}
+
+// An adapter of at most 128 tokens: its packed rows (two K steps at most) stay
+// in LDS for the whole run, and only the activations' columns change from tile
+// to tile; they are asked for as soon as the tile before is read.
+template <class T, bool DA>
+__device__ __forceinline__ void short_run(const GradArgs &a, const SegEntry &sg, int m, int i, int begin, int end, int width,
+                                          int col, uint16_t *out, uint16_t *dbias) {
+    using Op = GradOp<T, DA>;
+    using ASide = typename Op::ASide;
+    using PSide = typename Op::PSide;
+    constexpr int BA = DA ? T::BM : T::BN, BR = DA ? T::BN : T::BM;
+    const int r = a.rank, half = packed_half(r), row_len = packed_row(r), steps = (sg.count + kStepK - 1) / kStepK;
+    const lds_byte *lds = (const lds_byte *)g_lds;
+    const uint32_t base = lds_address(g_lds);
+    // LDS: the packed rows of both steps, then the activations of both (of one step: of two tiles)
+    constexpr uint32_t kActs = 2 * PSide::kBytes;
+    const uint16_t *row[2][ASide::kInstr];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int j = 0; j < ASide::kInstr; ++j) {
+            const int k = b * kStepK + ASide::row(j);
+            const int t = a.sorted[sg.start + min(k, sg.count - 1)];
+            row[b][j] = k < sg.count && (unsigned)t < (unsigned)a.num_tokens ? a.act + (int64_t)t * a.ldact + col : nullptr;
+        }
+    auto copy = [&](int c0, int b, uint32_t to) {
+#pragma unroll
+        for (int j = 0; j < ASide::kInstr; ++j) {
+            const uint16_t *p = b ? row[1][j] : row[0][j];
+            dma16(p ? p + min(c0 + ASide::elem(j), width - 8) : zero_page, to + ASide::dst(j));
+        }
+    };
+    for (int b = 0; b < steps; ++b)
+#pragma unroll
+        for (int j = 0; j < PSide::kInstr; ++j) {
+            const int c = PSide::elem(j), k = b * kStepK + PSide::row(j);
+            const int from = c < BR ? packed_at(min(c, r - 8), half) : packed_at(min(c - BR, r - 8), half) + half;
+            dma16(k < sg.count ? a.packed + ((int64_t)i * a.num_tokens + sg.start + k) * row_len + from : zero_page,
+                  base + b * PSide::kBytes + PSide::dst(j));
+        }
+    const int ahead = steps == 1 ? 2 : 1;    // tiles in LDS
+    for (int t = 0; t < ahead; ++t)
+        for (int b = 0; b < steps; ++b)
+            if (begin + t * BA < end) copy(begin + t * BA, b, base + kActs + (t + b) * ASide::kBytes);
+    int slot = 0;
+    for (int c0 = begin; c0 < end; c0 += BA) {
+        typename T::Acc acc;
+        clear<T>(acc);
+        Op op;
+        op.sums = !DA && dbias && T::wave_m() == 0;
+#pragma unroll
+        for (int nt = 0; nt < (DA ? 1 : T::NT); ++nt) op.colsum[nt] = floatx4{0.f, 0.f, 0.f, 0.f};
+        wait_loads_barrier<0>();
+        for (int b = 0; b < steps; ++b) {
+            const lds_byte *packed = lds + b * PSide::kBytes, *acts = lds + kActs + (slot + b) * ASide::kBytes;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                typename T::Half x;
+                T::read_m(x, DA ? acts : packed, h);
+                T::read_n(x, (DA ? packed : acts) - T::MSide::kBytes, h);
+                op.mma(x, acc, b, h);
+            }
+        }
+        own_reads_barrier();
+        if (c0 + ahead * BA < end)
+            for (int b = 0; b < steps; ++b) copy(c0 + ahead * BA, b, base + kActs + (slot + b) * ASide::kBytes);
+        slot ^= steps == 1;
+        grad_store<T, DA>(acc, op.colsum, out, dbias, m, c0, width, r);
+    }
+}
+
 template <class T, bool DA>
 __global__ __launch_bounds__(T::kThreads, 2) void grad_kernel(GradArgs a) {
     using Op = GradOp<T, DA>;
@@ -798,9 +892,11 @@ __global__ __launch_bounds__(T::kThreads, 2) void grad_kernel(GradArgs a) {
     const SegEntry sg = a.segs[m];
     const int steps = (sg.count + kStepK - 1) / kStepK;
     uint16_t *out = select_slice(a.out, i), *dbias = DA ? nullptr : select_slice(a.dbias, i);
+    if (sg.count > 0 && steps <= 2) {
+        short_run<T, DA>(a, sg, m, i, begin, end, width, col, out, dbias);
+        return;
+    }
     const int half = packed_half(r), row_len = packed_row(r);
-    // the tiles of a run one after the other: an adapter of few tokens is a step
-    // or two a tile, and a workgroup a tile would be all latency
     for (int c0 = begin; c0 < end; c0 += BA) {
         Op op;
         typename T::Acc acc;
@@ -829,26 +925,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void grad_kernel(GradArgs a) {
             mma_begin<T>(op, steps, g_lds);
             mma_loop<T>(op, sg.count / kStepK, steps, acc, g_lds);
         }
-        if (out) {
-#pragma unroll
-            for (int nt = 0; nt < T::NT; ++nt)
-#pragma unroll
-                for (int mt = 0; mt < T::MT; ++mt) {
-                    const floatx4 v = acc[mt][nt];
-                    const int j = DA ? T::n_of(nt) : T::m_of(mt), c = c0 + (DA ? T::m_of(mt) : T::n_of(nt));
-                    if (j >= r || c >= width) continue;
-                    uint16_t *at = out + (DA ? ((int64_t)m * r + j) * width + c : ((int64_t)m * width + c) * r + j);
-                    *reinterpret_cast<u32x2g *>(at) = u32x2g{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-                }
-        }
-        if constexpr (!DA) {
-            if (op.sums && lane_id() < 16)
-#pragma unroll
-                for (int nt = 0; nt < T::NT; ++nt) {
-                    const int c = c0 + T::n_of(nt);
-                    if (c < width) dbias[(int64_t)m * width + c] = (uint16_t)float_to_bf16_bits(op.colsum[nt][0]);
-                }
-        }
+        grad_store<T, DA>(acc, op.colsum, out, dbias, m, c0, width, r);
     }
 }
 
