@@ -483,6 +483,12 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(LinearArgs a) {
 // Up to 32 tokens: a call is one pass over W and the adapters, bound by their
 // bytes and by latency, so it is two launches without a sort or a split over
 // workgroups.  s: 16 ranks of one token and slice a workgroup, 4 lanes a rank.
+// Batches of up to kRowsShrinks such workgroups that read up to kRowsBytes of
+// adapters (once a token) take s from the same kernel, packed too: the shrink
+// kernels, which read an adapter once for all of its tokens, need three launches
+// (zeroing, shrink, pack) for that.  517 tokens, 2 slices of rank 8 over 520 (9
+// MB): 8 us against 13; 256 tokens, 3 slices of rank 16 over 4096 (100 MB): 19
+// against 17.
 struct RowsArgs {
     const int32_t *ids, *no_lora;   // a batch without adapters has no ids
     const uint16_t *x;
@@ -493,11 +499,14 @@ struct RowsArgs {
     const uint16_t *la[LORA_MAX_SLICES], *lb[LORA_MAX_SLICES], *bias[LORA_MAX_SLICES];
     int32_t width[LORA_MAX_SLICES], col[LORA_MAX_SLICES];
     float *buf;
+    const int32_t *sorted;       // with packed: tokens in sorted order
+    uint16_t *packed;            // NULL: s in buf alone, tokens in batch order
     uint16_t *y;
     int64_t ldy;
-    int32_t num_tokens, cols, k, rank, slices, max_loras;
+    int32_t num_tokens, cols, k, rank, slices, max_loras, row_len;
     float scale;
 };
+constexpr long kRowsShrinks = 1536, kRowsBytes = 32L << 20;
 constexpr int kRowsTokens = 32, kRowsWaves = 16, kRowsCols = 32, kRowsThreads = kRowsWaves * kWave;
 constexpr int kRowsRanks = 16, kRowsShrinkWaves = 16;
 
@@ -514,9 +523,10 @@ __device__ __forceinline__ void fma_bf16x8(const u32x4 &a, const u32x4 &b, float
 
 __global__ __launch_bounds__(kRowsShrinkWaves *kWave) void rows_shrink_kernel(RowsArgs a) {
     __shared__ float s_part[kRowsShrinkWaves][kRowsRanks];
-    const int per = (a.rank + kRowsRanks - 1) / kRowsRanks;
-    const int t = blockIdx.x / (per * a.slices), i = blockIdx.x / per % a.slices, r0 = blockIdx.x % per * kRowsRanks;
-    const int none = *a.no_lora, id = a.ids[t];
+    const int per = a.packed ? a.row_len / (2 * kRowsRanks) : (a.rank + kRowsRanks - 1) / kRowsRanks;
+    const int p = blockIdx.x / (per * a.slices), i = blockIdx.x / per % a.slices, r0 = blockIdx.x % per * kRowsRanks;
+    const int none = *a.no_lora, st = a.packed ? a.sorted[p] : p;
+    const int t = (unsigned)st < (unsigned)a.num_tokens ? st : 0, id = a.ids[t];
     if (none || id < 0 || id >= a.max_loras) return;
     const int rank = min(r0 + (lane_id() >> 2), a.rank - 1), first = (wave_id() * 4 + (lane_id() & 3)) * 8;
     const uint16_t *row = select_slice(a.la, i) + ((int64_t)id * a.rank + rank) * a.k, *x = a.x + t * a.ldx;
@@ -529,11 +539,21 @@ __global__ __launch_bounds__(kRowsShrinkWaves *kWave) void rows_shrink_kernel(Ro
     sum += __shfl_xor(sum, 2);
     if ((lane_id() & 3) == 0) s_part[wave_id()][lane_id() >> 2] = sum;
     __syncthreads();
-    if (threadIdx.x < kRowsRanks && r0 + (int)threadIdx.x < a.rank) {
+    if (threadIdx.x < kRowsRanks) {
+        const int j = r0 + (int)threadIdx.x;
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < kRowsShrinkWaves; ++w) v += s_part[w][threadIdx.x];
-        a.buf[((int64_t)i * a.num_tokens + t) * a.rank + r0 + threadIdx.x] = a.scale * v;
+        v = j < a.rank ? a.scale * v : 0.f;
+        if (j < a.rank) a.buf[((int64_t)i * a.num_tokens + t) * a.rank + j] = v;
+        if (a.packed) {
+            const int half = packed_half(a.rank);
+            uint16_t *out = a.packed + ((int64_t)i * a.num_tokens + p) * a.row_len + packed_at(j, half);
+            uint32_t h, l;
+            split_hi_lo(v, h, l);
+            out[0] = (uint16_t)h;
+            out[half] = (uint16_t)l;
+        }
     }
 }
 
@@ -1165,11 +1185,16 @@ int lora_linear(const void *x, int64_t ldx, int num_tokens, int hidden, const vo
     const Layout l = layout(num_tokens, meta->max_loras, num_slices, rank, u, false);
     if (l.total > workspace_bytes) return LORA_ERR_BUFFER;
     if (num_tokens == 0) return LORA_OK;
-    if (num_tokens <= kRowsTokens) {
+    char *ws = static_cast<char *>(workspace);
+    const MetaView view = view_of(meta);
+    uint16_t *packed = reinterpret_cast<uint16_t *>(ws + l.s);
+    const bool few = num_tokens <= kRowsTokens;
+    const long shrinks = (long)num_tokens * num_slices * (few ? ceil_div(rank, kRowsRanks) : packed_row(rank) / (2 * kRowsRanks));
+    if (few || (shrinks <= kRowsShrinks && (long)num_tokens * num_slices * rank * hidden * 2 <= kRowsBytes)) {
         RowsArgs r;
         memset(&r, 0, sizeof r);
         r.ids = meta->token_lora_mapping;
-        r.no_lora = view_of(meta).no_lora;
+        r.no_lora = view.no_lora;
         r.x = static_cast<const uint16_t *>(x);
         r.ldx = ldx;
         r.w = static_cast<const uint16_t *>(w);
@@ -1183,6 +1208,9 @@ int lora_linear(const void *x, int64_t ldx, int num_tokens, int hidden, const vo
             r.col[i] = off;
         }
         r.buf = buf;
+        r.sorted = view.sorted;
+        r.packed = few ? nullptr : packed;
+        r.row_len = packed_row(rank);
         r.y = static_cast<uint16_t *>(y);
         r.ldy = ldy;
         r.num_tokens = num_tokens;
@@ -1192,22 +1220,21 @@ int lora_linear(const void *x, int64_t ldx, int num_tokens, int hidden, const vo
         r.slices = num_slices;
         r.max_loras = meta->max_loras;
         r.scale = scale;
-        const unsigned shrinks = (unsigned)(num_tokens * num_slices * (int)ceil_div(rank, kRowsRanks));
-        hipLaunchKernelGGL(rows_shrink_kernel, dim3(shrinks), dim3(kRowsShrinkWaves * kWave), 0, stream, r);
+        hipLaunchKernelGGL(rows_shrink_kernel, dim3((unsigned)shrinks), dim3(kRowsShrinkWaves * kWave), 0, stream, r);
         if (hipGetLastError() != hipSuccess) return LORA_ERR_LAUNCH;
-        const dim3 grid((unsigned)ceil_div(out_features, kRowsCols)), block(kRowsThreads);
-        if (num_tokens <= 16)
-            hipLaunchKernelGGL(rows_kernel<1>, grid, block, 0, stream, r);
-        else
-            hipLaunchKernelGGL(rows_kernel<2>, grid, block, 0, stream, r);
-        return hipGetLastError() == hipSuccess ? LORA_OK : LORA_ERR_LAUNCH;
+        if (few) {
+            const dim3 grid((unsigned)ceil_div(out_features, kRowsCols)), block(kRowsThreads);
+            if (num_tokens <= 16)
+                hipLaunchKernelGGL(rows_kernel<1>, grid, block, 0, stream, r);
+            else
+                hipLaunchKernelGGL(rows_kernel<2>, grid, block, 0, stream, r);
+            return hipGetLastError() == hipSuccess ? LORA_OK : LORA_ERR_LAUNCH;
+        }
+    } else {
+        if ((st = shrink_fresh(x, ldx, num_tokens, hidden, lora_a, num_slices, rank, buf, meta, scale, stream))) return st;
+        if (launch_pack(meta, view, buf, packed, num_slices, rank, ws, nullptr, nullptr, stream) != hipSuccess)
+            return LORA_ERR_LAUNCH;
     }
-    char *ws = static_cast<char *>(workspace);
-    if ((st = shrink_fresh(x, ldx, num_tokens, hidden, lora_a, num_slices, rank, buf, meta, scale, stream))) return st;
-    const MetaView view = view_of(meta);
-    uint16_t *packed = reinterpret_cast<uint16_t *>(ws + l.s);
-    if (launch_pack(meta, view, buf, packed, num_slices, rank, ws, nullptr, nullptr, stream) != hipSuccess)
-        return LORA_ERR_LAUNCH;
     LinearArgs a;
     memset(&a, 0, sizeof a);
     a.meta = view;
