@@ -19,6 +19,9 @@
 // and the piece's rows of dw.  Only the tokens that count take part: a first
 // launch lists them in order.  g is rounded to bf16 because the matrix
 // products take bf16; its fp32 value is formed from fp32 logits before that.
+// A token's largest entry of g is most often its target's, and its rounding
+// alone then adds as much error to dx as dx's own rounding: what it loses is
+// kept in fp32 and comes back as one more row of w at the end.
 #include <string.h>
 
 #include <type_traits>
@@ -60,6 +63,7 @@ struct LogitArgs {
     const float *lse, *dloss;
     uint16_t *g;                // [listed token][ldg]
     int64_t ldg;
+    float *lost;                // [listed token]: the target's g less its rounded value
     int32_t num_tokens, hidden, first, rows, vocab;   // piece: vocabulary [first, first + rows)
     int32_t mtiles, ntiles, group;
 };
@@ -167,6 +171,10 @@ __global__ __launch_bounds__(T::kThreads) void logit_kernel(LogitArgs a) {
                     const float p = exp_of(acc[mt + x / 4][nt][x % 4] - lse[nt]);
                     g[x] = v + x < a.rows ? (p - (v + x == target[nt] ? 1.f : 0.f)) * dl[nt] : 0.f;
                 }
+                if ((unsigned)(target[nt] - v) < 4u * kStep)   // one lane of one piece
+#pragma unroll
+                    for (int x = 0; x < 4 * kStep; ++x)
+                        if (v + x == target[nt]) a.lost[p0 + r] = g[x] - bf16_bits_to_float(float_to_bf16_bits(g[x]));
                 if constexpr (kStep == 2)
                     *reinterpret_cast<u32x4 *>(row + v) =
                         u32x4{pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]), pack_bf16(g[4], g[5]), pack_bf16(g[6], g[7])};
@@ -330,6 +338,10 @@ __global__ __launch_bounds__(T::kThreads) void dx_kernel(DxArgs a) {
 struct FinishArgs {
     const float *planes;
     const int32_t *place;
+    const float *lost;
+    const int32_t *targets;
+    const uint16_t *w;
+    int64_t ldw;
     uint16_t *dx;
     int64_t lddx;
     int32_t num_tokens, hidden, splits;
@@ -341,12 +353,22 @@ __global__ __launch_bounds__(256) void finish_kernel(FinishArgs a) {
         const int64_t t = i / per;
         const int c = (int)(i % per) * 8, p = a.place[t];
         floatx4 v0 = {0.f, 0.f, 0.f, 0.f}, v1 = v0;
-        if (p >= 0)
+        if (p >= 0) {
+            const float lost = a.lost[p];
+            const u32x4 w = *reinterpret_cast<const u32x4 *>(a.w + (int64_t)a.targets[t] * a.ldw + c);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                float lo, hi;
+                unpack_bf16(w[x], lo, hi);
+                (x < 2 ? v0 : v1)[2 * (x & 1)] = lost * lo;
+                (x < 2 ? v0 : v1)[2 * (x & 1) + 1] = lost * hi;
+            }
             for (int s = 0; s < a.splits; ++s) {
                 const floatx4 *q = reinterpret_cast<const floatx4 *>(a.planes + ((int64_t)s * a.num_tokens + p) * a.hidden + c);
                 v0 += q[0];
                 v1 += q[1];
             }
+        }
         *reinterpret_cast<u32x4 *>(a.dx + t * a.lddx + c) =
             u32x4{pack_bf16(v0[0], v0[1]), pack_bf16(v0[2], v0[3]), pack_bf16(v1[0], v1[1]), pack_bf16(v1[2], v1[3])};
     }
@@ -463,7 +485,7 @@ LossPlan plan_loss(long n, long hidden, long vocab) {
 }
 
 struct LossLayout {
-    size_t status, target_logit, stats, list, place, count, x, g, planes, total;
+    size_t status, target_logit, stats, list, place, count, lost, x, g, planes, total;
 };
 LossLayout loss_layout(const LossPlan &p, long n, long hidden, bool train) {
     LossLayout l;
@@ -483,6 +505,7 @@ LossLayout loss_layout(const LossPlan &p, long n, long hidden, bool train) {
     l.list = take(train ? sizeof(int32_t) * (size_t)n : 0);
     l.place = take(train ? sizeof(int32_t) * (size_t)n : 0);
     l.count = take(train ? sizeof(int32_t) : 0);
+    l.lost = take(train ? sizeof(float) * (size_t)n : 0);
     l.x = take(train ? sizeof(uint16_t) * (size_t)n * (size_t)hidden : 0);
     l.g = take(train ? sizeof(uint16_t) * (size_t)n * (size_t)p.piece : 0);
     l.planes = take(train ? sizeof(float) * (size_t)p.splits * (size_t)n * (size_t)hidden : 0);
@@ -632,6 +655,7 @@ int lora_cross_entropy_backward(const void *x, int64_t ldx, int num_tokens, int 
             a.dloss = dloss;
             a.g = g;
             a.ldg = ldg;
+            a.lost = reinterpret_cast<float *>(ws + l.lost);
             a.num_tokens = num_tokens;
             a.hidden = hidden;
             a.first = (int)first;
@@ -698,6 +722,10 @@ int lora_cross_entropy_backward(const void *x, int64_t ldx, int num_tokens, int 
         FinishArgs f;
         f.planes = planes;
         f.place = la.place;
+        f.lost = reinterpret_cast<const float *>(ws + l.lost);
+        f.targets = targets;
+        f.w = static_cast<const uint16_t *>(w);
+        f.ldw = ldw;
         f.dx = static_cast<uint16_t *>(dx);
         f.lddx = lddx;
         f.num_tokens = num_tokens;
