@@ -55,6 +55,7 @@ typedef enum lora_status {
 #define LORA_MAX_RANK 128
 #define LORA_MAX_TOKENS 2097152  /* tokens per batch */
 #define LORA_MAX_VOCAB 16777216  /* rows of a vocabulary matrix */
+#define LORA_MAX_HIDDEN 16777216 /* width of a token in lora_linear and lora_cross_entropy */
 
 /*
  * Per-batch kernel metadata (LoRAKernelMeta on the "lora_kernel_metadata"
@@ -322,7 +323,8 @@ int lora_prepare_meta_launches(int num_tokens, int max_loras);
  *   w_bias  NULL or bf16 [out_features]; y bf16 [num_tokens][ldy]
  *   bias    NULL, or host array [num_slices] of (NULL | device bf16 [max_loras][width])
  *   buf     float32 [num_slices][num_tokens][rank], written as a fresh buffer
- *   ldx, ldw, ldy, out_features, offset_start, hidden, rank: multiples of 8
+ *   ldx, ldw, ldy, out_features, offset_start, hidden, rank: multiples of 8;
+ *           hidden up to LORA_MAX_HIDDEN
  *   workspace  device memory, 256-byte aligned, workspace_bytes of it: at least
  *           what lora_linear_workspace_bytes gives for these sizes
  * The workspace must be zeroed once before its first use; every call leaves
@@ -371,7 +373,7 @@ size_t lora_linear_workspace_bytes(int num_tokens, int max_loras, int hidden, co
  *     loss[t] = lse[t] - z[targets[t]],  0 for an ignored token (target -1)
  *   x bf16 [num_tokens][ldx]; w bf16 [vocab][ldw]; targets int32 [num_tokens]
  *   loss, lse float32 [num_tokens]; any vocab from 1 to LORA_MAX_VOCAB;
- *   hidden, ldx, ldw multiples of 8, operands 16-byte aligned
+ *   hidden (up to LORA_MAX_HIDDEN), ldx, ldw multiples of 8, operands 16-byte aligned
  *   workspace  device memory, 256-byte aligned, of at least
  *           lora_cross_entropy_workspace_bytes; its contents are ignored
  * A target outside [-1, vocab) counts as ignored and is reported: the first
@@ -389,7 +391,8 @@ int lora_cross_entropy(const void *x, int64_t ldx, int num_tokens, int hidden, c
  *     dw[v]    = sum_t g[t][v] x[t]      bf16 [vocab][lddw]
  * dx or dw may be NULL (not needed: a frozen vocabulary matrix has no dw).
  * The logits are computed again piece by piece; g is held as bf16 for one
- * piece.  Sums are float32 and each result is rounded once.  Ignored tokens'
+ * piece, and what the entry of a token's target loses to that is added to dx
+ * and dw in float32.  Sums are float32 and each result is rounded once.  Ignored tokens'
  * x, lse and dloss are not used.  Deterministic.
  */
 int lora_cross_entropy_backward(const void *x, int64_t ldx, int num_tokens, int hidden, const void *w, int64_t ldw,

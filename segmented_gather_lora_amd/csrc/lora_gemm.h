@@ -115,6 +115,11 @@ struct Side {
     __device__ __forceinline__ static int koff(int j) { return STRIDED ? row(j) : elem(j); }
     __device__ __forceinline__ static uint32_t dst(int j) { return (uint32_t)(wave_id() * kInstr + j) * 1024u; }
 
+    // strided: byte of K row k, element v of the side's own index
+    __device__ __forceinline__ static int at(int k, int v) {
+        return k * (ROWS * 2) + 32 * ((v >> 4) ^ f_k(k)) + 2 * (v & 15);
+    }
+
     // operand of the 16-row tile `t` counted from row `base` (a multiple of 16;
     // of 64 with QUADS), half h of the step in the stage at `st`
     __device__ __forceinline__ static bf16x8 read(const lds_byte *st, int base, int t, int h) {
@@ -382,6 +387,27 @@ struct Walk {
     __device__ __forceinline__ void issue(uint32_t at) {
 #pragma unroll
         for (int j = 0; j < S::kInstr; ++j) dma16(S::koff(j) < left ? p[j] : zero_page, at + S::dst(j));
+        next();
+    }
+};
+
+// The same from a scalar base with 32-bit offsets of the lanes: half the
+// registers, where 64 K rows are less than 4 GB.
+template <class S>
+struct OffsetWalk {
+    const uint16_t *base;
+    uint32_t off[S::kInstr];   // bytes
+    int64_t step;
+    int left;
+    __device__ __forceinline__ void load(uint32_t at, int j) { dma16(base, off[j], at + S::dst(j)); }
+    __device__ __forceinline__ void next() {
+        base += step;
+        left -= kStepK;
+    }
+    __device__ __forceinline__ void issue(uint32_t at) {
+#pragma unroll
+        for (int j = 0; j < S::kInstr; ++j)
+            dma16(S::koff(j) < left ? base + off[j] / 2 : zero_page, at + S::dst(j));
         next();
     }
 };

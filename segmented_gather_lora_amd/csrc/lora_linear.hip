@@ -1039,7 +1039,7 @@ int check_sizes(int num_tokens, int max_loras, int hidden, const int *slice_widt
     if (max_loras < 1 || max_loras > LORA_MAX_LORAS) return LORA_ERR_MAX_LORAS;
     if (num_slices < 1 || num_slices > LORA_MAX_SLICES) return LORA_ERR_SLICES;
     if (!slice_widths) return LORA_ERR_NULL;
-    if (hidden < 8 || hidden % 8) return LORA_ERR_SHAPE;
+    if (hidden < 8 || hidden % 8 || hidden > LORA_MAX_HIDDEN) return LORA_ERR_SHAPE;
     if (rank < 8 || rank > LORA_MAX_RANK || rank % 8) return LORA_ERR_SHAPE;
     for (int i = 0; i < num_slices; ++i)
         if (slice_widths[i] <= 0 || slice_widths[i] % 8) return LORA_ERR_SHAPE;

@@ -20,8 +20,9 @@
 // launch lists them in order.  g is rounded to bf16 because the matrix
 // products take bf16; its fp32 value is formed from fp32 logits before that.
 // A token's largest entry of g is most often its target's, and its rounding
-// alone then adds as much error to dx as dx's own rounding: what it loses is
-// kept in fp32 and comes back as one more row of w at the end.
+// alone then adds as much error to dx and dw as their own rounding: what it
+// loses is kept in fp32 and comes back, to dx as one more row of w at the end,
+// to dw as one more K step of the tokens whose target a tile holds.
 #include <string.h>
 
 #include <type_traits>
@@ -237,6 +238,7 @@ __global__ __launch_bounds__(kJoinParts *kJoinTokens) void join_kernel(JoinArgs 
 struct ListArgs {
     const int32_t *targets;
     int32_t *list, *place, *count;   // listed tokens; each token's place in the list or -1
+    int32_t *list_targets;           // targets of the listed tokens
     int32_t num_tokens, vocab;
 };
 constexpr int kListThreads = 1024;
@@ -258,7 +260,10 @@ __global__ __launch_bounds__(kListThreads) void list_kernel(ListArgs a) {
             all += s_wsum[w];
         }
         const int p = before + __popcll(mask & lanemask_lt());
-        if (counts) a.list[p] = t;
+        if (counts) {
+            a.list[p] = t;
+            a.list_targets[p] = target;
+        }
         if (t < a.num_tokens) a.place[t] = counts ? p : -1;
         base += all;
         __syncthreads();
@@ -381,10 +386,79 @@ struct DwArgs {
     int64_t ldg;
     uint16_t *dw;               // the piece's first row
     int64_t lddw;
-    const int32_t *count;
-    int32_t hidden, rows;
+    const int32_t *count, *targets;   // targets: of the listed tokens
+    const float *lost;
+    int32_t hidden, first, rows;
     int32_t mtiles, ntiles, group;
 };
+
+// dw's tile += sum over the listed tokens p whose target it holds of lost[p]
+// x[p]: K steps of 64 such tokens in list order, the N side built in LDS (one
+// entry a K row).  About one step a tile.
+template <class T>
+__device__ __forceinline__ void add_lost(const DwArgs &a, int n, int m0, int v0, typename T::Acc &acc) {
+    constexpr int kChunk = 4;
+    __shared__ int s_match[kChunk * T::kThreads], s_wave[kChunk][T::kWaves];   // place << 8 | row of the tile
+    static_assert(T::BN <= 256 && LORA_MAX_TOKENS <= 1 << 22, "a match in 31 bits");
+    const lds_byte *lds = (const lds_byte *)g_lds;
+    const uint32_t base = lds_address(g_lds);
+    const int tid = threadIdx.x, width = min(T::BN, a.rows - v0);
+    own_reads_barrier();   // the stages are free
+    for (int from = 0; from < n; from += kChunk * T::kThreads) {
+        int row[kChunk], at[kChunk];
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) {
+            const int p = from + i * T::kThreads + tid;
+            row[i] = p < n ? a.targets[p] - a.first - v0 : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) {
+            const uint64_t mask = ballot((unsigned)row[i] < (unsigned)width);
+            at[i] = __popcll(mask & lanemask_lt());
+            if (lane_id() == 0) s_wave[i][wave_id()] = __popcll(mask);
+        }
+        __syncthreads();
+        int total = 0;
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i)
+#pragma unroll
+            for (int w = 0; w < T::kWaves; ++w) {
+                at[i] += w == wave_id() ? total : 0;
+                total += s_wave[i][w];
+            }
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i)
+            if ((unsigned)row[i] < (unsigned)width) s_match[at[i]] = (from + i * T::kThreads + tid) << 8 | row[i];
+        __syncthreads();
+        total = __builtin_amdgcn_readfirstlane(total);
+        for (int k0 = 0; k0 < total; k0 += kStepK) {
+            const int count = min(kStepK, total - k0);
+#pragma unroll
+            for (int j = 0; j < T::MSide::kInstr; ++j) {
+                const int k = T::MSide::row(j), p = s_match[k0 + min(k, count - 1)] >> 8;
+                dma16(k < count ? a.x + (int64_t)p * a.ldx + min(m0 + T::MSide::elem(j), a.hidden - 8) : zero_page,
+                      base + T::MSide::dst(j));
+            }
+            for (int o = 16 * tid; o < T::NSide::kBytes; o += 16 * T::kThreads)
+                *reinterpret_cast<u32x4 *>(g_lds + T::MSide::kBytes + o) = u32x4{0u, 0u, 0u, 0u};
+            __syncthreads();
+            if (tid < count) {
+                const int match = s_match[k0 + tid];
+                *reinterpret_cast<uint16_t *>(g_lds + T::MSide::kBytes + T::NSide::at(tid, match & 255)) =
+                    (uint16_t)float_to_bf16_bits(a.lost[match >> 8]);
+            }
+            wait_loads_barrier<0>();
+            typename T::Half r;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                T::read(r, lds, h);
+                T::mma(r, acc);
+            }
+            own_reads_barrier();
+        }
+        __syncthreads();
+    }
+}
 // dw[v] = sum over the listed tokens of g[p][v] x[p]: both sides have K
 // (the tokens) as their row index.
 template <class T>
@@ -395,19 +469,21 @@ __global__ __launch_bounds__(T::kThreads) void dw_kernel(DwArgs a) {
     typename T::Acc acc;
     clear<T>(acc);
     if (n > 0) {
-        PlainOp<T> op;
+        PairOp<T, OffsetWalk<typename T::MSide>, OffsetWalk<typename T::NSide>> op;
 #pragma unroll
         for (int j = 0; j < T::MSide::kInstr; ++j)
-            op.wm.p[j] = a.x + (int64_t)T::MSide::row(j) * a.ldx + min(m0 + T::MSide::elem(j), a.hidden - 8);
+            op.wm.off[j] = 2u * ((uint32_t)T::MSide::row(j) * (uint32_t)a.ldx + min(m0 + T::MSide::elem(j), a.hidden - 8));
+        op.wm.base = a.x;
         op.wm.step = (int64_t)kStepK * a.ldx;
-        op.wm.left = n;
 #pragma unroll
         for (int j = 0; j < T::NSide::kInstr; ++j)
-            op.wn.p[j] = a.g + (int64_t)T::NSide::row(j) * a.ldg + min(v0 + T::NSide::elem(j), (int)a.ldg - 8);
+            op.wn.off[j] = 2u * ((uint32_t)T::NSide::row(j) * (uint32_t)a.ldg + min(v0 + T::NSide::elem(j), (int)a.ldg - 8));
+        op.wn.base = a.g;
         op.wn.step = (int64_t)kStepK * a.ldg;
-        op.wn.left = n;
+        op.wm.left = op.wn.left = n;
         mma_begin<T>(op, (n + kStepK - 1) / kStepK, g_lds);
         mma_loop<T>(op, n / kStepK, (n + kStepK - 1) / kStepK, acc, g_lds);
+        add_lost<T>(a, n, m0, v0, acc);
     }
 #pragma unroll
     for (int nt = 0; nt < T::NT; ++nt) {
@@ -485,7 +561,7 @@ LossPlan plan_loss(long n, long hidden, long vocab) {
 }
 
 struct LossLayout {
-    size_t status, target_logit, stats, list, place, count, lost, x, g, planes, total;
+    size_t status, target_logit, stats, list, list_targets, place, count, lost, x, g, planes, total;
 };
 LossLayout loss_layout(const LossPlan &p, long n, long hidden, bool train) {
     LossLayout l;
@@ -503,6 +579,7 @@ LossLayout loss_layout(const LossPlan &p, long n, long hidden, bool train) {
     const size_t forward = at;
     at = begin;
     l.list = take(train ? sizeof(int32_t) * (size_t)n : 0);
+    l.list_targets = take(train ? sizeof(int32_t) * (size_t)n : 0);
     l.place = take(train ? sizeof(int32_t) * (size_t)n : 0);
     l.count = take(train ? sizeof(int32_t) : 0);
     l.lost = take(train ? sizeof(float) * (size_t)n : 0);
@@ -515,7 +592,7 @@ LossLayout loss_layout(const LossPlan &p, long n, long hidden, bool train) {
 
 int check_sizes(int num_tokens, int hidden, int vocab) {
     if (num_tokens < 0 || num_tokens > LORA_MAX_TOKENS) return LORA_ERR_NUM_TOKENS;
-    if (hidden < 8 || hidden % 8 || vocab < 1 || vocab > LORA_MAX_VOCAB) return LORA_ERR_SHAPE;
+    if (hidden < 8 || hidden % 8 || hidden > LORA_MAX_HIDDEN || vocab < 1 || vocab > LORA_MAX_VOCAB) return LORA_ERR_SHAPE;
     return LORA_OK;
 }
 int check_loss(const void *x, int64_t ldx, int num_tokens, int hidden, const void *w, int64_t ldw, int vocab,
@@ -616,6 +693,7 @@ int lora_cross_entropy_backward(const void *x, int64_t ldx, int num_tokens, int 
     ListArgs la;
     la.targets = targets;
     la.list = reinterpret_cast<int32_t *>(ws + l.list);
+    la.list_targets = reinterpret_cast<int32_t *>(ws + l.list_targets);
     la.place = reinterpret_cast<int32_t *>(ws + l.place);
     la.count = reinterpret_cast<int32_t *>(ws + l.count);
     la.num_tokens = num_tokens;
@@ -705,7 +783,10 @@ int lora_cross_entropy_backward(const void *x, int64_t ldx, int num_tokens, int 
             d.dw = static_cast<uint16_t *>(dw) + first * lddw;
             d.lddw = lddw;
             d.count = la.count;
+            d.targets = la.list_targets;
+            d.lost = reinterpret_cast<const float *>(ws + l.lost);
             d.hidden = hidden;
+            d.first = (int)first;
             d.rows = rows;
             d.mtiles = (int)ceil_div(hidden, tile_m(p.dw));
             d.ntiles = (int)ceil_div(rows, tile_n(p.dw));

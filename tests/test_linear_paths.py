@@ -8,7 +8,7 @@ import pytest
 import torch
 
 sys.path.insert(0, os.path.dirname(__file__))
-from test_linear import Case, Run, check  # noqa: E402
+from test_linear import Case, Run, check, lib  # noqa: E402
 
 ALL = ("y", "dx", "s", "u", "da", "db", "dbias")
 
@@ -140,3 +140,10 @@ def test_graph_replays_of_one_token():
         torch.cuda.synchronize()
         assert torch.equal(r.outputs()["y"], eager)
         r.x.mul_(1.0)   # eager work between the replays
+
+
+def test_widths_past_the_limit_are_refused():
+    sgl = lib()
+    assert sgl.lora_linear_workspace_bytes(16, 4, 1 << 24, [64], 8) > 0
+    with pytest.raises(sgl.LoraError):
+        sgl.lora_linear_workspace_bytes(16, 4, (1 << 24) + 8, [64], 8)
