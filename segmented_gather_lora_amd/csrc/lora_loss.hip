@@ -69,6 +69,9 @@ struct LogitArgs {
     int32_t mtiles, ntiles, group;
 };
 
+// 4096 tokens by 128256 entries over 4096: statistics 3.17 ms (1.36 PFLOP/s, bound
+// by power), g 0.84 ms a piece of 32256; 256 tokens 0.22 ms; 16 tokens 167 us (W
+// at 6.3 TB/s).
 template <class T, bool GRAD>
 __global__ __launch_bounds__(T::kThreads) void logit_kernel(LogitArgs a) {
     __shared__ Stat s_stat[GRAD ? 1 : T::WM][GRAD ? 1 : T::BN];
@@ -197,7 +200,8 @@ struct JoinArgs {
     int32_t num_tokens, mtiles, vocab;
 };
 
-// 16 tokens a workgroup, 64 threads each, eight pairs at a time.
+// 16 tokens a workgroup, 64 threads each, eight pairs at a time: 5 to 7 us from 16
+// to 4096 tokens of 128256 entries, mostly latency.
 constexpr int kJoinParts = 64, kJoinTokens = 16, kJoinChunk = 8;
 __global__ __launch_bounds__(kJoinParts *kJoinTokens) void join_kernel(JoinArgs a) {
     __shared__ Stat s_part[kJoinParts][kJoinTokens];
@@ -243,7 +247,8 @@ struct ListArgs {
 };
 constexpr int kListThreads = 1024;
 
-// One workgroup: the list is short against the products it shortens.
+// One workgroup (5 us for 4096 tokens): the list is short against the products it
+// shortens.
 __global__ __launch_bounds__(kListThreads) void list_kernel(ListArgs a) {
     __shared__ int s_wsum[kListThreads / kWave];
     int base = 0;
@@ -302,7 +307,8 @@ struct DxArgs {
     int32_t mtiles, group, splits, split_steps;
 };
 
-// planes[split][p] (+)= sum over the split's vocabulary rows of g[p][v] w[v].
+// planes[split][p] (+)= sum over the split's vocabulary rows of g[p][v] w[v].  0.74
+// ms a piece of 32256 entries for 3686 tokens over 4096 (1.31 PFLOP/s, by power).
 template <class T>
 __global__ __launch_bounds__(T::kThreads) void dx_kernel(DxArgs a) {
     const int n = *a.count, ntiles = (n + T::BN - 1) / T::BN;
@@ -460,7 +466,8 @@ __device__ __forceinline__ void add_lost(const DwArgs &a, int n, int m0, int v0,
     }
 }
 // dw[v] = sum over the listed tokens of g[p][v] x[p]: both sides have K
-// (the tokens) as their row index.
+// (the tokens) as their row index.  0.86 ms a piece of 32256 entries for 3686
+// tokens over 4096 (1.13 PFLOP/s: transposing LDS reads for both sides).
 template <class T>
 __global__ __launch_bounds__(T::kThreads) void dw_kernel(DwArgs a) {
     TileAt at;
