@@ -149,6 +149,7 @@ struct LinearArgs {
     const uint16_t *bias[LORA_MAX_SLICES];
     int32_t width[LORA_MAX_SLICES], col[LORA_MAX_SLICES];
     const uint16_t *packed;                     // s or u: [slices][n][packed_row]
+    const float *s;                             // the same in fp32: [slices][n][rank], batch order
     uint16_t *y;                                // y or dx
     int64_t ldy;
     int32_t num_tokens, cols, k, rank, slices, max_loras;
@@ -304,6 +305,79 @@ struct LinearOp : PlainOp<T> {
     }
 };
 
+// The adapters' share of a 64 x 64 tile as fp32 dot products, a lane for its
+// token and 16 of the tile's columns, in place of a step of the K walk for every 32
+// ranks, adapter and slice.  y reads 16 contiguous rows of B a lane and gains from
+// four adapters in a tile on (38 tokens of 26 adapters, 3 slices of rank 80: 160 us
+// with the steps, 38 with the products; 64 tokens of 4, rank 64: 24 and 24).  dx
+// waits for a row of A a rank and gains from about 20 (training step, 88 tokens of
+// 32 adapters, rank 32: 204 us and 164; 64 tokens of 4, 3 slices of rank 128: 134
+// and 236).
+template <bool BWD>
+constexpr int kDotSegs = BWD ? 20 : 4;
+template <class T, bool BWD>
+__device__ __forceinline__ void add_dots(const LinearArgs &a, const SliceEntry *slices, int m0, int t, int id,
+                                         typename T::Acc &acc) {
+    static_assert(T::NT == 1 && T::MT == 4, "one token a lane");
+    const int r = a.rank;
+    auto matrices = [&](int i) {
+        return reinterpret_cast<const uint16_t *>(slices[i].weights[0] | (uint64_t)slices[i].weights[1] << 32);
+    };
+    if (BWD) {
+        for (int i = 0; i < a.slices; ++i) {
+            const uint16_t *w = matrices(i) + (int64_t)id * r * a.cols;
+            const float *s = a.s + ((int64_t)i * a.num_tokens + t) * r;
+#pragma unroll 4
+            for (int j = 0; j < r; ++j, w += a.cols) {
+                const float sj = s[j];
+#pragma unroll
+                for (int mt = 0; mt < T::MT; ++mt) {
+                    const int c = min(m0 + T::m_of(mt), a.cols - 4);
+                    const u32x2g v = *reinterpret_cast<const u32x2g *>(w + c);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        float p, q;
+                        unpack_bf16(v[x], p, q);
+                        acc[mt][0][2 * x] = fmaf(p, sj, acc[mt][0][2 * x]);
+                        acc[mt][0][2 * x + 1] = fmaf(q, sj, acc[mt][0][2 * x + 1]);
+                    }
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int mt = 0; mt < T::MT; mt += 2) {      // 8 columns, never across a slice's edge
+            const int c = m0 + T::m_of(mt);
+            for (int i = 0; i < a.slices; ++i) {
+                const int in = c - slices[i].col, width = slices[i].width;
+                if (in < 0 || in >= width) continue;
+                const uint16_t *b = matrices(i) + ((int64_t)id * width + in) * r;
+                const float *s = a.s + ((int64_t)i * a.num_tokens + t) * r;
+                float sum[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) sum[x] = 0.f;
+                for (int j = 0; j < r; j += 8) {
+                    const floatx4 s0 = *reinterpret_cast<const floatx4 *>(s + j), s1 = *reinterpret_cast<const floatx4 *>(s + j + 4);
+                    u32x4 v[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) v[x] = *reinterpret_cast<const u32x4 *>(b + x * r + j);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            float p, q;
+                            unpack_bf16(v[x][k], p, q);
+                            sum[x] = fmaf(p, k < 2 ? s0[2 * k] : s1[2 * k - 4], sum[x]);
+                            sum[x] = fmaf(q, k < 2 ? s0[2 * k + 1] : s1[2 * k - 3], sum[x]);
+                        }
+                }
+#pragma unroll
+                for (int x = 0; x < 8; ++x) acc[mt + x / 4][0][x % 4] += sum[x];
+            }
+        }
+    }
+}
+
 // A tile of y or dx.  16384 tokens, 128 adapters of rank 128: y (10240 columns
 // over 8192) 2.5 ms, dx (8192 over 10240, three slices) 3.3 ms, of which W's
 // product is 2.0 ms each at 1.37 PFLOP/s, bound by power; the rest are the
@@ -315,6 +389,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(LinearArgs a) {
     __shared__ SegRow s_seg[T::BN];
     __shared__ SliceEntry s_slice[LORA_MAX_SLICES];
     static_assert(T::BN <= T::kThreads, "a thread a token row");
+    constexpr bool kDots = T::BM == 64 && T::BN == 64;
     const int tid = threadIdx.x;
     TileAt at;
     if (!tile_at(blockIdx.x, a.mtiles, a.ntiles, a.group, at)) return;
@@ -373,7 +448,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(LinearArgs a) {
         }
     if (tid < T::BN) {
         s_tok[tid] = own;
-        s_id[tid] = none || (BWD || !a.has_bias) ? -1 : a.ids[own];
+        s_id[tid] = none || (!kDots && (BWD || !a.has_bias)) ? -1 : a.ids[own];
     }
     if (!none)
         for (int k = tid; k < a.meta.nslots; k += T::kThreads) {
@@ -403,13 +478,20 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(LinearArgs a) {
                 op.sl1 = i + 1;
             }
     }
-    const int units = op.sl1 > op.sl0 ? nseg * (op.sl1 - op.sl0) * op.per_seg() : 0;
+    const bool dots = kDots && nseg >= kDotSegs<BWD>;
+    const int units = op.sl1 > op.sl0 && !dots ? nseg * (op.sl1 - op.sl0) * op.per_seg() : 0;
     const int steps = main + (op.blocks ? units : (units + 1) / 2);
     if (units > 0) op.start(units);
     if (!early) mma_begin<T>(op, steps, g_lds);
     typename T::Acc acc;
     clear<T>(acc);
     mma_loop<T>(op, a.k / kStepK, steps, acc, g_lds);
+
+    if constexpr (kDots)
+        if (dots) {
+            const int row = T::n_of(0), m = s_id[row];
+            if (row < rows && m >= 0 && m < a.max_loras) add_dots<T, BWD>(a, s_slice, m0, s_tok[row], m, acc);
+        }
 
     // biases: of the projection for every token, of the adapter where there is one
     if constexpr (T::QUADS) {
@@ -1265,6 +1347,7 @@ int lora_linear(const void *x, int64_t ldx, int num_tokens, int hidden, const vo
         off += slice_widths[i];
     }
     a.packed = packed;
+    a.s = buf;
     a.y = static_cast<uint16_t *>(y);
     a.ldy = ldy;
     a.num_tokens = num_tokens;
@@ -1347,6 +1430,7 @@ int lora_linear_backward(const void *dy, int64_t lddy, const void *x, int64_t ld
         a.ldw = ldw;
         for (int i = 0; i < num_slices; ++i) a.lw[i] = static_cast<const uint16_t *>(lora_a[i]);
         a.packed = up;
+        a.s = dbuf;
         a.y = static_cast<uint16_t *>(dx);
         a.ldy = lddx;
         a.num_tokens = num_tokens;

@@ -147,3 +147,23 @@ def test_widths_past_the_limit_are_refused():
     assert sgl.lora_linear_workspace_bytes(16, 4, 1 << 24, [64], 8) > 0
     with pytest.raises(sgl.LoraError):
         sgl.lora_linear_workspace_bytes(16, 4, (1 << 24) + 8, [64], 8)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,loras,widths,rank", [(38, 26, [24, 48, 56], 80), (70, 40, [72, 8], 8), (130, 90, [136], 128),
+                                                 (64, 4, [40], 16), (64, 3, [40], 16)])
+def test_many_adapters_in_a_tile(n, loras, widths, rank):
+    """Tiles that meet more and fewer adapters than a step of the walk is worth, y and dx."""
+    c = Case(n=n, hidden=136, widths=widths, rank=rank, loras=loras, offset=8, extra=8)
+    r = Run(c)
+    r.forward()
+    r.backward()
+    check(c, r.outputs())
+    r.a[0][0] = float("nan")        # what is not finite stays with its adapter's tokens
+    r.b[0][0] = float("inf")
+    before = r.outputs()
+    r.forward()
+    r.backward()
+    after = r.outputs()
+    rows = c.ids != 0
+    assert torch.equal(before["y"][rows], after["y"][rows]) and torch.equal(before["dx"][rows], after["dx"][rows])
