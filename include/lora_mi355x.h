@@ -370,7 +370,9 @@ size_t lora_linear_workspace_bytes(int num_tokens, int max_loras, int hidden, co
  * taken of them), in pieces, without the logits in memory.  For every token t:
  *     z[v] = sum_k x[t][k] w[v][k]                       (float32)
  *     lse[t]  = log sum_v exp z[v]
- *     loss[t] = lse[t] - z[targets[t]],  0 for an ignored token (target -1)
+ *     loss[t] = lse[t] - z[targets[t]],  0 for an ignored token (target -1); formed as
+ *               (max_v z[v] - z[targets[t]]) + log sum_v exp(z[v] - max), whose digits
+ *               do not depend on the size of the logits
  *   x bf16 [num_tokens][ldx]; w bf16 [vocab][ldw]; targets int32 [num_tokens]
  *   loss, lse float32 [num_tokens]; any vocab from 1 to LORA_MAX_VOCAB;
  *   hidden (up to LORA_MAX_HIDDEN), ldx, ldw multiples of 8, operands 16-byte aligned

@@ -228,10 +228,12 @@ __global__ __launch_bounds__(kJoinParts *kJoinTokens) void join_kernel(JoinArgs 
         if (part < w) s_part[part][tok] = s = join(s, s_part[part + w][tok]);
     }
     if (part == 0 && t < a.num_tokens) {
-        const float lse = s.max + logf(s.sum);
+        // the loss from its two terms: lse, rounded at the logits' size, would lose the
+        // digits of a loss that is small against them
+        const float log_sum = logf(s.sum);
         const int target = a.targets[t];
-        a.lse[t] = lse;
-        a.loss[t] = target >= 0 && target < a.vocab ? lse - a.target_logit[t] : 0.f;
+        a.lse[t] = s.max + log_sum;
+        a.loss[t] = target >= 0 && target < a.vocab ? (s.max - a.target_logit[t]) + log_sum : 0.f;
         if (target < -1 || target >= a.vocab)
             __hip_atomic_store(a.status, (int)LORA_ERR_ID_RANGE, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
