@@ -36,6 +36,7 @@ extern __shared__ __attribute__((aligned(1024))) unsigned char g_lds[];
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kMaxFloat = 0x1.fffffep127f;
 
 // exp(d): the hardware's 2^x of d log2(e).
 __device__ __forceinline__ float exp_of(float d) { return __builtin_amdgcn_exp2f(d * kLog2e); }
@@ -43,9 +44,13 @@ __device__ __forceinline__ float exp_of(float d) { return __builtin_amdgcn_exp2f
 struct Stat {
     float max, sum;   // sum of exp(z - max)
 };
+// What exponents are taken against: the maximum, or the finite number next to an
+// infinite one, so that its own terms do not become infinity - infinity (all
+// entries -inf: a sum of 0; an entry of +inf: a sum of +inf).
+__device__ __forceinline__ float exp_base(float max) { return fminf(fmaxf(max, -kMaxFloat), kMaxFloat); }
 __device__ __forceinline__ Stat join(const Stat &a, const Stat &b) {
     const float m = fmaxf(a.max, b.max);
-    const float base = m == kNegInf ? 0.f : m;
+    const float base = exp_base(m);
     return Stat{m, a.sum * exp_of(a.max - base) + b.sum * exp_of(b.max - base)};
 }
 
@@ -129,7 +134,7 @@ __global__ __launch_bounds__(T::kThreads) void logit_kernel(LogitArgs a) {
             // the maximum of this token's four lanes first: one scale for all of their terms
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
-            const float base = top == kNegInf ? 0.f : top;
+            const float base = exp_base(top);
             float sum = 0.f;
 #pragma unroll
             for (int mt = 0; mt < T::MT; ++mt)
