@@ -359,8 +359,9 @@ int lora_linear_backward(const void *dy, int64_t lddy, const void *x, int64_t ld
                          void *const *dbias, int offset_start, const lora_meta_t *meta, float scale, void *workspace,
                          size_t workspace_bytes, hipStream_t stream);
 
-/* Bytes of workspace for batches of num_tokens tokens (backward != 0: for
- * lora_linear_backward too).  0 if a size is out of range.  Host only. */
+/* Bytes of workspace for batches of up to num_tokens tokens (backward != 0: for
+ * lora_linear_backward too): never less than for fewer tokens.  0 if a size is
+ * out of range.  Host only. */
 size_t lora_linear_workspace_bytes(int num_tokens, int max_loras, int hidden, const int *slice_widths, int num_slices,
                                    int rank, int backward);
 

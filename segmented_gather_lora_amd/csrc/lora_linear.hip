@@ -1079,12 +1079,13 @@ LinearPlan plan_linear(long n, long cols) {
     return p;
 }
 
-constexpr int kCounterWords = 1024;   // units of the u product whose K may be split
+constexpr int kCounterWords = 1024;   // at least the units of the u product whose K may be split (kSplitUnits / 2)
 
 struct UPlan {
     int bm, tile_tokens, tiles_cap, splits;
     size_t slot_bytes;
 };
+constexpr long kSplitUnits = 768, kMaxSplits = 8;   // workgroups that a split K is to give
 UPlan plan_u(long n, int max_loras, int slices, int rank, long widest) {
     UPlan p;
     p.bm = rank <= 32 ? 32 : rank <= 64 ? 64 : 128;
@@ -1092,13 +1093,16 @@ UPlan plan_u(long n, int max_loras, int slices, int rank, long widest) {
     const long segs = n < max_loras ? n : max_loras;
     p.tiles_cap = (int)(ceil_div(n, p.tile_tokens) + segs);
     const long units = (long)p.tiles_cap * slices;
-    long splits = 768 / (units > 0 ? units : 1);
     const long steps = ceil_div(widest, kStepK);
-    if (splits > steps / 8) splits = steps / 8;
-    if (splits > 8) splits = 8;
-    if (splits < 1 || units > kCounterWords) splits = 1;
+    const long most = steps / 8 < kMaxSplits ? steps / 8 : kMaxSplits;
+    long splits = kSplitUnits / (units > 0 ? units : 1);
+    if (splits > most) splits = most;
+    if (splits < 1) splits = 1;
     p.splits = (int)splits;
-    p.slot_bytes = splits > 1 ? sizeof(float) * (size_t)units * splits * p.bm * p.tile_tokens : 0;
+    // room for every smaller batch too, which may split more: `units` grows with n,
+    // and units * splits is at most kSplitUnits where K is split at all
+    const long slots = units * most < kSplitUnits ? units * most : kSplitUnits;
+    p.slot_bytes = most > 1 ? sizeof(float) * (size_t)slots * p.bm * p.tile_tokens : 0;
     return p;
 }
 

@@ -1,0 +1,40 @@
+"""A workspace that is sized for the largest batch serves every smaller one."""
+import os
+import sys
+
+import pytest
+import torch
+
+sys.path.insert(0, os.path.dirname(__file__))
+import test_linear as linear  # noqa: E402
+
+
+def _never_decreases(size, most):
+    last = 0
+    for n in list(range(0, min(most, 6000))) + list(range(6000, most, 997)):
+        now = size(n)
+        assert now >= last, "%d tokens need %d bytes, fewer need %d" % (n, now, last)
+        last = now
+
+
+@pytest.mark.parametrize("loras,hidden,widths,rank", [
+    (32, 4096, [4096, 1024, 1024], 128), (128, 8192, [8192, 1024, 1024], 64), (4, 72, [4104, 72], 16),
+    (1023, 520, [136], 8), (1, 8, [1024], 24)])
+@pytest.mark.parametrize("backward", [False, True])
+def test_linear_sizes_never_decrease(loras, hidden, widths, rank, backward):
+    sgl = linear.lib()
+    _never_decreases(lambda n: sgl.lora_linear_workspace_bytes(n, loras, hidden, widths, rank, backward), 70000)
+
+
+@pytest.mark.gpu
+def test_a_large_batchs_workspace_serves_small_ones():
+    """A ragged last batch with the buffers of the full one."""
+    sgl = linear.lib()
+    for n in (1, 70, 517, 1100):
+        c = linear.Case(n=n, hidden=136, widths=[1160, 72], rank=24, loras=5)
+        r = linear.Run(c)
+        r.workspace = torch.zeros(sgl.lora_linear_workspace_bytes(1100, c.loras, c.hidden, c.widths, c.rank, True),
+                                  dtype=torch.uint8, device="cuda")
+        r.forward()
+        r.backward()
+        linear.check(c, r.outputs())
