@@ -406,7 +406,8 @@ int lora_cross_entropy_backward(const void *x, int64_t ldx, int num_tokens, int 
                                 hipStream_t stream);
 
 /* Bytes of workspace of lora_cross_entropy (backward != 0: of both calls) for
- * these sizes.  0 if a size is out of range.  Host only. */
+ * batches of up to num_tokens tokens: never less than for fewer tokens.  0 if a
+ * size is out of range.  Host only. */
 size_t lora_cross_entropy_workspace_bytes(int num_tokens, int hidden, int vocab, int backward);
 
 /* Static description of a status code. */

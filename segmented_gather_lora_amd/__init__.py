@@ -594,8 +594,8 @@ def lora_linear_backward(dy, x, w, lora_a: Sequence, lora_b: Sequence, buf, dbuf
 
 
 def lora_cross_entropy_workspace_bytes(num_tokens: int, hidden: int, vocab: int, backward: bool = False) -> int:
-    """Bytes of the workspace of lora_cross_entropy (backward: of both calls):
-    a uint8 device tensor."""
+    """Bytes of the workspace of lora_cross_entropy (backward: of both calls) for
+    batches of up to num_tokens tokens: a uint8 device tensor."""
     n = int(_lib().lora_cross_entropy_workspace_bytes(int(num_tokens), int(hidden), int(vocab), 1 if backward else 0))
     if n == 0:
         raise LoraError(LORA_ERR_SHAPE, "lora_cross_entropy_workspace_bytes")

@@ -542,6 +542,7 @@ struct LossPlan {
 // g's buffer: 2^27 elements (256 MB, the size of the last-level cache), at
 // least 4096 vocabulary rows.
 constexpr long kPieceElems = 1L << 27, kPieceMin = 4096;
+constexpr long kMaxSplits = 16, kSplitSteps = 16;   // dx: parts of a split K, steps of each at least
 
 LossPlan plan_loss(long n, long hidden, long vocab) {
     LossPlan p;
@@ -555,12 +556,12 @@ LossPlan plan_loss(long n, long hidden, long vocab) {
     p.piece = piece;
     p.grad = pick_tile(piece, n);
     const long steps = piece / kStepK;
-    // dx: K (the piece) is split until the CUs are full, into parts of at least 16 steps
+    // dx: K (the piece) is split until the CUs are full
     auto splits_of = [&](LossTile t) {
         const long tiles = ceil_div(hidden, tile_m(t)) * ceil_div(n > 0 ? n : 1, tile_n(t));
         long s = (t == kBig ? 256 : 512) / tiles;
-        if (s > steps / 16) s = steps / 16;
-        if (s > 16) s = 16;
+        if (s > steps / kSplitSteps) s = steps / kSplitSteps;
+        if (s > kMaxSplits) s = kMaxSplits;
         return s < 1 ? 1 : s;
     };
     p.dx = kRow;
@@ -577,8 +578,28 @@ LossPlan plan_loss(long n, long hidden, long vocab) {
 struct LossLayout {
     size_t status, target_logit, stats, list, list_targets, place, count, lost, x, g, planes, total;
 };
-LossLayout loss_layout(const LossPlan &p, long n, long hidden, bool train) {
+size_t least(size_t a, size_t b) { return a < b ? a : b; }
+size_t largest(size_t a, size_t b) { return a > b ? a : b; }
+// The areas whose sizes follow the plan have room for every smaller batch too,
+// whose plan may need more of them (more vocabulary tiles, larger pieces, a split
+// K): each is a bound on the plans of up to n tokens that grows with n.
+//   stats   128 x 32 and 128 x 128 tiles serve up to 128 tokens, 256 x 256 tiles the
+//           largest batches; other 128 x 128 ones are fewer than 192 tiles of
+//           256 x 256, 64 x 64 ones fewer than 384 of 128 x 128 (tokens times vocabulary
+//           tiles: below 2 * 256 * 192 and 2 * 128 * 384)
+//   g       a piece is at most the vocabulary, and at most kPieceElems elements or
+//           kPieceMin rows
+//   planes  a split K fills at most 256 workgroups of 256 x 256 or 512 smaller ones, and
+//           has at most kMaxSplits parts of at least kSplitSteps steps
+LossLayout loss_layout(const LossPlan &p, long n, long hidden, long vocab, bool train) {
     LossLayout l;
+    const size_t tokens = (size_t)n, whole = (size_t)ceil_div(vocab, 256) * 256;
+    size_t stats = tokens * (size_t)ceil_div(vocab, 256);
+    stats = largest(stats, least(tokens, 128) * (size_t)ceil_div(vocab, 128));
+    stats = largest(stats, least(tokens * (size_t)ceil_div(vocab, 64), 2 * 256 * 192));
+    const size_t g = least(tokens * whole, largest((size_t)kPieceElems, tokens * (size_t)kPieceMin));
+    const size_t parts = least(kMaxSplits, whole / kStepK / kSplitSteps);
+    const size_t planes = largest(tokens, least(tokens * parts, ceil_div((size_t)256 * 256 * 256, hidden)));
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t o = at;
@@ -589,7 +610,7 @@ LossLayout loss_layout(const LossPlan &p, long n, long hidden, bool train) {
     // the forward pass's areas and the backward pass's are not in use together
     const size_t begin = at;
     l.target_logit = take(sizeof(float) * (size_t)n);
-    l.stats = take(sizeof(Stat) * (size_t)p.mtiles * (size_t)n);
+    l.stats = take(sizeof(Stat) * largest(stats, (size_t)p.mtiles * tokens));
     const size_t forward = at;
     at = begin;
     l.list = take(train ? sizeof(int32_t) * (size_t)n : 0);
@@ -598,8 +619,8 @@ LossLayout loss_layout(const LossPlan &p, long n, long hidden, bool train) {
     l.count = take(train ? sizeof(int32_t) : 0);
     l.lost = take(train ? sizeof(float) * (size_t)n : 0);
     l.x = take(train ? sizeof(uint16_t) * (size_t)n * (size_t)hidden : 0);
-    l.g = take(train ? sizeof(uint16_t) * (size_t)n * (size_t)p.piece : 0);
-    l.planes = take(train ? sizeof(float) * (size_t)p.splits * (size_t)n * (size_t)hidden : 0);
+    l.g = take(train ? sizeof(uint16_t) * largest(g, tokens * (size_t)p.piece) : 0);
+    l.planes = take(train ? sizeof(float) * largest(planes, tokens * (size_t)p.splits) * (size_t)hidden : 0);
     l.total = at > forward ? at : forward;
     return l;
 }
@@ -618,7 +639,7 @@ int check_loss(const void *x, int64_t ldx, int num_tokens, int hidden, const voi
     if (!aligned16(w) || (num_tokens > 0 && !aligned16(x))) return LORA_ERR_ALIGN;
     if ((reinterpret_cast<uintptr_t>(workspace) & (kRound - 1)) != 0) return LORA_ERR_BUFFER;
     const LossPlan p = plan_loss(num_tokens, hidden, vocab);
-    if (loss_layout(p, num_tokens, hidden, train).total > workspace_bytes) return LORA_ERR_BUFFER;
+    if (loss_layout(p, num_tokens, hidden, vocab, train).total > workspace_bytes) return LORA_ERR_BUFFER;
     return LORA_OK;
 }
 
@@ -642,7 +663,7 @@ extern "C" {
 
 size_t lora_cross_entropy_workspace_bytes(int num_tokens, int hidden, int vocab, int backward) {
     if (check_sizes(num_tokens, hidden, vocab)) return 0;
-    return loss_layout(plan_loss(num_tokens, hidden, vocab), num_tokens, hidden, backward != 0).total;
+    return loss_layout(plan_loss(num_tokens, hidden, vocab), num_tokens, hidden, vocab, backward != 0).total;
 }
 
 int lora_cross_entropy(const void *x, int64_t ldx, int num_tokens, int hidden, const void *w, int64_t ldw, int vocab,
@@ -653,7 +674,7 @@ int lora_cross_entropy(const void *x, int64_t ldx, int num_tokens, int hidden, c
     if (num_tokens > 0 && (!loss || !lse)) return LORA_ERR_NULL;
     if (num_tokens == 0) return LORA_OK;
     const LossPlan p = plan_loss(num_tokens, hidden, vocab);
-    const LossLayout l = loss_layout(p, num_tokens, hidden, false);
+    const LossLayout l = loss_layout(p, num_tokens, hidden, vocab, false);
     char *ws = static_cast<char *>(workspace);
     LogitArgs a;
     memset(&a, 0, sizeof a);
@@ -702,7 +723,7 @@ int lora_cross_entropy_backward(const void *x, int64_t ldx, int num_tokens, int 
     if (!aligned16(dx) || !aligned16(dw)) return LORA_ERR_ALIGN;
     if (!dx && !dw) return LORA_OK;
     const LossPlan p = plan_loss(num_tokens, hidden, vocab);
-    const LossLayout l = loss_layout(p, num_tokens, hidden, true);
+    const LossLayout l = loss_layout(p, num_tokens, hidden, vocab, true);
     char *ws = static_cast<char *>(workspace);
     ListArgs la;
     la.targets = targets;

@@ -7,6 +7,7 @@ import torch
 
 sys.path.insert(0, os.path.dirname(__file__))
 import test_linear as linear  # noqa: E402
+import test_loss as loss  # noqa: E402
 
 
 def _never_decreases(size, most):
@@ -26,6 +27,14 @@ def test_linear_sizes_never_decrease(loras, hidden, widths, rank, backward):
     _never_decreases(lambda n: sgl.lora_linear_workspace_bytes(n, loras, hidden, widths, rank, backward), 70000)
 
 
+@pytest.mark.parametrize("hidden,vocab", [(4096, 128256), (8192, 32000), (72, 5003), (264, 1 << 20), (8, 300),
+                                          (16384, 256), (8, 1 << 24)])
+@pytest.mark.parametrize("backward", [False, True])
+def test_loss_sizes_never_decrease(hidden, vocab, backward):
+    sgl = loss.lib()
+    _never_decreases(lambda n: sgl.lora_cross_entropy_workspace_bytes(n, hidden, vocab, backward), 140000)
+
+
 @pytest.mark.gpu
 def test_a_large_batchs_workspace_serves_small_ones():
     """A ragged last batch with the buffers of the full one."""
@@ -38,3 +47,11 @@ def test_a_large_batchs_workspace_serves_small_ones():
         r.forward()
         r.backward()
         linear.check(c, r.outputs())
+    for n in (1, 40, 300, 1100):
+        c = loss.Case(n=n, hidden=72, vocab=5003)
+        r = loss.Run(c)
+        r.workspace = torch.full((sgl.lora_cross_entropy_workspace_bytes(1100, 72, 5003, True),), 0xff,
+                                 dtype=torch.uint8, device="cuda")
+        r.forward()
+        r.backward()
+        loss.check(c, r.outputs())
