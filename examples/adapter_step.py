@@ -44,9 +44,9 @@ def train(steps=12, tokens=192, hidden=256, width=264, rank=16, loras=5, vocab=1
     loss, lse = torch.empty(tokens, **dev), torch.empty(tokens, **dev)
     dloss = torch.full((tokens,), 1.0 / counted, **dev)
     da, db = torch.empty_like(a32, dtype=torch.bfloat16), torch.empty_like(b32, dtype=torch.bfloat16)
-    linear = torch.zeros(sgl.lora_linear_workspace_bytes(tokens, loras, hidden, [width], rank, True),
+    linear = torch.empty(sgl.lora_linear_workspace_bytes(tokens, loras, hidden, [width], rank, True),
                          dtype=torch.uint8, **dev)
-    entropy = torch.zeros(sgl.lora_cross_entropy_workspace_bytes(tokens, width, vocab, True), dtype=torch.uint8, **dev)
+    entropy = torch.empty(sgl.lora_cross_entropy_workspace_bytes(tokens, width, vocab, True), dtype=torch.uint8, **dev)
 
     sgl.lora_prepare_meta(ids, meta)
     losses = []

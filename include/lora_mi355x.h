@@ -327,9 +327,9 @@ int lora_prepare_meta_launches(int num_tokens, int max_loras);
  *           hidden up to LORA_MAX_HIDDEN
  *   workspace  device memory, 256-byte aligned, workspace_bytes of it: at least
  *           what lora_linear_workspace_bytes gives for these sizes
- * The workspace must be zeroed once before its first use; every call leaves
- * its counters zero.  One workspace serves any number of calls that do not
- * overlap, of any sizes that fit.  buf is deterministic where lora_shrink is;
+ * The workspace's contents are ignored and nothing is kept in it between calls:
+ * the same memory serves any number of calls that do not overlap, of these and
+ * of the loss, of any sizes that fit.  buf is deterministic where lora_shrink is;
  * given buf, y is.
  */
 int lora_linear(const void *x, int64_t ldx, int num_tokens, int hidden, const void *w, int64_t ldw, int out_features,

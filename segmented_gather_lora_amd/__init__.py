@@ -451,7 +451,7 @@ def lora_linear_workspace_bytes(num_tokens: int, max_loras: int, hidden: int, wi
                                 backward: bool = False) -> int:
     """Bytes of the workspace of lora_linear (backward: and of
     lora_linear_backward) for batches of up to num_tokens tokens: a uint8 device
-    tensor, zeroed once."""
+    tensor, whose contents do not matter."""
     n = int(_lib().lora_linear_workspace_bytes(int(num_tokens), int(max_loras), int(hidden), _widths_array(widths),
                                                len(widths), int(rank), 1 if backward else 0))
     if n == 0:

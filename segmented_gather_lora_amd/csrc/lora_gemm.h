@@ -490,9 +490,9 @@ using PlainOp = PairOp<T, Walk<typename T::MSide>, Walk<typename T::NSide>>;
 // Adds up the partial sums of `splits` workgroups that share a tile, each over
 // its own K steps.  Every workgroup stores its sums in its slot and counts
 // itself; the one that comes last adds the slots in split order (so the result
-// does not depend on the order of arrival), sets the counter back to zero and
-// returns true: it writes the tile.  Nobody waits.  `rows` N rows of the tile
-// are in use.  The slots are stored and loaded at device scope, since the
+// does not depend on the order of arrival) and returns true: it writes the tile.
+// Nobody waits.  The counter starts at zero.  `rows` N rows of the tile are in
+// use.  The slots are stored and loaded at device scope, since the
 // workgroups run on different XCDs.
 constexpr int kScopeDevice = 16;   // sc1
 typedef int32_t i32x4g __attribute__((ext_vector_type(4)));
@@ -518,7 +518,6 @@ __device__ __forceinline__ bool combine_splits(typename T::Acc &acc, float *slot
         *s_flag = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == splits - 1;
     __syncthreads();
     if (!*s_flag) return false;
-    if (tid == 0) __hip_atomic_store(counter, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     typename T::Acc own;
 #pragma unroll
     for (int mt = 0; mt < T::MT; ++mt)

@@ -63,8 +63,10 @@ struct PackArgs {
     SegEntry *segs;       // NULL: no tables
     UTile *tiles;
     int32_t *num_tiles;
+    int32_t *counters;    // of the u product's split K (kCounterWords of them)
     int32_t num_tokens, rank, slices, max_loras, tile_tokens, tiles_cap;
 };
+constexpr int kCounterWords = 1024;   // at least the units of the u product whose K may be split (kSplitUnits / 2)
 
 constexpr int kPackThreads = 256;
 
@@ -75,12 +77,14 @@ __device__ __forceinline__ void split_hi_lo(float v, uint32_t &h, uint32_t &l) {
 
 // buf's rows in sorted order as packed rows, bound by its launch and bytes (13 us
 // for 16384 tokens, 3 slices of rank 128);
-// workgroup 0 also writes the tables when they are asked for.
+// workgroup 0 also writes the tables when they are asked for, and sets the u
+// product's counters to zero.
 __global__ __launch_bounds__(kPackThreads) void pack_kernel(PackArgs a) {
     const bool none = *a.meta.no_lora != 0;
     const int tid = threadIdx.x;
     if (a.segs && blockIdx.x == 0) {
         __shared__ int s_wsum[kPackThreads / kWave];
+        for (int k = tid; k < kCounterWords; k += kPackThreads) a.counters[k] = 0;
         for (int m = tid; m < a.max_loras; m += kPackThreads) a.segs[m] = SegEntry{0, 0};
         __syncthreads();
         constexpr int kPer = (LORA_MAX_LORAS + 1 + kPackThreads - 1) / kPackThreads;
@@ -1079,13 +1083,12 @@ LinearPlan plan_linear(long n, long cols) {
     return p;
 }
 
-constexpr int kCounterWords = 1024;   // at least the units of the u product whose K may be split (kSplitUnits / 2)
-
 struct UPlan {
     int bm, tile_tokens, tiles_cap, splits;
     size_t slot_bytes;
 };
 constexpr long kSplitUnits = 768, kMaxSplits = 8;   // workgroups that a split K is to give
+static_assert(kSplitUnits / 2 <= kCounterWords, "a counter for each unit whose K is split");
 UPlan plan_u(long n, int max_loras, int slices, int rank, long widest) {
     UPlan p;
     p.bm = rank <= 32 ? 32 : rank <= 64 ? 64 : 128;
@@ -1185,6 +1188,7 @@ hipError_t launch_pack(const lora_meta_t *meta, const MetaView &view, const floa
         a.segs = reinterpret_cast<SegEntry *>(ws + l->segs);
         a.tiles = reinterpret_cast<UTile *>(ws + l->tiles);
         a.num_tiles = reinterpret_cast<int32_t *>(ws + l->num_tiles);
+        a.counters = reinterpret_cast<int32_t *>(ws + l->counters);
         a.tiles_cap = u->tiles_cap;
         a.tile_tokens = u->tile_tokens;
     }

@@ -1,4 +1,5 @@
-"""A workspace that is sized for the largest batch serves every smaller one."""
+"""The workspaces of lora_linear and of the loss: one that is sized for the
+largest batch serves every smaller one, whatever it holds."""
 import os
 import sys
 
@@ -55,3 +56,19 @@ def test_a_large_batchs_workspace_serves_small_ones():
         r.forward()
         r.backward()
         loss.check(c, r.outputs())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,widths", [(1, [4104, 72]), (70, [4104, 72]), (300, [2056]), (1500, [72])])
+def test_what_a_linear_workspace_holds_does_not_matter(n, widths):
+    """The same memory serves the loss in between, or holds anything."""
+    c = linear.Case(n=n, hidden=72, widths=widths, rank=16, loras=6)
+    r = linear.Run(c)
+    for held in (0xff, 0x01, None):
+        if held is not None:
+            r.workspace.fill_(held)
+        for t in [r.buf, r.dbuf, r.y, r.dx] + r.da + r.db + r.dbias:
+            t.fill_(float("nan"))
+        r.forward()
+        r.backward()
+        linear.check(c, r.outputs())
