@@ -319,6 +319,8 @@ int lora_prepare_meta_launches(int num_tokens, int max_loras);
  * the shared projection alone); rows of buf of such tokens are not touched.
  * A value that is not finite reaches only what it belongs to: a token's row,
  * an adapter's tokens, a column of w.
+ * An infinite weight gives the infinities of the formula; an infinite s_i[t] may
+ * also make other columns of its token's row NaN.
  *   x       bf16 [num_tokens][ldx]; w bf16 [out_features][ldw] (ldw >= hidden);
  *   w_bias  NULL or bf16 [out_features]; y bf16 [num_tokens][ldy]
  *   bias    NULL, or host array [num_slices] of (NULL | device bf16 [max_loras][width])

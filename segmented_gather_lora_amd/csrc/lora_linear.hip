@@ -16,10 +16,13 @@
 // sums stay in the MFMA accumulators, so y and dx are rounded once and are
 // written once; no pass over y adds the adapters afterwards.
 //
-// s and u are fp32.  They enter the products as two bf16 parts, hi = rne(v)
-// and lo = rne(v - hi) (about 16 mantissa bits together), side by side as 2 r
+// s and u are fp32.  They enter the products as two bf16 parts, hi and
+// lo = rne(v - hi) (to 2^-16 of the value together), side by side as 2 r
 // K elements; a single bf16 part would add an error as large as the result's
-// own rounding, and the ranks are a small share of the work.
+// own rounding, and the ranks are a small share of the work.  hi is the largest
+// bf16 below v in magnitude, so that lo has v's sign and is not zero: an infinite
+// weight times either part is the infinity that it is times v (a nearest hi leaves
+// remainders of 0 or of the other sign, and infinity less infinity).
 //
 // A packed row (one token, one slice) is made of blocks of 32 ranks, [32 hi |
 // 32 lo] each, or of a single block [16 hi | 16 lo] for ranks up to 16; ranks
@@ -71,8 +74,13 @@ constexpr int kCounterWords = 1024;   // at least the units of the u product who
 constexpr int kPackThreads = 256;
 
 __device__ __forceinline__ void split_hi_lo(float v, uint32_t &h, uint32_t &l) {
-    h = float_to_bf16_bits(v);
-    l = (h & 0x7f80u) == 0x7f80u ? 0u : float_to_bf16_bits(v - bf16_bits_to_float(h));   // inf and NaN: hi alone
+    const uint32_t bits = __float_as_uint(v), mag = bits & 0x7fffffffu;
+    if (mag >= 0x7f800000u) {   // inf and NaN: both parts
+        h = l = float_to_bf16_bits(v);
+    } else {
+        h = (bits - (mag != 0u)) >> 16;   // one less in magnitude, cut off
+        l = float_to_bf16_bits(v - bf16_bits_to_float(h));
+    }
 }
 
 // buf's rows in sorted order as packed rows, bound by its launch and bytes (13 us
