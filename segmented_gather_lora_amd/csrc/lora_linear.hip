@@ -246,7 +246,8 @@ struct LinearOp : PlainOp<T> {
     // stage holds: their products are not added), then the ranks of its matrix.
     // H: the half of the step that it fills, or -1 for both.  Lane offsets are 32
     // bits from scalar bases; only a tile across a slice's edge and a block with
-    // ranks past the last take the checked way.
+    // ranks past the last take the checked way.  Those ranks are zeros on both
+    // sides: another rank's weight, which may be infinite, times zero would be NaN.
     template <int H>
     __device__ __forceinline__ void unit(uint32_t at) {
         const int r = a.rank, row_len = a.row_len;
@@ -269,14 +270,18 @@ struct LinearOp : PlainOp<T> {
             // half of the side's instructions hold the half's 32 K rows
             constexpr int kHalf = T::MSide::kInstr / 2, kRows = 64 / T::MSide::kLanesPerK;
             const uint16_t *block = lw + (uint64_t)(uint32_t)(H < 0 ? kb * 32 : 0) * (uint32_t)width;
+            const int ranks = r - (H < 0 ? kb * 32 : 0);
 #pragma unroll
             for (int j = 0; j < kHalf; ++j) {
                 const int i = wave_id() * kHalf + j + (H > 0 ? T::kWaves * kHalf : 0);
                 const int k = i * kRows + lane_id() / T::MSide::kLanesPerK;
-                int rank = H < 0 ? k : k & 15;
-                if (!full) rank = min(rank, r - 1 - (H < 0 ? kb * 32 : 0));
+                const int rank = H < 0 ? k : k & 15;
                 const int c = min(m0 + T::MSide::elem_of(k), width - 8);
-                dma16(block, 2u * (uint32_t)(rank * width + c), at + i * 1024u);
+                const uint32_t offset = 2u * (uint32_t)(rank * width + c);
+                if (full)
+                    dma16(block, offset, at + i * 1024u);
+                else
+                    dma16(rank < ranks ? block + offset / 2 : zero_page, at + i * 1024u);
             }
         } else {        // B_i: rows are the slice's columns, ranks contiguous
             const bool inside = full && m0 >= col && m0 + T::BM <= col + width;
@@ -289,8 +294,8 @@ struct LinearOp : PlainOp<T> {
                     if (inside) {
                         dma16(block, 2u * (uint32_t)(__umul24(row, r) + rank), at + T::MSide::dst(j));
                     } else {
-                        const int c = m0 + row - col, last = r - 8 - (H < 0 ? kb * 32 : 0);
-                        dma16(c >= 0 && c < width ? block + row * r + min(rank, last) : zero_page, at + T::MSide::dst(j));
+                        const int c = m0 + row - col, ranks = r - (H < 0 ? kb * 32 : 0);
+                        dma16(c >= 0 && c < width && rank < ranks ? block + row * r + rank : zero_page, at + T::MSide::dst(j));
                     }
                 }
             }

@@ -48,7 +48,7 @@ SIZES = [(20, 136, [136, 40]), (300, 136, [136, 40]), (2050, 136, [5400, 72]), (
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("n,hidden,widths", SIZES)
-@pytest.mark.parametrize("rank", [16, 32, 128])
+@pytest.mark.parametrize("rank", [8, 16, 24, 32, 72, 128])
 def test_infinite_adapter_weights(n, hidden, widths, rank):
     """One infinite entry of B is an infinite column of y for the adapter's
     tokens, with the sign of s; one of A, an infinite column of dx with the sign of u."""
