@@ -67,14 +67,16 @@ constexpr int kStepK = 64;
 // Zeros that lanes without data read (K tails, rows outside a segment).
 static __device__ __attribute__((aligned(256))) uint16_t zero_page[128];
 
-// 64 lanes x 16 bytes from each lane's `src` to LDS byte `dst` + 16 * lane.
+// 64 lanes x 16 bytes from each lane's `src` to LDS byte `dst` + 16 * lane.  The LDS
+// address goes through M0, named as the operand's register, so that the compiler
+// knows what is written there (s_nop: the wait state between that write and the load).
 __device__ __forceinline__ void dma16(const uint16_t *src, uint32_t dst) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(dst), "v"(src) : "memory");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"{m0}"(dst), "v"(src) : "memory");
 }
 
 // The same from a scalar base and a lane's byte offset.
 __device__ __forceinline__ void dma16(const uint16_t *base, uint32_t offset, uint32_t dst) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst), "v"(offset), "s"(base) : "memory");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(dst), "v"(offset), "s"(base) : "memory");
 }
 
 // Which rows (or K rows) and chunks of a side's stage a lane copies, and where
