@@ -384,7 +384,8 @@ size_t lora_linear_workspace_bytes(int num_tokens, int max_loras, int hidden, co
  *   workspace  device memory, 256-byte aligned, of at least
  *           lora_cross_entropy_workspace_bytes; its contents are ignored
  * A target outside [-1, vocab) counts as ignored and is reported: the first
- * int32 of the workspace is LORA_ERR_ID_RANGE after the call, else 0.
+ * int32 of the workspace is LORA_ERR_ID_RANGE after the call, else 0.  (An empty
+ * batch has no targets and launches nothing: the workspace stays as it was.)
  * Deterministic.
  */
 int lora_cross_entropy(const void *x, int64_t ldx, int num_tokens, int hidden, const void *w, int64_t ldw, int vocab,

@@ -633,7 +633,8 @@ def lora_cross_entropy(x, w, targets, loss, lse, workspace, stream=None) -> None
     lse[t] = logsumexp of x @ w^T, without the logits in memory.  x bf16
     [N][H]; w bf16 [V][H]; targets int32 [N]; loss, lse float32 [N];
     workspace uint8 of lora_cross_entropy_workspace_bytes, whose first int32
-    reports targets outside [-1, V) (LORA_ERR_ID_RANGE; they are ignored)."""
+    reports targets outside [-1, V) (LORA_ERR_ID_RANGE; they are ignored) where
+    there are tokens at all."""
     import torch
     where = "lora_cross_entropy"
     n, h, v = _loss_checks(where, x, w, targets, workspace)

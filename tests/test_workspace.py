@@ -72,3 +72,14 @@ def test_what_a_linear_workspace_holds_does_not_matter(n, widths):
         r.forward()
         r.backward()
         linear.check(c, r.outputs())
+
+
+@pytest.mark.gpu
+def test_an_empty_batch_launches_nothing():
+    """The status of a call without tokens is not written: the workspace stays as it was."""
+    c = loss.Case(n=0, hidden=16, vocab=300)
+    r = loss.Run(c)
+    before = r.workspace.clone()
+    r.forward()
+    torch.cuda.synchronize()
+    assert torch.equal(r.workspace, before)
