@@ -156,7 +156,6 @@ struct Tile {
     static constexpr int kStage = MSide::kBytes + NSide::kBytes;
     static constexpr int kLds = kStages * kStage;
     typedef floatx4 Acc[MT][NT];
-    static constexpr bool kEven = true;           // every wave makes the same copies of a pinned step
 
     __device__ __forceinline__ static int wave_m() { return wave_id() % WM; }
     __device__ __forceinline__ static int wave_n() { return wave_id() / WM; }
@@ -326,7 +325,7 @@ __device__ __forceinline__ void mma_loop(Op &op, int plain, int nsteps, typename
         // groups of a step: one 16-row tile of the N side, half 0 then half 1
         constexpr int G = 2 * T::NT, R = T::kReads, D = T::kLoads;
         constexpr int F = T::NT > 1 ? T::NT * 3 / 4 : 1, L = T::NT + T::NT / 4;
-        constexpr int kInFlight = T::kEven ? D * (L - F) / (G - F) : 0;
+        constexpr int kInFlight = D * (L - F) / (G - F);   // (every wave makes the same copies of a pinned step)
         typename T::Half r0, r1;
         wait_loads_barrier<Op::kLast>();
         T::read(r0, lds, 0);

@@ -70,7 +70,7 @@ struct LogitArgs {
     uint16_t *g;                // [listed token][ldg]
     int64_t ldg;
     float *lost;                // [listed token]: the target's g less its rounded value
-    int32_t num_tokens, hidden, first, rows, vocab;   // piece: vocabulary [first, first + rows)
+    int32_t num_tokens, hidden, first, rows;   // piece: vocabulary [first, first + rows)
     int32_t mtiles, ntiles, group;
 };
 
@@ -169,26 +169,23 @@ __global__ __launch_bounds__(T::kThreads) void logit_kernel(LogitArgs a) {
             const int r = T::n_of(nt);
             if (r >= rows) continue;
             uint16_t *row = a.g + (int64_t)(p0 + r) * a.ldg;
-            constexpr int kStep = T::QUADS ? 2 : 1;
+            static_assert(T::QUADS, "8 consecutive entries a lane");
 #pragma unroll
-            for (int mt = 0; mt < T::MT; mt += kStep) {
+            for (int mt = 0; mt < T::MT; mt += 2) {
                 const int v = m0 + T::m_of(mt);
                 if (v >= a.ldg) continue;
-                float g[4 * kStep];
+                float g[8];
 #pragma unroll
-                for (int x = 0; x < 4 * kStep; ++x) {
+                for (int x = 0; x < 8; ++x) {
                     const float p = exp_of(acc[mt + x / 4][nt][x % 4] - lse[nt]);
                     g[x] = v + x < a.rows ? (p - (v + x == target[nt] ? 1.f : 0.f)) * dl[nt] : 0.f;
                 }
-                if ((unsigned)(target[nt] - v) < 4u * kStep)   // one lane of one piece
+                if ((unsigned)(target[nt] - v) < 8u)   // one lane of one piece
 #pragma unroll
-                    for (int x = 0; x < 4 * kStep; ++x)
+                    for (int x = 0; x < 8; ++x)
                         if (v + x == target[nt]) a.lost[p0 + r] = g[x] - bf16_bits_to_float(float_to_bf16_bits(g[x]));
-                if constexpr (kStep == 2)
-                    *reinterpret_cast<u32x4 *>(row + v) =
-                        u32x4{pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]), pack_bf16(g[4], g[5]), pack_bf16(g[6], g[7])};
-                else
-                    *reinterpret_cast<u32x2g *>(row + v) = u32x2g{pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3])};
+                *reinterpret_cast<u32x4 *>(row + v) =
+                    u32x4{pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]), pack_bf16(g[4], g[5]), pack_bf16(g[6], g[7])};
             }
         }
     }
@@ -525,10 +522,10 @@ enum LossTile { kBig, kMid, kSmall, kRow };
 // (one workgroup each), else 128 x 128 where there are two a CU, else 64 x 64,
 // whose workgroups are short enough for the smallest sizes (a step
 // of 301 tokens by 5003 entries over 264: 59 us with 128 x 128, 47 us); 128 x 32 for few tokens.
-LossTile pick_tile(long m, long n, long splits = 1) {
-    if (n > 128 && ceil_div(m, 256) * ceil_div(n, 256) * splits >= 192) return kBig;
+LossTile pick_tile(long m, long n) {
+    if (n > 128 && ceil_div(m, 256) * ceil_div(n, 256) >= 192) return kBig;
     if (n <= 32) return kRow;
-    return ceil_div(m, 128) * ceil_div(n, 128) * splits >= 384 ? kMid : kSmall;
+    return ceil_div(m, 128) * ceil_div(n, 128) >= 384 ? kMid : kSmall;
 }
 int tile_m(LossTile t) { return t == kBig ? 256 : t == kSmall ? 64 : 128; }
 int tile_n(LossTile t) { return t == kBig ? 256 : t == kMid ? 128 : t == kSmall ? 64 : 32; }
@@ -643,15 +640,18 @@ int check_loss(const void *x, int64_t ldx, int num_tokens, int hidden, const voi
     return LORA_OK;
 }
 
-// Runs F with the tile type of `t` (M side strided: MS, N side: NS).
+// Runs F with the tile type of `t` (M side strided: MS, N side: NS).  The 128 x 32
+// tile is for few tokens on the N side; dw has vocabulary entries there, 256 or more.
 template <bool MS, bool NS, class F>
 hipError_t with_tile(LossTile t, F f) {
     switch (t) {
         case kBig: return f(Tile<256, 256, 4, 2, MS, NS>{});
         case kMid: return f(Tile<128, 128, 2, 2, MS, NS>{});
         case kSmall: return f(Tile<64, 64, 1, 4, MS, NS, 0, 4>{});
-        default: return f(Tile<128, 32, 2, 2, MS, NS, 0, 4>{});
+        case kRow:
+            if constexpr (!NS) return f(Tile<128, 32, 2, 2, MS, NS, 0, 4>{});
     }
+    return hipErrorInvalidValue;
 }
 
 }  // namespace
@@ -688,7 +688,7 @@ int lora_cross_entropy(const void *x, int64_t ldx, int num_tokens, int hidden, c
     a.status = reinterpret_cast<int32_t *>(ws + l.status);
     a.num_tokens = num_tokens;
     a.hidden = hidden;
-    a.rows = a.vocab = vocab;
+    a.rows = vocab;
     a.mtiles = (int)p.mtiles;
     a.ntiles = (int)ceil_div(num_tokens, tile_n(p.logits));
     a.group = 8;
@@ -773,7 +773,6 @@ int lora_cross_entropy_backward(const void *x, int64_t ldx, int num_tokens, int 
             a.hidden = hidden;
             a.first = (int)first;
             a.rows = rows;
-            a.vocab = vocab;
             a.mtiles = (int)ceil_div(rows, tile_m(p.grad));
             a.ntiles = (int)ceil_div(num_tokens, tile_n(p.grad));
             a.group = 8;
