@@ -324,12 +324,14 @@ struct LinearOp : PlainOp<T> {
 
 // The adapters' share of a 64 x 64 tile as fp32 dot products, a lane for its
 // token and 16 of the tile's columns, in place of a step of the K walk for every 32
-// ranks, adapter and slice.  y reads 16 contiguous rows of B a lane and gains from
-// four adapters in a tile on (38 tokens of 26 adapters, 3 slices of rank 80: 160 us
-// with the steps, 38 with the products; 64 tokens of 4, rank 64: 24 and 24).  dx
-// waits for a row of A a rank and gains from about 20 (training step, 88 tokens of
-// 32 adapters, rank 32: 204 us and 164; 64 tokens of 4, 3 slices of rank 128: 134
-// and 236).
+// ranks, adapter and slice.  us with the products and with the steps, for so many
+// adapters in each tile:
+//   y   gains from four on, at every rank (64 tokens by 1024 over 1024): 2: 31, 25;
+//       4: 31, 33; 8: 31, 50 (rank 128); 4: 18, 18; 8: 18, 21 (rank 16)
+//   dx  waits for a row of A a rank and gains from 7 to 24 on (whole backward pass):
+//       12: 39, 40; 20: 39, 44 (rank 16); 12: 61, 59; 20: 62, 75 (rank 64); 16: 198,
+//       233 (3 slices of rank 128); 20: 135, 120; 32: 144, 155 (256 tokens by 2048
+//       over 4096, rank 64)
 template <bool BWD>
 constexpr int kDotSegs = BWD ? 20 : 4;
 template <class T, bool BWD>
@@ -1065,17 +1067,29 @@ constexpr size_t kRound = 256;
 size_t up(size_t v) { return (v + kRound - 1) / kRound * kRound; }
 long ceil_div(long a, long b) { return (a + b - 1) / b; }
 
-enum LinearTile { kBig, kMid, kFlat, kSmall };
+enum LinearTile { kBig, kMid, kSmall };
 struct LinearPlan {
     LinearTile tile;
     int mtiles, ntiles;
 };
 
-// The tile of y or dx (n x cols): the largest of 256 x 256, 128 x 128, 64
-// columns x 128 tokens and 64 x 64 of which there are enough for the GPU's 256
-// CUs (one of the first and third a CU at a time, two of the others; 256 tokens
-// by 6144 columns: 192 of 64 x 128 60 us, 384 of 64 x 64 53 us).  K is not split: joining fp32 partial tiles across XCDs took 22 of the 70 us of a
-// product of 256 tokens by 6144 columns over 4096.
+// The tile of y or dx (n x cols): the largest of 256 x 256, 128 x 128 and 64 x 64
+// of which there are enough for the GPU's 256 CUs (one of the first a CU at a time,
+// two of the others).  The limits lie where few adapters and many, which the host
+// does not know, part.  us of lora_linear over 4096, larger tile and smaller:
+//   256 x 256, 128 x 128
+//     128 tiles (2048 by 4096): 106, 89;  one adapter or 32 of rank 16: 112, 91
+//     160 (2048 by 5120): 112, 120;  128 adapters of rank 64, 3 slices: 366, 263
+//     192 (2048 by 6144): 116, 123;  200 (1100 by 10240), 32 of rank 64: 157, 156
+//   128 x 128, 64 x 64
+//     160 tiles (256 by 10240): 52, 56;  32 adapters of rank 16: 72, 61
+//     192 (129 by 12288): 51, 55;  32 adapters: 87, 57
+//     224 (256 by 14336): 54, 67;  8 adapters of rank 64: 77, 96
+//     240 (520 by 6144): 59, 73;  32 adapters of rank 16: 68, 76
+// 64 columns x 128 tokens is slower than one of its neighbours at every size (192
+// of the last two lists: 65, and 118 with 32 adapters).  K is not split: joining
+// fp32 partial tiles across XCDs took 22 of the 70 us of a product of 256 tokens by
+// 6144 columns over 4096.
 LinearPlan plan_linear(long n, long cols) {
     auto tiles = [&](long bm, long bn) { return ceil_div(cols, bm) * ceil_div(n, bn); };
     LinearPlan p;
@@ -1084,12 +1098,9 @@ LinearPlan plan_linear(long n, long cols) {
     if (n > 128 && tiles(256, 256) >= 192) {
         p.tile = kBig;
         bm = bn = 256;
-    } else if (tiles(128, 128) >= 256) {
+    } else if (tiles(128, 128) >= 224) {
         p.tile = kMid;
         bm = bn = 128;
-    } else if (tiles(64, 128) >= 384) {
-        p.tile = kFlat;
-        bn = 128;
     }
     p.mtiles = (int)ceil_div(cols, bm);
     p.ntiles = (int)ceil_div(n, bn);
@@ -1232,7 +1243,6 @@ hipError_t launch_linear(LinearArgs &a, hipStream_t s) {
     switch (p.tile) {
         case kBig: return launch(Tile<256, 256, 4, 2, BWD, false>{});
         case kMid: return launch(Tile<128, 128, 2, 2, BWD, false>{});
-        case kFlat: return launch(Tile<64, 128, 1, 4, BWD, false, 0, 5>{});
         default: return launch(Tile<64, 64, 1, 4, BWD, false, 0, 4>{});
     }
 }

@@ -14,8 +14,8 @@ import test_loss as loss  # noqa: E402
 LINEAR = {   # (case, results that the tile in question makes)
     "few tokens": (dict(n=20, hidden=264, widths=[136, 40], rank=24, loras=5), ("y", "dx", "s", "u", "da", "db", "dbias")),
     "64 x 64": (dict(n=200, hidden=136, widths=[72, 40], rank=40, loras=3), ("y", "dx", "s", "u", "da", "db", "dbias")),
-    "64 x 128, y": (dict(n=129, hidden=72, widths=[12800, 8], rank=40, loras=7), ("y", "s")),
-    "64 x 128, dx": (dict(n=129, hidden=12808, widths=[40, 24], rank=16, loras=7), ("dx", "u", "da", "db", "dbias")),
+    "64 x 64 in two rounds, y": (dict(n=129, hidden=72, widths=[12800, 8], rank=40, loras=7), ("y", "s")),
+    "64 x 64 in two rounds, dx": (dict(n=129, hidden=12808, widths=[40, 24], rank=16, loras=7), ("dx", "u", "da", "db", "dbias")),
     "128 x 128, y": (dict(n=520, hidden=136, widths=[8000, 200], rank=16, loras=5), ("y", "s")),
     "128 x 128, dx": (dict(n=520, hidden=8200, widths=[72, 64], rank=72, loras=5), ("dx", "u", "da", "db", "dbias")),
     "256 x 256, y": (dict(n=2050, hidden=200, widths=[5400, 72], rank=24, loras=9), ("y", "s")),
