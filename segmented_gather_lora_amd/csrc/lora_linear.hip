@@ -593,9 +593,10 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(LinearArgs a) {
 // Batches of up to kRowsShrinks such workgroups that read up to kRowsBytes of
 // adapters (once a token) take s from the same kernel, packed too: the shrink
 // kernels, which read an adapter once for all of its tokens, need three launches
-// (zeroing, shrink, pack) for that.  517 tokens, 2 slices of rank 8 over 520 (9
-// MB): 8 us against 13; 256 tokens, 3 slices of rank 16 over 4096 (100 MB): 19
-// against 17.
+// (zeroing, shrink, pack) for that.  us of lora_linear this way and that, 4 and 32
+// adapters: 64 MB (512 tokens, rank 16 over 4096) 29, 36 and 32, 36; 96 MB (256
+// tokens, 3 slices) 34, 36 and 42, 37; 2048 workgroups (2048 tokens, rank 16 over
+// 264) 20, 23 and 21, 25; 3000 (1000 tokens, 3 slices) 24, 23 and 26, 23.
 struct RowsArgs {
     const int32_t *ids, *no_lora;   // a batch without adapters has no ids
     const uint16_t *x;
@@ -613,7 +614,7 @@ struct RowsArgs {
     int32_t num_tokens, cols, k, rank, slices, max_loras, row_len;
     float scale;
 };
-constexpr long kRowsShrinks = 1536, kRowsBytes = 32L << 20;
+constexpr long kRowsShrinks = 2048, kRowsBytes = 64L << 20;
 constexpr int kRowsTokens = 32, kRowsWaves = 16, kRowsCols = 32, kRowsThreads = kRowsWaves * kWave;
 constexpr int kRowsRanks = 16, kRowsShrinkWaves = 16;
 
