@@ -518,14 +518,21 @@ long ceil_div(long a, long b) { return (a + b - 1) / b; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 enum LossTile { kBig, kMid, kSmall, kRow };
-// The tile of a product of m by n outputs: 256 x 256 where that fills the CUs
-// (one workgroup each), else 128 x 128 where there are two a CU, else 64 x 64,
-// whose workgroups are short enough for the smallest sizes (a step
-// of 301 tokens by 5003 entries over 264: 59 us with 128 x 128, 47 us); 128 x 32 for few tokens.
+// The tile of a product of m by n outputs: 256 x 256 where 128 x 128, two of which
+// run on a CU, would take a second round; 128 x 128 from 384 tiles on; 64 x 64 below;
+// 128 x 32 for few tokens.  us over 4096, larger tile and smaller:
+//   256 x 256, 128 x 128 (tiles of the latter)
+//     384 (129 tokens by 24576) 85, 76;  512 (2048 by 4096) 87, 82
+//     640 (2048 by 5120) 91, 119;  640 (256 by 40960) 108, 132;  g and dw, 2048 by
+//     5120 over 2048: 120, 147
+//   128 x 128, 64 x 64
+//     300 (301 by 12800) 69, 56;  384 (301 by 16384) 73, 71;  384 (256 by 24576) 77, 87
+//     420 (301 by 17920) 74, 77;  g and dw, 120 (301 by 5003 over 264): 30, 23
 LossTile pick_tile(long m, long n) {
-    if (n > 128 && ceil_div(m, 256) * ceil_div(n, 256) >= 192) return kBig;
     if (n <= 32) return kRow;
-    return ceil_div(m, 128) * ceil_div(n, 128) >= 384 ? kMid : kSmall;
+    const long tiles = ceil_div(m, 128) * ceil_div(n, 128);
+    if (n > 128 && tiles > 512) return kBig;
+    return tiles >= 384 ? kMid : kSmall;
 }
 int tile_m(LossTile t) { return t == kBig ? 256 : t == kSmall ? 64 : 128; }
 int tile_n(LossTile t) { return t == kBig ? 256 : t == kMid ? 128 : t == kSmall ? 64 : 32; }
@@ -553,7 +560,10 @@ LossPlan plan_loss(long n, long hidden, long vocab) {
     p.piece = piece;
     p.grad = pick_tile(piece, n);
     const long steps = piece / kStepK;
-    // dx: K (the piece) is split until the CUs are full
+    // dx: K (the piece) is split until the CUs are full; the tile is the largest that
+    // does so (us of g and dx, 256 x 256, 128 x 128 and 64 x 64: 2048 tokens by 4096 over
+    // 32000 849, 1013, 1553; 100 by 8192 over 32000 285, 263, 316; 301 by 264 over 5003
+    // 45, 35, 29; 600 by 264 over 20000 70, 57, 68)
     auto splits_of = [&](LossTile t) {
         const long tiles = ceil_div(hidden, tile_m(t)) * ceil_div(n > 0 ? n : 1, tile_n(t));
         long s = (t == kBig ? 256 : 512) / tiles;
@@ -581,9 +591,9 @@ size_t largest(size_t a, size_t b) { return a > b ? a : b; }
 // whose plan may need more of them (more vocabulary tiles, larger pieces, a split
 // K): each is a bound on the plans of up to n tokens that grows with n.
 //   stats   128 x 32 and 128 x 128 tiles serve up to 128 tokens, 256 x 256 tiles the
-//           largest batches; other 128 x 128 ones are fewer than 192 tiles of
-//           256 x 256, 64 x 64 ones fewer than 384 of 128 x 128 (tokens times vocabulary
-//           tiles: below 2 * 256 * 192 and 2 * 128 * 384)
+//           largest batches; other 128 x 128 tiles are at most 512, 64 x 64 ones fewer
+//           than 384 of 128 x 128 (tokens times vocabulary tiles: at most 128 * 512, and
+//           below 2 * 128 * 384)
 //   g       a piece is at most the vocabulary, and at most kPieceElems elements or
 //           kPieceMin rows
 //   planes  a split K fills at most 256 workgroups of 256 x 256 or 512 smaller ones, and
@@ -593,7 +603,7 @@ LossLayout loss_layout(const LossPlan &p, long n, long hidden, long vocab, bool 
     const size_t tokens = (size_t)n, whole = (size_t)ceil_div(vocab, 256) * 256;
     size_t stats = tokens * (size_t)ceil_div(vocab, 256);
     stats = largest(stats, least(tokens, 128) * (size_t)ceil_div(vocab, 128));
-    stats = largest(stats, least(tokens * (size_t)ceil_div(vocab, 64), 2 * 256 * 192));
+    stats = largest(stats, least(tokens * (size_t)ceil_div(vocab, 64), 2 * 128 * 384));
     const size_t g = least(tokens * whole, largest((size_t)kPieceElems, tokens * (size_t)kPieceMin));
     const size_t parts = least(kMaxSplits, whole / kStepK / kSplitSteps);
     const size_t planes = largest(tokens, least(tokens * parts, ceil_div((size_t)256 * 256 * 256, hidden)));
