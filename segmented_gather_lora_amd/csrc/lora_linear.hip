@@ -398,10 +398,10 @@ __device__ __forceinline__ void add_dots(const LinearArgs &a, const SliceEntry *
 }
 
 // A tile of y or dx.  16384 tokens, 128 adapters of rank 128: y (10240 columns
-// over 8192) 2.5 ms, dx (8192 over 10240, three slices) 3.3 ms, of which W's
-// product is 2.0 ms each at 1.37 PFLOP/s, bound by power; the rest are the
-// adapters' steps, each a barrier pair and a trip to memory for 32 ranks.  4096
-// tokens by 28672 over 4096: 0.82 ms.
+// over 8192) 2.4 ms, dx (8192 over 10240, three slices) 3.1 ms, of which W's
+// product is about 2.0 ms each; the rest are the adapters' steps, each a barrier
+// pair and a trip to memory for 32 ranks.  4096 tokens by 28672 over 4096, 16
+// adapters of rank 32: y 0.81 ms, dx 0.67 ms (1.19 and 1.43 PFLOP/s of W's product).
 template <class T, bool BWD>
 __global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(LinearArgs a) {
     __shared__ int s_tok[T::BN], s_id[T::BN], s_count;
@@ -669,8 +669,8 @@ __global__ __launch_bounds__(kRowsShrinkWaves *kWave) void rows_shrink_kernel(Ro
 // memory straight into the registers of the MFMA, and the waves' sums are added
 // in wave order through LDS.  A thread adds its column's and token's adapter as
 // a float32 dot product, whose loads travel with the first of W's.
-// One token by 6144 columns over 4096: 13.6 us, W at 3.7 TB/s (its 50 MB alone
-// take 8.6 us, a launch 3).
+// One token by 6144 columns over 4096: 13.8 us, W at 3.6 TB/s (a kernel that reads
+// its 50 MB and does nothing else takes 8.6 us).
 template <int NT>
 __global__ __launch_bounds__(kRowsThreads) void rows_kernel(RowsArgs a) {
     constexpr int kOut = kRowsCols * 16 * NT, kPer = kOut > kRowsThreads ? kOut / kRowsThreads : 1;
@@ -785,7 +785,7 @@ struct UArgs {
 
 // u_i[t] = scale * B_i[m]^T dy_i[t] for one tile of a segment's tokens and one
 // slice: K is the slice's width, all ranks are in the tile.  Bound by dy's and
-// B's bytes: 16384 tokens, 10240 columns, rank 128: 188 us for 670 MB.  Few tiles
+// B's bytes: 16384 tokens, 10240 columns, rank 128: 184 us for 670 MB.  Few tiles
 // split K (joined by the last to arrive) to fill the CUs.
 template <class T>
 __global__ __launch_bounds__(T::kThreads) void u_kernel(UArgs a) {
@@ -865,7 +865,7 @@ struct GradArgs {
 // (M side = s's hi and lo parts, N side = dy columns) over one segment's
 // tokens, one tile of the activation's columns.  An id without tokens gets
 // zeros: every adapter's gradient is written.  128 adapters of 100 tokens, rank
-// 128: dA (3 slices over 8192, 805 MB written) 442 us, dB (335 MB) 227 us.
+// 128: dA (3 slices over 8192, 805 MB written) 423 us, dB (335 MB) 217 us.
 template <class T, bool DA>
 struct GradOp {
     using ASide = typename std::conditional<DA, typename T::MSide, typename T::NSide>::type;   // activations

@@ -19,10 +19,13 @@
 // and the piece's rows of dw.  Only the tokens that count take part: a first
 // launch lists them in order.  g is rounded to bf16 because the matrix
 // products take bf16; its fp32 value is formed from fp32 logits before that.
-// A token's largest entry of g is most often its target's, and its rounding
-// alone then adds as much error to dx and dw as their own rounding: what it
+// The target's is always among a token's largest entries, and its rounding
+// alone can add as much error to dx and dw as their own rounding: what it
 // loses is kept in fp32 and comes back, to dx as one more row of w at the end,
-// to dw as one more K step of the tokens whose target a tile holds.
+// to dw as one more K step of the tokens whose target a tile holds.  The other
+// entries' rounding stays: rms errors of dx and dw are those of their own rounding
+// (0.00166) for flat softmaxes and sure targets, 0.0018 to 0.0020 where one to
+// sixteen wrong entries are 9 to 12 above the rest.
 #include <string.h>
 
 #include <type_traits>
@@ -74,9 +77,9 @@ struct LogitArgs {
     int32_t mtiles, ntiles, group;
 };
 
-// 4096 tokens by 128256 entries over 4096: statistics 3.17 ms (1.36 PFLOP/s, bound
-// by power), g 0.84 ms a piece of 32256; 256 tokens 0.22 ms; 16 tokens 167 us (W
-// at 6.3 TB/s).
+// 4096 tokens by 128256 entries over 4096: statistics 3.11 ms (1.38 PFLOP/s; the
+// library's product without them 3.07), g 0.83 ms a piece of 32256; 256 tokens 0.24
+// ms; 16 tokens 166 us (W at 6.3 TB/s).
 template <class T, bool GRAD>
 __global__ __launch_bounds__(T::kThreads) void logit_kernel(LogitArgs a) {
     __shared__ Stat s_stat[GRAD ? 1 : T::WM][GRAD ? 1 : T::BN];
@@ -202,7 +205,7 @@ struct JoinArgs {
     int32_t num_tokens, mtiles, vocab;
 };
 
-// 16 tokens a workgroup, 64 threads each, eight pairs at a time: 5 to 7 us from 16
+// 16 tokens a workgroup, 64 threads each, eight pairs at a time: 5 to 7 us for 16
 // to 4096 tokens of 128256 entries, mostly latency.
 constexpr int kJoinParts = 64, kJoinTokens = 16, kJoinChunk = 8;
 __global__ __launch_bounds__(kJoinParts *kJoinTokens) void join_kernel(JoinArgs a) {
@@ -311,8 +314,9 @@ struct DxArgs {
     int32_t mtiles, group, splits, split_steps;
 };
 
-// planes[split][p] (+)= sum over the split's vocabulary rows of g[p][v] w[v].  0.74
-// ms a piece of 32256 entries for 3686 tokens over 4096 (1.31 PFLOP/s, by power).
+// planes[split][p] (+)= sum over the split's vocabulary rows of g[p][v] w[v].  0.76
+// ms a piece of 32256 entries for 3686 tokens over 4096 (1.28 PFLOP/s; the library's
+// product of such strides 1.32).
 template <class T>
 __global__ __launch_bounds__(T::kThreads) void dx_kernel(DxArgs a) {
     const int n = *a.count, ntiles = (n + T::BN - 1) / T::BN;
@@ -470,8 +474,9 @@ __device__ __forceinline__ void add_lost(const DwArgs &a, int n, int m0, int v0,
     }
 }
 // dw[v] = sum over the listed tokens of g[p][v] x[p]: both sides have K
-// (the tokens) as their row index.  0.86 ms a piece of 32256 entries for 3686
-// tokens over 4096 (1.13 PFLOP/s: transposing LDS reads for both sides).
+// (the tokens) as their row index.  0.85 ms a piece of 32256 entries for 3686
+// tokens over 4096 (1.15 PFLOP/s: transposing LDS reads for both sides; the
+// library's product of such strides 1.11).
 template <class T>
 __global__ __launch_bounds__(T::kThreads) void dw_kernel(DwArgs a) {
     TileAt at;
