@@ -75,10 +75,16 @@ def algorithmic_bytes(wl) -> dict:
     return out
 
 
+# Sources of kernels that no workload here launches: the counters stay valid when they change.
+NOT_MEASURED = ("lora_gemm.h", "lora_linear.hip", "lora_loss.hip")
+
+
 def kernel_source_hash() -> str:
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "segmented_gather_lora_amd", "csrc")
     for f in sorted(os.listdir(csrc)):
+        if f in NOT_MEASURED:
+            continue
         with open(os.path.join(csrc, f), "rb") as fh:
             h.update(f.encode() + fh.read())
     return h.hexdigest()[:16]
