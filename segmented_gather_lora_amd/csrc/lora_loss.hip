@@ -64,8 +64,9 @@ struct LogitArgs {
     int64_t ldw;
     const int32_t *targets;
     // statistics
-    Stat *stats;                // [vocabulary tile][n]
-    float *target_logit;        // [n]
+    Stat *stats;                // [vocabulary tile][all_tokens]
+    float *target_logit;        // [num_tokens]
+    int32_t all_tokens;         // num_tokens, or more where a launch takes a part of them
     int32_t *status;
     // gradient
     const int32_t *list, *count;   // tokens that count
@@ -152,7 +153,7 @@ __global__ __launch_bounds__(T::kThreads) void logit_kernel(LogitArgs a) {
             Stat s = s_stat[0][r];
 #pragma unroll
             for (int w = 1; w < T::WM; ++w) s = join(s, s_stat[w][r]);
-            a.stats[(int64_t)at.m * a.num_tokens + p0 + r] = s;
+            a.stats[(int64_t)at.m * a.all_tokens + p0 + r] = s;
         }
     } else {
         // all the tokens' values in two round trips
@@ -542,6 +543,11 @@ LossTile pick_tile(long m, long n) {
 int tile_m(LossTile t) { return t == kBig ? 256 : t == kSmall ? 64 : 128; }
 int tile_n(LossTile t) { return t == kBig ? 256 : t == kMid ? 128 : t == kSmall ? 64 : 32; }
 
+// Tiles of a launch, whose threads are fewer than 2^32: past that the forward pass
+// takes the tokens in parts.  (g has at most kPieceElems elements or kPieceMin rows.)
+constexpr long kLaunchTiles = (1L << 32) / 512 - kNumXcd;
+static_assert(kLaunchTiles > LORA_MAX_VOCAB / 64, "a part has a tile of tokens at least");
+
 struct LossPlan {
     LossTile logits, grad, dx, dw;
     long mtiles;         // vocabulary tiles of the statistics
@@ -693,29 +699,35 @@ int lora_cross_entropy(const void *x, int64_t ldx, int num_tokens, int hidden, c
     char *ws = static_cast<char *>(workspace);
     LogitArgs a;
     memset(&a, 0, sizeof a);
-    a.x = static_cast<const uint16_t *>(x);
     a.ldx = ldx;
     a.w = static_cast<const uint16_t *>(w);
     a.ldw = ldw;
-    a.targets = targets;
-    a.stats = reinterpret_cast<Stat *>(ws + l.stats);
-    a.target_logit = reinterpret_cast<float *>(ws + l.target_logit);
     a.status = reinterpret_cast<int32_t *>(ws + l.status);
-    a.num_tokens = num_tokens;
     a.hidden = hidden;
     a.rows = vocab;
     a.mtiles = (int)p.mtiles;
-    a.ntiles = (int)ceil_div(num_tokens, tile_n(p.logits));
     a.group = 8;
-    const unsigned grid = tile_grid((long)a.mtiles * a.ntiles);
-    hipError_t e = with_tile<false, false>(p.logits, [&](auto tile) {
-        using T = decltype(tile);
-        return launch_tiles<logit_kernel<T, false>>(grid, T::kThreads, T::kLds, stream, a);
-    });
-    if (e != hipSuccess) return LORA_ERR_LAUNCH;
+    a.all_tokens = num_tokens;
+    Stat *stats = reinterpret_cast<Stat *>(ws + l.stats);
+    float *target_logit = reinterpret_cast<float *>(ws + l.target_logit);
+    const long part = kLaunchTiles / p.mtiles * tile_n(p.logits);
+    for (long t0 = 0; t0 < num_tokens; t0 += part) {
+        a.x = static_cast<const uint16_t *>(x) + t0 * ldx;
+        a.targets = targets + t0;
+        a.stats = stats + t0;
+        a.target_logit = target_logit + t0;
+        a.num_tokens = (int)(num_tokens - t0 < part ? num_tokens - t0 : part);
+        a.ntiles = (int)ceil_div(a.num_tokens, tile_n(p.logits));
+        const unsigned grid = tile_grid((long)a.mtiles * a.ntiles);
+        const hipError_t e = with_tile<false, false>(p.logits, [&](auto tile) {
+            using T = decltype(tile);
+            return launch_tiles<logit_kernel<T, false>>(grid, T::kThreads, T::kLds, stream, a);
+        });
+        if (e != hipSuccess) return LORA_ERR_LAUNCH;
+    }
     JoinArgs j;
-    j.stats = a.stats;
-    j.target_logit = a.target_logit;
+    j.stats = stats;
+    j.target_logit = target_logit;
     j.targets = targets;
     j.loss = loss;
     j.lse = lse;
