@@ -77,3 +77,20 @@ def test_ids_out_of_range_with_biases(n, widths, loras):
     assert int(r.meta.views()["status"].item()) == linear.lib().LORA_ERR_ID_RANGE
     c.ids = torch.where((given >= 0) & (given < loras), given, torch.full_like(given, -1)).to(torch.int32)
     linear.check(c, got)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,loras", [(1, 3), (20, 4), (64, 12), (300, 6), (2000, 300)])
+def test_batches_prepared_with_their_first_layer(n, loras):
+    """lora_prepare_shrink_expand writes the batch's metadata in its own launch (by
+    id, or sorted by every workgroup); lora_linear and its backward pass go by it."""
+    sgl = linear.lib()
+    c = linear.Case(n=n, hidden=136, widths=[72, 40], rank=16, loras=loras)
+    r = linear.Run(c)
+    r.meta = sgl.LoraMeta(c.loras, c.n)
+    y = torch.zeros(n, sum(c.widths), dtype=torch.bfloat16, device="cuda")
+    first = torch.empty_like(r.buf)
+    sgl.lora_prepare_shrink_expand(c.ids.cuda(), r.x, r.a, r.b, None, first, y, r.meta, c.scale)
+    r.forward()
+    r.backward()
+    linear.check(c, r.outputs())
