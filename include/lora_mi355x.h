@@ -374,8 +374,8 @@ size_t lora_linear_workspace_bytes(int num_tokens, int max_loras, int hidden, co
  *     z[v] = sum_k x[t][k] w[v][k]                       (float32)
  *     lse[t]  = log sum_v exp z[v]
  *     loss[t] = lse[t] - z[targets[t]],  0 for an ignored token (target -1); formed as
- *               (max_v z[v] - z[targets[t]]) + log sum_v exp(z[v] - max), whose digits
- *               do not depend on the size of the logits
+ *               (max_v z[v] - z[targets[t]]) + log sum_v exp(z[v] - max), whose own
+ *               rounding does not grow with the logits
  *     A logit of +inf makes lse +inf (and the loss, but of that entry: NaN); one of
  *     -inf leaves the sum.
  *   x bf16 [num_tokens][ldx]; w bf16 [vocab][ldw]; targets int32 [num_tokens]

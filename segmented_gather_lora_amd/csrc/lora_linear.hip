@@ -1076,10 +1076,11 @@ struct LinearPlan {
 
 // The tile of y or dx (n x cols): the largest of 256 x 256, 128 x 128 and 64 x 64
 // of which there are enough for the GPU's 256 CUs (one of the first a CU at a time,
-// two of the others).  The limits lie where few adapters and many, which the host
-// does not know, part.  us of lora_linear over 4096, larger tile and smaller:
+// two of the others).  The limits lie where batches of few adapters and of many,
+// which the host cannot tell apart, part.  us of lora_linear over 4096, larger tile
+// and smaller, one adapter of rank 16 first:
 //   256 x 256, 128 x 128
-//     128 tiles (2048 by 4096): 106, 89;  one adapter or 32 of rank 16: 112, 91
+//     128 tiles (2048 by 4096): 106, 89;  32 adapters of rank 16: 112, 91
 //     160 (2048 by 5120): 112, 120;  128 adapters of rank 64, 3 slices: 366, 263
 //     192 (2048 by 6144): 116, 123;  200 (1100 by 10240), 32 of rank 64: 157, 156
 //   128 x 128, 64 x 64
