@@ -19,6 +19,11 @@ LINEAR = {   # (case, results that the tile in question makes)
     "128 x 128, y": (dict(n=520, hidden=136, widths=[8000, 200], rank=16, loras=5), ("y", "s")),
     "128 x 128, dx": (dict(n=520, hidden=8200, widths=[72, 64], rank=72, loras=5), ("dx", "u", "da", "db", "dbias")),
     "256 x 256, y": (dict(n=2050, hidden=200, widths=[5400, 72], rank=24, loras=9), ("y", "s")),
+    "256 x 256, y, ranks up to 16": (dict(n=2050, hidden=200, widths=[5400, 72], rank=8, loras=90), ("y", "s")),
+    "256 x 256, y, many slices": (dict(n=2050, hidden=136, widths=[8, 16, 24, 5000, 40, 8, 16, 400], rank=128, loras=30),
+                                  ("y", "s")),
+    "256 x 256, dx, ranks up to 16": (dict(n=2050, hidden=5400, widths=[72, 40], rank=16, loras=90), ("dx", "u")),
+    "256 x 256, dx, many slices": (dict(n=2050, hidden=5400, widths=[8, 16, 24, 72], rank=128, loras=30), ("dx", "u")),
     "256 x 256, dx": (dict(n=2050, hidden=5400, widths=[136, 72], rank=40, loras=9), ("dx", "u", "da", "db", "dbias")),
 }
 
