@@ -165,7 +165,7 @@ def _prepare_quantize(case, seed):
     st = {"case": case, "x": x.to(TYPES[case["type"]])}
     if own:
         import segmented_gather_lora_amd as sgl
-        code_bytes, scale_bytes = sgl.lora_mxfp4_row_bytes(cols)
+        code_bytes, scale_bytes = sgl.lora_mx_row_bytes(cols)
         st["codes"] = torch.empty((rows, code_bytes), dtype=torch.uint8, device=DEVICE)
         st["scales"] = torch.empty((rows, scale_bytes), dtype=torch.uint8, device=DEVICE)
         st["out"] = torch.empty((rows, cols), dtype=torch.bfloat16, device=DEVICE)
@@ -202,7 +202,7 @@ def _prepare_linear(case, seed):
         st["buf"] = torch.empty((len(widths), n, rank), dtype=torch.float32, device=DEVICE)
         st["y"] = torch.empty((n, out), dtype=torch.bfloat16, device=DEVICE)
         st["workspace"] = torch.zeros(
-            sgl.lora_linear_mxfp4_workspace_bytes(n, loras, hidden, out, widths, rank, train),
+            sgl.lora_linear_mx_workspace_bytes(n, loras, hidden, out, widths, rank, train),
             dtype=torch.uint8, device=DEVICE)
         if train:
             st["dbuf"] = torch.empty_like(st["buf"])
@@ -259,19 +259,19 @@ def prepare(case, seed):
 
 def _own_quantize(st):
     import segmented_gather_lora_amd as sgl
-    sgl.lora_mxfp4_quantize(st["x"], st["codes"], st["scales"])
-    sgl.lora_mxfp4_dequantize(st["codes"], st["scales"], st["out"])
+    sgl.lora_mx_quantize(st["x"], st["codes"], st["scales"])
+    sgl.lora_mx_dequantize(st["codes"], st["scales"], st["out"])
     return st["out"]
 
 
 def _own_linear(st):
     import segmented_gather_lora_amd as sgl
-    sgl.lora_linear_mxfp4(st["x"], st["codes"], st["scales"], st["w_bias"], st["a"], st["b"], st["bias"], st["buf"],
+    sgl.lora_linear_mx(st["x"], st["codes"], st["scales"], st["w_bias"], st["a"], st["b"], st["bias"], st["buf"],
                           st["y"], st["meta"], st["scale"], st["workspace"],
                           quantize_x=st["case"]["acts"] == "mxfp4")
     if st["case"]["pass"] == "forward":
         return st["y"]
-    sgl.lora_linear_mxfp4_backward(st["dy"], st["x"], st["codes"], st["scales"], st["a"], st["b"], st["buf"],
+    sgl.lora_linear_mx_backward(st["dy"], st["x"], st["codes"], st["scales"], st["a"], st["b"], st["buf"],
                                    st["dbuf"], st["dx"], st["da"], st["db"], st["dbias"], st["meta"], st["scale"],
                                    st["workspace"])
     return {"y": st["y"], "dx": st["dx"], "da": st["da"], "db": st["db"],
