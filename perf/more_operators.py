@@ -246,7 +246,9 @@ def _prepare_clip(case, seed):
         import segmented_gather_lora_amd as sgl
         groups = loras if case["per_lora"] else 1
         st["norms"] = torch.empty(groups, dtype=torch.float32, device=DEVICE)
-        st["workspace"] = torch.zeros(sgl.lora_clip_gradients_workspace_bytes(grads, groups), dtype=torch.uint8,
+        # buffers of the gradients are made once, and so is the list of them
+        st["held"] = sgl.LoraGradients(grads, out=st["out"])
+        st["workspace"] = torch.zeros(sgl.lora_clip_gradients_workspace_bytes(st["held"], groups), dtype=torch.uint8,
                                       device=DEVICE)
     return st
 
@@ -280,7 +282,7 @@ def _own_linear(st):
 
 def _own_clip(st):
     import segmented_gather_lora_amd as sgl
-    sgl.lora_clip_gradients(st["grads"], st["norms"], st["max_norm"], st["workspace"], out=st["out"])
+    sgl.lora_clip_gradients(st["held"], st["norms"], st["max_norm"], st["workspace"])
     return {"norms": st["norms"], "grads": st["flat"]}
 
 
