@@ -56,6 +56,10 @@ typedef enum lora_status {
 #define LORA_MAX_TOKENS 2097152  /* tokens per batch */
 #define LORA_MAX_VOCAB 16777216  /* rows of a vocabulary matrix */
 #define LORA_MAX_HIDDEN 16777216 /* width of a token in lora_linear and lora_cross_entropy */
+#define LORA_MAX_TENSORS 65536   /* tensors of a call of lora_clip_gradients */
+
+/* Types of numbers, where a call takes more than one. */
+typedef enum lora_type { LORA_BF16 = 0, LORA_F32 = 1 } lora_type_t;
 
 /*
  * Per-batch kernel metadata (LoRAKernelMeta on the "lora_kernel_metadata"
@@ -415,6 +419,98 @@ int lora_cross_entropy_backward(const void *x, int64_t ldx, int num_tokens, int 
  * batches of up to num_tokens tokens: never less than for fewer tokens.  0 if a
  * size is out of range.  Host only. */
 size_t lora_cross_entropy_workspace_bytes(int num_tokens, int hidden, int vocab, int backward);
+
+/*
+ * Numbers in 4 bits with a power of two for every 32 of a row (the microscaled
+ * MXFP4 format: E2M1 codes 0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign, E8M0 powers).
+ * For every block of 32 consecutive numbers of a row (the last one of a row may
+ * hold 8, 16 or 24), max the largest magnitude in it:
+ *     p = floor(log2 max) - 2, at least -127            scale byte = p + 127
+ *     code = x / 2^p to the nearest, ties to the even code, held at +-6
+ * A block of zeros has byte 0; one with an infinity or a NaN has byte 255 (not a
+ * number) and codes 0.
+ *   x       type (LORA_BF16 or LORA_F32) [rows][ldx], rows and x 16-byte aligned;
+ *           cols a multiple of 8, up to LORA_MAX_HIDDEN
+ *   codes   [rows][ldcodes] bytes, two codes a byte, the first in the low half:
+ *           16 bytes a block; ldcodes >= 16 ceil(cols / 32), a multiple of 16;
+ *           16-byte aligned.  What a row's last block has past cols is written as 0.
+ *   scales  [rows][ldscales] bytes, one a block, written up to the next multiple of
+ *           4 (0 past the last block): ldscales >= that, a multiple of 4; 4-byte aligned
+ * rows up to 2^31 - 1; nothing is launched for 0.
+ */
+int lora_mx_quantize(const void *x, int type, int64_t ldx, int64_t rows, int cols, void *codes, int64_t ldcodes,
+                     void *scales, int64_t ldscales, hipStream_t stream);
+
+/* out = code * 2^(byte - 127), exact in either type (a magnitude of 2^128 or more,
+ * from bytes 252 to 254, is infinite); NaN where the byte is 255.  Layouts as for
+ * lora_mx_quantize; what codes and scales hold past cols is not used. */
+int lora_mx_dequantize(const void *codes, int64_t ldcodes, const void *scales, int64_t ldscales, int64_t rows, int cols,
+                       void *out, int type, int64_t ldout, hipStream_t stream);
+
+/*
+ * lora_linear with the shared projection's matrix held in 4 bits: w[o][k] is what
+ * row o of codes and scales ([out_features] rows of `hidden` numbers, as
+ * lora_mx_quantize lays them out) stands for.
+ * With quantize_x the rows of x are rounded to such numbers first, block by block
+ * as lora_mx_quantize rounds them, for the product with w (both of its sides are
+ * 4 bits then); the adapters read x as it is in either case:
+ *     y[t] = w q(x[t]) + w_bias + (slice i's columns) lora_b[i][m] s_i[t] + bias[i][m]
+ *     s_i[t] = buf[i][t] = scale * lora_a[i][m] x[t]
+ * Everything else is as for lora_linear; workspace_bytes is at least what
+ * lora_linear_mx_workspace_bytes gives.  A block of w whose byte is 255 makes its
+ * column of y NaN; a block of x that is not finite, with quantize_x, its token's row.
+ */
+int lora_linear_mx(const void *x, int64_t ldx, int num_tokens, int hidden, const void *codes, int64_t ldcodes,
+                   const void *scales, int64_t ldscales, int out_features, const void *w_bias, const void *const *lora_a,
+                   const void *const *lora_b, const void *const *bias, const int *slice_widths, int num_slices, int rank,
+                   float *buf, void *y, int64_t ldy, int offset_start, const lora_meta_t *meta, float scale,
+                   int quantize_x, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * lora_linear_backward over such a matrix (frozen, as there).  The gradient goes
+ * straight through the rounding of x, if the forward pass rounded it: dx = w^T dy
+ * + the adapters' part either way.
+ */
+int lora_linear_mx_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx, int num_tokens, int hidden,
+                            const void *codes, int64_t ldcodes, const void *scales, int64_t ldscales, int out_features,
+                            const void *const *lora_a, const void *const *lora_b, const int *slice_widths, int num_slices,
+                            int rank, const float *buf, float *dbuf, void *dx, int64_t lddx, void *const *da,
+                            void *const *db, void *const *dbias, int offset_start, const lora_meta_t *meta, float scale,
+                            void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace for batches of up to num_tokens tokens (backward != 0: for
+ * lora_linear_mx_backward too): never less than for fewer tokens.  0 if a size is
+ * out of range.  Host only. */
+size_t lora_linear_mx_workspace_bytes(int num_tokens, int max_loras, int hidden, int out_features, const int *slice_widths,
+                                      int num_slices, int rank, int backward);
+
+/*
+ * The norms of gradients held in many tensors, and the gradients scaled down to a
+ * largest norm.  Every tensor's elements fall into `groups` equal consecutive parts:
+ * one adapter's matrices, where the tensors are da, db and dbias of max_loras
+ * adapters (each is a training of its own) and groups is max_loras, or everything,
+ * with groups 1.  For every group g, over all tensors:
+ *     norms[g] = sqrt(sum of v^2)
+ *     out      = v * min(1, max_norm / (norms[g] + 1e-6)),  rounded once
+ *   grads, out  host arrays [num_tensors] of device pointers, contiguous; out[i] may be
+ *           grads[i] (in place: what is not scaled is not touched); otherwise it
+ *           overlaps no gradient, and no two results overlap (LORA_ERR_BUFFER)
+ *   sizes   host [num_tensors], elements, each a multiple of groups; 0 is allowed
+ *   types   host [num_tensors] of LORA_BF16 or LORA_F32 (aligned to their size only)
+ *   groups  1 .. LORA_MAX_LORAS; norms float32 [groups]
+ *   max_norm  above 0; infinity: nothing is scaled
+ *   workspace  device memory, 256-byte aligned, of at least
+ *           lora_clip_gradients_workspace_bytes; its contents are ignored
+ * A group whose norm is not finite keeps its gradients as they are.  Squares and
+ * sums are double, in a fixed order: deterministic.
+ */
+int lora_clip_gradients(const void *const *grads, void *const *out, const int64_t *sizes, const int *types,
+                        int num_tensors, int groups, double max_norm, float *norms, void *workspace,
+                        size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace of lora_clip_gradients for these tensors.  0 if a size is out of
+ * range.  Host only. */
+size_t lora_clip_gradients_workspace_bytes(const int64_t *sizes, const int *types, int num_tensors, int groups);
 
 /* Static description of a status code. */
 const char *lora_status_string(int status);

@@ -9,13 +9,17 @@ mirror the C ABI in include/lora_mi355x.h:
     lora_shrink_expand_noalloc, lora_linear, lora_linear_backward,
     lora_linear_workspace_bytes, lora_cross_entropy,
     lora_cross_entropy_backward, lora_cross_entropy_workspace_bytes,
+    lora_mx_quantize, lora_mx_dequantize, lora_linear_mx,
+    lora_linear_mx_backward, lora_linear_mx_workspace_bytes,
+    lora_clip_gradients, lora_clip_gradients_workspace_bytes,
     lora_status_string, and the measurement aids
     lora_shrink_expand_launches, lora_prepare_meta_launches, lora_probe_read,
     lora_probe_empty
 
 plus ``LoraMeta``, a holder that owns one device region sized by
 ``lora_meta_bytes`` (LoRAKernelMeta.make on the "lora_kernel_metadata" page)
-and exposes its arrays as tensor views.
+and exposes its arrays as tensor views, and ``LoraGradients``, the tensors of a
+training step's gradients as lora_clip_gradients takes them.
 
 The library is loaded on the first call; that call raises ImportError if the
 library has not been built (``python -m segmented_gather_lora_amd._build``):
@@ -46,11 +50,16 @@ LORA_MAX_LORAS = 1023
 LORA_MAX_SLICES = 8
 LORA_MAX_RANK = 128
 
+LORA_BF16 = 0
+LORA_F32 = 1
+
 EXPORTED = ("lora_meta_bytes", "lora_meta_bind", "lora_prepare_meta", "lora_shrink",
             "lora_expand", "lora_shrink_expand", "lora_prepare_shrink_expand", "lora_shrink_expand_launches",
             "lora_prepare_meta_launches",
             "lora_status_string", "lora_probe_read", "lora_probe_empty", "lora_shrink_expand_noalloc",
             "lora_linear", "lora_linear_backward", "lora_linear_workspace_bytes",
+            "lora_mx_quantize", "lora_mx_dequantize", "lora_linear_mx", "lora_linear_mx_backward",
+            "lora_linear_mx_workspace_bytes", "lora_clip_gradients", "lora_clip_gradients_workspace_bytes",
             "lora_cross_entropy", "lora_cross_entropy_backward", "lora_cross_entropy_workspace_bytes")
 
 
@@ -124,6 +133,22 @@ def _load() -> ctypes.CDLL:
     lib.lora_cross_entropy.argtypes = [P, i64, i32, i32, P, i64, i32, P, P, P, P, Z, P]
     lib.lora_cross_entropy_backward.restype = i32
     lib.lora_cross_entropy_backward.argtypes = [P, i64, i32, i32, P, i64, i32, P, P, P, P, i64, P, i64, P, Z, P]
+    lib.lora_mx_quantize.restype = i32
+    lib.lora_mx_quantize.argtypes = [P, i32, i64, i64, i32, P, i64, P, i64, P]
+    lib.lora_mx_dequantize.restype = i32
+    lib.lora_mx_dequantize.argtypes = [P, i64, P, i64, i64, i32, P, i32, i64, P]
+    lib.lora_linear_mx_workspace_bytes.restype = Z
+    lib.lora_linear_mx_workspace_bytes.argtypes = [i32, i32, i32, i32, P, i32, i32, i32]
+    lib.lora_linear_mx.restype = i32
+    lib.lora_linear_mx.argtypes = [P, i64, i32, i32, P, i64, P, i64, i32, P, P, P, P, P, i32, i32, P, P, i64, i32, META,
+                                   ctypes.c_float, i32, P, Z, P]
+    lib.lora_linear_mx_backward.restype = i32
+    lib.lora_linear_mx_backward.argtypes = [P, i64, P, i64, i32, i32, P, i64, P, i64, i32, P, P, P, i32, i32, P, P, P,
+                                            i64, P, P, P, i32, META, ctypes.c_float, P, Z, P]
+    lib.lora_clip_gradients_workspace_bytes.restype = Z
+    lib.lora_clip_gradients_workspace_bytes.argtypes = [P, P, i32, i32]
+    lib.lora_clip_gradients.restype = i32
+    lib.lora_clip_gradients.argtypes = [P, P, P, P, i32, i32, ctypes.c_double, P, P, Z, P]
     lib.lora_status_string.restype = ctypes.c_char_p
     lib.lora_status_string.argtypes = [i32]
     lib.lora_probe_read.restype = i32
@@ -481,14 +506,14 @@ def _matrix(t, dtype, device: int, shape) -> bool:
     return t.dtype is dtype and t.get_device() == device and t.shape == shape and t.stride(1) == 1
 
 
-def _linear_plain(meta, x, w, wide, lora_a, lora_b, bufs, widths, r: int, workspace, offset_start: int) -> bool:
+def _linear_plain(meta, x, out: int, wide, lora_a, lora_b, bufs, widths, r: int, workspace, offset_start: int) -> bool:
+    """All but the shared projection's matrix, which has `out` rows."""
     import torch
     n, h = x.shape
-    out, device, loras, bf16 = w.shape[0], meta.region.get_device(), lora_a[0].shape[0], torch.bfloat16
+    device, loras, bf16 = meta.region.get_device(), lora_a[0].shape[0], torch.bfloat16
     if not (device >= 0 and n == meta.num_tokens and loras >= meta.max_loras and len(lora_a) == len(lora_b)
             and 0 <= offset_start and offset_start + sum(widths) <= out
-            and _matrix(x, bf16, device, (n, h)) and _matrix(w, bf16, device, (out, h))
-            and _matrix(wide, bf16, device, (n, out)) and workspace.dtype is torch.uint8
+            and _matrix(x, bf16, device, (n, h)) and _matrix(wide, bf16, device, (n, out)) and workspace.dtype is torch.uint8
             and workspace.get_device() == device and workspace.dim() == 1 and workspace.is_contiguous()):
         return False
     for t in bufs:
@@ -500,17 +525,40 @@ def _linear_plain(meta, x, w, wide, lora_a, lora_b, bufs, widths, r: int, worksp
     return True
 
 
-def _projection(where: str, meta, h: int, w, wide, name: str, offset_start: int, widths) -> None:
-    """The shared projection's matrix [out][hidden] and the activations of its
-    output side (y or dy) of at least its columns."""
+def _projection(where: str, meta, h: int, w) -> None:
+    """The shared projection's matrix [out][hidden]."""
     import torch
+    if _matrix(w, torch.bfloat16, meta.region.get_device(), (w.shape[0], h)) and w.is_cuda:
+        return
     _dev(w, torch.bfloat16, meta, where, "w")
     _need(w.dim() == 2 and w.shape[1] == h, LORA_ERR_SHAPE, where, "w must be [out][%d]" % h)
+
+
+def _projected(where: str, meta, out: int, wide, name: str, offset_start: int, widths) -> None:
+    """The activations of the projection's output side (y or dy)."""
+    import torch
     _dev(wide, torch.bfloat16, meta, where, name)
-    _need(wide.dim() == 2 and wide.shape[0] == meta.num_tokens and wide.shape[1] == w.shape[0], LORA_ERR_SHAPE, where,
-          "%s must be [%d][%d]" % (name, meta.num_tokens, w.shape[0]))
-    _need(offset_start >= 0 and offset_start + sum(widths) <= w.shape[0], LORA_ERR_SHAPE, where,
+    _need(wide.dim() == 2 and wide.shape[0] == meta.num_tokens and wide.shape[1] == out, LORA_ERR_SHAPE, where,
+          "%s must be [%d][%d]" % (name, meta.num_tokens, out))
+    _need(offset_start >= 0 and offset_start + sum(widths) <= out, LORA_ERR_SHAPE, where,
           "the slices end past w's rows")
+
+
+def _w_bias(t, out: int, meta, where: str) -> None:
+    import torch
+    if t is not None:
+        _dev(t, torch.bfloat16, meta, where, "w_bias")
+        _need(t.dim() == 1 and t.shape[0] == out, LORA_ERR_SHAPE, where, "w_bias must be [%d]" % out)
+
+
+def _forward_checks(where: str, meta, x, out: int, y, lora_a, lora_b, buf, widths, r: int, workspace,
+                    offset_start: int) -> None:
+    s = len(lora_a)
+    if not _linear_plain(meta, x, out, y, lora_a, lora_b, (buf,), widths, r, workspace, offset_start):
+        _layer_checks(where, meta, x.shape[0], x=x, lora_a=lora_a, lora_b=lora_b, buf=buf, offset_start=offset_start)
+        _need(len(lora_b) == s and buf.shape[0] == s, LORA_ERR_SLICES, where, "one weight per buf slice")
+        _projected(where, meta, out, y, "y", offset_start, widths)
+        _workspace(workspace, meta.region.device, where)
 
 
 def lora_linear(x, w, w_bias, lora_a: Sequence, lora_b: Sequence, bias: Optional[Sequence], buf, y, meta: LoraMeta,
@@ -521,20 +569,14 @@ def lora_linear(x, w, w_bias, lora_a: Sequence, lora_b: Sequence, bias: Optional
     x bf16 [N][H]; w bf16 [out][H]; w_bias None or bf16 [out]; lora_a, lora_b,
     bias, buf as for lora_shrink_expand; y bf16 [N][out]; workspace uint8 of
     lora_linear_workspace_bytes."""
-    import torch
     where = "lora_linear"
     n, h = x.shape
     s, r = len(lora_a), lora_a[0].shape[1]
     widths = [t.shape[1] for t in lora_b]
-    if not _linear_plain(meta, x, w, y, lora_a, lora_b, (buf,), widths, r, workspace, offset_start):
-        _layer_checks(where, meta, n, x=x, lora_a=lora_a, lora_b=lora_b, buf=buf, offset_start=offset_start)
-        _need(len(lora_b) == s and buf.shape[0] == s, LORA_ERR_SLICES, where, "one weight per buf slice")
-        _projection(where, meta, h, w, y, "y", offset_start, widths)
-        _workspace(workspace, meta.region.device, where)
+    _forward_checks(where, meta, x, w.shape[0], y, lora_a, lora_b, buf, widths, r, workspace, offset_start)
+    _projection(where, meta, h, w)
     _bias(bias, widths, meta, where)
-    if w_bias is not None:
-        _dev(w_bias, torch.bfloat16, meta, where, "w_bias")
-        _need(w_bias.dim() == 1 and w_bias.shape[0] == w.shape[0], LORA_ERR_SHAPE, where, "w_bias must be [%d]" % w.shape[0])
+    _w_bias(w_bias, w.shape[0], meta, where)
     _check(_lib().lora_linear(x.data_ptr(), x.stride(0), n, h, w.data_ptr(), w.stride(0), w.shape[0],
                               None if w_bias is None else w_bias.data_ptr(), _ptr_array(lora_a), _ptr_array(lora_b),
                               None if bias is None else _ptr_array(bias), _widths_array(widths), s, r, buf.data_ptr(),
@@ -554,23 +596,15 @@ def _grads(ts, like, meta, where: str, name: str) -> None:
               "%s[%d] must be contiguous %s" % (name, i, tuple(shape)))
 
 
-def lora_linear_backward(dy, x, w, lora_a: Sequence, lora_b: Sequence, buf, dbuf, dx, da: Sequence, db: Sequence,
-                         dbias: Optional[Sequence], meta: LoraMeta, scale: float, workspace, offset_start: int = 0,
-                         stream=None) -> None:
-    """The gradients of lora_linear: dx = dy @ w + the adapters' part (dx may be
-    None), da[i], db[i] and dbias[i] (None: not wanted) like lora_a[i],
-    lora_b[i] and bias[i], zeros for ids without tokens.  buf is the forward
-    pass's; dbuf (like buf) is written: scale * dy_i[t] @ lora_b[i][id_t].
-    Matrices of ids from max_loras on are not touched."""
+def _backward_checks(where: str, meta, dy, x, out: int, lora_a, lora_b, buf, dbuf, dx, da, db, dbias, widths, r: int,
+                     workspace, offset_start: int) -> None:
     import torch
-    where = "lora_linear_backward"
     n, h = x.shape
-    s, r = len(lora_a), lora_a[0].shape[1]
-    widths = [t.shape[1] for t in lora_b]
-    if not _linear_plain(meta, x, w, dy, lora_a, lora_b, (buf, dbuf), widths, r, workspace, offset_start):
+    s = len(lora_a)
+    if not _linear_plain(meta, x, out, dy, lora_a, lora_b, (buf, dbuf), widths, r, workspace, offset_start):
         _layer_checks(where, meta, n, x=x, lora_a=lora_a, lora_b=lora_b, buf=buf)
         _need(len(lora_b) == s and buf.shape[0] == s, LORA_ERR_SLICES, where, "one weight per buf slice")
-        _projection(where, meta, h, w, dy, "dy", offset_start, widths)
+        _projected(where, meta, out, dy, "dy", offset_start, widths)
         _dev(dbuf, torch.float32, meta, where, "dbuf")
         _need(dbuf.shape == buf.shape and dbuf.is_contiguous(), LORA_ERR_SHAPE, where, "dbuf must be contiguous like buf")
         _workspace(workspace, meta.region.device, where)
@@ -584,6 +618,23 @@ def lora_linear_backward(dy, x, w, lora_a: Sequence, lora_b: Sequence, buf, dbuf
         for i, t in enumerate(dbias):
             if t is not None:
                 _grads([t], [lora_b[i].shape[:2]], meta, where, "dbias")
+
+
+def lora_linear_backward(dy, x, w, lora_a: Sequence, lora_b: Sequence, buf, dbuf, dx, da: Sequence, db: Sequence,
+                         dbias: Optional[Sequence], meta: LoraMeta, scale: float, workspace, offset_start: int = 0,
+                         stream=None) -> None:
+    """The gradients of lora_linear: dx = dy @ w + the adapters' part (dx may be
+    None), da[i], db[i] and dbias[i] (None: not wanted) like lora_a[i],
+    lora_b[i] and bias[i], zeros for ids without tokens.  buf is the forward
+    pass's; dbuf (like buf) is written: scale * dy_i[t] @ lora_b[i][id_t].
+    Matrices of ids from max_loras on are not touched."""
+    where = "lora_linear_backward"
+    n, h = x.shape
+    s, r = len(lora_a), lora_a[0].shape[1]
+    widths = [t.shape[1] for t in lora_b]
+    _backward_checks(where, meta, dy, x, w.shape[0], lora_a, lora_b, buf, dbuf, dx, da, db, dbias, widths, r, workspace,
+                     offset_start)
+    _projection(where, meta, h, w)
     _check(_lib().lora_linear_backward(dy.data_ptr(), dy.stride(0), x.data_ptr(), x.stride(0), n, h, w.data_ptr(),
                                        w.stride(0), w.shape[0], _ptr_array(lora_a), _ptr_array(lora_b),
                                        _widths_array(widths), s, r, buf.data_ptr(), dbuf.data_ptr(),
@@ -662,3 +713,215 @@ def lora_cross_entropy_backward(x, w, targets, lse, dloss, dx, dw, workspace, st
                                               None if dx is None else dx.data_ptr(), 0 if dx is None else dx.stride(0),
                                               None if dw is None else dw.data_ptr(), 0 if dw is None else dw.stride(0),
                                               workspace.data_ptr(), workspace.numel(), _stream(stream)), where)
+
+
+def lora_mx_row_bytes(cols: int) -> tuple:
+    """Bytes of a row of `cols` numbers in 4 bits: of its codes, and of its scales."""
+    _need(cols >= 8 and cols % 8 == 0, LORA_ERR_SHAPE, "lora_mx_row_bytes", "cols must be a multiple of 8")
+    blocks = (int(cols) + 31) // 32
+    return 16 * blocks, (blocks + 3) // 4 * 4
+
+
+def _mx_codes(where: str, device, codes, scales, rows: int, cols: int) -> None:
+    import torch
+    code_bytes, scale_bytes = lora_mx_row_bytes(cols)
+    for t, wide, name in ((codes, code_bytes, "codes"), (scales, scale_bytes, "scales")):
+        if t.get_device() == device.index and _matrix(t, torch.uint8, device.index, (rows, wide)):
+            continue
+        if not (t.is_cuda and t.device == device):
+            raise TypeError("%s: %s must be on %s (got %s)" % (where, name, device, t.device))
+        if t.dtype != torch.uint8:
+            raise TypeError("%s: %s must be torch.uint8 (got %s)" % (where, name, t.dtype))
+        _need(t.dim() == 2 and t.shape[0] == rows and t.shape[1] >= wide, LORA_ERR_SHAPE, where,
+              "%s must be [%d][>= %d]" % (name, rows, wide))
+        _need(t.stride(1) == 1, LORA_ERR_SHAPE, where, "%s needs unit stride in its last dimension" % name)
+
+
+def _type(t, where: str, name: str) -> int:
+    import torch
+    if t.dtype is torch.bfloat16:
+        return LORA_BF16
+    if t.dtype is torch.float32:
+        return LORA_F32
+    raise TypeError("%s: %s must be torch.bfloat16 or torch.float32 (got %s)" % (where, name, t.dtype))
+
+
+def _pitch(t) -> int:
+    """Distance of a matrix's rows; of a single row, its length rounded up as the
+    library's checks want it (there is no next row)."""
+    if t.shape[0] > 1:
+        return t.stride(0)
+    return max(t.stride(0), (t.shape[1] + 15) // 16 * 16)
+
+
+def _mx_numbers(where: str, t, name: str) -> None:
+    if not t.is_cuda:
+        raise TypeError("%s: %s must be on a GPU (got %s)" % (where, name, t.device))
+    _need(t.dim() == 2 and (t.stride(1) == 1 or t.numel() <= 1), LORA_ERR_SHAPE, where,
+          "%s must be a matrix with unit stride in its last dimension" % name)
+
+
+def lora_mx_quantize(x, codes, scales, stream=None) -> None:
+    """Rows of x (bf16 or float32 [N][K], K % 8 == 0) to microscaled 4-bit numbers:
+    codes uint8 [N][>= 16 ceil(K / 32)] (row distance a multiple of 16), two a byte,
+    and scales uint8 [N][>= ceil(K / 32), rounded up to 4] (a multiple of 4), a
+    power of two for every 32: the sizes of lora_mx_row_bytes."""
+    where = "lora_mx_quantize"
+    _mx_numbers(where, x, "x")
+    kind = _type(x, where, "x")
+    n, k = x.shape
+    _mx_codes(where, x.device, codes, scales, n, k)
+    _check(_lib().lora_mx_quantize(x.data_ptr(), kind, _pitch(x), n, k, codes.data_ptr(), _pitch(codes),
+                                   scales.data_ptr(), _pitch(scales), _stream(stream)), where)
+
+
+def lora_mx_dequantize(codes, scales, out, stream=None) -> None:
+    """out (bf16 or float32 [N][K]) = the numbers that codes and scales stand for."""
+    where = "lora_mx_dequantize"
+    _mx_numbers(where, out, "out")
+    kind = _type(out, where, "out")
+    n, k = out.shape
+    _mx_codes(where, out.device, codes, scales, n, k)
+    _check(_lib().lora_mx_dequantize(codes.data_ptr(), _pitch(codes), scales.data_ptr(), _pitch(scales), n, k,
+                                     out.data_ptr(), kind, _pitch(out), _stream(stream)), where)
+
+
+def lora_linear_mx_workspace_bytes(num_tokens: int, max_loras: int, hidden: int, out_features: int, widths: Sequence,
+                                   rank: int, backward: bool = False) -> int:
+    """Bytes of the workspace of lora_linear_mx (backward: and of
+    lora_linear_mx_backward) for batches of up to num_tokens tokens: a uint8 device
+    tensor, whose contents do not matter."""
+    n = int(_lib().lora_linear_mx_workspace_bytes(int(num_tokens), int(max_loras), int(hidden), int(out_features),
+                                                  _widths_array(widths), len(widths), int(rank), 1 if backward else 0))
+    if n == 0:
+        raise LoraError(LORA_ERR_SHAPE, "lora_linear_mx_workspace_bytes")
+    return n
+
+
+def lora_linear_mx(x, codes, scales, w_bias, lora_a: Sequence, lora_b: Sequence, bias: Optional[Sequence], buf, y,
+                   meta: LoraMeta, scale: float, workspace, offset_start: int = 0, quantize_x: bool = False,
+                   stream=None) -> None:
+    """lora_linear with the shared projection's matrix [out][H] in microscaled 4-bit
+    numbers: codes and scales as lora_mx_quantize writes them.  quantize_x: x is
+    rounded to such numbers too for the product with that matrix (the adapters read
+    it as it is).  Everything else as for lora_linear; workspace uint8 of
+    lora_linear_mx_workspace_bytes."""
+    where = "lora_linear_mx"
+    n, h = x.shape
+    s, r = len(lora_a), lora_a[0].shape[1]
+    out = codes.shape[0]
+    widths = [t.shape[1] for t in lora_b]
+    _forward_checks(where, meta, x, out, y, lora_a, lora_b, buf, widths, r, workspace, offset_start)
+    _mx_codes(where, meta.region.device, codes, scales, out, h)
+    _bias(bias, widths, meta, where)
+    _w_bias(w_bias, out, meta, where)
+    _check(_lib().lora_linear_mx(x.data_ptr(), x.stride(0), n, h, codes.data_ptr(), _pitch(codes), scales.data_ptr(),
+                                 _pitch(scales), out, None if w_bias is None else w_bias.data_ptr(), _ptr_array(lora_a),
+                                 _ptr_array(lora_b), None if bias is None else _ptr_array(bias), _widths_array(widths), s,
+                                 r, buf.data_ptr(), y.data_ptr(), y.stride(0), int(offset_start),
+                                 ctypes.byref(meta.struct), float(scale), 1 if quantize_x else 0, workspace.data_ptr(),
+                                 workspace.numel(), _stream(stream)), where)
+
+
+def lora_linear_mx_backward(dy, x, codes, scales, lora_a: Sequence, lora_b: Sequence, buf, dbuf, dx, da: Sequence,
+                            db: Sequence, dbias: Optional[Sequence], meta: LoraMeta, scale: float, workspace,
+                            offset_start: int = 0, stream=None) -> None:
+    """lora_linear_backward over such a matrix, which is frozen.  The gradient goes
+    straight through the rounding of x, if the forward pass rounded it."""
+    where = "lora_linear_mx_backward"
+    n, h = x.shape
+    s, r = len(lora_a), lora_a[0].shape[1]
+    out = codes.shape[0]
+    widths = [t.shape[1] for t in lora_b]
+    _backward_checks(where, meta, dy, x, out, lora_a, lora_b, buf, dbuf, dx, da, db, dbias, widths, r, workspace,
+                     offset_start)
+    _mx_codes(where, meta.region.device, codes, scales, out, h)
+    _check(_lib().lora_linear_mx_backward(dy.data_ptr(), dy.stride(0), x.data_ptr(), x.stride(0), n, h, codes.data_ptr(),
+                                          _pitch(codes), scales.data_ptr(), _pitch(scales), out, _ptr_array(lora_a),
+                                          _ptr_array(lora_b), _widths_array(widths), s, r, buf.data_ptr(),
+                                          dbuf.data_ptr(), None if dx is None else dx.data_ptr(),
+                                          0 if dx is None else dx.stride(0), _ptr_array(da), _ptr_array(db),
+                                          None if dbias is None else _ptr_array(dbias), int(offset_start),
+                                          ctypes.byref(meta.struct), float(scale), workspace.data_ptr(),
+                                          workspace.numel(), _stream(stream)), where)
+
+
+class LoraGradients:
+    """The tensors of a training step's gradients (bf16 or float32, contiguous, on one
+    GPU), and of the scaled ones: `out`, tensors like them, or None to scale in
+    place.  Made once for buffers that stay; a call looks whether the tensors have
+    moved."""
+
+    def __init__(self, grads: Sequence, out: Optional[Sequence] = None):
+        self.grads = list(grads)
+        self.out = self.grads if out is None else list(out)
+        self._marshal()
+
+    def _where(self) -> list:
+        return [t.data_ptr() for t in self.grads], None if self.out is self.grads else [t.data_ptr() for t in self.out]
+
+    def _marshal(self) -> None:
+        where, n = "LoraGradients", len(self.grads)
+        _need(len(self.out) == n, LORA_ERR_SHAPE, where, "one result per gradient")
+        self.device = self.grads[0].device if n else None
+        kinds = []
+        for i, (t, o) in enumerate(zip(self.grads, self.out)):
+            if not (t.is_cuda and t.device == self.device and o.device == self.device):
+                raise TypeError("%s: gradient and result %d must be on %s" % (where, i, self.device))
+            kinds.append(_type(t, where, "grads[%d]" % i))
+            if o.dtype != t.dtype:
+                raise TypeError("%s: out[%d] must be %s (got %s)" % (where, i, t.dtype, o.dtype))
+            _need(t.is_contiguous() and o.is_contiguous() and o.shape == t.shape, LORA_ERR_SHAPE, where,
+                  "gradient and result %d must be contiguous and of one shape" % i)
+        self._at = self._where()
+        self._in = (ctypes.c_void_p * n)(*self._at[0])
+        self._out = self._in if self._at[1] is None else (ctypes.c_void_p * n)(*self._at[1])
+        self._sizes = (ctypes.c_int64 * n)(*[t.numel() for t in self.grads])
+        self._types = (ctypes.c_int * n)(*kinds)
+        self._heads = {t.shape[0] if t.dim() else 1 for t in self.grads}
+
+    def _current(self) -> "LoraGradients":
+        if self._where() != self._at:
+            self._marshal()
+        return self
+
+
+def _gradients(grads, out=None) -> LoraGradients:
+    if isinstance(grads, LoraGradients):
+        _need(out is None, LORA_ERR_SHAPE, "lora_clip_gradients", "a LoraGradients holds its results")
+        return grads._current()
+    return LoraGradients(grads, out)
+
+
+def lora_clip_gradients_workspace_bytes(grads, groups: int = 1) -> int:
+    """Bytes of the workspace of lora_clip_gradients for these gradients (a sequence
+    of tensors, or a LoraGradients) and so many norms: a uint8 device tensor, whose
+    contents do not matter."""
+    g = _gradients(grads)
+    n = int(_lib().lora_clip_gradients_workspace_bytes(g._sizes, g._types, len(g.grads), int(groups)))
+    if n == 0:
+        raise LoraError(LORA_ERR_SHAPE, "lora_clip_gradients_workspace_bytes")
+    return n
+
+
+def lora_clip_gradients(grads, norms, max_norm: float, workspace, out: Optional[Sequence] = None, stream=None) -> None:
+    """Norms of gradients over many tensors, and the gradients times
+    min(1, max_norm / (norm + 1e-6)), into `out` (like grads) or in place.  grads: a
+    sequence of bf16 or float32 tensors, or a LoraGradients.  norms float32 [groups]
+    is written: one norm over everything for groups 1, else norms[g] is that of the
+    tensors' entries [g] (the gradients of adapter g: every tensor's first dimension
+    is groups).  max_norm infinity: the norms alone.  A group whose norm is not finite
+    keeps its gradients.  workspace uint8 of lora_clip_gradients_workspace_bytes."""
+    import torch
+    where = "lora_clip_gradients"
+    g = _gradients(grads, out)
+    if not norms.is_cuda or (g.device is not None and norms.device != g.device):
+        raise TypeError("%s: norms must be on one GPU with the gradients (got %s)" % (where, norms.device))
+    _on(norms, torch.float32, norms.device, norms.shape, where, "norms")
+    _need(norms.dim() == 1 and norms.shape[0] >= 1, LORA_ERR_SHAPE, where, "norms must be [groups]")
+    groups = norms.shape[0]
+    _need(groups == 1 or g._heads <= {groups}, LORA_ERR_SHAPE, where,
+          "every gradient's first dimension must be the number of norms, %d" % groups)
+    _workspace(workspace, norms.device, where)
+    _check(_lib().lora_clip_gradients(g._in, g._out, g._sizes, g._types, len(g.grads), groups, float(max_norm),
+                                      norms.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(stream)), where)

@@ -1,5 +1,5 @@
 // lora_gemm.h -- the tile product shared by the kernels of the projection with
-// adapters (lora_linear.hip) and of the vocabulary cross entropy
+// adapters (lora_linear.h) and of the vocabulary cross entropy
 // (lora_loss.hip).
 //
 // A workgroup computes one tile  D[m][n] = sum_k M[m][k] * N[n][k]  on the bf16

@@ -1,0 +1,299 @@
+// lora_mx.hip -- microscaled 4-bit numbers (E2M1 codes with a power of two for
+// every 32 of a row): from and to bfloat16 and float32, and the entry points of the
+// shared projection with adapters whose matrix is held so.
+#include "lora_linear.h"
+
+using namespace lora;
+
+namespace lora {
+namespace {
+
+constexpr int kMxBlock = 32;
+int64_t mx_blocks(int64_t cols) { return (cols + kMxBlock - 1) / kMxBlock; }
+int64_t mx_code_bytes(int64_t cols) { return 16 * mx_blocks(cols); }
+int64_t mx_scale_bytes(int64_t cols) { return (mx_blocks(cols) + 3) / 4 * 4; }
+
+// Sixteen lanes take 128 numbers of a row, 8 each, and with them one dword of
+// scales; a lane's codes are a dword.
+constexpr int kMxThreads = 256, kMxGroup = 16, kMxSpan = 128, kMxPer = 2;
+
+struct MxArgs {
+    char *x, *codes, *scales;            // x: the numbers, read or written
+    int64_t ldx, ldcodes, ldscales;      // bytes
+    int64_t rows;
+    int32_t cols, blocks, spans;         // of a row
+};
+
+// The lane's span: row and number within the row.
+struct MxAt {
+    int64_t row;
+    int32_t span;
+};
+__device__ __forceinline__ MxAt mx_at(int64_t first, int i, int spans) {
+    const int64_t row0 = first / spans;                 // (uniform)
+    const uint32_t in = (uint32_t)(first - row0 * spans) + (uint32_t)i;
+    const uint32_t r = in / (uint32_t)spans;
+    return MxAt{row0 + r, (int32_t)(in - r * (uint32_t)spans)};
+}
+
+// 8 numbers of a row as float bits, zeros past its end (which is a multiple of 8).
+__device__ __forceinline__ void mx_load(const uint16_t *p, bool in, float v[8]) {
+    const u32x4 q = in ? *reinterpret_cast<const u32x4 *>(p) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int x = 0; x < 4; ++x) unpack_bf16(q[x], v[2 * x], v[2 * x + 1]);
+}
+__device__ __forceinline__ void mx_load(const float *p, bool in, float v[8]) {
+    const floatx4 z = {0.f, 0.f, 0.f, 0.f};
+    const floatx4 a = in ? *reinterpret_cast<const floatx4 *>(p) : z, b = in ? *reinterpret_cast<const floatx4 *>(p + 4) : z;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        v[x] = a[x];
+        v[4 + x] = b[x];
+    }
+}
+
+// The scale byte (the power's exponent plus 127) of a block whose largest magnitude
+// has these bits: floor(log2) - 2, 2 being E2M1's largest exponent; 255 (not a
+// number) for a block that is not finite.
+__device__ __forceinline__ int mx_scale_of(uint32_t top) {
+    const int e = (int)(top >> 23);
+    return e == 255 ? 255 : e > 2 ? e - 2 : 0;
+}
+// 8 codes: v over the power (exact, but for what is far below half of the smallest
+// code), to the nearest, ties to even, held at 6.
+__device__ __forceinline__ uint32_t mx_codes_of(const float v[8], int scale) {
+    if (scale == 255) return 0u;
+    const float inv = __uint_as_float((uint32_t)(254 - scale) << 23);
+    uint32_t c = 0;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[0] * inv, v[1] * inv, 1.f, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2] * inv, v[3] * inv, 1.f, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4] * inv, v[5] * inv, 1.f, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6] * inv, v[7] * inv, 1.f, 3);
+    return c;
+}
+
+// Bound by the bytes.
+template <class F>
+__global__ __launch_bounds__(kMxThreads) void quantize_kernel(MxArgs a) {
+    constexpr int kSpans = kMxThreads / kMxGroup;
+    const int l = threadIdx.x % kMxGroup, g = threadIdx.x / kMxGroup;
+    float v[kMxPer][8];
+    MxAt at[kMxPer];
+#pragma unroll
+    for (int q = 0; q < kMxPer; ++q) {
+        at[q] = mx_at((int64_t)blockIdx.x * (kSpans * kMxPer), q * kSpans + g, a.spans);
+        const int k = at[q].span * kMxSpan + 8 * l;
+        mx_load(reinterpret_cast<const F *>(a.x + at[q].row * a.ldx) + k, at[q].row < a.rows && k < a.cols, v[q]);
+    }
+#pragma unroll
+    for (int q = 0; q < kMxPer; ++q) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) top = max(top, __float_as_uint(v[q][x]) & 0x7fffffffu);
+        top = max(top, (uint32_t)__shfl_xor((int)top, 1));
+        top = max(top, (uint32_t)__shfl_xor((int)top, 2));
+        const int scale = mx_scale_of(top), block = at[q].span * 4 + l / 4;
+        const uint32_t codes = mx_codes_of(v[q], scale);
+        // four blocks' bytes to one lane
+        uint32_t s = block < a.blocks ? (uint32_t)scale << 8 * (l / 4) : 0u;
+        s |= (uint32_t)__shfl_xor((int)s, 4);
+        s |= (uint32_t)__shfl_xor((int)s, 8);
+        if (at[q].row >= a.rows) continue;
+        if (block < a.blocks)
+            *reinterpret_cast<uint32_t *>(a.codes + at[q].row * a.ldcodes + at[q].span * 64 + 4 * l) = codes;
+        if (l == 0) *reinterpret_cast<uint32_t *>(a.scales + at[q].row * a.ldscales + at[q].span * 4) = s;
+    }
+}
+
+// Exact in float32 and bfloat16: a code has two bits and every power a place in both
+// (the smallest as a subnormal number).
+template <class F>
+__global__ __launch_bounds__(kMxThreads) void dequantize_kernel(MxArgs a) {
+    constexpr int kSpans = kMxThreads / kMxGroup;
+    const int l = threadIdx.x % kMxGroup, g = threadIdx.x / kMxGroup;
+    uint32_t c[kMxPer], s[kMxPer];
+    MxAt at[kMxPer];
+    bool in[kMxPer];
+#pragma unroll
+    for (int q = 0; q < kMxPer; ++q) {
+        at[q] = mx_at((int64_t)blockIdx.x * (kSpans * kMxPer), q * kSpans + g, a.spans);
+        in[q] = at[q].row < a.rows && at[q].span * kMxSpan + 8 * l < a.cols;
+        c[q] = s[q] = 0;
+        if (in[q]) {
+            c[q] = *reinterpret_cast<const uint32_t *>(a.codes + at[q].row * a.ldcodes + at[q].span * 64 + 4 * l);
+            s[q] = (uint8_t)a.scales[at[q].row * a.ldscales + at[q].span * 4 + l / 4];
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < kMxPer; ++q) {
+        if (!in[q]) continue;
+        F *o = reinterpret_cast<F *>(a.x + at[q].row * a.ldx) + at[q].span * kMxSpan + 8 * l;
+        const float scale = __uint_as_float(s[q] << 23);   // (the conversion reads the exponent alone)
+        const u32x4 b = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[q], scale, 0)),
+                         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[q], scale, 1)),
+                         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[q], scale, 2)),
+                         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[q], scale, 3))};
+        if constexpr (sizeof(F) == 2) {
+            *reinterpret_cast<u32x4 *>(o) = b;
+        } else {
+            float v[8];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) unpack_bf16(b[x], v[2 * x], v[2 * x + 1]);
+            *reinterpret_cast<floatx4 *>(o) = floatx4{v[0], v[1], v[2], v[3]};
+            *reinterpret_cast<floatx4 *>(o + 4) = floatx4{v[4], v[5], v[6], v[7]};
+        }
+    }
+}
+
+int check_codes(const void *codes, int64_t ldcodes, const void *scales, int64_t ldscales, int64_t rows, int64_t cols) {
+    if (rows < 0 || rows > INT32_MAX || cols < 8 || cols % 8 || cols > LORA_MAX_HIDDEN) return LORA_ERR_SHAPE;
+    if (ldcodes < mx_code_bytes(cols) || ldcodes % 16 || ldscales < mx_scale_bytes(cols) || ldscales % 4) return LORA_ERR_SHAPE;
+    if (rows > 0 && (!codes || !scales)) return LORA_ERR_NULL;
+    if (!aligned16(codes) || (reinterpret_cast<uintptr_t>(scales) & 3u) != 0) return LORA_ERR_ALIGN;
+    return LORA_OK;
+}
+
+// The numbers' own checks: bfloat16 or float32 rows.
+int check_numbers(const void *x, int type, int64_t ldx, int64_t rows, int64_t cols) {
+    if (type != LORA_BF16 && type != LORA_F32) return LORA_ERR_SHAPE;
+    if (ldx < cols || ldx % (type == LORA_BF16 ? 8 : 4)) return LORA_ERR_SHAPE;
+    if (rows > 0 && !x) return LORA_ERR_NULL;
+    return aligned16(x) ? LORA_OK : LORA_ERR_ALIGN;
+}
+
+// Rows to (TO) or from codes.
+template <bool TO>
+hipError_t launch_mx(const void *x, int type, int64_t ldx, int64_t rows, int cols, const void *codes, int64_t ldcodes,
+                     const void *scales, int64_t ldscales, hipStream_t s) {
+    MxArgs a;
+    memset(&a, 0, sizeof a);
+    a.cols = cols;
+    a.blocks = (int32_t)mx_blocks(cols);
+    a.spans = (a.blocks + 3) / 4;
+    a.ldx = ldx * (type == LORA_BF16 ? 2 : 4);
+    a.ldcodes = ldcodes;
+    a.ldscales = ldscales;
+    constexpr int kSpans = kMxThreads / kMxGroup * kMxPer;
+    const int64_t most = ((int64_t)1 << 23) * kSpans / a.spans;   // a launch has fewer than 2^32 threads
+    for (int64_t r = 0; r < rows; r += most) {
+        a.rows = rows - r < most ? rows - r : most;
+        a.x = static_cast<char *>(const_cast<void *>(x)) + r * a.ldx;
+        a.codes = static_cast<char *>(const_cast<void *>(codes)) + r * ldcodes;
+        a.scales = static_cast<char *>(const_cast<void *>(scales)) + r * ldscales;
+        const dim3 grid((unsigned)((a.rows * a.spans + kSpans - 1) / kSpans)), block(kMxThreads);
+        if (TO && type == LORA_BF16)
+            hipLaunchKernelGGL(quantize_kernel<uint16_t>, grid, block, 0, s, a);
+        else if (TO)
+            hipLaunchKernelGGL(quantize_kernel<float>, grid, block, 0, s, a);
+        else if (type == LORA_BF16)
+            hipLaunchKernelGGL(dequantize_kernel<uint16_t>, grid, block, 0, s, a);
+        else
+            hipLaunchKernelGGL(dequantize_kernel<float>, grid, block, 0, s, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+// The workspace: that of the bf16 projection, then its matrix and the rounded
+// activations with their codes.
+struct MxLayout {
+    size_t w, x, codes, scales, total;
+};
+MxLayout mx_layout(size_t linear, long n, int hidden, int out) {
+    MxLayout l;
+    l.w = linear;
+    l.x = l.w + up(2 * (size_t)out * hidden);
+    l.codes = l.x + up(2 * (size_t)n * hidden);
+    l.scales = l.codes + up((size_t)n * mx_code_bytes(hidden));
+    l.total = l.scales + up((size_t)n * mx_scale_bytes(hidden));
+    return l;
+}
+
+}  // namespace
+}  // namespace lora
+
+extern "C" {
+
+int lora_mx_quantize(const void *x, int type, int64_t ldx, int64_t rows, int cols, void *codes, int64_t ldcodes,
+                     void *scales, int64_t ldscales, hipStream_t stream) {
+    int st = check_codes(codes, ldcodes, scales, ldscales, rows, cols);
+    if (st || (st = check_numbers(x, type, ldx, rows, cols))) return st;
+    return launch_mx<true>(x, type, ldx, rows, cols, codes, ldcodes, scales, ldscales, stream) == hipSuccess ? LORA_OK
+                                                                                                             : LORA_ERR_LAUNCH;
+}
+
+int lora_mx_dequantize(const void *codes, int64_t ldcodes, const void *scales, int64_t ldscales, int64_t rows, int cols,
+                       void *out, int type, int64_t ldout, hipStream_t stream) {
+    int st = check_codes(codes, ldcodes, scales, ldscales, rows, cols);
+    if (st || (st = check_numbers(out, type, ldout, rows, cols))) return st;
+    return launch_mx<false>(out, type, ldout, rows, cols, codes, ldcodes, scales, ldscales, stream) == hipSuccess
+               ? LORA_OK
+               : LORA_ERR_LAUNCH;
+}
+
+size_t lora_linear_mx_workspace_bytes(int num_tokens, int max_loras, int hidden, int out_features, const int *slice_widths,
+                                      int num_slices, int rank, int backward) {
+    if (check_sizes(num_tokens, max_loras, hidden, slice_widths, num_slices, rank)) return 0;
+    if (out_features < 8 || out_features % 8) return 0;
+    const UPlan u = plan_u(num_tokens, max_loras, num_slices, rank, widest(slice_widths, num_slices));
+    return mx_layout(layout(num_tokens, max_loras, num_slices, rank, u, backward != 0).total, num_tokens, hidden, out_features).total;
+}
+
+int lora_linear_mx(const void *x, int64_t ldx, int num_tokens, int hidden, const void *codes, int64_t ldcodes,
+                   const void *scales, int64_t ldscales, int out_features, const void *w_bias, const void *const *lora_a,
+                   const void *const *lora_b, const void *const *bias, const int *slice_widths, int num_slices, int rank,
+                   float *buf, void *y, int64_t ldy, int offset_start, const lora_meta_t *meta, float scale,
+                   int quantize_x, void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    int st = check_call(ldx, num_tokens, hidden, codes, (hidden + 7) / 8 * 8, out_features, lora_a, lora_b, slice_widths, num_slices,
+                        rank, ldy, offset_start, meta, workspace);
+    if (st) return st;
+    if ((st = check_codes(codes, ldcodes, scales, ldscales, out_features, hidden))) return st;
+    if ((st = check_forward(x, num_tokens, w_bias, bias, num_slices, buf, y))) return st;
+    const UPlan u = plan_u(num_tokens, meta->max_loras, num_slices, rank, widest(slice_widths, num_slices));
+    const Layout l = layout(num_tokens, meta->max_loras, num_slices, rank, u, false);
+    const MxLayout m = mx_layout(l.total, num_tokens, hidden, out_features);
+    if (m.total > workspace_bytes) return LORA_ERR_BUFFER;
+    if (num_tokens == 0) return LORA_OK;
+    char *ws = static_cast<char *>(workspace);
+    if (launch_mx<false>(ws + m.w, LORA_BF16, hidden, out_features, hidden, codes, ldcodes, scales, ldscales, stream) != hipSuccess)
+        return LORA_ERR_LAUNCH;
+    LinearCall c = {x, x, ldx, ldx, ws + m.w, hidden, w_bias, lora_a, lora_b, bias, slice_widths, num_tokens, hidden, out_features,
+                    num_slices, rank, offset_start, meta, scale, ws, stream};
+    if (quantize_x) {
+        const int64_t lc = mx_code_bytes(hidden), ls = mx_scale_bytes(hidden);
+        if (launch_mx<true>(x, LORA_BF16, ldx, num_tokens, hidden, ws + m.codes, lc, ws + m.scales, ls, stream) != hipSuccess ||
+            launch_mx<false>(ws + m.x, LORA_BF16, hidden, num_tokens, hidden, ws + m.codes, lc, ws + m.scales, ls, stream) != hipSuccess)
+            return LORA_ERR_LAUNCH;
+        c.in = ws + m.x;
+        c.ldin = hidden;
+    }
+    return linear_forward(c, l, buf, y, ldy);
+}
+
+int lora_linear_mx_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx, int num_tokens, int hidden,
+                            const void *codes, int64_t ldcodes, const void *scales, int64_t ldscales, int out_features,
+                            const void *const *lora_a, const void *const *lora_b, const int *slice_widths, int num_slices,
+                            int rank, const float *buf, float *dbuf, void *dx, int64_t lddx, void *const *da,
+                            void *const *db, void *const *dbias, int offset_start, const lora_meta_t *meta, float scale,
+                            void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    int st = check_call(ldx, num_tokens, hidden, codes, (hidden + 7) / 8 * 8, out_features, lora_a, lora_b, slice_widths, num_slices,
+                        rank, lddy, offset_start, meta, workspace);
+    if (st) return st;
+    if ((st = check_codes(codes, ldcodes, scales, ldscales, out_features, hidden))) return st;
+    const Gradients g = {dy, lddy, buf, dbuf, dx, lddx, da, db, dbias};
+    if ((st = check_gradients(g, x, num_tokens, hidden, num_slices))) return st;
+    const UPlan u = plan_u(num_tokens, meta->max_loras, num_slices, rank, widest(slice_widths, num_slices));
+    const Layout l = layout(num_tokens, meta->max_loras, num_slices, rank, u, true);
+    const MxLayout m = mx_layout(l.total, num_tokens, hidden, out_features);
+    if (m.total > workspace_bytes) return LORA_ERR_BUFFER;
+    char *ws = static_cast<char *>(workspace);
+    if (dx && num_tokens > 0 &&
+        launch_mx<false>(ws + m.w, LORA_BF16, hidden, out_features, hidden, codes, ldcodes, scales, ldscales, stream) != hipSuccess)
+        return LORA_ERR_LAUNCH;
+    const LinearCall c = {x, x, ldx, ldx, ws + m.w, hidden, nullptr, lora_a, lora_b, nullptr, slice_widths, num_tokens, hidden,
+                          out_features, num_slices, rank, offset_start, meta, scale, ws, stream};
+    return linear_backward(c, l, u, g);
+}
+
+}  // extern "C"
