@@ -51,6 +51,8 @@
 // order them are the explicit ones of the loops.
 #pragma once
 
+#include <type_traits>
+
 #include "lora_internal.h"
 
 namespace lora {
@@ -206,6 +208,80 @@ struct Tile {
     }
 };
 
+// The same tile over microscaled 4-bit numbers on both sides
+// (v_mfma_scale_f32_16x16x128_f8f6f4): a step's 128 bytes of a row are 256 codes, a
+// lane's 16 bytes of a half one block of 32, and the MFMA takes a scale byte a lane
+// for either side.  Everything that moves bytes is the plain tile's.  A step's
+// scales follow its rows in the stage, 512 bytes for every 64 rows of a side:
+// [half][g][l16][t], so that a lane's dword holds its scales of four MFMA tiles (the
+// instruction picks the byte), in that order in memory already (see scale_at).
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+template <class B>
+struct ScaledTile : B {
+    static constexpr int kScales = (B::BM + B::BN) * 8, kScaleAt = B::kStage;   // bytes of a step's scales, where
+    static constexpr int kStage = B::kStage + kScales, kLds = B::kStages * kStage;
+    static constexpr int kMGroups = B::BM / 64, kPieces = kScales / 1024;       // 1 KB a copy
+    static constexpr int NG = (B::NT + 3) / 4;
+    static constexpr int kReads = B::kReads + 1 + NG, kLoads = B::kLoads + 1;
+    static_assert(!B::MS && !B::NS && B::SPLIT == 0 && B::QUADS && B::MT == 4, "64 rows of the M side a wave");
+    static_assert(B::NT % 4 == 0 || B::NT == 1, "whole groups of 64 N rows, or a quarter of one");
+    struct Half : B::Half {
+        uint32_t sm, sn[NG];
+    };
+    // where byte (row r of a 64-row group, block b of the step) is
+    __host__ __device__ static int scale_at(bool m, int r, int b) {
+        const int t = m ? r >> 2 & 3 : r >> 4, l16 = m ? (r >> 4) * 4 + (r & 3) : r & 15;
+        return (b >> 2) * 256 + (b & 3) * 64 + l16 * 4 + t;
+    }
+    __device__ __forceinline__ static uint32_t read_scale(const lds_byte *st, int group, int h) {
+        return *(const __attribute__((address_space(3))) uint32_t *)(st + kScaleAt + group * 512 + h * 256 + lane_id() / 16 * 64 +
+                                                                     (lane_id() & 15) * 4);
+    }
+    __device__ __forceinline__ static void read_one(Half &r, const lds_byte *st, int h, int i) {
+        if (i < B::kReads) {
+            B::read_one(r, st, h, i);
+        } else if (i == B::kReads) {
+            r.sm = read_scale(st, B::wave_m(), h);
+        } else if (B::NT >= 4) {
+            r.sn[i - B::kReads - 1] = read_scale(st, kMGroups + B::wave_n() * NG + (i - B::kReads - 1), h);
+        } else {   // a quarter of a group: its byte moved to the lowest place
+            r.sn[0] = read_scale(st, kMGroups + B::wave_n() / 4, h) >> 8 * (B::wave_n() & 3);
+        }
+    }
+    __device__ __forceinline__ static void read(Half &r, const lds_byte *st, int h) {
+#pragma unroll
+        for (int i = 0; i < kReads; ++i) read_one(r, st, h, i);
+    }
+    template <int MT, int NT>
+    __device__ __forceinline__ static void mma_at(const Half &r, typename B::Acc &acc, int nt) {
+        const u32x4 m = __builtin_bit_cast(u32x4, r.m[MT]), n = __builtin_bit_cast(u32x4, r.n[nt]);
+        const i32x8 mm = __builtin_bit_cast(i32x8, __builtin_shufflevector(m, m, 0, 1, 2, 3, -1, -1, -1, -1));
+        const i32x8 nn = __builtin_bit_cast(i32x8, __builtin_shufflevector(n, n, 0, 1, 2, 3, -1, -1, -1, -1));
+        // 4: E2M1 on that side
+        acc[MT][nt] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mm, nn, acc[MT][nt], 4, 4, MT, (int)r.sm, NT,
+                                                                       (int)r.sn[nt / 4]);
+    }
+    template <int NT>
+    __device__ __forceinline__ static void mma_of(const Half &r, typename B::Acc &acc, int nt) {
+        mma_at<0, NT>(r, acc, nt);
+        mma_at<1, NT>(r, acc, nt);
+        mma_at<2, NT>(r, acc, nt);
+        mma_at<3, NT>(r, acc, nt);
+    }
+    __device__ __forceinline__ static void mma_n(const Half &r, typename B::Acc &acc, int nt) {
+        switch (nt & 3) {
+            case 0: mma_of<0>(r, acc, nt); break;
+            case 1: mma_of<1>(r, acc, nt); break;
+            case 2: mma_of<2>(r, acc, nt); break;
+            default: mma_of<3>(r, acc, nt); break;
+        }
+    }
+    __device__ __forceinline__ static void mma(const Half &r, typename B::Acc &acc) {
+#pragma unroll
+        for (int nt = 0; nt < B::NT; ++nt) mma_n(r, acc, nt);
+    }
+};
+
 // The product into the N rows [lo, hi) of the tile only: no other row's sums
 // are touched, whatever the operands hold.
 template <class T>
@@ -264,6 +340,14 @@ __device__ __forceinline__ void mma_begin(Op &op, int nsteps, unsigned char *lds
     for (int i = 0; i < kAhead<T> && i < nsteps; ++i) op.issue(base + i * T::kStage);
 }
 
+// Whether an op's first main_steps steps are multiplied in a way of their own
+// (op.mma_first): they have a loop of their own then, since a branch between the two
+// costs the registers of a second set of sums.
+template <class Op, class = void>
+struct two_kinds : std::false_type {};
+template <class Op>
+struct two_kinds<Op, std::enable_if_t<Op::kTwoKinds>> : std::true_type {};
+
 // Small tiles: one barrier a step, kStages - 2 steps' copies in flight across it.
 template <class T, class Op>
 __device__ __forceinline__ void ring_loop(Op &op, int plain, int nsteps, typename T::Acc &acc, const lds_byte *lds,
@@ -294,6 +378,22 @@ __device__ __forceinline__ void ring_loop(Op &op, int plain, int nsteps, typenam
         }
         turn();
     }
+    if constexpr (two_kinds<Op>::value)
+        for (; s < op.main_steps; ++s) {
+            if (s + S - 1 <= plain)
+                wait_loads_barrier<(S - 2) * T::kLoads>();
+            else if (s + S - 1 <= nsteps)
+                wait_loads_barrier<(S - 2) * Op::kLast>();
+            else
+                wait_loads_barrier<0>();
+            if (s + S - 1 < nsteps) op.issue(base + to);
+            typename T::Half r0, r1;
+            T::read(r0, lds + cur, 0);
+            T::read(r1, lds + cur, 1);
+            op.mma_first(r0, acc);
+            op.mma_first(r1, acc);
+            turn();
+        }
     for (; s < nsteps; ++s) {
         if (s + S - 1 <= plain)
             wait_loads_barrier<(S - 2) * T::kLoads>();
@@ -355,13 +455,28 @@ __device__ __forceinline__ void mma_loop(Op &op, int plain, int nsteps, typename
             }
         }
     }
-    for (; s < nsteps; ++s) {
-        const uint32_t cur = (uint32_t)(s & 1) * T::kStage;
-        // step s has landed; of step s + 1 the copies that every wave makes last may be in flight
+    // step s has landed; of step s + 1 the copies that every wave makes last may be in flight
+    auto wait = [&] {
         if (s + 1 < nsteps)
             wait_loads_barrier<Op::kLast>();
         else
             wait_loads_barrier<0>();
+    };
+    if constexpr (two_kinds<Op>::value)
+        for (; s < op.main_steps; ++s) {
+            const uint32_t cur = (uint32_t)(s & 1) * T::kStage;
+            wait();
+            typename T::Half r;
+            T::read(r, lds + cur, 0);
+            op.mma_first(r, acc);
+            T::read(r, lds + cur, 1);
+            own_reads_barrier();
+            if (s + 2 < nsteps) op.issue(base + cur);
+            op.mma_first(r, acc);
+        }
+    for (; s < nsteps; ++s) {
+        const uint32_t cur = (uint32_t)(s & 1) * T::kStage;
+        wait();
         typename T::Half r;
         op.read(r, lds + cur, s, 0);
         op.mma(r, acc, s, 0);

@@ -152,6 +152,11 @@ __global__ __launch_bounds__(kPackThreads) void pack_kernel(PackArgs a) {
 
 // ---------------------------------------------------------------- y and dx
 
+// What the shared projection's product reads: bf16 on both sides, or codes of 4 bits
+// on both (the operands' rows then hold 4 codes an element, k counts such elements,
+// and the token rows lie in sorted order already).
+enum Operands { kWide, kCodes };
+
 struct LinearArgs {
     MetaView meta;
     const int32_t *ids;
@@ -169,6 +174,7 @@ struct LinearArgs {
     int64_t ldy;
     int32_t num_tokens, cols, k, rank, slices, max_loras;
     int32_t mtiles, ntiles, group, has_bias, row_len;   // row_len: packed_row(rank)
+    const uint8_t *mscales, *nscales;           // codes: [64 rows][step][512], as ScaledTile reads them
 };
 
 // The adapters' share of a tile's K walk is made of units, for every slice that
@@ -190,9 +196,16 @@ struct SegRow {
 };
 __device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-template <class T, bool BWD>
-struct LinearOp : PlainOp<T> {
+// (codes: the rows of both sides follow one another, so that a lane's place is 32 bits)
+template <class T, Operands O>
+using WalkOp = std::conditional_t<O == kCodes, PairOp<T, OffsetWalk<typename T::MSide>, OffsetWalk<typename T::NSide>>, PlainOp<T>>;
+
+template <class T, bool BWD, Operands O>
+struct LinearOp : WalkOp<T, O> {
+    using Main = WalkOp<T, O>;
     static constexpr int kLast = T::MSide::kInstr / 2;
+    static constexpr bool kTwoKinds = O == kCodes;   // steps that differ in how they are multiplied
+    const uint8_t *scales;     // codes: of this lane's copy in the next step
     const LinearArgs &a;
     const SegRow *segs;        // LDS
     const SliceEntry *slices;  // LDS
@@ -228,8 +241,9 @@ struct LinearOp : PlainOp<T> {
     // are not finite stays without effect on the others in the tile
     // (W's last steps go the same way with all rows: a branch here would cost the
     // registers of a second set of sums)
+    __device__ __forceinline__ void mma_first(const typename T::Half &h, typename T::Acc &acc) { T::mma(h, acc); }
     __device__ __forceinline__ void mma(const typename T::Half &h, typename T::Acc &acc, int s, int half) {
-        const bool all = s < main_steps;
+        const bool all = O == kWide && s < main_steps;
         mma_rows<T>(h, acc, all ? 0 : scalar(mlo), all ? T::BN : munits > 0 ? scalar(mhi) : 0);
         if (!all && (half == 1 || blocks == 0)) {
             --munits;
@@ -241,8 +255,19 @@ struct LinearOp : PlainOp<T> {
             }
         }
     }
+    __device__ __forceinline__ void load(uint32_t at, int i) {
+        if (O == kCodes && i == T::kLoads - 1)
+            load_scales(at);
+        else
+            Main::load(at, i);
+    }
+    __device__ __forceinline__ void load_scales(uint32_t at) {
+        if constexpr (O == kCodes)
+            dma16(reinterpret_cast<const uint16_t *>(scales), at + T::kScaleAt + wave_id() % T::kPieces * 1024u);
+    }
     __device__ __forceinline__ void next() {
-        PlainOp<T>::next();
+        Main::next();
+        if (O == kCodes) scales += 512;
         --main_left;
     }
     // copies of a unit: N rows of its adapter's tokens (other rows keep what the
@@ -314,7 +339,9 @@ struct LinearOp : PlainOp<T> {
     }
     __device__ __forceinline__ void issue(uint32_t at) {
         if (main_left > 0) {
-            PlainOp<T>::issue(at);
+            load_scales(at);
+            if (O == kCodes) scales += 512;
+            Main::issue(at);
             --main_left;
         } else if (blocks) {
             unit<-1>(at);
@@ -405,8 +432,9 @@ __device__ __forceinline__ void add_dots(const LinearArgs &a, const SliceEntry *
 // product is about 2.0 ms each; the rest are the adapters' steps, each a barrier
 // pair and a trip to memory for 32 ranks.  4096 tokens by 28672 over 4096, 16
 // adapters of rank 32: y 0.81 ms, dx 0.67 ms (1.19 and 1.43 PFLOP/s of W's product).
-template <class T, bool BWD>
+template <class T, bool BWD, Operands O>
 __global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(LinearArgs a) {
+    static_assert(!BWD || O == kWide, "the gradient reads W as numbers");
     __shared__ int s_tok[T::BN], s_id[T::BN], s_count;
     __shared__ SegRow s_seg[T::BN];
     __shared__ SliceEntry s_slice[LORA_MAX_SLICES];
@@ -434,27 +462,43 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(LinearArgs a) {
         st = a.meta.start_loc[tid];
         count = a.meta.counts[tid];
     }
-    LinearOp<T, BWD> op(a, s_seg, s_slice);
+    LinearOp<T, BWD, O> op(a, s_seg, s_slice);
     op.m0 = m0;
     op.p0 = p0;
     op.blocks = a.rank <= 16 ? 0 : (a.rank + 31) / 32;
-#pragma unroll
-    for (int j = 0; j < T::NSide::kInstr; ++j)
-        op.wn.p[j] = a.in + (int64_t)token(T::NSide::row(j)) * a.ldin + T::NSide::elem(j);
-    op.wn.step = kStepK;
-    op.wn.left = a.k;
-#pragma unroll
-    for (int j = 0; j < T::MSide::kInstr; ++j) {
-        if (BWD) {
-            const int c = m0 + T::MSide::elem(j);
-            op.wm.p[j] = a.w + (int64_t)T::MSide::row(j) * a.ldw + (c < a.cols ? c : a.cols - 8);
-        } else {
-            op.wm.p[j] = a.w + (int64_t)min(m0 + T::MSide::row(j), a.cols - 1) * a.ldw + T::MSide::elem(j);
-        }
-    }
-    op.wm.step = BWD ? (int64_t)kStepK * a.ldw : kStepK;
-    op.wm.left = a.k;
     const int main = (a.k + kStepK - 1) / kStepK;
+    if constexpr (O == kCodes) {
+        op.wn.base = a.in + (int64_t)p0 * a.ldin;
+#pragma unroll
+        for (int j = 0; j < T::NSide::kInstr; ++j)
+            op.wn.off[j] = 2u * (uint32_t)(min(T::NSide::row(j), rows - 1) * (int)a.ldin + T::NSide::elem(j));
+        op.wm.base = a.w + (int64_t)m0 * a.ldw;
+#pragma unroll
+        for (int j = 0; j < T::MSide::kInstr; ++j)
+            op.wm.off[j] = 2u * ((uint32_t)min(T::MSide::row(j), a.cols - 1 - m0) * (uint32_t)a.ldw + (uint32_t)T::MSide::elem(j));
+        op.wm.step = kStepK;
+        // the copy's 1 KB: two groups of 64 rows, M's groups first
+        const int group = wave_id() % T::kPieces * 2 + lane_id() / 32;
+        op.scales = (group < T::kMGroups ? a.mscales + (int64_t)(m0 / 64 + group) * main * 512
+                                         : a.nscales + (int64_t)(p0 / 64 + group - T::kMGroups) * main * 512) +
+                    (lane_id() & 31) * 16;
+    } else {
+#pragma unroll
+        for (int j = 0; j < T::NSide::kInstr; ++j)
+            op.wn.p[j] = a.in + (int64_t)token(T::NSide::row(j)) * a.ldin + T::NSide::elem(j);
+#pragma unroll
+        for (int j = 0; j < T::MSide::kInstr; ++j) {
+            if (BWD) {
+                const int c = m0 + T::MSide::elem(j);
+                op.wm.p[j] = a.w + (int64_t)T::MSide::row(j) * a.ldw + (c < a.cols ? c : a.cols - 8);
+            } else {
+                op.wm.p[j] = a.w + (int64_t)min(m0 + T::MSide::row(j), a.cols - 1) * a.ldw + T::MSide::elem(j);
+            }
+        }
+        op.wm.step = BWD ? (int64_t)kStepK * a.ldw : kStepK;
+    }
+    op.wn.step = kStepK;
+    op.wm.left = op.wn.left = a.k;
     op.main_left = op.main_steps = main;
     const bool early = main >= kAhead<T>;
     if (early) mma_begin<T>(op, main, g_lds);
@@ -1233,7 +1277,7 @@ hipError_t launch_pack(const lora_meta_t *meta, const MetaView &view, const floa
     return hipGetLastError();
 }
 
-template <bool BWD>
+template <bool BWD, Operands O>
 hipError_t launch_linear(LinearArgs &a, hipStream_t s) {
     const LinearPlan p = plan_linear(a.num_tokens, a.cols);
     a.mtiles = p.mtiles;
@@ -1242,8 +1286,13 @@ hipError_t launch_linear(LinearArgs &a, hipStream_t s) {
     a.row_len = packed_row(a.rank);
     const unsigned grid = tile_grid((long)p.mtiles * p.ntiles);
     auto launch = [&](auto tile) {
-        using T = decltype(tile);
-        return launch_tiles<linear_kernel<T, BWD>>(grid, T::kThreads, T::kLds, s, a);
+        using B = decltype(tile);
+        if constexpr (O == kCodes) {
+            using T = ScaledTile<B>;
+            return launch_tiles<linear_kernel<T, BWD, O>>(grid, T::kThreads, T::kLds, s, a);
+        } else {
+            return launch_tiles<linear_kernel<B, BWD, O>>(grid, B::kThreads, B::kLds, s, a);
+        }
     };
     switch (p.tile) {
         case kBig: return launch(Tile<256, 256, 4, 2, BWD, false>{});
@@ -1290,6 +1339,8 @@ hipError_t launch_grads(GradArgs &a, int max_loras, hipStream_t s) {
 struct LinearCall {
     const void *x, *in;
     int64_t ldx, ldin;
+    const uint8_t *mscales, *nscales;
+    int k;                        // of W's product, in elements of `in` and `w`
     const void *w;
     int64_t ldw;
     const void *w_bias;
@@ -1302,6 +1353,7 @@ struct LinearCall {
     hipStream_t stream;
 };
 
+template <Operands O>
 int linear_forward(const LinearCall &c, const Layout &l, float *buf, void *y, int64_t ldy) {
     const MetaView view = view_of(c.meta);
     uint16_t *packed = reinterpret_cast<uint16_t *>(c.ws + l.s);
@@ -1379,11 +1431,13 @@ int linear_forward(const LinearCall &c, const Layout &l, float *buf, void *y, in
     a.ldy = ldy;
     a.num_tokens = c.num_tokens;
     a.cols = c.out;
-    a.k = c.hidden;
+    a.k = c.k;
+    a.mscales = c.mscales;
+    a.nscales = c.nscales;
     a.rank = c.rank;
     a.slices = c.slices;
     a.max_loras = c.meta->max_loras;
-    return launch_linear<false>(a, c.stream) == hipSuccess ? LORA_OK : LORA_ERR_LAUNCH;
+    return launch_linear<false, O>(a, c.stream) == hipSuccess ? LORA_OK : LORA_ERR_LAUNCH;
 }
 
 // The forward pass' own checks.
@@ -1481,7 +1535,7 @@ int linear_backward(const LinearCall &c, const Layout &l, const UPlan &u, const 
         a.rank = c.rank;
         a.slices = c.slices;
         a.max_loras = c.meta->max_loras;
-        if (launch_linear<true>(a, c.stream) != hipSuccess) return LORA_ERR_LAUNCH;
+        if (launch_linear<true, kWide>(a, c.stream) != hipSuccess) return LORA_ERR_LAUNCH;
     }
     GradArgs g;
     memset(&g, 0, sizeof g);

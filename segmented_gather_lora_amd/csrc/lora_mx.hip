@@ -195,18 +195,94 @@ hipError_t launch_mx(const void *x, int type, int64_t ldx, int64_t rows, int col
     return hipSuccess;
 }
 
-// The workspace: that of the bf16 projection, then its matrix and the rounded
-// activations with their codes.
+// ---------------------------------------------------------------- both sides in 4 bits
+
+// What the product of codes with codes reads beside the matrix' own codes: the rows of
+// x in sorted order as codes, and both sides' scales in the order of ScaledTile's
+// stages, [64 rows][step of 256 numbers][512 bytes].  Bound by x' bytes (the matrix'
+// scales are 1/16 of its codes).
+struct PrepArgs {
+    const uint16_t *x;
+    int64_t ldx;
+    const int32_t *sorted, *no_lora;
+    const uint8_t *scales;
+    int64_t ldscales;
+    uint8_t *codes, *nscales, *mscales;
+    int32_t num_tokens, hidden, out, blocks, steps, x_groups;
+};
+constexpr int kPrepSteps = 8;    // of the matrix' scales, a workgroup
+using AnyScaled = ScaledTile<Tile<64, 64, 1, 4, false, false, 0, 4>>;
+
+__global__ __launch_bounds__(kMxThreads) void prep_kernel(PrepArgs a) {
+    __shared__ __attribute__((aligned(16))) uint8_t s_scale[kPrepSteps * 512];
+    const int tid = threadIdx.x;
+    if ((int)blockIdx.x < a.x_groups * a.steps) {
+        const int group = blockIdx.x / a.steps, step = blockIdx.x % a.steps;
+        const int l = tid % kMxGroup, g = tid / kMxGroup;
+        constexpr int kPer = 64 * 2 / (kMxThreads / kMxGroup);
+        const bool none = *a.no_lora != 0;
+        float v[kPer][8];
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) {
+            const int i = q * (kMxThreads / kMxGroup) + g, p = group * 64 + i / 2, k = step * 256 + i % 2 * 128 + 8 * l;
+            const bool in = p < a.num_tokens && k < a.hidden;
+            const int at = in && !none ? a.sorted[p] : p, t = (unsigned)at < (unsigned)a.num_tokens ? at : 0;
+            mx_load(a.x + t * a.ldx + k, in, v[q]);
+        }
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) {
+            const int i = q * (kMxThreads / kMxGroup) + g, r = i / 2, p = group * 64 + r, b = i % 2 * 4 + l / 4;
+            uint32_t top = 0;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) top = max(top, __float_as_uint(v[q][x]) & 0x7fffffffu);
+            top = max(top, (uint32_t)__shfl_xor((int)top, 1));
+            top = max(top, (uint32_t)__shfl_xor((int)top, 2));
+            const int scale = mx_scale_of(top);
+            if (l % 4 == 0) s_scale[AnyScaled::scale_at(false, r, b)] = (uint8_t)scale;
+            if (p < a.num_tokens && step * 8 + b < a.blocks)
+                *reinterpret_cast<uint32_t *>(a.codes + ((int64_t)p * a.blocks + step * 8 + b) * 16 + l % 4 * 4) = mx_codes_of(v[q], scale);
+        }
+        __syncthreads();
+        if (tid < 32)
+            *reinterpret_cast<u32x4 *>(a.nscales + ((int64_t)group * a.steps + step) * 512 + 16 * tid) =
+                *reinterpret_cast<const u32x4 *>(s_scale + 16 * tid);
+        return;
+    }
+    const int chunks = (a.steps + kPrepSteps - 1) / kPrepSteps, u = blockIdx.x - a.x_groups * a.steps;
+    const int group = u / chunks, step0 = u % chunks * kPrepSteps;
+#pragma unroll
+    for (int q = 0; q < 64 * kPrepSteps * 2 / kMxThreads; ++q) {
+        const int i = q * kMxThreads + tid, r = i / (kPrepSteps * 2), d = i % (kPrepSteps * 2), b = (step0 * 2 + d) * 4;
+        const int64_t row = min(group * 64 + r, a.out - 1);
+        const uint32_t v = b < a.blocks ? *reinterpret_cast<const uint32_t *>(a.scales + row * a.ldscales + b) : 0u;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)   // (past the last block: any power, the codes are zeros there)
+            s_scale[d / 2 * 512 + AnyScaled::scale_at(true, r, d % 2 * 4 + x)] = b + x < a.blocks ? (uint8_t)(v >> 8 * x) : 0;
+    }
+    __syncthreads();
+    if (step0 + tid / 32 < a.steps)
+        *reinterpret_cast<u32x4 *>(a.mscales + ((int64_t)group * a.steps + step0) * 512 + 16 * tid) =
+            *reinterpret_cast<const u32x4 *>(s_scale + 16 * tid);
+}
+
+// ---------------------------------------------------------------- plans
+
+// The workspace: that of the bf16 projection, then its matrix as numbers, the rounded
+// activations and their codes (few tokens), or what prep_kernel writes.
 struct MxLayout {
-    size_t w, x, codes, scales, total;
+    size_t w, x, codes, scales, mscales, total;
+    int steps;
 };
 MxLayout mx_layout(size_t linear, long n, int hidden, int out) {
     MxLayout l;
+    l.steps = (int)((mx_blocks(hidden) + 7) / 8);
+    const size_t groups = (size_t)(n + 255) / 256 * 4, wide = (size_t)(out + 255) / 256 * 4;   // whole tiles
     l.w = linear;
     l.x = l.w + up(2 * (size_t)out * hidden);
-    l.codes = l.x + up(2 * (size_t)n * hidden);
+    l.codes = l.x + up(2 * (size_t)(n < kRowsTokens ? n : kRowsTokens) * hidden);
     l.scales = l.codes + up((size_t)n * mx_code_bytes(hidden));
-    l.total = l.scales + up((size_t)n * mx_scale_bytes(hidden));
+    l.mscales = l.scales + up(groups * l.steps * 512);
+    l.total = l.mscales + up(wide * l.steps * 512);
     return l;
 }
 
@@ -256,10 +332,41 @@ int lora_linear_mx(const void *x, int64_t ldx, int num_tokens, int hidden, const
     if (m.total > workspace_bytes) return LORA_ERR_BUFFER;
     if (num_tokens == 0) return LORA_OK;
     char *ws = static_cast<char *>(workspace);
+    LinearCall c = {x, x, ldx, ldx, nullptr, nullptr, hidden, ws + m.w, hidden, w_bias, lora_a, lora_b, bias, slice_widths, num_tokens,
+                    hidden, out_features, num_slices, rank, offset_start, meta, scale, ws, stream};
+    if (quantize_x && num_tokens > kRowsTokens) {
+        PrepArgs p;
+        memset(&p, 0, sizeof p);
+        const MetaView view = view_of(meta);
+        p.x = static_cast<const uint16_t *>(x);
+        p.ldx = ldx;
+        p.sorted = view.sorted;
+        p.no_lora = view.no_lora;
+        p.scales = static_cast<const uint8_t *>(scales);
+        p.ldscales = ldscales;
+        p.codes = reinterpret_cast<uint8_t *>(ws + m.codes);
+        p.nscales = reinterpret_cast<uint8_t *>(ws + m.scales);
+        p.mscales = reinterpret_cast<uint8_t *>(ws + m.mscales);
+        p.num_tokens = num_tokens;
+        p.hidden = hidden;
+        p.out = out_features;
+        p.blocks = (int)mx_blocks(hidden);
+        p.steps = m.steps;
+        p.x_groups = (int)ceil_div(num_tokens, 64);
+        const long grid = (long)p.x_groups * m.steps + ceil_div(out_features, 64) * ceil_div(m.steps, kPrepSteps);
+        hipLaunchKernelGGL(prep_kernel, dim3((unsigned)grid), dim3(kMxThreads), 0, stream, p);
+        if (hipGetLastError() != hipSuccess) return LORA_ERR_LAUNCH;
+        c.in = p.codes;
+        c.ldin = 8 * (int64_t)p.blocks;
+        c.w = codes;
+        c.ldw = ldcodes / 2;
+        c.k = 8 * p.blocks;
+        c.mscales = p.mscales;
+        c.nscales = p.nscales;
+        return linear_forward<kCodes>(c, l, buf, y, ldy);
+    }
     if (launch_mx<false>(ws + m.w, LORA_BF16, hidden, out_features, hidden, codes, ldcodes, scales, ldscales, stream) != hipSuccess)
         return LORA_ERR_LAUNCH;
-    LinearCall c = {x, x, ldx, ldx, ws + m.w, hidden, w_bias, lora_a, lora_b, bias, slice_widths, num_tokens, hidden, out_features,
-                    num_slices, rank, offset_start, meta, scale, ws, stream};
     if (quantize_x) {
         const int64_t lc = mx_code_bytes(hidden), ls = mx_scale_bytes(hidden);
         if (launch_mx<true>(x, LORA_BF16, ldx, num_tokens, hidden, ws + m.codes, lc, ws + m.scales, ls, stream) != hipSuccess ||
@@ -268,7 +375,7 @@ int lora_linear_mx(const void *x, int64_t ldx, int num_tokens, int hidden, const
         c.in = ws + m.x;
         c.ldin = hidden;
     }
-    return linear_forward(c, l, buf, y, ldy);
+    return linear_forward<kWide>(c, l, buf, y, ldy);
 }
 
 int lora_linear_mx_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx, int num_tokens, int hidden,
@@ -291,7 +398,7 @@ int lora_linear_mx_backward(const void *dy, int64_t lddy, const void *x, int64_t
     if (dx && num_tokens > 0 &&
         launch_mx<false>(ws + m.w, LORA_BF16, hidden, out_features, hidden, codes, ldcodes, scales, ldscales, stream) != hipSuccess)
         return LORA_ERR_LAUNCH;
-    const LinearCall c = {x, x, ldx, ldx, ws + m.w, hidden, nullptr, lora_a, lora_b, nullptr, slice_widths, num_tokens, hidden,
+    const LinearCall c = {x, x, ldx, ldx, nullptr, nullptr, hidden, ws + m.w, hidden, nullptr, lora_a, lora_b, nullptr, slice_widths, num_tokens, hidden,
                           out_features, num_slices, rank, offset_start, meta, scale, ws, stream};
     return linear_backward(c, l, u, g);
 }
