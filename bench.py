@@ -76,7 +76,7 @@ def algorithmic_bytes(wl) -> dict:
 
 
 # Sources of kernels that no workload here launches: the counters stay valid when they change.
-NOT_MEASURED = ("lora_clip.hip", "lora_gemm.h", "lora_linear.h", "lora_linear.hip", "lora_loss.hip", "lora_mx.hip")
+NOT_MEASURED = ("lora_clip.hip", "lora_gemm.h", "lora_linear.h", "lora_linear.hip", "lora_loss.hip", "lora_mx.h", "lora_mx.hip")
 
 
 def kernel_source_hash() -> str:

@@ -216,6 +216,12 @@ struct Tile {
 // [half][g][l16][t], so that a lane's dword holds its scales of four MFMA tiles (the
 // instruction picks the byte), in that order in memory already (see scale_at).
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+template <int MBYTE, int NBYTE>   // which byte of a lane's scales
+__device__ __forceinline__ floatx4 mfma_codes(const u32x4 &m, const u32x4 &n, const floatx4 &c, uint32_t sm, uint32_t sn) {
+    const i32x8 mm = __builtin_bit_cast(i32x8, __builtin_shufflevector(m, m, 0, 1, 2, 3, -1, -1, -1, -1));
+    const i32x8 nn = __builtin_bit_cast(i32x8, __builtin_shufflevector(n, n, 0, 1, 2, 3, -1, -1, -1, -1));
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mm, nn, c, 4, 4, MBYTE, (int)sm, NBYTE, (int)sn);   // 4: E2M1
+}
 template <class B>
 struct ScaledTile : B {
     static constexpr int kScales = (B::BM + B::BN) * 8, kScaleAt = B::kStage;   // bytes of a step's scales, where
@@ -254,12 +260,8 @@ struct ScaledTile : B {
     }
     template <int MT, int NT>
     __device__ __forceinline__ static void mma_at(const Half &r, typename B::Acc &acc, int nt) {
-        const u32x4 m = __builtin_bit_cast(u32x4, r.m[MT]), n = __builtin_bit_cast(u32x4, r.n[nt]);
-        const i32x8 mm = __builtin_bit_cast(i32x8, __builtin_shufflevector(m, m, 0, 1, 2, 3, -1, -1, -1, -1));
-        const i32x8 nn = __builtin_bit_cast(i32x8, __builtin_shufflevector(n, n, 0, 1, 2, 3, -1, -1, -1, -1));
-        // 4: E2M1 on that side
-        acc[MT][nt] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mm, nn, acc[MT][nt], 4, 4, MT, (int)r.sm, NT,
-                                                                       (int)r.sn[nt / 4]);
+        acc[MT][nt] = mfma_codes<MT, NT>(__builtin_bit_cast(u32x4, r.m[MT]), __builtin_bit_cast(u32x4, r.n[nt]), acc[MT][nt], r.sm,
+                                         r.sn[nt / 4]);
     }
     template <int NT>
     __device__ __forceinline__ static void mma_of(const Half &r, typename B::Acc &acc, int nt) {

@@ -34,7 +34,7 @@
 
 #include <type_traits>
 
-#include "lora_gemm.h"
+#include "lora_mx.h"
 
 namespace lora {
 namespace {
@@ -152,10 +152,10 @@ __global__ __launch_bounds__(kPackThreads) void pack_kernel(PackArgs a) {
 
 // ---------------------------------------------------------------- y and dx
 
-// What the shared projection's product reads: bf16 on both sides, or codes of 4 bits
-// on both (the operands' rows then hold 4 codes an element, k counts such elements,
-// and the token rows lie in sorted order already).
-enum Operands { kWide, kCodes };
+// What the shared projection's product reads: bf16 on both sides, W's side as codes of
+// 4 bits, or both as codes (tiles: the operands' rows then hold 4 codes an element, k
+// counts such elements, and the token rows lie in sorted order already).
+enum Operands { kWide, kMixed, kCodes };
 
 struct LinearArgs {
     MetaView meta;
@@ -660,6 +660,8 @@ struct RowsArgs {
     int64_t ldy;
     int32_t num_tokens, cols, k, rank, slices, max_loras, row_len;
     float scale;
+    const uint8_t *scales;       // of W where it is codes (w's rows then hold 4 an element)
+    int64_t ldscales;
 };
 constexpr long kRowsShrinks = 2048, kRowsBytes = 64L << 20;
 constexpr int kRowsTokens = 32, kRowsWaves = 16, kRowsCols = 32, kRowsThreads = kRowsWaves * kWave;
@@ -712,6 +714,60 @@ __global__ __launch_bounds__(kRowsShrinkWaves *kWave) void rows_shrink_kernel(Ro
     }
 }
 
+// What a thread adds to its outputs of few tokens (column c0 + o % 32 of token o / 32,
+// o = thread + 1024 q): the biases and its token's adapter as a float32 dot product.
+template <int PER>
+__device__ __forceinline__ void rows_adapters(const RowsArgs &a, int c0, float (&add)[PER]) {
+    const int tid = threadIdx.x;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+        const int o = tid + q * kRowsThreads, c = c0 + o % kRowsCols, t = o / kRowsCols;
+        add[q] = 0.f;
+        if (t >= a.num_tokens || c >= a.cols) continue;
+        const int none = *a.no_lora, id = a.ids[t];
+        if (a.w_bias) add[q] = bf16_bits_to_float(a.w_bias[c]);
+        if (none || id < 0 || id >= a.max_loras) continue;
+        for (int i = 0; i < a.slices; ++i) {
+            const int in = c - select_slice(a.col, i), width = select_slice(a.width, i);
+            if (in < 0 || in >= width) continue;
+            const uint16_t *b = select_slice(a.lb, i) + ((int64_t)id * width + in) * a.rank;
+            const float *s = a.buf + ((int64_t)i * a.num_tokens + t) * a.rank;
+            float dot = 0.f;
+            for (int j = 0; j < a.rank; j += 8) {
+                const u32x4 v = *reinterpret_cast<const u32x4 *>(b + j);
+                const floatx4 s0 = *reinterpret_cast<const floatx4 *>(s + j), s1 = *reinterpret_cast<const floatx4 *>(s + j + 4);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    float b0, b1;
+                    unpack_bf16(v[x], b0, b1);
+                    dot = fmaf(b0, x < 2 ? s0[2 * x] : s1[2 * x - 4], dot);
+                    dot = fmaf(b1, x < 2 ? s0[2 * x + 1] : s1[2 * x - 3], dot);
+                }
+            }
+            const uint16_t *bias = select_slice(a.bias, i);
+            if (bias) dot += bf16_bits_to_float(bias[(int64_t)id * width + in]);
+            add[q] += dot;
+        }
+    }
+}
+
+// The waves' sums (in s_sum) added in wave order, and what the adapters add, to y.
+template <int NT, int PER>
+__device__ __forceinline__ void rows_store(const RowsArgs &a, int c0, const float (&s_sum)[kRowsWaves][16 * NT][kRowsCols],
+                                           const float (&add)[PER]) {
+    constexpr int kOut = kRowsCols * 16 * NT;
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+        const int o = threadIdx.x + q * kRowsThreads, c = o % kRowsCols, t = o / kRowsCols;
+        if (o >= kOut || t >= a.num_tokens || c0 + c >= a.cols) continue;
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kRowsWaves; ++w) v += s_sum[w][t][c ^ t];
+        a.y[t * a.ldy + c0 + c] = (uint16_t)float_to_bf16_bits(v + add[q]);
+    }
+}
+
 // y: 32 columns a workgroup; its 16 waves share K, every operand goes from
 // memory straight into the registers of the MFMA, and the waves' sums are added
 // in wave order through LDS.  A thread adds its column's and token's adapter as
@@ -752,36 +808,7 @@ __global__ __launch_bounds__(kRowsThreads) void rows_kernel(RowsArgs a) {
     load(k0);
 
     float add[kPer];
-#pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-        const int o = tid + q * kRowsThreads, c = c0 + o % kRowsCols, t = o / kRowsCols;
-        add[q] = 0.f;
-        if (t >= a.num_tokens || c >= a.cols) continue;
-        const int none = *a.no_lora, id = a.ids[t];
-        if (a.w_bias) add[q] = bf16_bits_to_float(a.w_bias[c]);
-        if (none || id < 0 || id >= a.max_loras) continue;
-        for (int i = 0; i < a.slices; ++i) {
-            const int in = c - select_slice(a.col, i), width = select_slice(a.width, i);
-            if (in < 0 || in >= width) continue;
-            const uint16_t *b = select_slice(a.lb, i) + ((int64_t)id * width + in) * a.rank;
-            const float *s = a.buf + ((int64_t)i * a.num_tokens + t) * a.rank;
-            float dot = 0.f;
-            for (int j = 0; j < a.rank; j += 8) {
-                const u32x4 v = *reinterpret_cast<const u32x4 *>(b + j);
-                const floatx4 s0 = *reinterpret_cast<const floatx4 *>(s + j), s1 = *reinterpret_cast<const floatx4 *>(s + j + 4);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    float b0, b1;
-                    unpack_bf16(v[x], b0, b1);
-                    dot = fmaf(b0, x < 2 ? s0[2 * x] : s1[2 * x - 4], dot);
-                    dot = fmaf(b1, x < 2 ? s0[2 * x + 1] : s1[2 * x - 3], dot);
-                }
-            }
-            const uint16_t *bias = select_slice(a.bias, i);
-            if (bias) dot += bf16_bits_to_float(bias[(int64_t)id * width + in]);
-            add[q] += dot;
-        }
-    }
+    rows_adapters(a, c0, add);
 
     for (;;) {
 #pragma unroll
@@ -800,16 +827,95 @@ __global__ __launch_bounds__(kRowsThreads) void rows_kernel(RowsArgs a) {
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int x = 0; x < 4; ++x) s_sum[wave_id()][16 * t + l16][(16 * m + 4 * g + x) ^ (16 * t + l16)] = acc[m][t][x];
-    __syncthreads();
+    rows_store<NT>(a, c0, s_sum, add);
+}
+
+// The same over W's codes.  A lane holds whole blocks of 32: those of W are turned
+// into four bf16 operands each, against x' numbers in the same order, or (BOTH) x'
+// blocks are rounded to codes in the registers and one scaled MFMA takes both.
+// One token by 6144 columns over 4096: 0.0 us, W's 13.4 MB.
+template <int NT, bool BOTH>
+__global__ __launch_bounds__(kRowsThreads) void rows_codes_kernel(RowsArgs a) {
+    constexpr int kOut = kRowsCols * 16 * NT, kPer = kOut > kRowsThreads ? kOut / kRowsThreads : 1;
+    __shared__ float s_sum[kRowsWaves][16 * NT][kRowsCols];   // column c of token t in slot c ^ t: 64 banks
+    const int tid = threadIdx.x, l16 = lane_id() & 15, g = lane_id() >> 4, c0 = blockIdx.x * kRowsCols;
+    const uint8_t *wp[2], *sp[2];
+    const uint16_t *xp[NT];
 #pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-        const int o = tid + q * kRowsThreads, c = o % kRowsCols, t = o / kRowsCols;
-        if (o >= kOut || t >= a.num_tokens || c0 + c >= a.cols) continue;
-        float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < kRowsWaves; ++w) v += s_sum[w][t][c ^ t];
-        a.y[t * a.ldy + c0 + c] = (uint16_t)float_to_bf16_bits(v + add[q]);
+    for (int m = 0; m < 2; ++m) {
+        const int64_t row = min(c0 + 16 * m + l16, a.cols - 1);
+        wp[m] = reinterpret_cast<const uint8_t *>(a.w + row * a.ldw);
+        sp[m] = a.scales + row * a.ldscales;
     }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) xp[t] = a.x + (int64_t)min(16 * t + l16, a.num_tokens - 1) * a.ldx;
+    floatx4 acc[2][NT];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[m][t] = floatx4{0.f, 0.f, 0.f, 0.f};
+
+    // the wave's K: chunks of 4 blocks wave, wave + 16, ..., two at a time (what 128 registers hold)
+    constexpr int kChunk = 2 / NT, kStride = kRowsWaves * 4;
+    u32x4 wv[kChunk][2], xv[kChunk][NT][4];
+    uint32_t sv[kChunk][2];
+    auto load = [&](int b0) {
+#pragma unroll
+        for (int q = 0; q < kChunk; ++q) {
+            const int b = b0 + q * kStride + g;
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const bool in = b * kMxBlock < a.k;
+                wv[q][m] = in ? *reinterpret_cast<const u32x4 *>(wp[m] + 16 * (int64_t)b) : u32x4{0u, 0u, 0u, 0u};
+                sv[q][m] = in ? sp[m][b] : 0u;
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    xv[q][t][j] = b * kMxBlock + 8 * j < a.k ? *reinterpret_cast<const u32x4 *>(xp[t] + b * kMxBlock + 8 * j)
+                                                             : u32x4{0u, 0u, 0u, 0u};
+        }
+    };
+    int b0 = wave_id() * 4;
+    load(b0);
+
+    float add[kPer];
+    rows_adapters(a, c0, add);
+
+    for (;;) {
+#pragma unroll
+        for (int q = 0; q < kChunk; ++q) {
+            if constexpr (BOTH) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    u32x4 xc;
+                    const int scale = mx_block_codes(xv[q][t], xc);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) acc[m][t] = mfma_codes<0, 0>(wv[q][m], xc, acc[m][t], sv[q][m], (uint32_t)scale);
+                }
+            } else {
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const bf16x8 w = as_bf16x8(mx_numbers(wv[q][m][j], sv[q][m]));
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) acc[m][t] = mfma16x16x32(w, as_bf16x8(xv[q][t][j]), acc[m][t]);
+                    }
+            }
+        }
+        b0 += kChunk * kStride;
+        if (b0 * kMxBlock >= a.k) break;
+        load(b0);
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) s_sum[wave_id()][16 * t + l16][(16 * m + 4 * g + x) ^ (16 * t + l16)] = acc[m][t][x];
+    rows_store<NT>(a, c0, s_sum, add);
 }
 
 // ---------------------------------------------------------------- u
@@ -1340,6 +1446,7 @@ struct LinearCall {
     const void *x, *in;
     int64_t ldx, ldin;
     const uint8_t *mscales, *nscales;
+    int64_t ldscales;
     int k;                        // of W's product, in elements of `in` and `w`
     const void *w;
     int64_t ldw;
@@ -1392,13 +1499,16 @@ int linear_forward(const LinearCall &c, const Layout &l, float *buf, void *y, in
         hipLaunchKernelGGL(rows_shrink_kernel, dim3((unsigned)shrinks), dim3(kRowsShrinkWaves * kWave), 0, c.stream, r);
         if (hipGetLastError() != hipSuccess) return LORA_ERR_LAUNCH;
         if (few) {
-            r.x = static_cast<const uint16_t *>(c.in);
-            r.ldx = c.ldin;
+            r.scales = c.mscales;
+            r.ldscales = c.ldscales;
             const dim3 grid((unsigned)ceil_div(c.out, kRowsCols)), block(kRowsThreads);
-            if (c.num_tokens <= 16)
-                hipLaunchKernelGGL(rows_kernel<1>, grid, block, 0, c.stream, r);
+            auto launch = [&](auto one, auto two) {
+                hipLaunchKernelGGL(c.num_tokens <= 16 ? one : two, grid, block, 0, c.stream, r);
+            };
+            if constexpr (O == kWide)
+                launch(rows_kernel<1>, rows_kernel<2>);
             else
-                hipLaunchKernelGGL(rows_kernel<2>, grid, block, 0, c.stream, r);
+                launch(rows_codes_kernel<1, O == kCodes>, rows_codes_kernel<2, O == kCodes>);
             return hipGetLastError() == hipSuccess ? LORA_OK : LORA_ERR_LAUNCH;
         }
     } else {
@@ -1437,7 +1547,10 @@ int linear_forward(const LinearCall &c, const Layout &l, float *buf, void *y, in
     a.rank = c.rank;
     a.slices = c.slices;
     a.max_loras = c.meta->max_loras;
-    return launch_linear<false, O>(a, c.stream) == hipSuccess ? LORA_OK : LORA_ERR_LAUNCH;
+    if constexpr (O == kMixed)
+        return LORA_ERR_SHAPE;   // (few tokens alone)
+    else
+        return launch_linear<false, O>(a, c.stream) == hipSuccess ? LORA_OK : LORA_ERR_LAUNCH;
 }
 
 // The forward pass' own checks.

@@ -8,11 +8,6 @@ using namespace lora;
 namespace lora {
 namespace {
 
-constexpr int kMxBlock = 32;
-int64_t mx_blocks(int64_t cols) { return (cols + kMxBlock - 1) / kMxBlock; }
-int64_t mx_code_bytes(int64_t cols) { return 16 * mx_blocks(cols); }
-int64_t mx_scale_bytes(int64_t cols) { return (mx_blocks(cols) + 3) / 4 * 4; }
-
 // Sixteen lanes take 128 numbers of a row, 8 each, and with them one dword of
 // scales; a lane's codes are a dword.
 constexpr int kMxThreads = 256, kMxGroup = 16, kMxSpan = 128, kMxPer = 2;
@@ -50,26 +45,6 @@ __device__ __forceinline__ void mx_load(const float *p, bool in, float v[8]) {
         v[x] = a[x];
         v[4 + x] = b[x];
     }
-}
-
-// The scale byte (the power's exponent plus 127) of a block whose largest magnitude
-// has these bits: floor(log2) - 2, 2 being E2M1's largest exponent; 255 (not a
-// number) for a block that is not finite.
-__device__ __forceinline__ int mx_scale_of(uint32_t top) {
-    const int e = (int)(top >> 23);
-    return e == 255 ? 255 : e > 2 ? e - 2 : 0;
-}
-// 8 codes: v over the power (exact, but for what is far below half of the smallest
-// code), to the nearest, ties to even, held at 6.
-__device__ __forceinline__ uint32_t mx_codes_of(const float v[8], int scale) {
-    if (scale == 255) return 0u;
-    const float inv = __uint_as_float((uint32_t)(254 - scale) << 23);
-    uint32_t c = 0;
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[0] * inv, v[1] * inv, 1.f, 0);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2] * inv, v[3] * inv, 1.f, 1);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4] * inv, v[5] * inv, 1.f, 2);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6] * inv, v[7] * inv, 1.f, 3);
-    return c;
 }
 
 // Bound by the bytes.
@@ -128,11 +103,7 @@ __global__ __launch_bounds__(kMxThreads) void dequantize_kernel(MxArgs a) {
     for (int q = 0; q < kMxPer; ++q) {
         if (!in[q]) continue;
         F *o = reinterpret_cast<F *>(a.x + at[q].row * a.ldx) + at[q].span * kMxSpan + 8 * l;
-        const float scale = __uint_as_float(s[q] << 23);   // (the conversion reads the exponent alone)
-        const u32x4 b = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[q], scale, 0)),
-                         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[q], scale, 1)),
-                         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[q], scale, 2)),
-                         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[q], scale, 3))};
+        const u32x4 b = mx_numbers(c[q], s[q]);
         if constexpr (sizeof(F) == 2) {
             *reinterpret_cast<u32x4 *>(o) = b;
         } else {
@@ -267,10 +238,10 @@ __global__ __launch_bounds__(kMxThreads) void prep_kernel(PrepArgs a) {
 
 // ---------------------------------------------------------------- plans
 
-// The workspace: that of the bf16 projection, then its matrix as numbers, the rounded
-// activations and their codes (few tokens), or what prep_kernel writes.
+// The workspace: that of the bf16 projection, then its matrix as numbers, and what
+// prep_kernel writes.
 struct MxLayout {
-    size_t w, x, codes, scales, mscales, total;
+    size_t w, codes, scales, mscales, total;
     int steps;
 };
 MxLayout mx_layout(size_t linear, long n, int hidden, int out) {
@@ -278,8 +249,7 @@ MxLayout mx_layout(size_t linear, long n, int hidden, int out) {
     l.steps = (int)((mx_blocks(hidden) + 7) / 8);
     const size_t groups = (size_t)(n + 255) / 256 * 4, wide = (size_t)(out + 255) / 256 * 4;   // whole tiles
     l.w = linear;
-    l.x = l.w + up(2 * (size_t)out * hidden);
-    l.codes = l.x + up(2 * (size_t)(n < kRowsTokens ? n : kRowsTokens) * hidden);
+    l.codes = l.w + up(2 * (size_t)out * hidden);
     l.scales = l.codes + up((size_t)n * mx_code_bytes(hidden));
     l.mscales = l.scales + up(groups * l.steps * 512);
     l.total = l.mscales + up(wide * l.steps * 512);
@@ -332,7 +302,7 @@ int lora_linear_mx(const void *x, int64_t ldx, int num_tokens, int hidden, const
     if (m.total > workspace_bytes) return LORA_ERR_BUFFER;
     if (num_tokens == 0) return LORA_OK;
     char *ws = static_cast<char *>(workspace);
-    LinearCall c = {x, x, ldx, ldx, nullptr, nullptr, hidden, ws + m.w, hidden, w_bias, lora_a, lora_b, bias, slice_widths, num_tokens,
+    LinearCall c = {x, x, ldx, ldx, nullptr, nullptr, 0, hidden, ws + m.w, hidden, w_bias, lora_a, lora_b, bias, slice_widths, num_tokens,
                     hidden, out_features, num_slices, rank, offset_start, meta, scale, ws, stream};
     if (quantize_x && num_tokens > kRowsTokens) {
         PrepArgs p;
@@ -365,16 +335,15 @@ int lora_linear_mx(const void *x, int64_t ldx, int num_tokens, int hidden, const
         c.nscales = p.nscales;
         return linear_forward<kCodes>(c, l, buf, y, ldy);
     }
+    if (num_tokens <= kRowsTokens) {
+        c.w = codes;
+        c.ldw = ldcodes / 2;
+        c.mscales = static_cast<const uint8_t *>(scales);
+        c.ldscales = ldscales;
+        return quantize_x ? linear_forward<kCodes>(c, l, buf, y, ldy) : linear_forward<kMixed>(c, l, buf, y, ldy);
+    }
     if (launch_mx<false>(ws + m.w, LORA_BF16, hidden, out_features, hidden, codes, ldcodes, scales, ldscales, stream) != hipSuccess)
         return LORA_ERR_LAUNCH;
-    if (quantize_x) {
-        const int64_t lc = mx_code_bytes(hidden), ls = mx_scale_bytes(hidden);
-        if (launch_mx<true>(x, LORA_BF16, ldx, num_tokens, hidden, ws + m.codes, lc, ws + m.scales, ls, stream) != hipSuccess ||
-            launch_mx<false>(ws + m.x, LORA_BF16, hidden, num_tokens, hidden, ws + m.codes, lc, ws + m.scales, ls, stream) != hipSuccess)
-            return LORA_ERR_LAUNCH;
-        c.in = ws + m.x;
-        c.ldin = hidden;
-    }
     return linear_forward<kWide>(c, l, buf, y, ldy);
 }
 
@@ -398,7 +367,7 @@ int lora_linear_mx_backward(const void *dy, int64_t lddy, const void *x, int64_t
     if (dx && num_tokens > 0 &&
         launch_mx<false>(ws + m.w, LORA_BF16, hidden, out_features, hidden, codes, ldcodes, scales, ldscales, stream) != hipSuccess)
         return LORA_ERR_LAUNCH;
-    const LinearCall c = {x, x, ldx, ldx, nullptr, nullptr, hidden, ws + m.w, hidden, nullptr, lora_a, lora_b, nullptr, slice_widths, num_tokens, hidden,
+    const LinearCall c = {x, x, ldx, ldx, nullptr, nullptr, 0, hidden, ws + m.w, hidden, nullptr, lora_a, lora_b, nullptr, slice_widths, num_tokens, hidden,
                           out_features, num_slices, rank, offset_start, meta, scale, ws, stream};
     return linear_backward(c, l, u, g);
 }
