@@ -81,22 +81,28 @@ __device__ __forceinline__ void dma16(const uint16_t *base, uint32_t offset, uin
     asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(dst), "v"(offset), "s"(base) : "memory");
 }
 
+// 4 bytes a lane.
+__device__ __forceinline__ void dma4(const void *src, uint32_t dst) {
+    asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, off" ::"{m0}"(dst), "v"(src) : "memory");
+}
+
 // Which rows (or K rows) and chunks of a side's stage a lane copies, and where
 // it reads its operands.  ROWS: rows of the tile's side; WAVES: waves that
-// share the copy.  QUADS (contiguous sides): rows of a 64-row group are dealt
-// to its four MFMA tiles by fours (row 16 q + 4 t + e is row 4 q + e of tile
-// t), so that a lane's outputs of the four tiles are 16 consecutive elements.
-template <int ROWS, int WAVES, bool STRIDED, bool QUADS>
+// share the copy.  DEAL (contiguous sides): rows of a group of 16 DEAL are dealt
+// to its DEAL MFMA tiles by fours (row 4 (DEAL q + t) + e is row 4 q + e of tile
+// t), so that a lane's outputs of the tiles are 4 DEAL consecutive elements.
+template <int ROWS, int WAVES, bool STRIDED, int DEAL>
 struct Side {
     static constexpr int kInstr = ROWS / 8 / WAVES;
     static constexpr int kBytes = ROWS * 128;
     static constexpr int kPairs = ROWS / 16;            // 32-byte pieces of a strided K row
     static constexpr int kLanesPerK = ROWS / 8;         // lanes that copy one K row
+    static_assert(DEAL == 1 || DEAL == 2 || DEAL == 4, "rows by fours");
     static_assert(ROWS % (8 * WAVES) == 0, "every wave copies whole instructions");
     static_assert(!STRIDED || (ROWS >= 16 && ROWS <= 512 && (ROWS & (ROWS - 1)) == 0), "strided rows");
 
     __device__ __forceinline__ static int f_row(int r) {
-        return QUADS ? ((r & 3) | ((r >> 4) & 1) << 2) : (r & 7);
+        return DEAL > 1 ? ((r & 3) | ((r >> (DEAL == 4 ? 4 : 3)) & 1) << 2) : (r & 7);
     }
     __device__ __forceinline__ static int f_k(int k) { return ((k & 3) | ((k >> 3) & 3) << 2) & (kPairs - 1); }
 
@@ -125,7 +131,7 @@ struct Side {
     }
 
     // operand of the 16-row tile `t` counted from row `base` (a multiple of 16;
-    // of 64 with QUADS), half h of the step in the stage at `st`
+    // of 16 DEAL with DEAL > 1, whose log2 is DEAL / 2), half h of the step in the stage at `st`
     __device__ __forceinline__ static bf16x8 read(const lds_byte *st, int base, int t, int h) {
         const int l16 = lane_id() & 15, g = lane_id() >> 4;
         if (STRIDED) {
@@ -137,8 +143,8 @@ struct Side {
             const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * (ROWS * 2)));
             return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
         }
-        const int r = QUADS ? base + 64 * (t >> 2) + 16 * (l16 >> 2) + 4 * (t & 3) + (l16 & 3) : base + 16 * t + l16;
-        return *(const lds_bf16x8 *)(st + r * 128 + 16 * ((4 * h + g) ^ f_row(QUADS ? (l16 & 3) | (l16 >> 2 & 1) << 4 : l16)));
+        const int r = DEAL > 1 ? base + 16 * DEAL * (t >> DEAL / 2) + 4 * DEAL * (l16 >> 2) + 4 * (t & (DEAL - 1)) + (l16 & 3) : base + 16 * t + l16;
+        return *(const lds_bf16x8 *)(st + r * 128 + 16 * ((4 * h + g) ^ f_row(DEAL > 1 ? (l16 & 3) | (l16 >> 2 & 1) << (DEAL == 4 ? 4 : 3) : l16)));
     }
 };
 
@@ -151,20 +157,21 @@ struct Tile {
     static constexpr bool MS = MS_, NS = NS_;
     static constexpr int kWaves = WM * WN, kThreads = kWaves * kWave;
     static constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
-    static constexpr bool QUADS = !MS && MT % 4 == 0;
+    static constexpr int DEAL = MS ? 1 : MT % 4 == 0 ? 4 : MT % 2 == 0 ? 2 : 1;
     static constexpr int MROWS = BM * (SPLIT == 1 ? 2 : 1), NROWS = BN * (SPLIT == 2 ? 2 : 1);
-    using MSide = Side<MROWS, kWaves, MS, QUADS>;
-    using NSide = Side<NROWS, kWaves, NS, false>;
+    using MSide = Side<MROWS, kWaves, MS, DEAL>;
+    using NSide = Side<NROWS, kWaves, NS, 1>;
     static constexpr int kStage = MSide::kBytes + NSide::kBytes;
     static constexpr int kLds = kStages * kStage;
     typedef floatx4 Acc[MT][NT];
 
+    using Plain = Tile;
     __device__ __forceinline__ static int wave_m() { return wave_id() % WM; }
     __device__ __forceinline__ static int wave_n() { return wave_id() / WM; }
     // tile row (output column) of element 0 of acc[mt][..] in this lane
     __device__ __forceinline__ static int m_of(int mt) {
         const int g = lane_id() >> 4;
-        return wave_m() * (BM / WM) + (QUADS ? 64 * (mt >> 2) + 16 * g + 4 * (mt & 3) : 16 * mt + 4 * g);
+        return wave_m() * (BM / WM) + (DEAL > 1 ? 16 * DEAL * (mt >> DEAL / 2) + 4 * DEAL * g + 4 * (mt & (DEAL - 1)) : 16 * mt + 4 * g);
     }
     __device__ __forceinline__ static int n_of(int nt) { return wave_n() * (BN / WN) + 16 * nt + (lane_id() & 15); }
 
@@ -229,7 +236,7 @@ struct ScaledTile : B {
     static constexpr int kMGroups = B::BM / 64, kPieces = kScales / 1024;       // 1 KB a copy
     static constexpr int NG = (B::NT + 3) / 4;
     static constexpr int kReads = B::kReads + 1 + NG, kLoads = B::kLoads + 1;
-    static_assert(!B::MS && !B::NS && B::SPLIT == 0 && B::QUADS && B::MT == 4, "64 rows of the M side a wave");
+    static_assert(!B::MS && !B::NS && B::SPLIT == 0 && B::DEAL == 4 && B::MT == 4, "64 rows of the M side a wave");
     static_assert(B::NT % 4 == 0 || B::NT == 1, "whole groups of 64 N rows, or a quarter of one");
     struct Half : B::Half {
         uint32_t sm, sn[NG];

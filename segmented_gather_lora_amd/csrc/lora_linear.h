@@ -174,7 +174,8 @@ struct LinearArgs {
     int64_t ldy;
     int32_t num_tokens, cols, k, rank, slices, max_loras;
     int32_t mtiles, ntiles, group, has_bias, row_len;   // row_len: packed_row(rank)
-    const uint8_t *mscales, *nscales;           // codes: [64 rows][step][512], as ScaledTile reads them
+    const uint8_t *mscales, *nscales;           // codes: [64 rows][step][512], as ScaledTile reads them;
+    int64_t ldscales;                           // mixed: mscales are W's rows of them
 };
 
 // The adapters' share of a tile's K walk is made of units, for every slice that
@@ -199,6 +200,26 @@ __device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirst
 // (codes: the rows of both sides follow one another, so that a lane's place is 32 bits)
 template <class T, Operands O>
 using WalkOp = std::conditional_t<O == kCodes, PairOp<T, OffsetWalk<typename T::MSide>, OffsetWalk<typename T::NSide>>, PlainOp<T>>;
+
+// Mixed operands: W's rows and their scales, the tokens' rows.
+template <class T>
+struct Mixed : MixedWalk<T> {
+    template <class Row>
+    __device__ __forceinline__ void start(const LinearArgs &a, int m0, Row row) {
+#pragma unroll
+        for (int j = 0; j < T::kNInstr; ++j) this->n[j] = row(T::n_copy_row(j)) + 8 * T::n_copy_chunk(j);
+        this->m = reinterpret_cast<const uint8_t *>(a.w + (int64_t)min(m0 + T::m_copy_row(), a.cols - 1) * a.ldw) + 16 * T::m_copy_chunk();
+        this->scales = a.mscales;
+        this->ldscales = a.ldscales;
+        this->m0 = m0;
+        this->cols = a.cols;
+        this->k = a.k;
+        this->blocks = (a.k + kMxBlock - 1) / kMxBlock;
+        this->step = 0;
+    }
+    __device__ __forceinline__ int steps() const { return (this->blocks + 3) / 4; }
+};
+struct NoWalk {};
 
 template <class T, bool BWD, Operands O>
 struct LinearOp : WalkOp<T, O> {
@@ -353,7 +374,7 @@ struct LinearOp : WalkOp<T, O> {
 };
 
 // The adapters' share of a 64 x 64 tile as fp32 dot products, a lane for its
-// token and 16 of the tile's columns, in place of a step of the K walk for every 32
+// tokens and columns (16 of one token, or 8 of two), in place of a step of the K walk for every 32
 // ranks, adapter and slice.  us with the products and with the steps, for so many
 // adapters in each tile:
 //   y   gains from four on, at every rank (64 tokens by 1024 over 1024): 2: 31, 25;
@@ -366,8 +387,7 @@ template <bool BWD>
 constexpr int kDotSegs = BWD ? 20 : 4;
 template <class T, bool BWD>
 __device__ __forceinline__ void add_dots(const LinearArgs &a, const SliceEntry *slices, int m0, int t, int id,
-                                         typename T::Acc &acc) {
-    static_assert(T::NT == 1 && T::MT == 4, "one token a lane");
+                                         typename T::Acc &acc, int nt) {
     const int r = a.rank;
     auto matrices = [&](int i) {
         return reinterpret_cast<const uint16_t *>(slices[i].weights[0] | (uint64_t)slices[i].weights[1] << 32);
@@ -387,8 +407,8 @@ __device__ __forceinline__ void add_dots(const LinearArgs &a, const SliceEntry *
                     for (int x = 0; x < 2; ++x) {
                         float p, q;
                         unpack_bf16(v[x], p, q);
-                        acc[mt][0][2 * x] = fmaf(p, sj, acc[mt][0][2 * x]);
-                        acc[mt][0][2 * x + 1] = fmaf(q, sj, acc[mt][0][2 * x + 1]);
+                        acc[mt][nt][2 * x] = fmaf(p, sj, acc[mt][nt][2 * x]);
+                        acc[mt][nt][2 * x + 1] = fmaf(q, sj, acc[mt][nt][2 * x + 1]);
                     }
                 }
             }
@@ -421,7 +441,7 @@ __device__ __forceinline__ void add_dots(const LinearArgs &a, const SliceEntry *
                         }
                 }
 #pragma unroll
-                for (int x = 0; x < 8; ++x) acc[mt + x / 4][0][x % 4] += sum[x];
+                for (int x = 0; x < 8; ++x) acc[mt + x / 4][nt][x % 4] += sum[x];
             }
         }
     }
@@ -462,12 +482,18 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(LinearArgs a) {
         st = a.meta.start_loc[tid];
         count = a.meta.counts[tid];
     }
-    LinearOp<T, BWD, O> op(a, s_seg, s_slice);
+    // (mixed: W's walk is its own, and the adapters' steps follow on plain stages)
+    using A = std::conditional_t<O == kMixed, typename T::Plain, T>;
+    LinearOp<A, BWD, O> op(a, s_seg, s_slice);
     op.m0 = m0;
     op.p0 = p0;
     op.blocks = a.rank <= 16 ? 0 : (a.rank + 31) / 32;
-    const int main = (a.k + kStepK - 1) / kStepK;
-    if constexpr (O == kCodes) {
+    const int main = O == kMixed ? 0 : (a.k + kStepK - 1) / kStepK;
+    typedef typename std::conditional_t<O == kMixed, Mixed<T>, NoWalk> MainWalk;
+    MainWalk walk;
+    if constexpr (O == kMixed) {
+        walk.start(a, m0, [&](int r) { return a.in + (int64_t)token(r) * a.ldin; });
+    } else if constexpr (O == kCodes) {
         op.wn.base = a.in + (int64_t)p0 * a.ldin;
 #pragma unroll
         for (int j = 0; j < T::NSide::kInstr; ++j)
@@ -497,11 +523,14 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(LinearArgs a) {
         }
         op.wm.step = BWD ? (int64_t)kStepK * a.ldw : kStepK;
     }
-    op.wn.step = kStepK;
-    op.wm.left = op.wn.left = a.k;
+    if constexpr (O != kMixed) {
+        op.wn.step = kStepK;
+        op.wm.left = op.wn.left = a.k;
+    }
     op.main_left = op.main_steps = main;
-    const bool early = main >= kAhead<T>;
-    if (early) mma_begin<T>(op, main, g_lds);
+    const bool early = O != kMixed && main >= kAhead<T>;
+    if constexpr (O == kMixed) mixed_begin(walk, walk.steps(), g_lds);
+    if (early) mma_begin<A>(op, main, g_lds);
 
     // while they land: the tile's tokens and ids, and the adapters it meets
     // (any order: each token takes part in one of them)
@@ -548,19 +577,22 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(LinearArgs a) {
     const int units = op.sl1 > op.sl0 && !dots ? nseg * (op.sl1 - op.sl0) * op.per_seg() : 0;
     const int steps = main + (op.blocks ? units : (units + 1) / 2);
     if (units > 0) op.start(units);
-    if (!early) mma_begin<T>(op, steps, g_lds);
     typename T::Acc acc;
     clear<T>(acc);
-    mma_loop<T>(op, a.k / kStepK, steps, acc, g_lds);
+    if constexpr (O == kMixed) mixed_loop(walk, walk.steps(), acc, g_lds);
+    if (!early) mma_begin<A>(op, steps, g_lds);
+    mma_loop<A>(op, O == kMixed ? 0 : a.k / kStepK, steps, acc, g_lds);
 
     if constexpr (kDots)
-        if (dots) {
-            const int row = T::n_of(0), m = s_id[row];
-            if (row < rows && m >= 0 && m < a.max_loras) add_dots<T, BWD>(a, s_slice, m0, s_tok[row], m, acc);
-        }
+        if (dots)
+#pragma unroll
+            for (int nt = 0; nt < T::NT; ++nt) {
+                const int row = T::n_of(nt), m = s_id[row];
+                if (row < rows && m >= 0 && m < a.max_loras) add_dots<T, BWD>(a, s_slice, m0, s_tok[row], m, acc, nt);
+            }
 
     // biases: of the projection for every token, of the adapter where there is one
-    if constexpr (T::QUADS) {
+    if constexpr (T::DEAL > 1) {
         // groups of 8 consecutive columns (never across a slice's edge); a group's loads are issued together
 #pragma unroll
         for (int mt = 0; mt < T::MT; mt += 2) {
@@ -1393,17 +1425,24 @@ hipError_t launch_linear(LinearArgs &a, hipStream_t s) {
     const unsigned grid = tile_grid((long)p.mtiles * p.ntiles);
     auto launch = [&](auto tile) {
         using B = decltype(tile);
-        if constexpr (O == kCodes) {
+        if constexpr (O == kMixed) {
+            using T = MixedTile<B>;
+            return launch_tiles<linear_kernel<T, BWD, O>>(grid, T::kThreads, T::kLds, s, a);
+        } else if constexpr (O == kCodes) {
             using T = ScaledTile<B>;
             return launch_tiles<linear_kernel<T, BWD, O>>(grid, T::kThreads, T::kLds, s, a);
         } else {
             return launch_tiles<linear_kernel<B, BWD, O>>(grid, B::kThreads, B::kLds, s, a);
         }
     };
-    switch (p.tile) {
-        case kBig: return launch(Tile<256, 256, 4, 2, BWD, false>{});
-        case kMid: return launch(Tile<128, 128, 2, 2, BWD, false>{});
-        default: return launch(Tile<64, 64, 1, 4, BWD, false, 0, 4>{});
+    if constexpr (O == kMixed) {
+        return launch(Tile<64, 64, 2, 2, BWD, false, 0, 3>{});   // (four and six stages: the same)
+    } else {
+        switch (p.tile) {
+            case kBig: return launch(Tile<256, 256, 4, 2, BWD, false>{});
+            case kMid: return launch(Tile<128, 128, 2, 2, BWD, false>{});
+            default: return launch(Tile<64, 64, 1, 4, BWD, false, 0, 4>{});
+        }
     }
 }
 
@@ -1544,13 +1583,11 @@ int linear_forward(const LinearCall &c, const Layout &l, float *buf, void *y, in
     a.k = c.k;
     a.mscales = c.mscales;
     a.nscales = c.nscales;
+    a.ldscales = c.ldscales;
     a.rank = c.rank;
     a.slices = c.slices;
     a.max_loras = c.meta->max_loras;
-    if constexpr (O == kMixed)
-        return LORA_ERR_SHAPE;   // (few tokens alone)
-    else
-        return launch_linear<false, O>(a, c.stream) == hipSuccess ? LORA_OK : LORA_ERR_LAUNCH;
+    return launch_linear<false, O>(a, c.stream) == hipSuccess ? LORA_OK : LORA_ERR_LAUNCH;
 }
 
 // The forward pass' own checks.

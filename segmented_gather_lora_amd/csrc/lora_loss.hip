@@ -173,7 +173,7 @@ __global__ __launch_bounds__(T::kThreads) void logit_kernel(LogitArgs a) {
             const int r = T::n_of(nt);
             if (r >= rows) continue;
             uint16_t *row = a.g + (int64_t)(p0 + r) * a.ldg;
-            static_assert(T::QUADS, "8 consecutive entries a lane");
+            static_assert(T::DEAL > 1, "8 consecutive entries a lane");
 #pragma unroll
             for (int mt = 0; mt < T::MT; mt += 2) {
                 const int v = m0 + T::m_of(mt);

@@ -60,4 +60,163 @@ __device__ __forceinline__ u32x4 mx_numbers(uint32_t codes, uint32_t scale) {
                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 3))};
 }
 
+// A tile whose M side is codes and whose N side is bf16, K in steps of 128, for batches
+// that neither the MFMA nor memory bounds: what counts is that copies, reads,
+// conversions and MFMAs of different steps overlap, since a SIMD has one or two waves.
+// A stage holds the N rows' 256 bytes and the M rows' 64.  The M rows' scales come 32
+// steps at a time (128 bytes a row, into one of two buffers): a copy of four bytes a
+// row every step would look up as many lines as all the rest.  A lane's 16 bytes of codes
+// are one block of 32 (its own scale), which it turns into the operands of four MFMAs; the
+// N side is read in the same order of K.  Waves that share M rows convert them each for
+// itself, hence two by two of them, not one by four.  256 tokens by 6144 columns over
+// 4096 without adapters: 33 us, of which 25 remain without the copies and 22 without the
+// rest.  (Eight waves in two groups that take the steps in turn: 37.)
+template <class B>
+struct MixedTile : B {
+    static constexpr int kStepK = 128, kNBytes = B::BN * 256, kMBytes = B::BM * 64;
+    static constexpr int kMAt = kNBytes, kStage = kNBytes + kMBytes;
+    static constexpr int kScaleSteps = 32, kScaleBytes = B::BM * 4 * kScaleSteps, kScaleCopies = kScaleBytes / 256 / B::kWaves;
+    static constexpr int kScaleAt = B::kStages * kStage, kLds = kScaleAt + 2 * kScaleBytes;
+    static constexpr int kNInstr = B::BN / 4 / B::kWaves, kLoads = kNInstr + 2;
+    static_assert(B::BM == 64 && B::DEAL == 2 && B::MT == 2 && B::kWaves == 4, "32 rows of the M side a wave, a tile of 16 a copy");
+    static_assert((kScaleCopies & (kScaleCopies - 1)) == 0 && kScaleCopies <= kScaleSteps / 2, "the next scales land in time");
+
+    // tile row in place p of the M side: tile by tile, so that a tile's 16 rows are together
+    __device__ __forceinline__ static int m_row(int p) {
+        const int l16 = p & 15, t = p >> 4;
+        return 32 * (t >> 1) + 8 * (l16 >> 2) + 4 * (t & 1) + (l16 & 3);
+    }
+    // copies: row and 16-byte chunk of this lane (N: of instruction j)
+    __device__ __forceinline__ static int n_copy_row(int j) { return (wave_id() * kNInstr + j) * 4 + lane_id() / 16; }
+    __device__ __forceinline__ static int n_copy_chunk(int j) { return (lane_id() & 15) ^ (n_copy_row(j) & 15); }
+    __device__ __forceinline__ static int m_copy_row() { return m_row(wave_id() * 16 + lane_id() / 4); }
+    __device__ __forceinline__ static int m_copy_chunk() { return (lane_id() & 3) ^ (lane_id() >> 3 & 3); }   // (place / 2) & 3
+    // scales: place and step (of 32) that a lane copies with instruction i; a place's
+    // dwords are turned by its number, so that 16 rows' bytes of a step are in 16 banks
+    __device__ __forceinline__ static int scale_copy_place(int i) { return (wave_id() * kScaleCopies + i) * 2 + lane_id() / 32; }
+    __device__ __forceinline__ static int scale_copy_step(int i) { return (lane_id() - scale_copy_place(i)) & 31; }
+
+    struct Step {
+        u32x4 codes[B::MT];
+        uint32_t scale[B::MT];
+        bf16x8 n[B::NT][4];
+    };
+    // of the stage at st, step s of K
+    __device__ __forceinline__ static void read(Step &r, const lds_byte *lds, const lds_byte *st, int s) {
+        const int l16 = lane_id() & 15, g = lane_id() >> 4;
+#pragma unroll
+        for (int t = 0; t < B::MT; ++t) {
+            const int place = 16 * (B::wave_m() * B::MT + t) + l16;
+            r.codes[t] = *(const __attribute__((address_space(3))) u32x4 *)(st + kMAt + place * 64 + 16 * (g ^ (l16 >> 1 & 3)));
+            r.scale[t] = *(lds + kScaleAt + ((uint32_t)s / kScaleSteps & 1) * kScaleBytes + place * 128 + ((s + place) & 31) * 4 + g);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int t = 0; t < B::NT; ++t) {
+                const int row = B::wave_n() * (B::BN / B::WN) + 16 * t + l16;
+                r.n[t][j] = *(const lds_bf16x8 *)(st + row * 256 + 16 * ((4 * g + j) ^ l16));
+            }
+    }
+    // keep: 0 where the lane's block is past the last (its scale may be anything, its codes are zeros)
+    __device__ __forceinline__ static void mma(const Step &r, typename B::Acc &acc, uint32_t keep) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int m = 0; m < B::MT; ++m) {
+                const bf16x8 w = as_bf16x8(mx_numbers(r.codes[m][j], r.scale[m] & keep));
+#pragma unroll
+                for (int t = 0; t < B::NT; ++t) acc[m][t] = mfma16x16x32(w, r.n[t][j], acc[m][t]);
+            }
+    }
+};
+
+// The two sides' walk: lanes past the end of K read zeros.
+template <class T>
+struct MixedWalk {
+    const uint16_t *n[T::kNInstr];
+    const uint8_t *m, *scales;  // (scales: row 0 of W)
+    int64_t ldscales;
+    int m0, cols;               // first row of the tile, rows of W
+    int k, blocks, step;        // of the rows; next step to copy
+    // instruction i of the scales of 32 steps; past the last dword any of the row's
+    __device__ __forceinline__ void copy_scales(uint32_t base, int group, int i) {
+        const int d = min(group * T::kScaleSteps + T::scale_copy_step(i), (blocks - 1) / 4);
+        const int row = min(m0 + T::m_row(T::scale_copy_place(i)), cols - 1);
+        dma4(scales + row * ldscales + 4 * (int64_t)d,
+             base + T::kScaleAt + (group & 1) * T::kScaleBytes + (wave_id() * T::kScaleCopies + i) * 256u);
+    }
+    // n and m are this lane's places in the next step
+    __device__ __forceinline__ void issue(uint32_t base, uint32_t at) {
+        const uint32_t to = at + wave_id() * T::kNInstr * 1024u, mto = at + T::kMAt + wave_id() * 1024u;
+        const uint16_t *codes = reinterpret_cast<const uint16_t *>(m);
+        if ((step + 1) * T::kStepK <= k) {
+#pragma unroll
+            for (int j = 0; j < T::kNInstr; ++j) dma16(n[j], to + j * 1024u);
+            dma16(codes, mto);
+        } else {
+#pragma unroll
+            for (int j = 0; j < T::kNInstr; ++j)
+                dma16(step * T::kStepK + 8 * T::n_copy_chunk(j) < k ? n[j] : zero_page, to + j * 1024u);
+            dma16(step * 4 + T::m_copy_chunk() < blocks ? codes : zero_page, mto);
+        }
+#pragma unroll
+        for (int j = 0; j < T::kNInstr; ++j) n[j] += T::kStepK;
+        m += 64;
+        // the scales of the 32 steps after those that are being read, whose buffer the
+        // 32 before them have left (every step makes one copy, some again, so that all make as many)
+        const int now = step - (T::kStages - 1);
+        copy_scales(base, now < 0 ? 0 : now / T::kScaleSteps + 1, step & (T::kScaleCopies - 1));
+        ++step;
+    }
+};
+
+template <class T>
+__device__ __forceinline__ void mixed_begin(MixedWalk<T> &w, int nsteps, unsigned char *lds) {
+    const uint32_t base = lds_address(lds);
+#pragma unroll
+    for (int i = 0; i < T::kScaleCopies; ++i) w.copy_scales(base, 0, i);
+    for (int i = 0; i < T::kStages && i < nsteps; ++i) w.issue(base, base + i * T::kStage);
+}
+// A step's operands are read while the step before is multiplied.  One barrier a step:
+// every wave has read the step before, whose stage takes the copies of kStages steps on.
+// At the end nothing is in flight and every wave is done with the stages.
+template <class T>
+__device__ __forceinline__ void mixed_loop(MixedWalk<T> &w, int nsteps, typename T::Acc &acc, unsigned char *lds_generic) {
+    constexpr int S = T::kStages;
+    const lds_byte *lds = (const lds_byte *)lds_generic;
+    const uint32_t base = lds_address(lds_generic);
+    int cur = 0, s = 0;       // stage and number of the step to be read next
+    auto read = [&](typename T::Step &r) {
+        T::read(r, lds, lds + cur, s);
+        cur = cur + T::kStage == T::kScaleAt ? 0 : cur + T::kStage;
+        ++s;
+    };
+    // reads step s while step s - 1 is multiplied
+    auto turn = [&](typename T::Step &next, const typename T::Step &now) {
+        const bool more = s < nsteps;
+        const uint32_t keep = (s - 1) * 4 + lane_id() / 16 < w.blocks ? 0xffu : 0u;
+        if (more) {
+            const int before = (cur == 0 ? T::kScaleAt : cur) - T::kStage;
+            if (s + S - 1 <= nsteps)
+                wait_loads_barrier<(S - 2) * T::kLoads>();
+            else
+                wait_loads_barrier<0>();
+            if (s - 1 + S < nsteps) w.issue(base, base + before);
+            read(next);
+        }
+        T::mma(now, acc, keep);
+        return more;
+    };
+    typename T::Step a, b;
+    if (S <= nsteps)      // the first step has landed
+        wait_loads_barrier<(S - 1) * T::kLoads>();
+    else
+        wait_loads_barrier<0>();
+    read(a);
+    while (turn(b, a) && turn(a, b)) {
+    }
+    __syncthreads();
+}
+
 }  // namespace lora
