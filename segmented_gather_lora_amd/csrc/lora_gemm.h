@@ -349,13 +349,11 @@ __device__ __forceinline__ void mma_begin(Op &op, int nsteps, unsigned char *lds
     for (int i = 0; i < kAhead<T> && i < nsteps; ++i) op.issue(base + i * T::kStage);
 }
 
-// Whether an op's first main_steps steps are multiplied in a way of their own
-// (op.mma_first): they have a loop of their own then, since a branch between the two
-// costs the registers of a second set of sums.
+// Whether nothing but an op's own steps follows in its loop's stages (Op::kAlone).
 template <class Op, class = void>
-struct two_kinds : std::false_type {};
+struct alone : std::false_type {};
 template <class Op>
-struct two_kinds<Op, std::enable_if_t<Op::kTwoKinds>> : std::true_type {};
+struct alone<Op, std::enable_if_t<Op::kAlone>> : std::true_type {};
 
 // Small tiles: one barrier a step, kStages - 2 steps' copies in flight across it.
 template <class T, class Op>
@@ -387,22 +385,6 @@ __device__ __forceinline__ void ring_loop(Op &op, int plain, int nsteps, typenam
         }
         turn();
     }
-    if constexpr (two_kinds<Op>::value)
-        for (; s < op.main_steps; ++s) {
-            if (s + S - 1 <= plain)
-                wait_loads_barrier<(S - 2) * T::kLoads>();
-            else if (s + S - 1 <= nsteps)
-                wait_loads_barrier<(S - 2) * Op::kLast>();
-            else
-                wait_loads_barrier<0>();
-            if (s + S - 1 < nsteps) op.issue(base + to);
-            typename T::Half r0, r1;
-            T::read(r0, lds + cur, 0);
-            T::read(r1, lds + cur, 1);
-            op.mma_first(r0, acc);
-            op.mma_first(r1, acc);
-            turn();
-        }
     for (; s < nsteps; ++s) {
         if (s + S - 1 <= plain)
             wait_loads_barrier<(S - 2) * T::kLoads>();
@@ -463,29 +445,37 @@ __device__ __forceinline__ void mma_loop(Op &op, int plain, int nsteps, typename
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
+        if constexpr (alone<Op>::value) {
+            if (plain == nsteps) {   // the last two steps in the same order, without copies
+#pragma unroll
+                for (int last = 0; last < 2; ++last, ++s) {
+                    const uint32_t cur = (uint32_t)(s & 1) * T::kStage, nxt = T::kStage - cur;
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        if (g == L && last == 0) wait_loads_barrier<0>();
+                        if (g < F) {
+#pragma unroll
+                            for (int i = g * R / F; i < (g + 1) * R / F; ++i) T::read_one(r1, lds + cur, 1, i);
+                        }
+                        if (g >= L && last == 0) {
+#pragma unroll
+                            for (int i = (g - L) * R / (G - L); i < (g - L + 1) * R / (G - L); ++i) T::read_one(r0, lds + nxt, 0, i);
+                        }
+                        op.mma_n(g < T::NT ? r0 : r1, acc, g % T::NT);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+                return;
+            }
+        }
     }
-    // step s has landed; of step s + 1 the copies that every wave makes last may be in flight
-    auto wait = [&] {
+    for (; s < nsteps; ++s) {
+        const uint32_t cur = (uint32_t)(s & 1) * T::kStage;
+        // step s has landed; of step s + 1 the copies that every wave makes last may be in flight
         if (s + 1 < nsteps)
             wait_loads_barrier<Op::kLast>();
         else
             wait_loads_barrier<0>();
-    };
-    if constexpr (two_kinds<Op>::value)
-        for (; s < op.main_steps; ++s) {
-            const uint32_t cur = (uint32_t)(s & 1) * T::kStage;
-            wait();
-            typename T::Half r;
-            T::read(r, lds + cur, 0);
-            op.mma_first(r, acc);
-            T::read(r, lds + cur, 1);
-            own_reads_barrier();
-            if (s + 2 < nsteps) op.issue(base + cur);
-            op.mma_first(r, acc);
-        }
-    for (; s < nsteps; ++s) {
-        const uint32_t cur = (uint32_t)(s & 1) * T::kStage;
-        wait();
         typename T::Half r;
         op.read(r, lds + cur, s, 0);
         op.mma(r, acc, s, 0);

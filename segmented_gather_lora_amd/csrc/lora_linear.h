@@ -197,9 +197,60 @@ struct SegRow {
 };
 __device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// (codes: the rows of both sides follow one another, so that a lane's place is 32 bits)
-template <class T, Operands O>
-using WalkOp = std::conditional_t<O == kCodes, PairOp<T, OffsetWalk<typename T::MSide>, OffsetWalk<typename T::NSide>>, PlainOp<T>>;
+// The adapter's steps of a tile whose rows are all of one adapter: no masks (ranks above
+// 16 alone: of two units in a step the second may have no rows).
+template <class T, class Op>
+struct WholeOp : Op {
+    __device__ __forceinline__ explicit WholeOp(const Op &o) : Op(o) {}
+    __device__ __forceinline__ void mma(const typename T::Half &h, typename T::Acc &acc, int, int) { T::mma(h, acc); }
+};
+
+// Codes on both sides: the rows of either follow one another, so that a lane's places are
+// 32 bits; a step's scales are one more copy of every wave (1 KB: two groups of 64 rows,
+// M's groups first; waves past the last piece copy one again).
+template <class T>
+struct Codes : PairOp<T, OffsetWalk<typename T::MSide>, OffsetWalk<typename T::NSide>> {
+    using Pair = PairOp<T, OffsetWalk<typename T::MSide>, OffsetWalk<typename T::NSide>>;
+    static constexpr bool kAlone = true;
+    const uint8_t *scales;     // of this lane's copy in the next step
+    int all;
+    __device__ __forceinline__ void start(const LinearArgs &a, int m0, int p0, int rows) {
+        all = (a.k + kStepK - 1) / kStepK;
+        this->wn.base = a.in + (int64_t)p0 * a.ldin;
+#pragma unroll
+        for (int j = 0; j < T::NSide::kInstr; ++j)
+            this->wn.off[j] = 2u * ((uint32_t)min(T::NSide::row(j), rows - 1) * (uint32_t)a.ldin + (uint32_t)T::NSide::elem(j));
+        this->wm.base = a.w + (int64_t)m0 * a.ldw;
+#pragma unroll
+        for (int j = 0; j < T::MSide::kInstr; ++j)
+            this->wm.off[j] = 2u * ((uint32_t)min(T::MSide::row(j), a.cols - 1 - m0) * (uint32_t)a.ldw + (uint32_t)T::MSide::elem(j));
+        this->wm.step = this->wn.step = kStepK;
+        this->wm.left = this->wn.left = a.k;
+        const int group = wave_id() % T::kPieces * 2 + lane_id() / 32;
+        scales = (group < T::kMGroups ? a.mscales + (int64_t)(m0 / 64 + group) * all * 512
+                                      : a.nscales + (int64_t)(p0 / 64 + group - T::kMGroups) * all * 512) +
+                 (lane_id() & 31) * 16;
+    }
+    __device__ __forceinline__ int steps() const { return all; }
+    __device__ __forceinline__ void load_scales(uint32_t at) {
+        dma16(reinterpret_cast<const uint16_t *>(scales), at + T::kScaleAt + wave_id() % T::kPieces * 1024u);
+    }
+    __device__ __forceinline__ void load(uint32_t at, int i) {
+        if (i == T::kLoads - 1)
+            load_scales(at);
+        else
+            Pair::load(at, i);
+    }
+    __device__ __forceinline__ void next() {
+        Pair::next();
+        scales += 512;
+    }
+    __device__ __forceinline__ void issue(uint32_t at) {
+        load_scales(at);
+        scales += 512;
+        Pair::issue(at);
+    }
+};
 
 // Mixed operands: W's rows and their scales, the tokens' rows.
 template <class T>
@@ -219,14 +270,25 @@ struct Mixed : MixedWalk<T> {
     }
     __device__ __forceinline__ int steps() const { return (this->blocks + 3) / 4; }
 };
+// W's walk beside the adapters' steps (wide: it is theirs).
 struct NoWalk {};
+template <class T, Operands O>
+struct WalkOf {
+    using type = NoWalk;
+};
+template <class T>
+struct WalkOf<T, kMixed> {
+    using type = Mixed<T>;
+};
+template <class T>
+struct WalkOf<T, kCodes> {
+    using type = Codes<T>;
+};
 
-template <class T, bool BWD, Operands O>
-struct LinearOp : WalkOp<T, O> {
-    using Main = WalkOp<T, O>;
+// ALONE: a loop of the adapters' steps alone (W's product is done).
+template <class T, bool BWD, bool ALONE>
+struct LinearOp : PlainOp<T> {
     static constexpr int kLast = T::MSide::kInstr / 2;
-    static constexpr bool kTwoKinds = O == kCodes;   // steps that differ in how they are multiplied
-    const uint8_t *scales;     // codes: of this lane's copy in the next step
     const LinearArgs &a;
     const SegRow *segs;        // LDS
     const SliceEntry *slices;  // LDS
@@ -255,16 +317,15 @@ struct LinearOp : WalkOp<T, O> {
     __device__ __forceinline__ void read(typename T::Half &r, const lds_byte *st, int s, int h, const typename T::Half &first) {
         T::read_n(r, st, h);
         // a block's lo part meets the same ranks as its hi part
-        const int hm = s < main_steps || blocks == 0 ? h : 0;
+        const int hm = (!ALONE && s < main_steps) || blocks == 0 ? h : 0;
         if (&r != &first || hm == h) T::read_m(r, st, hm);
     }
     // an adapter's units touch its own tokens' sums alone: one whose weights
     // are not finite stays without effect on the others in the tile
     // (W's last steps go the same way with all rows: a branch here would cost the
     // registers of a second set of sums)
-    __device__ __forceinline__ void mma_first(const typename T::Half &h, typename T::Acc &acc) { T::mma(h, acc); }
     __device__ __forceinline__ void mma(const typename T::Half &h, typename T::Acc &acc, int s, int half) {
-        const bool all = O == kWide && s < main_steps;
+        const bool all = !ALONE && s < main_steps;
         mma_rows<T>(h, acc, all ? 0 : scalar(mlo), all ? T::BN : munits > 0 ? scalar(mhi) : 0);
         if (!all && (half == 1 || blocks == 0)) {
             --munits;
@@ -276,19 +337,8 @@ struct LinearOp : WalkOp<T, O> {
             }
         }
     }
-    __device__ __forceinline__ void load(uint32_t at, int i) {
-        if (O == kCodes && i == T::kLoads - 1)
-            load_scales(at);
-        else
-            Main::load(at, i);
-    }
-    __device__ __forceinline__ void load_scales(uint32_t at) {
-        if constexpr (O == kCodes)
-            dma16(reinterpret_cast<const uint16_t *>(scales), at + T::kScaleAt + wave_id() % T::kPieces * 1024u);
-    }
     __device__ __forceinline__ void next() {
-        Main::next();
-        if (O == kCodes) scales += 512;
+        PlainOp<T>::next();
         --main_left;
     }
     // copies of a unit: N rows of its adapter's tokens (other rows keep what the
@@ -359,10 +409,8 @@ struct LinearOp : WalkOp<T, O> {
         }
     }
     __device__ __forceinline__ void issue(uint32_t at) {
-        if (main_left > 0) {
-            load_scales(at);
-            if (O == kCodes) scales += 512;
-            Main::issue(at);
+        if (!ALONE && main_left > 0) {
+            PlainOp<T>::issue(at);
             --main_left;
         } else if (blocks) {
             unit<-1>(at);
@@ -482,32 +530,18 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(LinearArgs a) {
         st = a.meta.start_loc[tid];
         count = a.meta.counts[tid];
     }
-    // (mixed: W's walk is its own, and the adapters' steps follow on plain stages)
-    using A = std::conditional_t<O == kMixed, typename T::Plain, T>;
-    LinearOp<A, BWD, O> op(a, s_seg, s_slice);
+    // (codes: W's walk is a loop of its own, and the adapters' steps follow on plain stages)
+    using A = typename T::Plain;
+    LinearOp<A, BWD, O != kWide> op(a, s_seg, s_slice);
     op.m0 = m0;
     op.p0 = p0;
     op.blocks = a.rank <= 16 ? 0 : (a.rank + 31) / 32;
-    const int main = O == kMixed ? 0 : (a.k + kStepK - 1) / kStepK;
-    typedef typename std::conditional_t<O == kMixed, Mixed<T>, NoWalk> MainWalk;
-    MainWalk walk;
+    const int main = O == kWide ? (a.k + kStepK - 1) / kStepK : 0;
+    typename WalkOf<T, O>::type walk;
     if constexpr (O == kMixed) {
         walk.start(a, m0, [&](int r) { return a.in + (int64_t)token(r) * a.ldin; });
     } else if constexpr (O == kCodes) {
-        op.wn.base = a.in + (int64_t)p0 * a.ldin;
-#pragma unroll
-        for (int j = 0; j < T::NSide::kInstr; ++j)
-            op.wn.off[j] = 2u * (uint32_t)(min(T::NSide::row(j), rows - 1) * (int)a.ldin + T::NSide::elem(j));
-        op.wm.base = a.w + (int64_t)m0 * a.ldw;
-#pragma unroll
-        for (int j = 0; j < T::MSide::kInstr; ++j)
-            op.wm.off[j] = 2u * ((uint32_t)min(T::MSide::row(j), a.cols - 1 - m0) * (uint32_t)a.ldw + (uint32_t)T::MSide::elem(j));
-        op.wm.step = kStepK;
-        // the copy's 1 KB: two groups of 64 rows, M's groups first
-        const int group = wave_id() % T::kPieces * 2 + lane_id() / 32;
-        op.scales = (group < T::kMGroups ? a.mscales + (int64_t)(m0 / 64 + group) * main * 512
-                                         : a.nscales + (int64_t)(p0 / 64 + group - T::kMGroups) * main * 512) +
-                    (lane_id() & 31) * 16;
+        walk.start(a, m0, p0, rows);
     } else {
 #pragma unroll
         for (int j = 0; j < T::NSide::kInstr; ++j)
@@ -522,14 +556,13 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(LinearArgs a) {
             }
         }
         op.wm.step = BWD ? (int64_t)kStepK * a.ldw : kStepK;
-    }
-    if constexpr (O != kMixed) {
         op.wn.step = kStepK;
         op.wm.left = op.wn.left = a.k;
     }
     op.main_left = op.main_steps = main;
-    const bool early = O != kMixed && main >= kAhead<T>;
+    const bool early = O == kWide && main >= kAhead<T>;
     if constexpr (O == kMixed) mixed_begin(walk, walk.steps(), g_lds);
+    if constexpr (O == kCodes) mma_begin<T>(walk, walk.steps(), g_lds);
     if (early) mma_begin<A>(op, main, g_lds);
 
     // while they land: the tile's tokens and ids, and the adapters it meets
@@ -573,6 +606,31 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(LinearArgs a) {
                 op.sl1 = i + 1;
             }
     }
+    // codes: the biases of the tile's columns, added up for each of a few adapters while the
+    // first copies land (read a lane at a time at the end they took 10 of 165 us of 8192
+    // tokens by 6144 columns over 4096)
+    constexpr int kBiasRows = O == kWide ? 1 : 5, kBiasCols = O == kWide ? 1 : T::BM;
+    __shared__ __attribute__((aligned(16))) float s_bias[kBiasRows][kBiasCols];   // no adapter, then by segment
+    __shared__ int s_which[O == kWide ? 1 : T::BN];
+    const bool table = O != kWide && (a.has_bias ? nseg < kBiasRows : a.w_bias != nullptr);
+    if (table) {
+        for (int i = tid; i < (a.has_bias ? nseg + 1 : 1) * T::BM; i += T::kThreads) {
+            const int e = i / T::BM, c = m0 + i % T::BM;
+            float v = a.w_bias && c < a.cols ? bf16_bits_to_float(a.w_bias[c]) : 0.f;
+            for (int q = op.sl0; e > 0 && q < op.sl1; ++q) {
+                const int in = c - select_slice(a.col, q), wide = select_slice(a.width, q);
+                const uint16_t *b = select_slice(a.bias, q);
+                if (b && in >= 0 && in < wide) v += bf16_bits_to_float(b[(int64_t)s_seg[e - 1].id * wide + in]);
+            }
+            s_bias[e % kBiasRows][(c - m0) % kBiasCols] = v;
+        }
+        if (tid < T::BN) {
+            int e = 0;
+            for (int q = 0; a.has_bias && q < nseg; ++q)
+                if (tid >= s_seg[q].lo && tid < s_seg[q].hi) e = q + 1;
+            s_which[O == kWide ? 0 : tid] = e;
+        }
+    }
     const bool dots = kDots && nseg >= kDotSegs<BWD>;
     const int units = op.sl1 > op.sl0 && !dots ? nseg * (op.sl1 - op.sl0) * op.per_seg() : 0;
     const int steps = main + (op.blocks ? units : (units + 1) / 2);
@@ -580,8 +638,23 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(LinearArgs a) {
     typename T::Acc acc;
     clear<T>(acc);
     if constexpr (O == kMixed) mixed_loop(walk, walk.steps(), acc, g_lds);
-    if (!early) mma_begin<A>(op, steps, g_lds);
-    mma_loop<A>(op, O == kMixed ? 0 : a.k / kStepK, steps, acc, g_lds);
+    if constexpr (O == kCodes) {
+        mma_loop<T>(walk, a.k / kStepK, walk.steps(), acc, g_lds);
+        __syncthreads();   // every wave is done with the stages
+    }
+    bool whole = false;
+    if constexpr (O == kCodes) {
+        whole = op.blocks > 0 && nseg == 1 && scalar(s_seg[0].lo) == 0 && scalar(s_seg[0].hi) == rows;
+        if (whole) {
+            WholeOp<A, decltype(op)> one(op);
+            mma_begin<A>(one, steps, g_lds);
+            mma_loop<A>(one, 0, steps, acc, g_lds);
+        }
+    }
+    if (!whole) {
+        if (!early) mma_begin<A>(op, steps, g_lds);
+        mma_loop<A>(op, O == kWide ? a.k / kStepK : 0, steps, acc, g_lds);
+    }
 
     if constexpr (kDots)
         if (dots)
@@ -598,6 +671,18 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(LinearArgs a) {
         for (int mt = 0; mt < T::MT; mt += 2) {
             const int c = m0 + T::m_of(mt);
             if (c >= a.cols) continue;
+            if (table) {
+#pragma unroll
+                for (int nt = 0; nt < T::NT; ++nt) {
+                    const int r = T::n_of(nt);
+                    const floatx4 *b = reinterpret_cast<const floatx4 *>(&s_bias[s_which[r]][T::m_of(mt)]);
+                    const floatx4 v = acc[mt][nt] + b[0], w = acc[mt + 1][nt] + b[1];
+                    if (r < rows)
+                        *reinterpret_cast<u32x4 *>(a.y + (int64_t)s_tok[r] * a.ldy + c) =
+                            u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3])};
+                }
+                continue;
+            }
             float wb[8];
 #pragma unroll
             for (int x = 0; x < 8; ++x) wb[x] = 0.f;
@@ -1277,12 +1362,16 @@ struct LinearPlan {
 // of the last two lists: 65, and 118 with 32 adapters).  K is not split: joining
 // fp32 partial tiles across XCDs took 22 of the 70 us of a product of 256 tokens by
 // 6144 columns over 4096.
-LinearPlan plan_linear(long n, long cols) {
+// Codes on both sides take 128 x 128 tiles where numbers take 256 x 256 (big false): a
+// walk has a quarter of the steps, so that a tile's start and end count, which two
+// workgroups a CU cover for each other: 8192 by 6144 over 4096 124 us, 8 adapters of
+// rank 64 154, 256 x 256 tiles 134 and 179; over 16384 458 and 404.
+LinearPlan plan_linear(long n, long cols, bool big = true) {
     auto tiles = [&](long bm, long bn) { return ceil_div(cols, bm) * ceil_div(n, bn); };
     LinearPlan p;
     long bm = 64, bn = 64;
     p.tile = kSmall;
-    if (n > 128 && tiles(256, 256) >= 192) {
+    if (big && n > 128 && tiles(256, 256) >= 192) {
         p.tile = kBig;
         bm = bn = 256;
     } else if (tiles(128, 128) >= 224) {
@@ -1417,7 +1506,7 @@ hipError_t launch_pack(const lora_meta_t *meta, const MetaView &view, const floa
 
 template <bool BWD, Operands O>
 hipError_t launch_linear(LinearArgs &a, hipStream_t s) {
-    const LinearPlan p = plan_linear(a.num_tokens, a.cols);
+    const LinearPlan p = plan_linear(a.num_tokens, a.cols, O != kCodes);
     a.mtiles = p.mtiles;
     a.ntiles = p.ntiles;
     a.group = 8;
@@ -1435,7 +1524,10 @@ hipError_t launch_linear(LinearArgs &a, hipStream_t s) {
             return launch_tiles<linear_kernel<B, BWD, O>>(grid, B::kThreads, B::kLds, s, a);
         }
     };
-    if constexpr (O == kMixed) {
+    if constexpr (O == kCodes) {
+        if (p.tile == kMid) return launch(Tile<128, 128, 2, 2, BWD, false>{});
+        return launch(Tile<64, 64, 1, 4, BWD, false, 0, 4>{});
+    } else if constexpr (O == kMixed) {
         return launch(Tile<64, 64, 2, 2, BWD, false, 0, 3>{});   // (four and six stages: the same)
     } else {
         switch (p.tile) {
