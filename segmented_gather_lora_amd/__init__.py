@@ -858,7 +858,9 @@ class LoraGradients:
         self._marshal()
 
     def _where(self) -> list:
-        return [t.data_ptr() for t in self.grads], None if self.out is self.grads else [t.data_ptr() for t in self.out]
+        import torch
+        at = torch.Tensor.data_ptr
+        return list(map(at, self.grads)), None if self.out is self.grads else list(map(at, self.out))
 
     def _marshal(self) -> None:
         where, n = "LoraGradients", len(self.grads)

@@ -9,8 +9,11 @@
 // piece's sum of squares, the second adds a group's sums in their order (every
 // workgroup for itself: the same order, so the same bits) and scales the piece.
 // Both are bound by the bytes: read once for the norm, read and written once
-// for the scaling, which walks the pieces backwards, so that what the first
-// launch read last is still in the last-level cache.
+// for the scaling.  Where they are more than the last-level cache holds, the scaling
+// walks the pieces backwards, from what the first launch read last, and all else is read
+// and written past the cache: the gradients of 128 adapters of rank 128 (1.14 GB of
+// bfloat16) take 167 and 413 us, 6.8 and 5.5 TB/s; without either 227 and 425, with the
+// walk alone 209 and 418.
 //
 // Squares and sums are double: the square of a float32 may be beyond float32, and
 // the rate (a conversion and a multiply-add an element) is far from a bound.
@@ -25,12 +28,16 @@
 namespace lora {
 namespace {
 
-constexpr int kThreads = 256, kTensors = 120;   // tensors a launch takes: its arguments stay below 4 KB
+constexpr int kThreads = 256;
+constexpr size_t kArgBytes = 4000;               // of a launch, for its tensors' descriptions
 constexpr long kMinPiece = 32 << 10, kMaxPiece = 256 << 10, kPieces = 4096;   // bytes; pieces that are enough
 // Partial sums of a group that every workgroup adds up by itself; more are added
 // once, by a launch of their own.
 constexpr int kSelfSums = 2048;
 constexpr int64_t kMaxUnits = 1 << 23;   // workgroups of a launch
+// Gradients of so many bytes do not stay in the 256 MB of last-level cache from one
+// launch to the next; the end that the first launch leaves there.
+constexpr int64_t kStreamBytes = 192 << 20, kKeptBytes = 160 << 20;
 
 // A factor as two floats, v * first * second: one below 2^-60 by itself could be
 // subnormal and have lost its digits.
@@ -42,19 +49,24 @@ struct Factor {
 
 struct ClipTensor {
     const void *in;
-    void *out;
-    int64_t part;        // elements of one group
-    int32_t first;       // first piece (of a group) of this tensor, counted over the call's tensors
-    int32_t type;
+    uint32_t part;       // elements of one group
+    uint32_t first;      // first piece (of a group) of this tensor, counted over the call's tensors; top bit: float32
 };
-struct ClipArgs {
-    ClipTensor t[kTensors];
+// What every launch has, and its tensors: results of their own (OUT), or in place.
+struct ClipCall {
     double *sums;        // [groups][pieces of a group]
     Factor *factors;     // [groups] where a launch of its own makes them, or NULL
     float *norms;
     double max_norm;
-    int32_t count, groups, first, pieces, all_pieces;   // tensors; pieces of a group: first of this launch, of it, of the call
-    int32_t piece;       // bytes
+    int32_t count, first, pieces, all_pieces;   // tensors; pieces of a group: first of this launch, of it, of the call
+    int32_t piece, stream;                      // bytes of a piece; more than the cache holds
+};
+template <bool OUT>
+struct ClipArgs {
+    static constexpr int kTensors = (int)((kArgBytes - sizeof(ClipCall)) / (sizeof(ClipTensor) + (OUT ? sizeof(void *) : 0)));
+    ClipCall c;
+    ClipTensor t[kTensors];
+    void *out[OUT ? kTensors : 1];
 };
 
 template <class F>
@@ -108,26 +120,28 @@ __device__ __forceinline__ double workgroup_sum(double v) {
 
 struct Piece {
     int tensor, group, index;    // index: of the group's pieces, over the call
-    int64_t at;                  // first element of the tensor
-    int64_t count;
+    bool wide;                   // float32
+    int64_t at, count;           // first element of the tensor, elements
 };
-__device__ __forceinline__ Piece piece_at(const ClipArgs &a, int64_t unit) {
+template <class A>
+__device__ __forceinline__ Piece piece_at(const A &a, int64_t unit) {
     Piece p;
-    p.group = (int)(unit / a.pieces);
-    p.index = a.first + (int)(unit - (int64_t)p.group * a.pieces);
-    int lo = 0, hi = a.count;
+    p.group = (int)(unit / a.c.pieces);
+    p.index = a.c.first + (int)(unit - (int64_t)p.group * a.c.pieces);
+    int lo = 0, hi = a.c.count;
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
-        if (a.t[mid].first <= p.index)
+        if ((int)(a.t[mid].first & 0x7fffffffu) <= p.index)
             lo = mid;
         else
             hi = mid;
     }
     p.tensor = lo;
-    const int64_t each = a.piece / (a.t[lo].type == LORA_BF16 ? 2 : 4), part = a.t[lo].part;
-    const int64_t in = (p.index - a.t[lo].first) * each;
-    p.at = p.group * part + in;
-    p.count = part - in < each ? part - in : each;
+    const ClipTensor t = a.t[lo];
+    p.wide = t.first >> 31 != 0;
+    const int64_t each = a.c.piece / (p.wide ? 4 : 2), in = (p.index - (int)(t.first & 0x7fffffffu)) * each;
+    p.at = (int64_t)p.group * t.part + in;
+    p.count = t.part - in < each ? t.part - in : each;
     return p;
 }
 
@@ -140,7 +154,20 @@ __device__ __forceinline__ int64_t head_of(const F *p, int64_t count) {
 
 constexpr int kBatch = 8;   // vectors of a thread in flight
 
-template <class F>
+// PAST: past the last-level cache.
+template <bool PAST>
+__device__ __forceinline__ u32x4 load(const u32x4 *p) {
+    return PAST ? __builtin_nontemporal_load(p) : *p;
+}
+template <bool PAST>
+__device__ __forceinline__ void put(u32x4 *p, const u32x4 &v) {
+    if (PAST)
+        __builtin_nontemporal_store(v, p);
+    else
+        *p = v;
+}
+
+template <bool PAST, class F>
 __device__ __forceinline__ double squares(const F *p, int64_t count) {
     const int tid = threadIdx.x;
     double sum = 0.0;
@@ -156,7 +183,7 @@ __device__ __forceinline__ double squares(const F *p, int64_t count) {
     for (; i + (kBatch - 1) * kThreads < vectors; i += kBatch * kThreads) {
         u32x4 v[kBatch];
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) v[b] = q[i + b * kThreads];
+        for (int b = 0; b < kBatch; ++b) v[b] = load<PAST>(q + i + b * kThreads);
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) add_vector(v[b], sum, F());
     }
@@ -169,7 +196,7 @@ __device__ __forceinline__ double squares(const F *p, int64_t count) {
     return sum;
 }
 
-template <class F>
+template <bool PAST, class F>
 __device__ __forceinline__ void scale_piece(const F *p, F *o, int64_t count, Factor f) {
     const int tid = threadIdx.x;
     if (((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(o)) & 15) != 0) {
@@ -186,61 +213,79 @@ __device__ __forceinline__ void scale_piece(const F *p, F *o, int64_t count, Fac
     for (; i + (kBatch - 1) * kThreads < vectors; i += kBatch * kThreads) {
         u32x4 v[kBatch];
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) v[b] = q[i + b * kThreads];
+        for (int b = 0; b < kBatch; ++b) v[b] = load<PAST>(q + i + b * kThreads);
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) r[i + b * kThreads] = scaled(v[b], f, F());
+        for (int b = 0; b < kBatch; ++b) put<PAST>(r + i + b * kThreads, scaled(v[b], f, F()));
     }
     for (; i < vectors; i += kThreads) r[i] = scaled(q[i], f, F());
     const int64_t rest = head + vectors * kVec + tid;
     if (rest < count) store(o + rest, f.of(value(p[rest])));
 }
 
-__global__ __launch_bounds__(kThreads) void squares_kernel(ClipArgs a) {
+__global__ __launch_bounds__(kThreads) void squares_kernel(ClipArgs<false> a) {
     const Piece p = piece_at(a, blockIdx.x);
-    const ClipTensor &t = a.t[p.tensor];
-    double sum = t.type == LORA_BF16 ? squares(static_cast<const uint16_t *>(t.in) + p.at, p.count)
-                                     : squares(static_cast<const float *>(t.in) + p.at, p.count);
+    const uint16_t *half = static_cast<const uint16_t *>(a.t[p.tensor].in) + p.at;
+    const float *wide = static_cast<const float *>(a.t[p.tensor].in) + p.at;
+    const bool past = a.c.stream && (int64_t)(gridDim.x - blockIdx.x) * a.c.piece > kKeptBytes;
+    double sum;
+    if (past)
+        sum = p.wide ? squares<true>(wide, p.count) : squares<true>(half, p.count);
+    else
+        sum = p.wide ? squares<false>(wide, p.count) : squares<false>(half, p.count);
     sum = workgroup_sum(sum);
-    if (threadIdx.x == 0) a.sums[(int64_t)p.group * a.all_pieces + p.index] = sum;
+    if (threadIdx.x == 0) a.c.sums[(int64_t)p.group * a.c.all_pieces + p.index] = sum;
 }
 
 // A group's norm and factor; 1 where its gradients stay as they are (also where the norm is not finite).
-__device__ __forceinline__ Factor factor_of(const ClipArgs &a, int group, float &norm) {
-    const double *sums = a.sums + (int64_t)group * a.all_pieces;
+__device__ __forceinline__ Factor factor_of(const ClipCall &c, int group, float &norm) {
+    const double *sums = c.sums + (int64_t)group * c.all_pieces;
     double v = 0.0;
-    for (int i = threadIdx.x; i < a.all_pieces; i += kThreads) v += sums[i];
+    for (int i = threadIdx.x; i < c.all_pieces; i += kThreads) v += sums[i];
     const double n = sqrt(workgroup_sum(v));
     norm = (float)n;
-    const double f = a.max_norm / (n + 1e-6);
+    const double f = c.max_norm / (n + 1e-6);
     if (!(n < __builtin_huge_val() && f < 1.0)) return Factor{1.f, 1.f};
     return f < 0x1p-60 ? Factor{(float)(f * 0x1p60), 0x1p-60f} : Factor{(float)f, 1.f};
 }
 
-__global__ __launch_bounds__(kThreads) void factors_kernel(ClipArgs a) {
+__global__ __launch_bounds__(kThreads) void factors_kernel(ClipCall c) {
     float norm;
-    const Factor f = factor_of(a, blockIdx.x, norm);
+    const Factor f = factor_of(c, blockIdx.x, norm);
     if (threadIdx.x == 0) {
-        a.norms[blockIdx.x] = norm;
-        if (a.factors) a.factors[blockIdx.x] = f;
+        c.norms[blockIdx.x] = norm;
+        if (c.factors) c.factors[blockIdx.x] = f;
     }
 }
 
-__global__ __launch_bounds__(kThreads) void scale_kernel(ClipArgs a) {
+template <bool OUT>
+__global__ __launch_bounds__(kThreads) void scale_kernel(ClipArgs<OUT> a) {
     const Piece p = piece_at(a, (int64_t)gridDim.x - 1 - blockIdx.x);
-    const ClipTensor &t = a.t[p.tensor];
     Factor f;
-    if (a.factors) {
-        f = a.factors[p.group];
+    if (a.c.factors) {
+        f = a.c.factors[p.group];
     } else {
         float norm;
-        f = factor_of(a, p.group, norm);
-        if (p.index == 0 && threadIdx.x == 0) a.norms[p.group] = norm;
+        f = factor_of(a.c, p.group, norm);
+        if (p.index == 0 && threadIdx.x == 0) a.c.norms[p.group] = norm;
     }
-    if (f.one() && t.in == t.out) return;
-    if (t.type == LORA_BF16)
-        scale_piece(static_cast<const uint16_t *>(t.in) + p.at, static_cast<uint16_t *>(t.out) + p.at, p.count, f);
-    else
-        scale_piece(static_cast<const float *>(t.in) + p.at, static_cast<float *>(t.out) + p.at, p.count, f);
+    const void *in = a.t[p.tensor].in;
+    void *out = OUT ? a.out[p.tensor] : const_cast<void *>(in);
+    if (f.one() && in == out) return;
+    const uint16_t *half = static_cast<const uint16_t *>(in) + p.at;
+    const float *wide = static_cast<const float *>(in) + p.at;
+    uint16_t *half_out = static_cast<uint16_t *>(out) + p.at;
+    float *wide_out = static_cast<float *>(out) + p.at;
+    if (a.c.stream) {
+        if (p.wide)
+            scale_piece<true>(wide, wide_out, p.count, f);
+        else
+            scale_piece<true>(half, half_out, p.count, f);
+    } else {
+        if (p.wide)
+            scale_piece<false>(wide, wide_out, p.count, f);
+        else
+            scale_piece<false>(half, half_out, p.count, f);
+    }
 }
 
 int size_of(int type) { return type == LORA_BF16 ? 2 : 4; }
@@ -250,13 +295,14 @@ int check_tensors(const int64_t *sizes, const int *types, int num_tensors, int g
     if (num_tensors < 0 || num_tensors > LORA_MAX_TENSORS) return LORA_ERR_SLICES;
     if (num_tensors && (!sizes || !types)) return LORA_ERR_NULL;
     for (int i = 0; i < num_tensors; ++i)
-        if (sizes[i] < 0 || sizes[i] % groups || sizes[i] > ((int64_t)1 << 40) || (types[i] != LORA_BF16 && types[i] != LORA_F32))
+        if (sizes[i] < 0 || sizes[i] % groups || sizes[i] / groups > UINT32_MAX || (types[i] != LORA_BF16 && types[i] != LORA_F32))
             return LORA_ERR_SHAPE;
     return LORA_OK;
 }
 
 struct ClipPlan {
     int64_t piece, pieces;     // bytes; pieces of a group
+    bool stream;
     size_t factors, total;     // workspace
 };
 ClipPlan plan_clip(const int64_t *sizes, const int *types, int num_tensors, int groups) {
@@ -265,6 +311,7 @@ ClipPlan plan_clip(const int64_t *sizes, const int *types, int num_tensors, int 
     for (int i = 0; i < num_tensors; ++i) bytes += (double)sizes[i] * size_of(types[i]);
     p.piece = kMinPiece;
     while (p.piece < kMaxPiece && (double)p.piece * kPieces < bytes) p.piece *= 2;
+    p.stream = bytes > (double)kStreamBytes;
     p.pieces = 0;
     for (int i = 0; i < num_tensors; ++i) {
         const int64_t part = sizes[i] / groups * size_of(types[i]);
@@ -273,6 +320,64 @@ ClipPlan plan_clip(const int64_t *sizes, const int *types, int num_tensors, int 
     p.factors = ((size_t)p.pieces * groups * sizeof(double) + 255) / 256 * 256;
     p.total = p.factors + ((size_t)groups * sizeof(Factor) + 255) / 256 * 256;
     return p;
+}
+
+// Whether no two results share memory: one in two places would be scaled twice, or by
+// whoever comes last.  (Buffers made one after the other are in order: no sort.)
+bool apart(void *const *out, const int64_t *sizes, const int *types, int num_tensors) {
+    uintptr_t last = 0;
+    bool ordered = true;
+    for (int i = 0; i < num_tensors && ordered; ++i)
+        if (sizes[i]) {
+            const uintptr_t at = reinterpret_cast<uintptr_t>(out[i]);
+            ordered = at >= last;
+            last = at + (uintptr_t)sizes[i] * (uintptr_t)size_of(types[i]);
+        }
+    if (ordered) return true;
+    std::vector<std::pair<uintptr_t, uintptr_t>> spans;
+    spans.reserve((size_t)num_tensors);
+    for (int i = 0; i < num_tensors; ++i)
+        if (sizes[i]) {
+            const uintptr_t at = reinterpret_cast<uintptr_t>(out[i]);
+            spans.emplace_back(at, at + (uintptr_t)sizes[i] * (uintptr_t)size_of(types[i]));
+        }
+    std::sort(spans.begin(), spans.end());
+    for (size_t i = 1; i < spans.size(); ++i)
+        if (spans[i].first < spans[i - 1].second) return false;
+    return true;
+}
+
+// The tensors in launches of as many as their arguments hold.
+struct ClipList {
+    const void *const *grads;
+    void *const *out;
+    const int64_t *sizes;
+    const int *types;
+    int num_tensors, groups;
+    int64_t piece;
+};
+template <bool OUT, class K>
+int each_launch(const ClipList &l, const ClipCall &c, K kernel, hipStream_t stream) {
+    ClipArgs<OUT> a;
+    a.c = c;
+    int64_t at = 0;
+    for (int i = 0; i < l.num_tensors;) {
+        a.c.count = 0;
+        a.c.first = (int32_t)at;
+        for (; i < l.num_tensors && a.c.count < ClipArgs<OUT>::kTensors; ++i) {
+            const int64_t part = l.sizes[i] / l.groups;
+            if (part == 0) continue;
+            a.t[a.c.count] = ClipTensor{l.grads[i], (uint32_t)part, (uint32_t)at | (l.types[i] == LORA_F32 ? 0x80000000u : 0u)};
+            if (OUT) a.out[a.c.count] = l.out[i];
+            ++a.c.count;
+            at += (part * size_of(l.types[i]) + l.piece - 1) / l.piece;
+        }
+        a.c.pieces = (int32_t)(at - a.c.first);
+        if (a.c.count == 0) break;
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(a.c.pieces * (int64_t)l.groups)), dim3(kThreads), 0, stream, a);
+        if (hipGetLastError() != hipSuccess) return LORA_ERR_LAUNCH;
+    }
+    return LORA_OK;
 }
 
 }  // namespace
@@ -306,60 +411,30 @@ int lora_clip_gradients(const void *const *grads, void *const *out, const int64_
             return LORA_ERR_ALIGN;
         same = same && grads[i] == out[i];
     }
-    // two results in one place would be scaled twice, or by whoever comes last
     try {
-        std::vector<std::pair<uintptr_t, uintptr_t>> spans;
-        spans.reserve((size_t)num_tensors);
-        for (int i = 0; i < num_tensors; ++i)
-            if (sizes[i]) {
-                const uintptr_t at = reinterpret_cast<uintptr_t>(out[i]);
-                spans.emplace_back(at, at + (uintptr_t)sizes[i] * (uintptr_t)size_of(types[i]));
-            }
-        std::sort(spans.begin(), spans.end());
-        for (size_t i = 1; i < spans.size(); ++i)
-            if (spans[i].first < spans[i - 1].second) return LORA_ERR_BUFFER;
-    } catch (...) {
+        if (!apart(out, sizes, types, num_tensors)) return LORA_ERR_BUFFER;
+    } catch (...) {   // (no memory for the sort)
         return LORA_ERR_SCRATCH;
     }
 
-    ClipArgs a;
-    memset(&a, 0, sizeof a);
-    a.sums = static_cast<double *>(workspace);
-    a.norms = norms;
-    a.max_norm = max_norm;
-    a.groups = groups;
-    a.all_pieces = (int32_t)p.pieces;
-    a.piece = (int32_t)p.piece;
+    ClipCall c;
+    memset(&c, 0, sizeof c);
+    c.sums = static_cast<double *>(workspace);
+    c.norms = norms;
+    c.max_norm = max_norm;
+    c.all_pieces = (int32_t)p.pieces;
+    c.piece = (int32_t)p.piece;
+    c.stream = p.stream;
     const bool only_norms = same && isinf(max_norm), own_launch = only_norms || p.pieces > kSelfSums || p.pieces == 0;
-    Factor *factors = reinterpret_cast<Factor *>(static_cast<char *>(workspace) + p.factors);
-    // the tensors in launches of kTensors each
-    auto each_launch = [&](auto kernel, Factor *given) -> int {
-        int64_t at = 0;
-        a.factors = given;
-        for (int i = 0; i < num_tensors;) {
-            a.count = 0;
-            a.first = (int32_t)at;
-            for (; i < num_tensors && a.count < kTensors; ++i) {
-                const int64_t part = sizes[i] / groups;
-                if (part == 0) continue;
-                a.t[a.count++] = ClipTensor{grads[i], out[i], part, (int32_t)at, types[i]};
-                at += (part * size_of(types[i]) + p.piece - 1) / p.piece;
-            }
-            a.pieces = (int32_t)(at - a.first);
-            if (a.count == 0) break;
-            hipLaunchKernelGGL(kernel, dim3((unsigned)(a.pieces * (int64_t)groups)), dim3(kThreads), 0, stream, a);
-            if (hipGetLastError() != hipSuccess) return LORA_ERR_LAUNCH;
-        }
-        return LORA_OK;
-    };
-    if ((st = each_launch(squares_kernel, nullptr))) return st;
+    const ClipList list = {grads, out, sizes, types, num_tensors, groups, p.piece};
+    if ((st = each_launch<false>(list, c, squares_kernel, stream))) return st;
     if (own_launch) {
-        a.factors = only_norms ? nullptr : factors;
-        hipLaunchKernelGGL(factors_kernel, dim3((unsigned)groups), dim3(kThreads), 0, stream, a);
+        if (!only_norms) c.factors = reinterpret_cast<Factor *>(static_cast<char *>(workspace) + p.factors);
+        hipLaunchKernelGGL(factors_kernel, dim3((unsigned)groups), dim3(kThreads), 0, stream, c);
         if (hipGetLastError() != hipSuccess) return LORA_ERR_LAUNCH;
         if (only_norms) return LORA_OK;
     }
-    return each_launch(scale_kernel, own_launch ? factors : nullptr);
+    return same ? each_launch<false>(list, c, scale_kernel<false>, stream) : each_launch<true>(list, c, scale_kernel<true>, stream);
 }
 
 }  // extern "C"
