@@ -86,6 +86,28 @@ __device__ __forceinline__ void split_hi_lo(float v, uint32_t &h, uint32_t &l) {
     }
 }
 
+// Rows of buf in sorted order as packed rows, by workgroup `block` of `blocks`.
+__device__ __forceinline__ void pack_rows(const PackArgs &a, int block, int blocks) {
+    const int half = packed_half(a.rank), row_len = packed_row(a.rank), per_row = row_len / 8;
+    const int64_t work = (int64_t)a.slices * a.num_tokens * per_row;
+    for (int64_t w = (int64_t)block * kPackThreads + threadIdx.x; w < work; w += (int64_t)blocks * kPackThreads) {
+        const int q = (int)(w % per_row);             // 4 ranks
+        const int64_t row = w / per_row;              // slice * n + position
+        const int p = (int)(row % a.num_tokens);
+        const int64_t slice = row / a.num_tokens;
+        const int t = a.meta.sorted[p];
+        if ((unsigned)t >= (unsigned)a.num_tokens || a.ids[t] < 0) continue;
+        floatx4 v = {0.f, 0.f, 0.f, 0.f};
+        if (4 * q < a.rank) v = *reinterpret_cast<const floatx4 *>(a.buf + (slice * a.num_tokens + t) * a.rank + 4 * q);
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split_hi_lo(v[e], h[e], l[e]);
+        uint16_t *out = a.packed + row * row_len + packed_at(4 * q, half);
+        *reinterpret_cast<u32x2g *>(out) = u32x2g{h[0] | h[1] << 16, h[2] | h[3] << 16};
+        *reinterpret_cast<u32x2g *>(out + half) = u32x2g{l[0] | l[1] << 16, l[2] | l[3] << 16};
+    }
+}
+
 // buf's rows in sorted order as packed rows, bound by its launch and bytes (13 us
 // for 16384 tokens, 3 slices of rank 128);
 // workgroup 0 also writes the tables when they are asked for, and sets the u
@@ -129,25 +151,7 @@ __global__ __launch_bounds__(kPackThreads) void pack_kernel(PackArgs a) {
             for (int o = 0; o < cnt[i]; o += a.tile_tokens, ++at)
                 if (at < a.tiles_cap) a.tiles[at] = UTile{id[i], st[i] + o, min(a.tile_tokens, cnt[i] - o), 0};
     }
-    if (none) return;
-    const int half = packed_half(a.rank), row_len = packed_row(a.rank), per_row = row_len / 8;
-    const int64_t work = (int64_t)a.slices * a.num_tokens * per_row;
-    for (int64_t w = (int64_t)blockIdx.x * kPackThreads + tid; w < work; w += (int64_t)gridDim.x * kPackThreads) {
-        const int q = (int)(w % per_row);             // 4 ranks
-        const int64_t row = w / per_row;              // slice * n + position
-        const int p = (int)(row % a.num_tokens);
-        const int64_t slice = row / a.num_tokens;
-        const int t = a.meta.sorted[p];
-        if ((unsigned)t >= (unsigned)a.num_tokens || a.ids[t] < 0) continue;
-        floatx4 v = {0.f, 0.f, 0.f, 0.f};
-        if (4 * q < a.rank) v = *reinterpret_cast<const floatx4 *>(a.buf + (slice * a.num_tokens + t) * a.rank + 4 * q);
-        uint32_t h[4], l[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) split_hi_lo(v[e], h[e], l[e]);
-        uint16_t *out = a.packed + row * row_len + packed_at(4 * q, half);
-        *reinterpret_cast<u32x2g *>(out) = u32x2g{h[0] | h[1] << 16, h[2] | h[3] << 16};
-        *reinterpret_cast<u32x2g *>(out + half) = u32x2g{l[0] | l[1] << 16, l[2] | l[3] << 16};
-    }
+    if (!none) pack_rows(a, blockIdx.x, gridDim.x);
 }
 
 // ---------------------------------------------------------------- y and dx
@@ -1332,6 +1336,95 @@ __global__ __launch_bounds__(T::kThreads, 2) void grad_kernel(GradArgs a) {
     }
 }
 
+// ---------------------------------------------------------------- both sides in 4 bits
+
+// What the product of codes with codes reads beside the matrix' own codes: the rows of
+// x in sorted order as codes, and both sides' scales in the order of ScaledTile's
+// stages, [64 rows][step of 256 numbers][512 bytes].  Bound by x' bytes (the matrix'
+// scales are 1/16 of its codes).
+struct PrepArgs {
+    const uint16_t *x;
+    int64_t ldx;
+    const int32_t *sorted, *no_lora;
+    const uint8_t *scales;
+    int64_t ldscales;
+    uint8_t *codes, *nscales, *mscales;
+    int32_t num_tokens, hidden, out, blocks, steps, x_groups;
+};
+constexpr int kPrepSteps = 8;    // of the matrix' scales, a workgroup
+using AnyScaled = ScaledTile<Tile<64, 64, 1, 4, false, false, 0, 4>>;
+
+__device__ __forceinline__ void prep(const PrepArgs &a) {
+    __shared__ __attribute__((aligned(16))) uint8_t s_scale[kPrepSteps * 512];
+    const int tid = threadIdx.x;
+    if ((int)blockIdx.x < a.x_groups * a.steps) {
+        const int group = blockIdx.x / a.steps, step = blockIdx.x % a.steps;
+        const int l = tid % kMxGroup, g = tid / kMxGroup;
+        constexpr int kPer = 64 * 2 / (kMxThreads / kMxGroup);
+        const bool none = *a.no_lora != 0;
+        float v[kPer][8];
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) {
+            const int i = q * (kMxThreads / kMxGroup) + g, p = group * 64 + i / 2, k = step * 256 + i % 2 * 128 + 8 * l;
+            const bool in = p < a.num_tokens && k < a.hidden;
+            const int at = in && !none ? a.sorted[p] : p, t = (unsigned)at < (unsigned)a.num_tokens ? at : 0;
+            mx_load(a.x + t * a.ldx + k, in, v[q]);
+        }
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) {
+            const int i = q * (kMxThreads / kMxGroup) + g, r = i / 2, p = group * 64 + r, b = i % 2 * 4 + l / 4;
+            uint32_t top = 0;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) top = max(top, __float_as_uint(v[q][x]) & 0x7fffffffu);
+            top = max(top, (uint32_t)__shfl_xor((int)top, 1));
+            top = max(top, (uint32_t)__shfl_xor((int)top, 2));
+            const int scale = mx_scale_of(top);
+            if (l % 4 == 0) s_scale[AnyScaled::scale_at(false, r, b)] = (uint8_t)scale;
+            if (p < a.num_tokens && step * 8 + b < a.blocks)
+                *reinterpret_cast<uint32_t *>(a.codes + ((int64_t)p * a.blocks + step * 8 + b) * 16 + l % 4 * 4) = mx_codes_of(v[q], scale);
+        }
+        __syncthreads();
+        if (tid < 32)
+            *reinterpret_cast<u32x4 *>(a.nscales + ((int64_t)group * a.steps + step) * 512 + 16 * tid) =
+                *reinterpret_cast<const u32x4 *>(s_scale + 16 * tid);
+        return;
+    }
+    const int chunks = (a.steps + kPrepSteps - 1) / kPrepSteps, u = blockIdx.x - a.x_groups * a.steps;
+    const int group = u / chunks, step0 = u % chunks * kPrepSteps;
+#pragma unroll
+    for (int q = 0; q < 64 * kPrepSteps * 2 / kMxThreads; ++q) {
+        const int i = q * kMxThreads + tid, r = i / (kPrepSteps * 2), d = i % (kPrepSteps * 2), b = (step0 * 2 + d) * 4;
+        const int64_t row = min(group * 64 + r, a.out - 1);
+        const uint32_t v = b < a.blocks ? *reinterpret_cast<const uint32_t *>(a.scales + row * a.ldscales + b) : 0u;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)   // (past the last block: any power, the codes are zeros there)
+            s_scale[d / 2 * 512 + AnyScaled::scale_at(true, r, d % 2 * 4 + x)] = b + x < a.blocks ? (uint8_t)(v >> 8 * x) : 0;
+    }
+    __syncthreads();
+    if (step0 + tid / 32 < a.steps)
+        *reinterpret_cast<u32x4 *>(a.mscales + ((int64_t)group * a.steps + step0) * 512 + 16 * tid) =
+            *reinterpret_cast<const u32x4 *>(s_scale + 16 * tid);
+}
+
+__host__ __device__ inline unsigned prep_grid(const PrepArgs &a) {
+    return (unsigned)((long)a.x_groups * a.steps + ((a.out + 63) / 64) * (long)((a.steps + kPrepSteps - 1) / kPrepSteps));
+}
+// (templates: made where they are launched)
+template <class = void>
+__global__ __launch_bounds__(kMxThreads) void prep_kernel(PrepArgs a) {
+    prep(a);
+}
+// The same and the adapters' packed rows, which it does not need, in one launch.
+template <class = void>
+__global__ __launch_bounds__(kMxThreads) void prep_pack_kernel(PrepArgs a, PackArgs p) {
+    const int blocks = prep_grid(a);
+    if ((int)blockIdx.x < blocks)
+        prep(a);
+    else if (*p.meta.no_lora == 0)
+        pack_rows(p, blockIdx.x - blocks, gridDim.x - blocks);
+}
+static_assert(kMxThreads == kPackThreads, "one block size");
+
 // ---------------------------------------------------------------- plans
 
 constexpr size_t kRound = 256;
@@ -1476,14 +1569,25 @@ int widest(const int *w, int n) {
     return s;
 }
 
-hipError_t launch_pack(const lora_meta_t *meta, const MetaView &view, const float *buf, uint16_t *packed, int slices,
-                       int rank, char *ws, const Layout *l, const UPlan *u, hipStream_t s) {
+unsigned pack_grid(const PackArgs &a) {
+    const long grid = ceil_div((long)a.slices * a.num_tokens * (packed_row(a.rank) / 8), kPackThreads);
+    return (unsigned)(grid > 2048 ? 2048 : grid < 1 ? 1 : grid);
+}
+PackArgs pack_args(const lora_meta_t *meta, const MetaView &view, const float *buf, uint16_t *packed, int slices, int rank) {
     PackArgs a;
     memset(&a, 0, sizeof a);
     a.meta = view;
     a.ids = meta->token_lora_mapping;
     a.buf = buf;
     a.packed = packed;
+    a.num_tokens = meta->num_tokens;
+    a.rank = rank;
+    a.slices = slices;
+    a.max_loras = meta->max_loras;
+    return a;
+}
+// With the tables of the backward pass (l, u), or packed rows alone.
+hipError_t launch_pack(PackArgs a, char *ws, const Layout *l, const UPlan *u, hipStream_t s) {
     if (l) {
         a.segs = reinterpret_cast<SegEntry *>(ws + l->segs);
         a.tiles = reinterpret_cast<UTile *>(ws + l->tiles);
@@ -1492,15 +1596,7 @@ hipError_t launch_pack(const lora_meta_t *meta, const MetaView &view, const floa
         a.tiles_cap = u->tiles_cap;
         a.tile_tokens = u->tile_tokens;
     }
-    a.num_tokens = meta->num_tokens;
-    a.rank = rank;
-    a.slices = slices;
-    a.max_loras = meta->max_loras;
-    const long work = (long)slices * meta->num_tokens * (packed_row(rank) / 8);
-    long grid = ceil_div(work, kPackThreads);
-    if (grid > 2048) grid = 2048;
-    if (grid < 1) grid = 1;
-    hipLaunchKernelGGL(pack_kernel, dim3((unsigned)grid), dim3(kPackThreads), 0, s, a);
+    hipLaunchKernelGGL(pack_kernel, dim3(pack_grid(a)), dim3(kPackThreads), 0, s, a);
     return hipGetLastError();
 }
 
@@ -1578,6 +1674,7 @@ struct LinearCall {
     int64_t ldx, ldin;
     const uint8_t *mscales, *nscales;
     int64_t ldscales;
+    const PrepArgs *prep;         // codes: what makes x' (but for few tokens)
     int k;                        // of W's product, in elements of `in` and `w`
     const void *w;
     int64_t ldw;
@@ -1642,11 +1739,20 @@ int linear_forward(const LinearCall &c, const Layout &l, float *buf, void *y, in
                 launch(rows_codes_kernel<1, O == kCodes>, rows_codes_kernel<2, O == kCodes>);
             return hipGetLastError() == hipSuccess ? LORA_OK : LORA_ERR_LAUNCH;
         }
+        if constexpr (O == kCodes) {
+            hipLaunchKernelGGL(prep_kernel<>, dim3(prep_grid(*c.prep)), dim3(kPackThreads), 0, c.stream, *c.prep);
+            if (hipGetLastError() != hipSuccess) return LORA_ERR_LAUNCH;
+        }
     } else {
         const int st = shrink_fresh(c.x, c.ldx, c.num_tokens, c.hidden, c.lora_a, c.slices, c.rank, buf, c.meta, c.scale, c.stream);
         if (st) return st;
-        if (launch_pack(c.meta, view, buf, packed, c.slices, c.rank, c.ws, nullptr, nullptr, c.stream) != hipSuccess)
+        const PackArgs pack = pack_args(c.meta, view, buf, packed, c.slices, c.rank);
+        if constexpr (O == kCodes) {
+            hipLaunchKernelGGL(prep_pack_kernel<>, dim3(prep_grid(*c.prep) + pack_grid(pack)), dim3(kPackThreads), 0, c.stream, *c.prep, pack);
+            if (hipGetLastError() != hipSuccess) return LORA_ERR_LAUNCH;
+        } else if (launch_pack(pack, c.ws, nullptr, nullptr, c.stream) != hipSuccess) {
             return LORA_ERR_LAUNCH;
+        }
     }
     LinearArgs a;
     memset(&a, 0, sizeof a);
@@ -1724,7 +1830,7 @@ int linear_backward(const LinearCall &c, const Layout &l, const UPlan &u, const 
     const MetaView view = view_of(c.meta);
     uint16_t *s = reinterpret_cast<uint16_t *>(ws + l.s), *up = reinterpret_cast<uint16_t *>(ws + l.u);
     // (an empty batch still writes the adapters' gradients: zeros)
-    if (launch_pack(c.meta, view, q.buf, s, c.slices, c.rank, ws, &l, &u, c.stream) != hipSuccess) return LORA_ERR_LAUNCH;
+    if (launch_pack(pack_args(c.meta, view, q.buf, s, c.slices, c.rank), ws, &l, &u, c.stream) != hipSuccess) return LORA_ERR_LAUNCH;
     int cols[LORA_MAX_SLICES], off = c.offset;
     for (int i = 0; i < c.slices; ++i) {
         cols[i] = off;

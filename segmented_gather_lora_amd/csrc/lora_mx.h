@@ -60,6 +60,26 @@ __device__ __forceinline__ u32x4 mx_numbers(uint32_t codes, uint32_t scale) {
                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 3))};
 }
 
+// Sixteen lanes take 128 numbers of a row, 8 each, and with them one dword of
+// scales; a lane's codes are a dword.
+constexpr int kMxThreads = 256, kMxGroup = 16, kMxSpan = 128, kMxPer = 2;
+
+// 8 numbers of a row as float bits, zeros past its end (which is a multiple of 8).
+__device__ __forceinline__ void mx_load(const uint16_t *p, bool in, float v[8]) {
+    const u32x4 q = in ? *reinterpret_cast<const u32x4 *>(p) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int x = 0; x < 4; ++x) unpack_bf16(q[x], v[2 * x], v[2 * x + 1]);
+}
+__device__ __forceinline__ void mx_load(const float *p, bool in, float v[8]) {
+    const floatx4 z = {0.f, 0.f, 0.f, 0.f};
+    const floatx4 a = in ? *reinterpret_cast<const floatx4 *>(p) : z, b = in ? *reinterpret_cast<const floatx4 *>(p + 4) : z;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        v[x] = a[x];
+        v[4 + x] = b[x];
+    }
+}
+
 // A tile whose M side is codes and whose N side is bf16, K in steps of 128, for batches
 // that neither the MFMA nor memory bounds: what counts is that copies, reads,
 // conversions and MFMAs of different steps overlap, since a SIMD has one or two waves.

@@ -8,10 +8,6 @@ using namespace lora;
 namespace lora {
 namespace {
 
-// Sixteen lanes take 128 numbers of a row, 8 each, and with them one dword of
-// scales; a lane's codes are a dword.
-constexpr int kMxThreads = 256, kMxGroup = 16, kMxSpan = 128, kMxPer = 2;
-
 struct MxArgs {
     char *x, *codes, *scales;            // x: the numbers, read or written
     int64_t ldx, ldcodes, ldscales;      // bytes
@@ -29,22 +25,6 @@ __device__ __forceinline__ MxAt mx_at(int64_t first, int i, int spans) {
     const uint32_t in = (uint32_t)(first - row0 * spans) + (uint32_t)i;
     const uint32_t r = in / (uint32_t)spans;
     return MxAt{row0 + r, (int32_t)(in - r * (uint32_t)spans)};
-}
-
-// 8 numbers of a row as float bits, zeros past its end (which is a multiple of 8).
-__device__ __forceinline__ void mx_load(const uint16_t *p, bool in, float v[8]) {
-    const u32x4 q = in ? *reinterpret_cast<const u32x4 *>(p) : u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int x = 0; x < 4; ++x) unpack_bf16(q[x], v[2 * x], v[2 * x + 1]);
-}
-__device__ __forceinline__ void mx_load(const float *p, bool in, float v[8]) {
-    const floatx4 z = {0.f, 0.f, 0.f, 0.f};
-    const floatx4 a = in ? *reinterpret_cast<const floatx4 *>(p) : z, b = in ? *reinterpret_cast<const floatx4 *>(p + 4) : z;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-        v[x] = a[x];
-        v[4 + x] = b[x];
-    }
 }
 
 // Bound by the bytes.
@@ -166,76 +146,6 @@ hipError_t launch_mx(const void *x, int type, int64_t ldx, int64_t rows, int col
     return hipSuccess;
 }
 
-// ---------------------------------------------------------------- both sides in 4 bits
-
-// What the product of codes with codes reads beside the matrix' own codes: the rows of
-// x in sorted order as codes, and both sides' scales in the order of ScaledTile's
-// stages, [64 rows][step of 256 numbers][512 bytes].  Bound by x' bytes (the matrix'
-// scales are 1/16 of its codes).
-struct PrepArgs {
-    const uint16_t *x;
-    int64_t ldx;
-    const int32_t *sorted, *no_lora;
-    const uint8_t *scales;
-    int64_t ldscales;
-    uint8_t *codes, *nscales, *mscales;
-    int32_t num_tokens, hidden, out, blocks, steps, x_groups;
-};
-constexpr int kPrepSteps = 8;    // of the matrix' scales, a workgroup
-using AnyScaled = ScaledTile<Tile<64, 64, 1, 4, false, false, 0, 4>>;
-
-__global__ __launch_bounds__(kMxThreads) void prep_kernel(PrepArgs a) {
-    __shared__ __attribute__((aligned(16))) uint8_t s_scale[kPrepSteps * 512];
-    const int tid = threadIdx.x;
-    if ((int)blockIdx.x < a.x_groups * a.steps) {
-        const int group = blockIdx.x / a.steps, step = blockIdx.x % a.steps;
-        const int l = tid % kMxGroup, g = tid / kMxGroup;
-        constexpr int kPer = 64 * 2 / (kMxThreads / kMxGroup);
-        const bool none = *a.no_lora != 0;
-        float v[kPer][8];
-#pragma unroll
-        for (int q = 0; q < kPer; ++q) {
-            const int i = q * (kMxThreads / kMxGroup) + g, p = group * 64 + i / 2, k = step * 256 + i % 2 * 128 + 8 * l;
-            const bool in = p < a.num_tokens && k < a.hidden;
-            const int at = in && !none ? a.sorted[p] : p, t = (unsigned)at < (unsigned)a.num_tokens ? at : 0;
-            mx_load(a.x + t * a.ldx + k, in, v[q]);
-        }
-#pragma unroll
-        for (int q = 0; q < kPer; ++q) {
-            const int i = q * (kMxThreads / kMxGroup) + g, r = i / 2, p = group * 64 + r, b = i % 2 * 4 + l / 4;
-            uint32_t top = 0;
-#pragma unroll
-            for (int x = 0; x < 8; ++x) top = max(top, __float_as_uint(v[q][x]) & 0x7fffffffu);
-            top = max(top, (uint32_t)__shfl_xor((int)top, 1));
-            top = max(top, (uint32_t)__shfl_xor((int)top, 2));
-            const int scale = mx_scale_of(top);
-            if (l % 4 == 0) s_scale[AnyScaled::scale_at(false, r, b)] = (uint8_t)scale;
-            if (p < a.num_tokens && step * 8 + b < a.blocks)
-                *reinterpret_cast<uint32_t *>(a.codes + ((int64_t)p * a.blocks + step * 8 + b) * 16 + l % 4 * 4) = mx_codes_of(v[q], scale);
-        }
-        __syncthreads();
-        if (tid < 32)
-            *reinterpret_cast<u32x4 *>(a.nscales + ((int64_t)group * a.steps + step) * 512 + 16 * tid) =
-                *reinterpret_cast<const u32x4 *>(s_scale + 16 * tid);
-        return;
-    }
-    const int chunks = (a.steps + kPrepSteps - 1) / kPrepSteps, u = blockIdx.x - a.x_groups * a.steps;
-    const int group = u / chunks, step0 = u % chunks * kPrepSteps;
-#pragma unroll
-    for (int q = 0; q < 64 * kPrepSteps * 2 / kMxThreads; ++q) {
-        const int i = q * kMxThreads + tid, r = i / (kPrepSteps * 2), d = i % (kPrepSteps * 2), b = (step0 * 2 + d) * 4;
-        const int64_t row = min(group * 64 + r, a.out - 1);
-        const uint32_t v = b < a.blocks ? *reinterpret_cast<const uint32_t *>(a.scales + row * a.ldscales + b) : 0u;
-#pragma unroll
-        for (int x = 0; x < 4; ++x)   // (past the last block: any power, the codes are zeros there)
-            s_scale[d / 2 * 512 + AnyScaled::scale_at(true, r, d % 2 * 4 + x)] = b + x < a.blocks ? (uint8_t)(v >> 8 * x) : 0;
-    }
-    __syncthreads();
-    if (step0 + tid / 32 < a.steps)
-        *reinterpret_cast<u32x4 *>(a.mscales + ((int64_t)group * a.steps + step0) * 512 + 16 * tid) =
-            *reinterpret_cast<const u32x4 *>(s_scale + 16 * tid);
-}
-
 // ---------------------------------------------------------------- plans
 
 // The workspace: that of the bf16 projection, then its matrix as numbers, and what
@@ -302,7 +212,7 @@ int lora_linear_mx(const void *x, int64_t ldx, int num_tokens, int hidden, const
     if (m.total > workspace_bytes) return LORA_ERR_BUFFER;
     if (num_tokens == 0) return LORA_OK;
     char *ws = static_cast<char *>(workspace);
-    LinearCall c = {x, x, ldx, ldx, nullptr, nullptr, 0, hidden, ws + m.w, hidden, w_bias, lora_a, lora_b, bias, slice_widths, num_tokens,
+    LinearCall c = {x, x, ldx, ldx, nullptr, nullptr, 0, nullptr, hidden, ws + m.w, hidden, w_bias, lora_a, lora_b, bias, slice_widths, num_tokens,
                     hidden, out_features, num_slices, rank, offset_start, meta, scale, ws, stream};
     if (quantize_x && num_tokens > kRowsTokens) {
         PrepArgs p;
@@ -323,9 +233,6 @@ int lora_linear_mx(const void *x, int64_t ldx, int num_tokens, int hidden, const
         p.blocks = (int)mx_blocks(hidden);
         p.steps = m.steps;
         p.x_groups = (int)ceil_div(num_tokens, 64);
-        const long grid = (long)p.x_groups * m.steps + ceil_div(out_features, 64) * ceil_div(m.steps, kPrepSteps);
-        hipLaunchKernelGGL(prep_kernel, dim3((unsigned)grid), dim3(kMxThreads), 0, stream, p);
-        if (hipGetLastError() != hipSuccess) return LORA_ERR_LAUNCH;
         c.in = p.codes;
         c.ldin = 8 * (int64_t)p.blocks;
         c.w = codes;
@@ -333,6 +240,7 @@ int lora_linear_mx(const void *x, int64_t ldx, int num_tokens, int hidden, const
         c.k = 8 * p.blocks;
         c.mscales = p.mscales;
         c.nscales = p.nscales;
+        c.prep = &p;
         return linear_forward<kCodes>(c, l, buf, y, ldy);
     }
     // Where the bf16 projection takes 64 x 64 tiles, W's codes go into the product as they
@@ -371,7 +279,7 @@ int lora_linear_mx_backward(const void *dy, int64_t lddy, const void *x, int64_t
     if (dx && num_tokens > 0 &&
         launch_mx<false>(ws + m.w, LORA_BF16, hidden, out_features, hidden, codes, ldcodes, scales, ldscales, stream) != hipSuccess)
         return LORA_ERR_LAUNCH;
-    const LinearCall c = {x, x, ldx, ldx, nullptr, nullptr, 0, hidden, ws + m.w, hidden, nullptr, lora_a, lora_b, nullptr, slice_widths, num_tokens, hidden,
+    const LinearCall c = {x, x, ldx, ldx, nullptr, nullptr, 0, nullptr, hidden, ws + m.w, hidden, nullptr, lora_a, lora_b, nullptr, slice_widths, num_tokens, hidden,
                           out_features, num_slices, rank, offset_start, meta, scale, ws, stream};
     return linear_backward(c, l, u, g);
 }
