@@ -112,10 +112,10 @@ __device__ __forceinline__ void pack_rows(const PackArgs &a, int block, int bloc
 // for 16384 tokens, 3 slices of rank 128);
 // workgroup 0 also writes the tables when they are asked for, and sets the u
 // product's counters to zero.
-__global__ __launch_bounds__(kPackThreads) void pack_kernel(PackArgs a) {
+__device__ __forceinline__ void pack(const PackArgs &a, int block, int blocks) {
     const bool none = *a.meta.no_lora != 0;
     const int tid = threadIdx.x;
-    if (a.segs && blockIdx.x == 0) {
+    if (a.segs && block == 0) {
         __shared__ int s_wsum[kPackThreads / kWave];
         for (int k = tid; k < kCounterWords; k += kPackThreads) a.counters[k] = 0;
         for (int m = tid; m < a.max_loras; m += kPackThreads) a.segs[m] = SegEntry{0, 0};
@@ -151,15 +151,34 @@ __global__ __launch_bounds__(kPackThreads) void pack_kernel(PackArgs a) {
             for (int o = 0; o < cnt[i]; o += a.tile_tokens, ++at)
                 if (at < a.tiles_cap) a.tiles[at] = UTile{id[i], st[i] + o, min(a.tile_tokens, cnt[i] - o), 0};
     }
-    if (!none) pack_rows(a, blockIdx.x, gridDim.x);
+    if (!none) pack_rows(a, block, blocks);
 }
+__global__ __launch_bounds__(kPackThreads) void pack_kernel(PackArgs a) { pack(a, blockIdx.x, gridDim.x); }
 
+unsigned pack_grid(const PackArgs &a) {
+    const long grid = ((long)a.slices * a.num_tokens * (packed_row(a.rank) / 8) + kPackThreads - 1) / kPackThreads;
+    return (unsigned)(grid > 2048 ? 2048 : grid < 1 ? 1 : grid);
+}
+PackArgs pack_args(const lora_meta_t *meta, const MetaView &view, const float *buf, uint16_t *packed, int slices, int rank) {
+    PackArgs a;
+    memset(&a, 0, sizeof a);
+    a.meta = view;
+    a.ids = meta->token_lora_mapping;
+    a.buf = buf;
+    a.packed = packed;
+    a.num_tokens = meta->num_tokens;
+    a.rank = rank;
+    a.slices = slices;
+    a.max_loras = meta->max_loras;
+    return a;
+}
 // ---------------------------------------------------------------- y and dx
 
 // What the shared projection's product reads: bf16 on both sides, W's side as codes of
 // 4 bits, or both as codes (tiles: the operands' rows then hold 4 codes an element, k
-// counts such elements, and the token rows lie in sorted order already).
-enum Operands { kWide, kMixed, kCodes };
+// counts such elements, and the token rows lie in sorted order already).  kTurned: W's
+// codes are turned into numbers beforehand, for the kernels of kWide.
+enum Operands { kWide, kMixed, kCodes, kTurned };
 
 struct LinearArgs {
     MetaView meta;
@@ -1424,6 +1443,33 @@ __global__ __launch_bounds__(kMxThreads) void prep_pack_kernel(PrepArgs a, PackA
         pack_rows(p, blockIdx.x - blocks, gridDim.x - blocks);
 }
 static_assert(kMxThreads == kPackThreads, "one block size");
+// W's codes as numbers (by the first `blocks` workgroups), and the packed rows.
+template <class = void>
+__global__ __launch_bounds__(kMxThreads) void turn_pack_kernel(MxArgs m, int blocks, PackArgs p) {
+    if ((int)blockIdx.x < blocks)
+        dequantize<uint16_t>(m, blockIdx.x);
+    else
+        pack(p, blockIdx.x - blocks, gridDim.x - blocks);
+}
+// (pack NULL: W alone)
+template <class = void>
+hipError_t launch_turn(const MxArgs &m, const PackArgs *pack, hipStream_t s) {
+    PackArgs none;
+    memset(&none, 0, sizeof none);
+    const int64_t most = kMxMostBlocks * kMxSpans / m.spans;
+    for (int64_t r = 0; r < m.rows; r += most) {
+        const bool last = m.rows - r <= most;
+        MxArgs part = m;
+        part.rows = last ? m.rows - r : most;
+        part.x += r * m.ldx;
+        part.codes += r * m.ldcodes;
+        part.scales += r * m.ldscales;
+        const unsigned blocks = (unsigned)mx_grid(part);
+        hipLaunchKernelGGL(turn_pack_kernel<>, dim3(blocks + (pack && last ? pack_grid(*pack) : 0u)), dim3(kMxThreads), 0, s, part,
+                           (int)blocks, pack && last ? *pack : none);
+    }
+    return hipGetLastError();
+}
 
 // ---------------------------------------------------------------- plans
 
@@ -1569,33 +1615,16 @@ int widest(const int *w, int n) {
     return s;
 }
 
-unsigned pack_grid(const PackArgs &a) {
-    const long grid = ceil_div((long)a.slices * a.num_tokens * (packed_row(a.rank) / 8), kPackThreads);
-    return (unsigned)(grid > 2048 ? 2048 : grid < 1 ? 1 : grid);
+// The tables of the backward pass too.
+void pack_tables(PackArgs &a, char *ws, const Layout &l, const UPlan &u) {
+    a.segs = reinterpret_cast<SegEntry *>(ws + l.segs);
+    a.tiles = reinterpret_cast<UTile *>(ws + l.tiles);
+    a.num_tiles = reinterpret_cast<int32_t *>(ws + l.num_tiles);
+    a.counters = reinterpret_cast<int32_t *>(ws + l.counters);
+    a.tiles_cap = u.tiles_cap;
+    a.tile_tokens = u.tile_tokens;
 }
-PackArgs pack_args(const lora_meta_t *meta, const MetaView &view, const float *buf, uint16_t *packed, int slices, int rank) {
-    PackArgs a;
-    memset(&a, 0, sizeof a);
-    a.meta = view;
-    a.ids = meta->token_lora_mapping;
-    a.buf = buf;
-    a.packed = packed;
-    a.num_tokens = meta->num_tokens;
-    a.rank = rank;
-    a.slices = slices;
-    a.max_loras = meta->max_loras;
-    return a;
-}
-// With the tables of the backward pass (l, u), or packed rows alone.
-hipError_t launch_pack(PackArgs a, char *ws, const Layout *l, const UPlan *u, hipStream_t s) {
-    if (l) {
-        a.segs = reinterpret_cast<SegEntry *>(ws + l->segs);
-        a.tiles = reinterpret_cast<UTile *>(ws + l->tiles);
-        a.num_tiles = reinterpret_cast<int32_t *>(ws + l->num_tiles);
-        a.counters = reinterpret_cast<int32_t *>(ws + l->counters);
-        a.tiles_cap = u->tiles_cap;
-        a.tile_tokens = u->tile_tokens;
-    }
+hipError_t launch_pack(const PackArgs &a, hipStream_t s) {
     hipLaunchKernelGGL(pack_kernel, dim3(pack_grid(a)), dim3(kPackThreads), 0, s, a);
     return hipGetLastError();
 }
@@ -1675,6 +1704,7 @@ struct LinearCall {
     const uint8_t *mscales, *nscales;
     int64_t ldscales;
     const PrepArgs *prep;         // codes: what makes x' (but for few tokens)
+    const MxArgs *turn;           // turned: W's codes to `w`
     int k;                        // of W's product, in elements of `in` and `w`
     const void *w;
     int64_t ldw;
@@ -1735,7 +1765,7 @@ int linear_forward(const LinearCall &c, const Layout &l, float *buf, void *y, in
             };
             if constexpr (O == kWide)
                 launch(rows_kernel<1>, rows_kernel<2>);
-            else
+            else if constexpr (O != kTurned)   // (few tokens take the codes)
                 launch(rows_codes_kernel<1, O == kCodes>, rows_codes_kernel<2, O == kCodes>);
             return hipGetLastError() == hipSuccess ? LORA_OK : LORA_ERR_LAUNCH;
         }
@@ -1743,6 +1773,8 @@ int linear_forward(const LinearCall &c, const Layout &l, float *buf, void *y, in
             hipLaunchKernelGGL(prep_kernel<>, dim3(prep_grid(*c.prep)), dim3(kPackThreads), 0, c.stream, *c.prep);
             if (hipGetLastError() != hipSuccess) return LORA_ERR_LAUNCH;
         }
+        if constexpr (O == kTurned)
+            if (launch_turn(*c.turn, nullptr, c.stream) != hipSuccess) return LORA_ERR_LAUNCH;
     } else {
         const int st = shrink_fresh(c.x, c.ldx, c.num_tokens, c.hidden, c.lora_a, c.slices, c.rank, buf, c.meta, c.scale, c.stream);
         if (st) return st;
@@ -1750,7 +1782,9 @@ int linear_forward(const LinearCall &c, const Layout &l, float *buf, void *y, in
         if constexpr (O == kCodes) {
             hipLaunchKernelGGL(prep_pack_kernel<>, dim3(prep_grid(*c.prep) + pack_grid(pack)), dim3(kPackThreads), 0, c.stream, *c.prep, pack);
             if (hipGetLastError() != hipSuccess) return LORA_ERR_LAUNCH;
-        } else if (launch_pack(pack, c.ws, nullptr, nullptr, c.stream) != hipSuccess) {
+        } else if constexpr (O == kTurned) {
+            if (launch_turn(*c.turn, &pack, c.stream) != hipSuccess) return LORA_ERR_LAUNCH;
+        } else if (launch_pack(pack, c.stream) != hipSuccess) {
             return LORA_ERR_LAUNCH;
         }
     }
@@ -1785,7 +1819,7 @@ int linear_forward(const LinearCall &c, const Layout &l, float *buf, void *y, in
     a.rank = c.rank;
     a.slices = c.slices;
     a.max_loras = c.meta->max_loras;
-    return launch_linear<false, O>(a, c.stream) == hipSuccess ? LORA_OK : LORA_ERR_LAUNCH;
+    return launch_linear<false, O == kTurned ? kWide : O>(a, c.stream) == hipSuccess ? LORA_OK : LORA_ERR_LAUNCH;
 }
 
 // The forward pass' own checks.
@@ -1825,12 +1859,20 @@ int check_gradients(const Gradients &g, const void *x, int num_tokens, int hidde
     return LORA_OK;
 }
 
+template <Operands O>
 int linear_backward(const LinearCall &c, const Layout &l, const UPlan &u, const Gradients &q) {
     char *ws = c.ws;
     const MetaView view = view_of(c.meta);
     uint16_t *s = reinterpret_cast<uint16_t *>(ws + l.s), *up = reinterpret_cast<uint16_t *>(ws + l.u);
     // (an empty batch still writes the adapters' gradients: zeros)
-    if (launch_pack(pack_args(c.meta, view, q.buf, s, c.slices, c.rank), ws, &l, &u, c.stream) != hipSuccess) return LORA_ERR_LAUNCH;
+    PackArgs pack = pack_args(c.meta, view, q.buf, s, c.slices, c.rank);
+    pack_tables(pack, ws, l, u);
+    hipError_t packed = hipSuccess;
+    if constexpr (O == kTurned)
+        packed = q.dx && c.num_tokens > 0 ? launch_turn(*c.turn, &pack, c.stream) : launch_pack(pack, c.stream);
+    else
+        packed = launch_pack(pack, c.stream);
+    if (packed != hipSuccess) return LORA_ERR_LAUNCH;
     int cols[LORA_MAX_SLICES], off = c.offset;
     for (int i = 0; i < c.slices; ++i) {
         cols[i] = off;

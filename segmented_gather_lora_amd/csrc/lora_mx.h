@@ -4,6 +4,8 @@
 // of two plus 127.
 #pragma once
 
+#include <string.h>
+
 #include "lora_gemm.h"
 
 namespace lora {
@@ -77,6 +79,81 @@ __device__ __forceinline__ void mx_load(const float *p, bool in, float v[8]) {
     for (int x = 0; x < 4; ++x) {
         v[x] = a[x];
         v[4 + x] = b[x];
+    }
+}
+
+struct MxArgs {
+    char *x, *codes, *scales;            // x: the numbers, read or written
+    int64_t ldx, ldcodes, ldscales;      // bytes
+    int64_t rows;
+    int32_t cols, blocks, spans;         // of a row
+};
+
+// The lane's span: row and number within the row.
+struct MxAt {
+    int64_t row;
+    int32_t span;
+};
+__device__ __forceinline__ MxAt mx_at(int64_t first, int i, int spans) {
+    const int64_t row0 = first / spans;                 // (uniform)
+    const uint32_t in = (uint32_t)(first - row0 * spans) + (uint32_t)i;
+    const uint32_t r = in / (uint32_t)spans;
+    return MxAt{row0 + r, (int32_t)(in - r * (uint32_t)spans)};
+}
+
+constexpr int kMxSpans = kMxThreads / kMxGroup * kMxPer;   // of a workgroup
+constexpr int64_t kMxMostBlocks = 1 << 23;                 // a launch has fewer than 2^32 threads
+inline MxArgs mx_args(const void *x, int type, int64_t ldx, int64_t rows, int cols, const void *codes, int64_t ldcodes,
+                      const void *scales, int64_t ldscales) {
+    MxArgs a;
+    memset(&a, 0, sizeof a);
+    a.x = static_cast<char *>(const_cast<void *>(x));
+    a.codes = static_cast<char *>(const_cast<void *>(codes));
+    a.scales = static_cast<char *>(const_cast<void *>(scales));
+    a.ldx = ldx * (type == LORA_BF16 ? 2 : 4);
+    a.ldcodes = ldcodes;
+    a.ldscales = ldscales;
+    a.rows = rows;
+    a.cols = cols;
+    a.blocks = (int32_t)mx_blocks(cols);
+    a.spans = (a.blocks + 3) / 4;
+    return a;
+}
+__host__ __device__ inline int64_t mx_grid(const MxArgs &a) { return (a.rows * a.spans + kMxSpans - 1) / kMxSpans; }
+
+// Exact in float32 and bfloat16: a code has two bits and every power a place in both
+// (the smallest as a subnormal number).
+template <class F>
+__device__ __forceinline__ void dequantize(const MxArgs &a, int block) {
+    constexpr int kSpans = kMxThreads / kMxGroup;
+    const int l = threadIdx.x % kMxGroup, g = threadIdx.x / kMxGroup;
+    uint32_t c[kMxPer], s[kMxPer];
+    MxAt at[kMxPer];
+    bool in[kMxPer];
+#pragma unroll
+    for (int q = 0; q < kMxPer; ++q) {
+        at[q] = mx_at((int64_t)block * (kSpans * kMxPer), q * kSpans + g, a.spans);
+        in[q] = at[q].row < a.rows && at[q].span * kMxSpan + 8 * l < a.cols;
+        c[q] = s[q] = 0;
+        if (in[q]) {
+            c[q] = *reinterpret_cast<const uint32_t *>(a.codes + at[q].row * a.ldcodes + at[q].span * 64 + 4 * l);
+            s[q] = (uint8_t)a.scales[at[q].row * a.ldscales + at[q].span * 4 + l / 4];
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < kMxPer; ++q) {
+        if (!in[q]) continue;
+        F *o = reinterpret_cast<F *>(a.x + at[q].row * a.ldx) + at[q].span * kMxSpan + 8 * l;
+        const u32x4 b = mx_numbers(c[q], s[q]);
+        if constexpr (sizeof(F) == 2) {
+            *reinterpret_cast<u32x4 *>(o) = b;
+        } else {
+            float v[8];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) unpack_bf16(b[x], v[2 * x], v[2 * x + 1]);
+            *reinterpret_cast<floatx4 *>(o) = floatx4{v[0], v[1], v[2], v[3]};
+            *reinterpret_cast<floatx4 *>(o + 4) = floatx4{v[4], v[5], v[6], v[7]};
+        }
     }
 }
 

@@ -8,25 +8,6 @@ using namespace lora;
 namespace lora {
 namespace {
 
-struct MxArgs {
-    char *x, *codes, *scales;            // x: the numbers, read or written
-    int64_t ldx, ldcodes, ldscales;      // bytes
-    int64_t rows;
-    int32_t cols, blocks, spans;         // of a row
-};
-
-// The lane's span: row and number within the row.
-struct MxAt {
-    int64_t row;
-    int32_t span;
-};
-__device__ __forceinline__ MxAt mx_at(int64_t first, int i, int spans) {
-    const int64_t row0 = first / spans;                 // (uniform)
-    const uint32_t in = (uint32_t)(first - row0 * spans) + (uint32_t)i;
-    const uint32_t r = in / (uint32_t)spans;
-    return MxAt{row0 + r, (int32_t)(in - r * (uint32_t)spans)};
-}
-
 // Bound by the bytes.
 template <class F>
 __global__ __launch_bounds__(kMxThreads) void quantize_kernel(MxArgs a) {
@@ -60,40 +41,9 @@ __global__ __launch_bounds__(kMxThreads) void quantize_kernel(MxArgs a) {
     }
 }
 
-// Exact in float32 and bfloat16: a code has two bits and every power a place in both
-// (the smallest as a subnormal number).
 template <class F>
 __global__ __launch_bounds__(kMxThreads) void dequantize_kernel(MxArgs a) {
-    constexpr int kSpans = kMxThreads / kMxGroup;
-    const int l = threadIdx.x % kMxGroup, g = threadIdx.x / kMxGroup;
-    uint32_t c[kMxPer], s[kMxPer];
-    MxAt at[kMxPer];
-    bool in[kMxPer];
-#pragma unroll
-    for (int q = 0; q < kMxPer; ++q) {
-        at[q] = mx_at((int64_t)blockIdx.x * (kSpans * kMxPer), q * kSpans + g, a.spans);
-        in[q] = at[q].row < a.rows && at[q].span * kMxSpan + 8 * l < a.cols;
-        c[q] = s[q] = 0;
-        if (in[q]) {
-            c[q] = *reinterpret_cast<const uint32_t *>(a.codes + at[q].row * a.ldcodes + at[q].span * 64 + 4 * l);
-            s[q] = (uint8_t)a.scales[at[q].row * a.ldscales + at[q].span * 4 + l / 4];
-        }
-    }
-#pragma unroll
-    for (int q = 0; q < kMxPer; ++q) {
-        if (!in[q]) continue;
-        F *o = reinterpret_cast<F *>(a.x + at[q].row * a.ldx) + at[q].span * kMxSpan + 8 * l;
-        const u32x4 b = mx_numbers(c[q], s[q]);
-        if constexpr (sizeof(F) == 2) {
-            *reinterpret_cast<u32x4 *>(o) = b;
-        } else {
-            float v[8];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) unpack_bf16(b[x], v[2 * x], v[2 * x + 1]);
-            *reinterpret_cast<floatx4 *>(o) = floatx4{v[0], v[1], v[2], v[3]};
-            *reinterpret_cast<floatx4 *>(o + 4) = floatx4{v[4], v[5], v[6], v[7]};
-        }
-    }
+    dequantize<F>(a, blockIdx.x);
 }
 
 int check_codes(const void *codes, int64_t ldcodes, const void *scales, int64_t ldscales, int64_t rows, int64_t cols) {
@@ -116,22 +66,15 @@ int check_numbers(const void *x, int type, int64_t ldx, int64_t rows, int64_t co
 template <bool TO>
 hipError_t launch_mx(const void *x, int type, int64_t ldx, int64_t rows, int cols, const void *codes, int64_t ldcodes,
                      const void *scales, int64_t ldscales, hipStream_t s) {
-    MxArgs a;
-    memset(&a, 0, sizeof a);
-    a.cols = cols;
-    a.blocks = (int32_t)mx_blocks(cols);
-    a.spans = (a.blocks + 3) / 4;
-    a.ldx = ldx * (type == LORA_BF16 ? 2 : 4);
-    a.ldcodes = ldcodes;
-    a.ldscales = ldscales;
-    constexpr int kSpans = kMxThreads / kMxGroup * kMxPer;
-    const int64_t most = ((int64_t)1 << 23) * kSpans / a.spans;   // a launch has fewer than 2^32 threads
+    const MxArgs all = mx_args(x, type, ldx, rows, cols, codes, ldcodes, scales, ldscales);
+    const int64_t most = kMxMostBlocks * kMxSpans / all.spans;
     for (int64_t r = 0; r < rows; r += most) {
+        MxArgs a = all;
         a.rows = rows - r < most ? rows - r : most;
-        a.x = static_cast<char *>(const_cast<void *>(x)) + r * a.ldx;
-        a.codes = static_cast<char *>(const_cast<void *>(codes)) + r * ldcodes;
-        a.scales = static_cast<char *>(const_cast<void *>(scales)) + r * ldscales;
-        const dim3 grid((unsigned)((a.rows * a.spans + kSpans - 1) / kSpans)), block(kMxThreads);
+        a.x += r * a.ldx;
+        a.codes += r * ldcodes;
+        a.scales += r * ldscales;
+        const dim3 grid((unsigned)mx_grid(a)), block(kMxThreads);
         if (TO && type == LORA_BF16)
             hipLaunchKernelGGL(quantize_kernel<uint16_t>, grid, block, 0, s, a);
         else if (TO)
@@ -212,7 +155,7 @@ int lora_linear_mx(const void *x, int64_t ldx, int num_tokens, int hidden, const
     if (m.total > workspace_bytes) return LORA_ERR_BUFFER;
     if (num_tokens == 0) return LORA_OK;
     char *ws = static_cast<char *>(workspace);
-    LinearCall c = {x, x, ldx, ldx, nullptr, nullptr, 0, nullptr, hidden, ws + m.w, hidden, w_bias, lora_a, lora_b, bias, slice_widths, num_tokens,
+    LinearCall c = {x, x, ldx, ldx, nullptr, nullptr, 0, nullptr, nullptr, hidden, ws + m.w, hidden, w_bias, lora_a, lora_b, bias, slice_widths, num_tokens,
                     hidden, out_features, num_slices, rank, offset_start, meta, scale, ws, stream};
     if (quantize_x && num_tokens > kRowsTokens) {
         PrepArgs p;
@@ -254,9 +197,9 @@ int lora_linear_mx(const void *x, int64_t ldx, int num_tokens, int hidden, const
         c.ldscales = ldscales;
         return quantize_x ? linear_forward<kCodes>(c, l, buf, y, ldy) : linear_forward<kMixed>(c, l, buf, y, ldy);
     }
-    if (launch_mx<false>(ws + m.w, LORA_BF16, hidden, out_features, hidden, codes, ldcodes, scales, ldscales, stream) != hipSuccess)
-        return LORA_ERR_LAUNCH;
-    return linear_forward<kWide>(c, l, buf, y, ldy);
+    const MxArgs turn = mx_args(ws + m.w, LORA_BF16, hidden, out_features, hidden, codes, ldcodes, scales, ldscales);
+    c.turn = &turn;
+    return linear_forward<kTurned>(c, l, buf, y, ldy);
 }
 
 int lora_linear_mx_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx, int num_tokens, int hidden,
@@ -276,12 +219,10 @@ int lora_linear_mx_backward(const void *dy, int64_t lddy, const void *x, int64_t
     const MxLayout m = mx_layout(l.total, num_tokens, hidden, out_features);
     if (m.total > workspace_bytes) return LORA_ERR_BUFFER;
     char *ws = static_cast<char *>(workspace);
-    if (dx && num_tokens > 0 &&
-        launch_mx<false>(ws + m.w, LORA_BF16, hidden, out_features, hidden, codes, ldcodes, scales, ldscales, stream) != hipSuccess)
-        return LORA_ERR_LAUNCH;
-    const LinearCall c = {x, x, ldx, ldx, nullptr, nullptr, 0, nullptr, hidden, ws + m.w, hidden, nullptr, lora_a, lora_b, nullptr, slice_widths, num_tokens, hidden,
+    const MxArgs turn = mx_args(ws + m.w, LORA_BF16, hidden, out_features, hidden, codes, ldcodes, scales, ldscales);
+    const LinearCall c = {x, x, ldx, ldx, nullptr, nullptr, 0, nullptr, &turn, hidden, ws + m.w, hidden, nullptr, lora_a, lora_b, nullptr, slice_widths, num_tokens, hidden,
                           out_features, num_slices, rank, offset_start, meta, scale, ws, stream};
-    return linear_backward(c, l, u, g);
+    return linear_backward<kTurned>(c, l, u, g);
 }
 
 }  // extern "C"
