@@ -450,7 +450,7 @@ int lora_mx_dequantize(const void *codes, int64_t ldcodes, const void *scales, i
 /*
  * lora_linear with the shared projection's matrix held in 4 bits: w[o][k] is what
  * row o of codes and scales ([out_features] rows of `hidden` numbers, as
- * lora_mx_quantize lays them out) stands for.
+ * lora_mx_quantize lays them out; ldcodes up to 2^25) stands for.
  * With quantize_x the rows of x are rounded to such numbers first, block by block
  * as lora_mx_quantize rounds them, for the product with w (both of its sides are
  * 4 bits then); the adapters read x as it is in either case:

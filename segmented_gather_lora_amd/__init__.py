@@ -229,6 +229,18 @@ def _stream(stream) -> Optional[int]:
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
+def _stream_on(stream, device, where: str) -> Optional[int]:
+    """The stream for tensors on `device`, which has to be the current one: a kernel
+    launched on another device would not reach them."""
+    import torch
+    current = torch.cuda.current_device()
+    _need(device.index == current, LORA_ERR_SHAPE, where,
+          "the tensors are on %s, the current device is cuda:%d" % (device, current))
+    if stream is not None:
+        return stream if isinstance(stream, int) else stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(current)
+
+
 def _need(ok: bool, status: int, where: str, what: str) -> None:
     if not ok:
         raise LoraError(status, "%s: %s" % (where, what))
@@ -749,9 +761,7 @@ def _type(t, where: str, name: str) -> int:
 def _pitch(t) -> int:
     """Distance of a matrix's rows; of a single row, its length rounded up as the
     library's checks want it (there is no next row)."""
-    if t.shape[0] > 1:
-        return t.stride(0)
-    return max(t.stride(0), (t.shape[1] + 15) // 16 * 16)
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
 
 
 def _mx_numbers(where: str, t, name: str) -> None:
@@ -772,7 +782,7 @@ def lora_mx_quantize(x, codes, scales, stream=None) -> None:
     n, k = x.shape
     _mx_codes(where, x.device, codes, scales, n, k)
     _check(_lib().lora_mx_quantize(x.data_ptr(), kind, _pitch(x), n, k, codes.data_ptr(), _pitch(codes),
-                                   scales.data_ptr(), _pitch(scales), _stream(stream)), where)
+                                   scales.data_ptr(), _pitch(scales), _stream_on(stream, x.device, where)), where)
 
 
 def lora_mx_dequantize(codes, scales, out, stream=None) -> None:
@@ -783,7 +793,7 @@ def lora_mx_dequantize(codes, scales, out, stream=None) -> None:
     n, k = out.shape
     _mx_codes(where, out.device, codes, scales, n, k)
     _check(_lib().lora_mx_dequantize(codes.data_ptr(), _pitch(codes), scales.data_ptr(), _pitch(scales), n, k,
-                                     out.data_ptr(), kind, _pitch(out), _stream(stream)), where)
+                                     out.data_ptr(), kind, _pitch(out), _stream_on(stream, out.device, where)), where)
 
 
 def lora_linear_mx_workspace_bytes(num_tokens: int, max_loras: int, hidden: int, out_features: int, widths: Sequence,
@@ -820,7 +830,7 @@ def lora_linear_mx(x, codes, scales, w_bias, lora_a: Sequence, lora_b: Sequence,
                                  _ptr_array(lora_b), None if bias is None else _ptr_array(bias), _widths_array(widths), s,
                                  r, buf.data_ptr(), y.data_ptr(), y.stride(0), int(offset_start),
                                  ctypes.byref(meta.struct), float(scale), 1 if quantize_x else 0, workspace.data_ptr(),
-                                 workspace.numel(), _stream(stream)), where)
+                                 workspace.numel(), _stream_on(stream, meta.region.device, where)), where)
 
 
 def lora_linear_mx_backward(dy, x, codes, scales, lora_a: Sequence, lora_b: Sequence, buf, dbuf, dx, da: Sequence,
@@ -843,7 +853,7 @@ def lora_linear_mx_backward(dy, x, codes, scales, lora_a: Sequence, lora_b: Sequ
                                           0 if dx is None else dx.stride(0), _ptr_array(da), _ptr_array(db),
                                           None if dbias is None else _ptr_array(dbias), int(offset_start),
                                           ctypes.byref(meta.struct), float(scale), workspace.data_ptr(),
-                                          workspace.numel(), _stream(stream)), where)
+                                          workspace.numel(), _stream_on(stream, meta.region.device, where)), where)
 
 
 class LoraGradients:
@@ -926,4 +936,5 @@ def lora_clip_gradients(grads, norms, max_norm: float, workspace, out: Optional[
           "every gradient's first dimension must be the number of norms, %d" % groups)
     _workspace(workspace, norms.device, where)
     _check(_lib().lora_clip_gradients(g._in, g._out, g._sizes, g._types, len(g.grads), groups, float(max_norm),
-                                      norms.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(stream)), where)
+                                      norms.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                      _stream_on(stream, norms.device, where)), where)

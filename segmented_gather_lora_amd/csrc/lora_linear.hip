@@ -26,8 +26,8 @@ int lora_linear(const void *x, int64_t ldx, int num_tokens, int hidden, const vo
     const Layout l = layout(num_tokens, meta->max_loras, num_slices, rank, u, false);
     if (l.total > workspace_bytes) return LORA_ERR_BUFFER;
     if (num_tokens == 0) return LORA_OK;
-    const LinearCall c = {x, x, ldx, ldx, nullptr, nullptr, 0, nullptr, nullptr, hidden, w, ldw, w_bias, lora_a, lora_b, bias, slice_widths, num_tokens,
-                          hidden, out_features, num_slices, rank, offset_start, meta, scale, static_cast<char *>(workspace), stream};
+    const LinearCall c = linear_call(x, ldx, w, ldw, w_bias, lora_a, lora_b, bias, slice_widths, num_tokens, hidden, out_features,
+                                     num_slices, rank, offset_start, meta, scale, workspace, stream);
     return linear_forward<kWide>(c, l, buf, y, ldy);
 }
 
@@ -45,8 +45,8 @@ int lora_linear_backward(const void *dy, int64_t lddy, const void *x, int64_t ld
     const UPlan u = plan_u(num_tokens, meta->max_loras, num_slices, rank, widest(slice_widths, num_slices));
     const Layout l = layout(num_tokens, meta->max_loras, num_slices, rank, u, true);
     if (l.total > workspace_bytes) return LORA_ERR_BUFFER;
-    const LinearCall c = {x, x, ldx, ldx, nullptr, nullptr, 0, nullptr, nullptr, hidden, w, ldw, nullptr, lora_a, lora_b, nullptr, slice_widths, num_tokens,
-                          hidden, out_features, num_slices, rank, offset_start, meta, scale, static_cast<char *>(workspace), stream};
+    const LinearCall c = linear_call(x, ldx, w, ldw, nullptr, lora_a, lora_b, nullptr, slice_widths, num_tokens, hidden, out_features,
+                                     num_slices, rank, offset_start, meta, scale, workspace, stream);
     return linear_backward<kWide>(c, l, u, g);
 }
 

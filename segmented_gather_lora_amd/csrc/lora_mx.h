@@ -166,8 +166,9 @@ __device__ __forceinline__ void dequantize(const MxArgs &a, int block) {
 // are one block of 32 (its own scale), which it turns into the operands of four MFMAs; the
 // N side is read in the same order of K.  Waves that share M rows convert them each for
 // itself, hence two by two of them, not one by four.  256 tokens by 6144 columns over
-// 4096 without adapters: 33 us, of which 25 remain without the copies and 22 without the
-// rest.  (Eight waves in two groups that take the steps in turn: 37.)
+// 4096 without adapters: 33 us, 27 of them without the copies, 10 without the steps.
+// (Eight waves in two groups that take the steps in turn 37, tiles of 128 x 64 36, more
+// stages the same.)
 template <class B>
 struct MixedTile : B {
     static constexpr int kStepK = 128, kNBytes = B::BN * 256, kMBytes = B::BM * 64;

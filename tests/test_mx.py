@@ -267,6 +267,51 @@ def test_large_tiles(acts, n, hidden, widths, keys):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("acts,n,hidden,out", [
+    ("mxfp4", 520, 768, 6144),       # whole steps of 256 and no rest: three of them, four, five
+    ("mxfp4", 520, 1024, 6144),
+    ("mxfp4", 300, 1280, 264),       # small tiles
+    ("mxfp4", 129, 512, 264),
+    ("bf16", 40, 8328, 72),          # 66 steps of 128: the scales' two buffers, each twice
+    ("bf16", 70, 4096, 136),         # 32 steps
+    ("bf16", 33, 384, 64),
+    ("bf16", 100, 128, 200)])
+def test_whole_steps(acts, n, hidden, out):
+    for rank, none in ((8, 0.2), (40, 0.0)):
+        c = MxCase(acts=acts, n=n, hidden=hidden, widths=[out], rank=rank, loras=2, none=none, seed=rank)
+        r = MxRun(c)
+        r.forward()
+        check(c, r.outputs(), ("y", "s"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("acts", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("n", [128, 300])
+def test_one_adapter_has_whole_tiles(acts, n):
+    """One adapter for all tokens, ranks of one and of several blocks, slices that end
+    inside a tile; and adapters that change at a tile's edge."""
+    for rank in (16, 32, 72):
+        for ids in ([0] * n, [i // 128 for i in range(n)], [1] * 100 + [0] * (n - 100)):
+            c = MxCase(acts=acts, n=n, hidden=264, widths=[5000, 72, 10000], rank=rank, loras=3, ids=ids, extra=16)
+            r = MxRun(c, backward=False)
+            r.forward()
+            check(c, r.outputs(), ("y", "s"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("acts", ["bf16", "mxfp4"])
+def test_biases_of_few_and_of_many_adapters(acts):
+    for loras, seed in ((2, 0), (4, 1), (5, 2), (40, 3)):
+        for bias in (True, False):
+            c = MxCase(acts=acts, n=200, hidden=136, widths=[136, 40, 24], rank=8, loras=loras, seed=seed, bias=bias)
+            if not bias:      # the projection's alone
+                c.w_bias = torch.randn(c.out, generator=torch.Generator().manual_seed(seed)).to(torch.bfloat16)
+            r = MxRun(c, backward=False)
+            r.forward()
+            check(c, r.outputs(), ("y", "s"))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("acts", ["bf16", "mxfp4"])
 def test_powers_from_the_smallest_to_the_largest(acts):
     """Scale bytes over their whole range, where the sums stay in range."""
@@ -443,6 +488,7 @@ def test_refusals_of_the_projection():
         assert call(n=31) == sgl.LORA_ERR_NUM_TOKENS and call(r=12) == sgl.LORA_ERR_SHAPE and call(s=9) == sgl.LORA_ERR_SLICES
         assert call(codes=None) == sgl.LORA_ERR_NULL and call(scales=None) == sgl.LORA_ERR_NULL
         assert call(codes=0x20008) == sgl.LORA_ERR_ALIGN and call(scales=0x30002) == sgl.LORA_ERR_ALIGN
+        assert call(ldc=(1 << 25) + 16) == sgl.LORA_ERR_SHAPE
         assert call(ws=0xA0010) == sgl.LORA_ERR_BUFFER and call(wsb=256) == sgl.LORA_ERR_BUFFER
         assert call(x=0x10008) == sgl.LORA_ERR_ALIGN and call(y=None) == sgl.LORA_ERR_NULL
     assert forward(n=0, meta=_fake_meta(sgl, 0)) == sgl.LORA_OK
