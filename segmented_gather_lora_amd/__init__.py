@@ -734,19 +734,24 @@ def lora_mx_row_bytes(cols: int) -> tuple:
     return 16 * blocks, (blocks + 3) // 4 * 4
 
 
-def _mx_codes(where: str, device, codes, scales, rows: int, cols: int) -> None:
+def _mx_codes(where: str, device, codes, scales, rows: int, cols: int) -> tuple:
+    """Checks the codes and scales of [rows][cols] numbers; their rows' distances."""
     import torch
-    code_bytes, scale_bytes = lora_mx_row_bytes(cols)
+    code_bytes, scale_bytes = (cols + 31) // 32 * 16, (cols + 127) // 128 * 4
+    at, uint8 = device.index, torch.uint8
+    if (codes.dtype is uint8 and scales.dtype is uint8 and codes.get_device() == at and scales.get_device() == at
+            and codes.shape == (rows, code_bytes) and scales.shape == (rows, scale_bytes) and codes.is_contiguous()
+            and scales.is_contiguous()):
+        return code_bytes, scale_bytes
     for t, wide, name in ((codes, code_bytes, "codes"), (scales, scale_bytes, "scales")):
-        if t.get_device() == device.index and _matrix(t, torch.uint8, device.index, (rows, wide)):
-            continue
         if not (t.is_cuda and t.device == device):
             raise TypeError("%s: %s must be on %s (got %s)" % (where, name, device, t.device))
-        if t.dtype != torch.uint8:
+        if t.dtype != uint8:
             raise TypeError("%s: %s must be torch.uint8 (got %s)" % (where, name, t.dtype))
         _need(t.dim() == 2 and t.shape[0] == rows and t.shape[1] >= wide, LORA_ERR_SHAPE, where,
               "%s must be [%d][>= %d]" % (name, rows, wide))
         _need(t.stride(1) == 1, LORA_ERR_SHAPE, where, "%s needs unit stride in its last dimension" % name)
+    return _pitch(codes), _pitch(scales)
 
 
 def _type(t, where: str, name: str) -> int:
@@ -780,9 +785,9 @@ def lora_mx_quantize(x, codes, scales, stream=None) -> None:
     _mx_numbers(where, x, "x")
     kind = _type(x, where, "x")
     n, k = x.shape
-    _mx_codes(where, x.device, codes, scales, n, k)
-    _check(_lib().lora_mx_quantize(x.data_ptr(), kind, _pitch(x), n, k, codes.data_ptr(), _pitch(codes),
-                                   scales.data_ptr(), _pitch(scales), _stream_on(stream, x.device, where)), where)
+    ldc, lds = _mx_codes(where, x.device, codes, scales, n, k)
+    _check(_lib().lora_mx_quantize(x.data_ptr(), kind, _pitch(x), n, k, codes.data_ptr(), ldc, scales.data_ptr(), lds,
+                                   _stream_on(stream, x.device, where)), where)
 
 
 def lora_mx_dequantize(codes, scales, out, stream=None) -> None:
@@ -791,9 +796,9 @@ def lora_mx_dequantize(codes, scales, out, stream=None) -> None:
     _mx_numbers(where, out, "out")
     kind = _type(out, where, "out")
     n, k = out.shape
-    _mx_codes(where, out.device, codes, scales, n, k)
-    _check(_lib().lora_mx_dequantize(codes.data_ptr(), _pitch(codes), scales.data_ptr(), _pitch(scales), n, k,
-                                     out.data_ptr(), kind, _pitch(out), _stream_on(stream, out.device, where)), where)
+    ldc, lds = _mx_codes(where, out.device, codes, scales, n, k)
+    _check(_lib().lora_mx_dequantize(codes.data_ptr(), ldc, scales.data_ptr(), lds, n, k, out.data_ptr(), kind,
+                                     _pitch(out), _stream_on(stream, out.device, where)), where)
 
 
 def lora_linear_mx_workspace_bytes(num_tokens: int, max_loras: int, hidden: int, out_features: int, widths: Sequence,
@@ -822,11 +827,11 @@ def lora_linear_mx(x, codes, scales, w_bias, lora_a: Sequence, lora_b: Sequence,
     out = codes.shape[0]
     widths = [t.shape[1] for t in lora_b]
     _forward_checks(where, meta, x, out, y, lora_a, lora_b, buf, widths, r, workspace, offset_start)
-    _mx_codes(where, meta.region.device, codes, scales, out, h)
+    ldc, lds = _mx_codes(where, meta.region.device, codes, scales, out, h)
     _bias(bias, widths, meta, where)
     _w_bias(w_bias, out, meta, where)
-    _check(_lib().lora_linear_mx(x.data_ptr(), x.stride(0), n, h, codes.data_ptr(), _pitch(codes), scales.data_ptr(),
-                                 _pitch(scales), out, None if w_bias is None else w_bias.data_ptr(), _ptr_array(lora_a),
+    _check(_lib().lora_linear_mx(x.data_ptr(), x.stride(0), n, h, codes.data_ptr(), ldc, scales.data_ptr(), lds, out,
+                                 None if w_bias is None else w_bias.data_ptr(), _ptr_array(lora_a),
                                  _ptr_array(lora_b), None if bias is None else _ptr_array(bias), _widths_array(widths), s,
                                  r, buf.data_ptr(), y.data_ptr(), y.stride(0), int(offset_start),
                                  ctypes.byref(meta.struct), float(scale), 1 if quantize_x else 0, workspace.data_ptr(),
@@ -845,9 +850,9 @@ def lora_linear_mx_backward(dy, x, codes, scales, lora_a: Sequence, lora_b: Sequ
     widths = [t.shape[1] for t in lora_b]
     _backward_checks(where, meta, dy, x, out, lora_a, lora_b, buf, dbuf, dx, da, db, dbias, widths, r, workspace,
                      offset_start)
-    _mx_codes(where, meta.region.device, codes, scales, out, h)
+    ldc, lds = _mx_codes(where, meta.region.device, codes, scales, out, h)
     _check(_lib().lora_linear_mx_backward(dy.data_ptr(), dy.stride(0), x.data_ptr(), x.stride(0), n, h, codes.data_ptr(),
-                                          _pitch(codes), scales.data_ptr(), _pitch(scales), out, _ptr_array(lora_a),
+                                          ldc, scales.data_ptr(), lds, out, _ptr_array(lora_a),
                                           _ptr_array(lora_b), _widths_array(widths), s, r, buf.data_ptr(),
                                           dbuf.data_ptr(), None if dx is None else dx.data_ptr(),
                                           0 if dx is None else dx.stride(0), _ptr_array(da), _ptr_array(db),
