@@ -278,11 +278,14 @@ struct Codes : PairOp<T, OffsetWalk<typename T::MSide>, OffsetWalk<typename T::N
 // Mixed operands: W's rows and their scales, the tokens' rows.
 template <class T>
 struct Mixed : MixedWalk<T> {
-    template <class Row>
-    __device__ __forceinline__ void start(const LinearArgs &a, int m0, Row row) {
+    template <class Token>
+    __device__ __forceinline__ void start(const LinearArgs &a, int m0, Token token) {
+        this->nbase = a.in;
+        this->mbase = a.w + (int64_t)m0 * a.ldw;
 #pragma unroll
-        for (int j = 0; j < T::kNInstr; ++j) this->n[j] = row(T::n_copy_row(j)) + 8 * T::n_copy_chunk(j);
-        this->m = reinterpret_cast<const uint8_t *>(a.w + (int64_t)min(m0 + T::m_copy_row(), a.cols - 1) * a.ldw) + 16 * T::m_copy_chunk();
+        for (int j = 0; j < T::kNInstr; ++j)
+            this->n[j] = 2u * ((uint32_t)token(T::n_copy_row(j)) * (uint32_t)a.ldin + 8u * (uint32_t)T::n_copy_chunk(j));
+        this->m = 2u * (uint32_t)min(T::m_copy_row(), a.cols - 1 - m0) * (uint32_t)a.ldw + 16u * (uint32_t)T::m_copy_chunk();
         this->scales = a.mscales;
         this->ldscales = a.ldscales;
         this->m0 = m0;
@@ -562,7 +565,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_kernel(LinearArgs a) {
     const int main = O == kWide ? (a.k + kStepK - 1) / kStepK : 0;
     typename WalkOf<T, O>::type walk;
     if constexpr (O == kMixed) {
-        walk.start(a, m0, [&](int r) { return a.in + (int64_t)token(r) * a.ldin; });
+        walk.start(a, m0, token);
     } else if constexpr (O == kCodes) {
         walk.start(a, m0, p0, rows);
     } else {

@@ -175,9 +175,11 @@ struct MixedTile : B {
     static constexpr int kMAt = kNBytes, kStage = kNBytes + kMBytes;
     static constexpr int kScaleSteps = 32, kScaleBytes = B::BM * 4 * kScaleSteps, kScaleCopies = kScaleBytes / 256 / B::kWaves;
     static constexpr int kScaleAt = B::kStages * kStage, kLds = kScaleAt + 2 * kScaleBytes;
-    static constexpr int kNInstr = B::BN / 4 / B::kWaves, kLoads = kNInstr + 2;
-    static_assert(B::BM == 64 && B::DEAL == 2 && B::MT == 2 && B::kWaves == 4, "32 rows of the M side a wave, a tile of 16 a copy");
-    static_assert((kScaleCopies & (kScaleCopies - 1)) == 0 && kScaleCopies <= kScaleSteps / 2, "the next scales land in time");
+    static constexpr int kNInstr = B::BN / 4 / B::kWaves, kLoads = kNInstr + 1, kTokens = B::BN / 16;
+    static_assert(B::BM == 64 && B::DEAL == 2 && B::MT == 2 && B::WM == 2 && B::WN == 2 && kTokens == 2 * B::NT, "two by two waves");
+    typedef floatx4 Sums[B::MT][kTokens];   // of a wave's half of K, all tokens
+    // half of a step's K that a wave multiplies: codes 16 g .. of every block
+    __device__ __forceinline__ static int half() { return wave_id() / B::WM; }
 
     // tile row in place p of the M side: tile by tile, so that a tile's 16 rows are together
     __device__ __forceinline__ static int m_row(int p) {
@@ -195,9 +197,9 @@ struct MixedTile : B {
     __device__ __forceinline__ static int scale_copy_step(int i) { return (lane_id() - scale_copy_place(i)) & 31; }
 
     struct Step {
-        u32x4 codes[B::MT];
+        u32x2g codes[B::MT];
         uint32_t scale[B::MT];
-        bf16x8 n[B::NT][4];
+        bf16x8 n[kTokens][2];
     };
     // of the stage at st, step s of K
     __device__ __forceinline__ static void read(Step &r, const lds_byte *lds, const lds_byte *st, int s) {
@@ -205,66 +207,79 @@ struct MixedTile : B {
 #pragma unroll
         for (int t = 0; t < B::MT; ++t) {
             const int place = 16 * (B::wave_m() * B::MT + t) + l16;
-            r.codes[t] = *(const __attribute__((address_space(3))) u32x4 *)(st + kMAt + place * 64 + 16 * (g ^ (l16 >> 1 & 3)));
+            r.codes[t] = *(const __attribute__((address_space(3))) u32x2g *)(st + kMAt + place * 64 + 16 * (g ^ (l16 >> 1 & 3)) + 8 * half());
             r.scale[t] = *(lds + kScaleAt + ((uint32_t)s / kScaleSteps & 1) * kScaleBytes + place * 128 + ((s + place) & 31) * 4 + g);
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int t = 0; t < B::NT; ++t) {
-                const int row = B::wave_n() * (B::BN / B::WN) + 16 * t + l16;
-                r.n[t][j] = *(const lds_bf16x8 *)(st + row * 256 + 16 * ((4 * g + j) ^ l16));
-            }
+            for (int t = 0; t < kTokens; ++t)
+                r.n[t][j] = *(const lds_bf16x8 *)(st + (16 * t + l16) * 256 + 16 * ((4 * g + 2 * half() + j) ^ l16));
     }
     // keep: 0 where the lane's block is past the last (its scale may be anything, its codes are zeros)
-    __device__ __forceinline__ static void mma(const Step &r, typename B::Acc &acc, uint32_t keep) {
+    __device__ __forceinline__ static void mma(const Step &r, Sums &sums, uint32_t keep) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int m = 0; m < B::MT; ++m) {
                 const bf16x8 w = as_bf16x8(mx_numbers(r.codes[m][j], r.scale[m] & keep));
 #pragma unroll
-                for (int t = 0; t < B::NT; ++t) acc[m][t] = mfma16x16x32(w, r.n[t][j], acc[m][t]);
+                for (int t = 0; t < kTokens; ++t) sums[m][t] = mfma16x16x32(w, r.n[t][j], sums[m][t]);
             }
+    }
+    // Both halves of K added up: a wave keeps the tokens of the tile's own layout and hands
+    // the others to the wave that has the same rows (a 16 KB of `lds`, which no one reads).
+    __device__ __forceinline__ static void join(const Sums &sums, typename B::Acc &acc, unsigned char *lds) {
+        floatx4 *at = reinterpret_cast<floatx4 *>(lds) + lane_id();
+        const int mine = half(), wave = wave_id(), partner = wave ^ B::WM;
+#pragma unroll
+        for (int m = 0; m < B::MT; ++m)
+#pragma unroll
+            for (int t = 0; t < B::NT; ++t)
+                at[((wave * B::MT + m) * B::NT + t) * kWave] = mine ? sums[m][t] : sums[m][B::NT + t];
+        __syncthreads();
+#pragma unroll
+        for (int m = 0; m < B::MT; ++m)
+#pragma unroll
+            for (int t = 0; t < B::NT; ++t)
+                acc[m][t] = (mine ? sums[m][B::NT + t] : sums[m][t]) + at[((partner * B::MT + m) * B::NT + t) * kWave];
+        __syncthreads();
     }
 };
 
 // The two sides' walk: lanes past the end of K read zeros.
 template <class T>
 struct MixedWalk {
-    const uint16_t *n[T::kNInstr];
-    const uint8_t *m, *scales;  // (scales: row 0 of W)
+    const uint16_t *nbase, *mbase;      // of the next step: the tokens' and the tile's W rows
+    uint32_t n[T::kNInstr], m;          // this lane's places from there, bytes
+    const uint8_t *scales;              // row 0 of W
     int64_t ldscales;
     int m0, cols;               // first row of the tile, rows of W
     int k, blocks, step;        // of the rows; next step to copy
-    // instruction i of the scales of 32 steps; past the last dword any of the row's
-    __device__ __forceinline__ void copy_scales(uint32_t base, int group, int i) {
-        const int d = min(group * T::kScaleSteps + T::scale_copy_step(i), (blocks - 1) / 4);
-        const int row = min(m0 + T::m_row(T::scale_copy_place(i)), cols - 1);
-        dma4(scales + row * ldscales + 4 * (int64_t)d,
-             base + T::kScaleAt + (group & 1) * T::kScaleBytes + (wave_id() * T::kScaleCopies + i) * 256u);
+    // the scales of 32 steps; past the last dword any of the row's
+    __device__ __forceinline__ void copy_scales(uint32_t base, int group) {
+#pragma unroll
+        for (int i = 0; i < T::kScaleCopies; ++i) {
+            const int d = min(group * T::kScaleSteps + T::scale_copy_step(i), (blocks - 1) / 4);
+            const int row = min(m0 + T::m_row(T::scale_copy_place(i)), cols - 1);
+            dma4(scales + row * ldscales + 4 * (int64_t)d,
+                 base + T::kScaleAt + (group & 1) * T::kScaleBytes + (wave_id() * T::kScaleCopies + i) * 256u);
+        }
     }
-    // n and m are this lane's places in the next step
-    __device__ __forceinline__ void issue(uint32_t base, uint32_t at) {
+    __device__ __forceinline__ void issue(uint32_t at) {
         const uint32_t to = at + wave_id() * T::kNInstr * 1024u, mto = at + T::kMAt + wave_id() * 1024u;
-        const uint16_t *codes = reinterpret_cast<const uint16_t *>(m);
         if ((step + 1) * T::kStepK <= k) {
 #pragma unroll
-            for (int j = 0; j < T::kNInstr; ++j) dma16(n[j], to + j * 1024u);
-            dma16(codes, mto);
+            for (int j = 0; j < T::kNInstr; ++j) dma16(nbase, n[j], to + j * 1024u);
+            dma16(mbase, m, mto);
         } else {
 #pragma unroll
             for (int j = 0; j < T::kNInstr; ++j)
-                dma16(step * T::kStepK + 8 * T::n_copy_chunk(j) < k ? n[j] : zero_page, to + j * 1024u);
-            dma16(step * 4 + T::m_copy_chunk() < blocks ? codes : zero_page, mto);
+                dma16(step * T::kStepK + 8 * T::n_copy_chunk(j) < k ? nbase + n[j] / 2 : zero_page, to + j * 1024u);
+            dma16(step * 4 + T::m_copy_chunk() < blocks ? mbase + m / 2 : zero_page, mto);
         }
-#pragma unroll
-        for (int j = 0; j < T::kNInstr; ++j) n[j] += T::kStepK;
-        m += 64;
-        // the scales of the 32 steps after those that are being read, whose buffer the
-        // 32 before them have left (every step makes one copy, some again, so that all make as many)
-        const int now = step - (T::kStages - 1);
-        copy_scales(base, now < 0 ? 0 : now / T::kScaleSteps + 1, step & (T::kScaleCopies - 1));
+        nbase += T::kStepK;
+        mbase += 32;
         ++step;
     }
 };
@@ -272,9 +287,8 @@ struct MixedWalk {
 template <class T>
 __device__ __forceinline__ void mixed_begin(MixedWalk<T> &w, int nsteps, unsigned char *lds) {
     const uint32_t base = lds_address(lds);
-#pragma unroll
-    for (int i = 0; i < T::kScaleCopies; ++i) w.copy_scales(base, 0, i);
-    for (int i = 0; i < T::kStages && i < nsteps; ++i) w.issue(base, base + i * T::kStage);
+    w.copy_scales(base, 0);
+    for (int i = 0; i < T::kStages && i < nsteps; ++i) w.issue(base + i * T::kStage);
 }
 // A step's operands are read while the step before is multiplied.  One barrier a step:
 // every wave has read the step before, whose stage takes the copies of kStages steps on.
@@ -285,6 +299,11 @@ __device__ __forceinline__ void mixed_loop(MixedWalk<T> &w, int nsteps, typename
     const lds_byte *lds = (const lds_byte *)lds_generic;
     const uint32_t base = lds_address(lds_generic);
     int cur = 0, s = 0;       // stage and number of the step to be read next
+    typename T::Sums sums;
+#pragma unroll
+    for (int m = 0; m < T::MT; ++m)
+#pragma unroll
+        for (int t = 0; t < T::kTokens; ++t) sums[m][t] = floatx4{0.f, 0.f, 0.f, 0.f};
     auto read = [&](typename T::Step &r) {
         T::read(r, lds, lds + cur, s);
         cur = cur + T::kStage == T::kScaleAt ? 0 : cur + T::kStage;
@@ -300,10 +319,13 @@ __device__ __forceinline__ void mixed_loop(MixedWalk<T> &w, int nsteps, typename
                 wait_loads_barrier<(S - 2) * T::kLoads>();
             else
                 wait_loads_barrier<0>();
-            if (s - 1 + S < nsteps) w.issue(base, base + before);
+            // the scales of the 32 steps after the next 32 are asked for once the 32 before have
+            // left their buffer; ahead of the step's copies, so that the next wait covers them
+            if ((s & (T::kScaleSteps - 1)) == 1 && s + T::kScaleSteps - 1 < nsteps) w.copy_scales(base, s / T::kScaleSteps + 1);
+            if (s - 1 + S < nsteps) w.issue(base + before);
             read(next);
         }
-        T::mma(now, acc, keep);
+        T::mma(now, sums, keep);
         return more;
     };
     typename T::Step a, b;
@@ -315,6 +337,7 @@ __device__ __forceinline__ void mixed_loop(MixedWalk<T> &w, int nsteps, typename
     while (turn(b, a) && turn(a, b)) {
     }
     __syncthreads();
+    T::join(sums, acc, lds_generic);
 }
 
 }  // namespace lora
