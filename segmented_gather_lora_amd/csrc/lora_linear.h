@@ -1657,7 +1657,7 @@ hipError_t launch_linear(LinearArgs &a, hipStream_t s) {
         if (p.tile == kMid) return launch(Tile<128, 128, 2, 2, BWD, false>{});
         return launch(Tile<64, 64, 1, 4, BWD, false, 0, 4>{});
     } else if constexpr (O == kMixed) {
-        return launch(Tile<64, 64, 2, 2, BWD, false, 0, 3>{});   // (four and six stages: the same)
+        return launch(Tile<64, 64, 2, 2, BWD, false, 0, 3>{});
     } else {
         switch (p.tile) {
             case kBig: return launch(Tile<256, 256, 4, 2, BWD, false>{});

@@ -163,12 +163,13 @@ __device__ __forceinline__ void dequantize(const MxArgs &a, int block) {
 // A stage holds the N rows' 256 bytes and the M rows' 64.  The M rows' scales come 32
 // steps at a time (128 bytes a row, into one of two buffers): a copy of four bytes a
 // row every step would look up as many lines as all the rest.  A lane's 16 bytes of codes
-// are one block of 32 (its own scale), which it turns into the operands of four MFMAs; the
-// N side is read in the same order of K.  Waves that share M rows convert them each for
-// itself, hence two by two of them, not one by four.  256 tokens by 6144 columns over
-// 4096 without adapters: 33 us, 27 of them without the copies, 10 without the steps.
-// (Eight waves in two groups that take the steps in turn 37, tiles of 128 x 64 36, more
-// stages the same.)
+// are one block of 32 (its own scale), operands of four MFMAs; the N side is read in the
+// same order of K.  The four waves are two halves of the M rows by two halves of every
+// block, each wave over all 64 tokens, so that a code is converted once; the halves of K
+// are added up at the end.  256 tokens by 6144 columns over 4096 without adapters: 28 us,
+// where waves that share M rows and convert them each for itself took 33.  In a form that
+// took 31 the copies alone were 18, everything but the copies 27, but the MFMAs 23; six
+// stages, one workgroup a CU, 47.
 template <class B>
 struct MixedTile : B {
     static constexpr int kStepK = 128, kNBytes = B::BN * 256, kMBytes = B::BM * 64;
@@ -201,20 +202,31 @@ struct MixedTile : B {
         uint32_t scale[B::MT];
         bf16x8 n[kTokens][2];
     };
-    // of the stage at st, step s of K
-    __device__ __forceinline__ static void read(Step &r, const lds_byte *lds, const lds_byte *st, int s) {
-        const int l16 = lane_id() & 15, g = lane_id() >> 4;
+    // Where a lane reads: its first tile's codes and scales (the second tile's are 16 places
+    // on), its tokens' chunks of either j, in a stage and in the scales.
+    struct Places {
+        uint32_t codes, scales, n[2];
+        __device__ __forceinline__ void find() {
+            const uint32_t l16 = lane_id() & 15, g = lane_id() >> 4, place = 32 * B::wave_m() + l16;
+            codes = kMAt + place * 64 + 16 * (g ^ (l16 >> 1 & 3)) + 8 * half();
+            scales = kScaleAt + place * 128 + g;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) n[j] = l16 * 256 + 16 * ((4 * g + 2 * half() + j) ^ l16);
+        }
+    };
+    // of the stage at byte `cur`, step s of K
+    __device__ __forceinline__ static void read(Step &r, const Places &p, const lds_byte *lds, uint32_t cur, uint32_t s) {
+        const uint32_t turned = ((s + (lane_id() & 15)) & 31) * 4;
+        const lds_byte *scale = lds + p.scales + (s / kScaleSteps & 1) * kScaleBytes;
 #pragma unroll
         for (int t = 0; t < B::MT; ++t) {
-            const int place = 16 * (B::wave_m() * B::MT + t) + l16;
-            r.codes[t] = *(const __attribute__((address_space(3))) u32x2g *)(st + kMAt + place * 64 + 16 * (g ^ (l16 >> 1 & 3)) + 8 * half());
-            r.scale[t] = *(lds + kScaleAt + ((uint32_t)s / kScaleSteps & 1) * kScaleBytes + place * 128 + ((s + place) & 31) * 4 + g);
+            r.codes[t] = *(const __attribute__((address_space(3))) u32x2g *)(lds + cur + p.codes + t * 1024);
+            r.scale[t] = *(scale + t * 2048 + (turned ^ 64u * t));
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int t = 0; t < kTokens; ++t)
-                r.n[t][j] = *(const lds_bf16x8 *)(st + (16 * t + l16) * 256 + 16 * ((4 * g + 2 * half() + j) ^ l16));
+            for (int t = 0; t < kTokens; ++t) r.n[t][j] = *(const lds_bf16x8 *)(lds + cur + p.n[j] + t * 4096);
     }
     // keep: 0 where the lane's block is past the last (its scale may be anything, its codes are zeros)
     __device__ __forceinline__ static void mma(const Step &r, Sums &sums, uint32_t keep) {
@@ -304,8 +316,10 @@ __device__ __forceinline__ void mixed_loop(MixedWalk<T> &w, int nsteps, typename
     for (int m = 0; m < T::MT; ++m)
 #pragma unroll
         for (int t = 0; t < T::kTokens; ++t) sums[m][t] = floatx4{0.f, 0.f, 0.f, 0.f};
+    typename T::Places places;
+    places.find();
     auto read = [&](typename T::Step &r) {
-        T::read(r, lds, lds + cur, s);
+        T::read(r, places, lds, cur, s);
         cur = cur + T::kStage == T::kScaleAt ? 0 : cur + T::kStage;
         ++s;
     };
@@ -313,6 +327,9 @@ __device__ __forceinline__ void mixed_loop(MixedWalk<T> &w, int nsteps, typename
     auto turn = [&](typename T::Step &next, const typename T::Step &now) {
         const bool more = s < nsteps;
         const uint32_t keep = (s - 1) * 4 + lane_id() / 16 < w.blocks ? 0xffu : 0u;
+        // the step before is in its registers: said in a way that the compiler knows, or it
+        // would wait for the reads below before it multiplies
+        __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0)
         if (more) {
             const int before = (cur == 0 ? T::kScaleAt : cur) - T::kStage;
             if (s + S - 1 <= nsteps)

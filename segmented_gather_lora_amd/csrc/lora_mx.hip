@@ -194,7 +194,7 @@ int lora_linear_mx(const void *x, int64_t ldx, int num_tokens, int hidden, const
     // Where the bf16 projection takes 64 x 64 tiles, W's codes go into the product as they
     // are; larger tiles are bound by the MFMA or by x, and turn W into numbers first.  us of
     // the product from codes, and of both launches, over 4096 by 6144 columns, 32 adapters:
-    // 33 tokens 29, 45; 256: 38, 50; 512: 62, 66; (1024: 104, 77)
+    // 33 tokens 26, 45; 256: 31, 50; 512: 55, 66; (640: 63, 68; 1024: 90, 80)
     // (that product's places in x are 32 bits)
     const bool near = (int64_t)num_tokens * ldx * 2 < ((int64_t)1 << 32);
     if (num_tokens <= kRowsTokens || (!quantize_x && near && plan_linear(num_tokens, out_features).tile == kSmall)) {
