@@ -494,7 +494,7 @@ size_t lora_linear_mx_workspace_bytes(int num_tokens, int max_loras, int hidden,
  *     out      = v * min(1, max_norm / (norms[g] + 1e-6)),  rounded once
  *   grads, out  host arrays [num_tensors] of device pointers, contiguous; out[i] may be
  *           grads[i] (in place: what is not scaled is not touched); otherwise it
- *           overlaps no gradient, and no two results overlap (LORA_ERR_BUFFER)
+ *           overlaps no gradient, and no two results overlap (else LORA_ERR_BUFFER)
  *   sizes   host [num_tensors], elements, each a multiple of groups; 0 is allowed, a part
  *           has fewer than 2^32
  *   types   host [num_tensors] of LORA_BF16 or LORA_F32 (aligned to their size only)

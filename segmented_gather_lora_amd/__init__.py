@@ -864,8 +864,8 @@ def lora_linear_mx_backward(dy, x, codes, scales, lora_a: Sequence, lora_b: Sequ
 class LoraGradients:
     """The tensors of a training step's gradients (bf16 or float32, contiguous, on one
     GPU), and of the scaled ones: `out`, tensors like them, or None to scale in
-    place.  Made once for buffers that stay; a call looks whether the tensors have
-    moved."""
+    place.  Made once for buffers that keep their sizes and types; a call looks
+    whether the tensors have moved."""
 
     def __init__(self, grads: Sequence, out: Optional[Sequence] = None):
         self.grads = list(grads)

@@ -322,29 +322,38 @@ ClipPlan plan_clip(const int64_t *sizes, const int *types, int num_tensors, int 
     return p;
 }
 
-// Whether no two results share memory: one in two places would be scaled twice, or by
-// whoever comes last.  (Buffers made one after the other are in order: no sort.)
-bool apart(void *const *out, const int64_t *sizes, const int *types, int num_tensors) {
-    uintptr_t last = 0;
-    bool ordered = true;
-    for (int i = 0; i < num_tensors && ordered; ++i)
-        if (sizes[i]) {
-            const uintptr_t at = reinterpret_cast<uintptr_t>(out[i]);
-            ordered = at >= last;
-            last = at + (uintptr_t)sizes[i] * (uintptr_t)size_of(types[i]);
-        }
-    if (ordered) return true;
-    std::vector<std::pair<uintptr_t, uintptr_t>> spans;
+// Whether no result shares memory with another (one in two places would be scaled twice, or
+// by whoever comes last) or with a gradient but its own in its own place (it would be scaled
+// after it was written over).
+struct Span {
+    uintptr_t at, end;
+};
+std::vector<Span> spans_of(const void *const *p, const void *const *but, const int64_t *sizes, const int *types, int num_tensors) {
+    std::vector<Span> spans;
     spans.reserve((size_t)num_tensors);
-    for (int i = 0; i < num_tensors; ++i)
-        if (sizes[i]) {
-            const uintptr_t at = reinterpret_cast<uintptr_t>(out[i]);
-            spans.emplace_back(at, at + (uintptr_t)sizes[i] * (uintptr_t)size_of(types[i]));
+    bool ordered = true;   // (buffers made one after the other are: no sort)
+    for (int i = 0; i < num_tensors; ++i) {
+        if (!sizes[i] || (but && p[i] == but[i])) continue;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p[i]);
+        ordered = ordered && (spans.empty() || at >= spans.back().at);
+        spans.push_back(Span{at, at + (uintptr_t)sizes[i] * (uintptr_t)size_of(types[i])});
+    }
+    if (!ordered) std::sort(spans.begin(), spans.end(), [](const Span &a, const Span &b) { return a.at < b.at; });
+    return spans;
+}
+bool apart(const void *const *grads, void *const *out, const int64_t *sizes, const int *types, int num_tensors) {
+    const std::vector<Span> written = spans_of(out, nullptr, sizes, types, num_tensors), read = spans_of(grads, out, sizes, types, num_tensors);
+    uintptr_t written_to = 0, read_to = 0;
+    auto in = read.begin();
+    for (const Span &o : written) {
+        for (; in != read.end() && in->at <= o.at; ++in) {
+            if (in->at < written_to) return false;
+            read_to = std::max(read_to, in->end);
         }
-    std::sort(spans.begin(), spans.end());
-    for (size_t i = 1; i < spans.size(); ++i)
-        if (spans[i].first < spans[i - 1].second) return false;
-    return true;
+        if (o.at < written_to || o.at < read_to) return false;
+        written_to = o.end;
+    }
+    return in == read.end() || in->at >= written_to;
 }
 
 // The tensors in launches of as many as their arguments hold.
@@ -412,8 +421,8 @@ int lora_clip_gradients(const void *const *grads, void *const *out, const int64_
         same = same && grads[i] == out[i];
     }
     try {
-        if (!apart(out, sizes, types, num_tensors)) return LORA_ERR_BUFFER;
-    } catch (...) {   // (no memory for the sort)
+        if (!apart(grads, out, sizes, types, num_tensors)) return LORA_ERR_BUFFER;
+    } catch (...) {   // (no memory for the spans)
         return LORA_ERR_SCRATCH;
     }
 

@@ -243,6 +243,47 @@ def test_refusals():
     assert sgl.lib.lora_clip_gradients_workspace_bytes(ok["s"], ok["t"], 2, 4) > 0
 
 
+def test_results_on_other_gradients_are_refused():
+    sgl = lib()
+    P = lambda *v: (ctypes.c_void_p * len(v))(*v)
+
+    def call(g, o, sizes=(64, 32, 0), types=(0, 1, 1)):       # 0x80 bytes either, and nothing
+        return sgl.lib.lora_clip_gradients(P(*g), P(*o), (ctypes.c_int64 * 3)(*sizes), (ctypes.c_int * 3)(*types), 3, 4, 1.0,
+                                           0x50000, 0x60000, 1 << 20, None)
+    a, b, c, d = 0x10000, 0x20000, 0x30000, 0x40000
+    assert call((a, b, 0), (b, a, 0)) == sgl.LORA_ERR_BUFFER             # each on the other
+    assert call((a, b, 0), (b, d, 0)) == sgl.LORA_ERR_BUFFER
+    assert call((a, b, 0), (c, a, 0)) == sgl.LORA_ERR_BUFFER
+    assert call((b, a, 0), (a, c, 0)) == sgl.LORA_ERR_BUFFER             # gradients out of order
+    assert call((a, b, 0), (a + 16, c, 0)) == sgl.LORA_ERR_BUFFER        # a part of its own
+    assert call((a + 16, b, 0), (a, c, 0)) == sgl.LORA_ERR_BUFFER
+    assert call((a, b, 0), (c, b + 0x7c, 0)) == sgl.LORA_ERR_BUFFER      # its last number
+    assert call((a, b, 0), (c, b - 0x7c, 0)) == sgl.LORA_ERR_BUFFER
+    assert call((a, a, 0), (a, c, 0)) == sgl.LORA_ERR_BUFFER             # in place, and read elsewhere
+    assert call((a, a + 0x40, 0), (c, a + 0x60, 0)) == sgl.LORA_ERR_BUFFER   # gradients that overlap
+
+
+@pytest.mark.gpu
+def test_results_between_the_gradients():
+    # gradients and results side by side in one buffer, in no order, one in place, one read twice
+    sgl = lib()
+    flat = torch.arange(1, 97, dtype=torch.float32, device="cuda")
+    at = lambda i: flat[8 * i:8 * i + 8]
+    grads, out = [at(5), at(1), at(8), at(3), at(3)], [at(4), at(2), at(8), at(0), at(9)]
+    want_in = [t.double() for t in grads]
+    norm = torch.cat(want_in).norm()
+    before = flat.clone()
+    norms, ws = torch.empty(1, device="cuda"), torch.empty(sgl.lora_clip_gradients_workspace_bytes(grads), dtype=torch.uint8, device="cuda")
+    sgl.lora_clip_gradients(grads, norms, 2.0, ws, out=out)
+    assert abs(float(norms) - float(norm)) <= 2 ** -23 * float(norm)
+    for w, o in zip(want_in, out):
+        # the factor's rounding, the product's
+        torch.testing.assert_close(o.double(), w * (2.0 / (norm + 1e-6)), rtol=3 * 2 ** -24, atol=0)
+    kept = torch.ones(12, dtype=torch.bool)
+    kept[[4, 2, 8, 0, 9]] = False
+    assert torch.equal(flat.reshape(12, 8)[kept.cuda()], before.reshape(12, 8)[kept.cuda()])
+
+
 @pytest.mark.gpu
 def test_refusals_of_the_binding():
     sgl = lib()
