@@ -29,6 +29,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from operator import attrgetter
 from typing import Optional, Sequence
 
 from ._build import LIB as _LIB_PATH
@@ -864,49 +865,52 @@ def lora_linear_mx_backward(dy, x, codes, scales, lora_a: Sequence, lora_b: Sequ
 class LoraGradients:
     """The tensors of a training step's gradients (bf16 or float32, contiguous, on one
     GPU), and of the scaled ones: `out`, tensors like them, or None to scale in
-    place.  Made once for buffers that keep their sizes and types; a call looks
-    whether the tensors have moved."""
+    place.  Made once for buffers that stay; a call looks whether any of them has
+    another address, size, type or order than in the call before, and goes by them as
+    they are."""
 
     def __init__(self, grads: Sequence, out: Optional[Sequence] = None):
         self.grads = list(grads)
         self.out = self.grads if out is None else list(out)
         self._marshal()
 
-    def _where(self) -> list:
+    def _seen(self, shapes: bool) -> list:
+        """What a call goes by; with one norm a tensor's shape does not matter beside its size."""
         import torch
-        at = torch.Tensor.data_ptr
-        return list(map(at, self.grads)), None if self.out is self.grads else list(map(at, self.out))
+        ts, one = self.grads if self.out is self.grads else self.grads + self.out, torch.Tensor
+        return [list(map(f, ts)) for f in (one.data_ptr, one.size if shapes else one.numel, attrgetter("dtype"),
+                                           one.is_contiguous)]
 
     def _marshal(self) -> None:
-        where, n = "LoraGradients", len(self.grads)
+        where, n, flat = "LoraGradients", len(self.grads), self._seen(False)
         _need(len(self.out) == n, LORA_ERR_SHAPE, where, "one result per gradient")
-        self.device = self.grads[0].device if n else None
+        device = self.grads[0].device if n else None
         kinds = []
         for i, (t, o) in enumerate(zip(self.grads, self.out)):
-            if not (t.is_cuda and t.device == self.device and o.device == self.device):
-                raise TypeError("%s: gradient and result %d must be on %s" % (where, i, self.device))
+            if not (t.is_cuda and t.device == device and o.device == device):
+                raise TypeError("%s: gradient and result %d must be on %s" % (where, i, device))
             kinds.append(_type(t, where, "grads[%d]" % i))
             if o.dtype != t.dtype:
                 raise TypeError("%s: out[%d] must be %s (got %s)" % (where, i, t.dtype, o.dtype))
             _need(t.is_contiguous() and o.is_contiguous() and o.shape == t.shape, LORA_ERR_SHAPE, where,
                   "gradient and result %d must be contiguous and of one shape" % i)
-        self._at = self._where()
-        self._in = (ctypes.c_void_p * n)(*self._at[0])
-        self._out = self._in if self._at[1] is None else (ctypes.c_void_p * n)(*self._at[1])
-        self._sizes = (ctypes.c_int64 * n)(*[t.numel() for t in self.grads])
+        self.device, self._as = device, (flat, self._seen(True))
+        self._in = (ctypes.c_void_p * n)(*flat[0][:n])
+        self._out = self._in if self.out is self.grads else (ctypes.c_void_p * n)(*flat[0][n:])
+        self._sizes = (ctypes.c_int64 * n)(*flat[1][:n])
         self._types = (ctypes.c_int * n)(*kinds)
         self._heads = {t.shape[0] if t.dim() else 1 for t in self.grads}
 
-    def _current(self) -> "LoraGradients":
-        if self._where() != self._at:
+    def _current(self, groups: int) -> "LoraGradients":
+        if self._seen(groups > 1) != self._as[groups > 1]:
             self._marshal()
         return self
 
 
-def _gradients(grads, out=None) -> LoraGradients:
+def _gradients(grads, groups: int, out=None) -> LoraGradients:
     if isinstance(grads, LoraGradients):
         _need(out is None, LORA_ERR_SHAPE, "lora_clip_gradients", "a LoraGradients holds its results")
-        return grads._current()
+        return grads._current(groups)
     return LoraGradients(grads, out)
 
 
@@ -914,7 +918,7 @@ def lora_clip_gradients_workspace_bytes(grads, groups: int = 1) -> int:
     """Bytes of the workspace of lora_clip_gradients for these gradients (a sequence
     of tensors, or a LoraGradients) and so many norms: a uint8 device tensor, whose
     contents do not matter."""
-    g = _gradients(grads)
+    g = _gradients(grads, int(groups))
     n = int(_lib().lora_clip_gradients_workspace_bytes(g._sizes, g._types, len(g.grads), int(groups)))
     if n == 0:
         raise LoraError(LORA_ERR_SHAPE, "lora_clip_gradients_workspace_bytes")
@@ -931,12 +935,12 @@ def lora_clip_gradients(grads, norms, max_norm: float, workspace, out: Optional[
     keeps its gradients.  workspace uint8 of lora_clip_gradients_workspace_bytes."""
     import torch
     where = "lora_clip_gradients"
-    g = _gradients(grads, out)
+    _need(norms.dim() == 1 and norms.shape[0] >= 1, LORA_ERR_SHAPE, where, "norms must be [groups]")
+    groups = norms.shape[0]
+    g = _gradients(grads, groups, out)
     if not norms.is_cuda or (g.device is not None and norms.device != g.device):
         raise TypeError("%s: norms must be on one GPU with the gradients (got %s)" % (where, norms.device))
     _on(norms, torch.float32, norms.device, norms.shape, where, "norms")
-    _need(norms.dim() == 1 and norms.shape[0] >= 1, LORA_ERR_SHAPE, where, "norms must be [groups]")
-    groups = norms.shape[0]
     _need(groups == 1 or g._heads <= {groups}, LORA_ERR_SHAPE, where,
           "every gradient's first dimension must be the number of norms, %d" % groups)
     _workspace(workspace, norms.device, where)
