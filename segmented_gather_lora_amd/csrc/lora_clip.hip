@@ -39,12 +39,14 @@ constexpr int64_t kMaxUnits = 1 << 23;   // workgroups of a launch
 // launch to the next; the end that the first launch leaves there.
 constexpr int64_t kStreamBytes = 192 << 20, kKeptBytes = 160 << 20;
 
-// A factor as two floats, v * first * second: one below 2^-60 by itself could be
-// subnormal and have lost its digits.
+// A factor as a float and a power of two: gradients near 2^128 and a small largest norm
+// give factors far below float32's (the product with the float is rounded in its normal
+// range, and the power then rounds subnormal results alone).
 struct Factor {
-    float first, second;
-    __device__ __forceinline__ float of(float v) const { return v * first * second; }
-    __device__ __forceinline__ bool one() const { return first == 1.f && second == 1.f; }
+    float first;
+    int power;
+    __device__ __forceinline__ float of(float v) const { return __builtin_amdgcn_ldexpf(v * first, power); }
+    __device__ __forceinline__ bool one() const { return first == 1.f && power == 0; }
 };
 
 struct ClipTensor {
@@ -244,8 +246,11 @@ __device__ __forceinline__ Factor factor_of(const ClipCall &c, int group, float 
     const double n = sqrt(workgroup_sum(v));
     norm = (float)n;
     const double f = c.max_norm / (n + 1e-6);
-    if (!(n < __builtin_huge_val() && f < 1.0)) return Factor{1.f, 1.f};
-    return f < 0x1p-60 ? Factor{(float)(f * 0x1p60), 0x1p-60f} : Factor{(float)f, 1.f};
+    if (!(n < __builtin_huge_val() && f < 1.0)) return Factor{1.f, 0};
+    if (f >= 0x1p-60) return Factor{(float)f, 0};
+    int power;
+    const float first = (float)frexp(f, &power);
+    return Factor{first, power};
 }
 
 __global__ __launch_bounds__(kThreads) void factors_kernel(ClipCall c) {
