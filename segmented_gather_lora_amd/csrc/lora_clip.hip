@@ -201,12 +201,23 @@ __device__ __forceinline__ double squares(const F *p, int64_t count) {
 template <bool PAST, class F>
 __device__ __forceinline__ void scale_piece(const F *p, F *o, int64_t count, Factor f) {
     const int tid = threadIdx.x;
+    const bool keep = f.one();   // bit for bit: a product with 1 changes NaN
+    auto one = [&](int64_t i) {
+        if (keep)
+            o[i] = p[i];
+        else
+            store(o + i, f.of(value(p[i])));
+    };
     if (((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(o)) & 15) != 0) {
-        for (int64_t i = tid; i < count; i += kThreads) store(o + i, f.of(value(p[i])));
+        for (int64_t i = tid; i < count; i += kThreads) one(i);
         return;
     }
+    auto many = [&](const u32x4 &v) {
+        const u32x4 s = scaled(v, f, F());
+        return u32x4{keep ? v[0] : s[0], keep ? v[1] : s[1], keep ? v[2] : s[2], keep ? v[3] : s[3]};
+    };
     const int64_t head = head_of(p, count);
-    if (tid < head) store(o + tid, f.of(value(p[tid])));
+    if (tid < head) one(tid);
     constexpr int kVec = 16 / (int)sizeof(F);
     const u32x4 *q = reinterpret_cast<const u32x4 *>(p + head);
     u32x4 *r = reinterpret_cast<u32x4 *>(o + head);
@@ -217,11 +228,11 @@ __device__ __forceinline__ void scale_piece(const F *p, F *o, int64_t count, Fac
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) v[b] = load<PAST>(q + i + b * kThreads);
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) put<PAST>(r + i + b * kThreads, scaled(v[b], f, F()));
+        for (int b = 0; b < kBatch; ++b) put<PAST>(r + i + b * kThreads, many(v[b]));
     }
-    for (; i < vectors; i += kThreads) r[i] = scaled(q[i], f, F());
+    for (; i < vectors; i += kThreads) r[i] = many(q[i]);
     const int64_t rest = head + vectors * kVec + tid;
-    if (rest < count) store(o + rest, f.of(value(p[rest])));
+    if (rest < count) one(rest);
 }
 
 __global__ __launch_bounds__(kThreads) void squares_kernel(ClipArgs<false> a) {
