@@ -496,7 +496,8 @@ size_t lora_linear_mx_workspace_bytes(int num_tokens, int max_loras, int hidden,
  *           grads[i] (in place: what is not scaled is not touched); otherwise it
  *           overlaps no gradient, and no two results overlap (else LORA_ERR_BUFFER)
  *   sizes   host [num_tensors], elements, each a multiple of groups; 0 is allowed, a part
- *           has fewer than 2^32
+ *           has fewer than 2^32; a call has at most 2^23 pieces (parts, those of more than
+ *           32 KB cut into pieces of 32 to 256 KB)
  *   types   host [num_tensors] of LORA_BF16 or LORA_F32 (aligned to their size only)
  *   groups  1 .. LORA_MAX_LORAS; norms float32 [groups]
  *   max_norm  above 0; infinity: nothing is scaled
@@ -510,7 +511,7 @@ int lora_clip_gradients(const void *const *grads, void *const *out, const int64_
                         size_t workspace_bytes, hipStream_t stream);
 
 /* Bytes of workspace of lora_clip_gradients for these tensors.  0 if a size is out of
- * range.  Host only. */
+ * range, or for more pieces than a call takes.  Host only. */
 size_t lora_clip_gradients_workspace_bytes(const int64_t *sizes, const int *types, int num_tensors, int groups);
 
 /* Static description of a status code. */

@@ -414,7 +414,8 @@ extern "C" {
 
 size_t lora_clip_gradients_workspace_bytes(const int64_t *sizes, const int *types, int num_tensors, int groups) {
     if (check_tensors(sizes, types, num_tensors, groups)) return 0;
-    return plan_clip(sizes, types, num_tensors, groups).total;
+    const ClipPlan p = plan_clip(sizes, types, num_tensors, groups);
+    return p.pieces * groups > kMaxUnits ? 0 : p.total;
 }
 
 int lora_clip_gradients(const void *const *grads, void *const *out, const int64_t *sizes, const int *types,
@@ -426,8 +427,8 @@ int lora_clip_gradients(const void *const *grads, void *const *out, const int64_
     if (!norms || !workspace || (num_tensors && (!grads || !out))) return LORA_ERR_NULL;
     if ((reinterpret_cast<uintptr_t>(norms) & 3u) != 0) return LORA_ERR_ALIGN;
     const ClipPlan p = plan_clip(sizes, types, num_tensors, groups);
-    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || p.total > workspace_bytes) return LORA_ERR_BUFFER;
     if (p.pieces * groups > kMaxUnits) return LORA_ERR_SHAPE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || p.total > workspace_bytes) return LORA_ERR_BUFFER;
     bool same = true;
     for (int i = 0; i < num_tensors; ++i) {
         if (!sizes[i]) continue;
