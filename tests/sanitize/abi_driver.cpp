@@ -1,5 +1,4 @@
-// Calls the entry points of include/lora_mi355x.h (but for those that
-// operators_driver.cpp calls) with arguments that the
+// Calls every entry point of include/lora_mi355x.h with arguments that the
 // host-side checks reject, plus the host-only calls (lora_meta_bytes,
 // lora_meta_bind on host memory, the launch-count query, lora_status_string),
 // in a build whose host code has AddressSanitizer and
