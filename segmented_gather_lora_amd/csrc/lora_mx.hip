@@ -95,12 +95,12 @@ hipError_t launch_mx(const void *x, int type, int64_t ldx, int64_t rows, int col
 constexpr int64_t kMaxPitch = 1 << 25;
 
 // The workspace: that of the bf16 projection, then its matrix as numbers, or what
-// prep_kernel writes (no call has both).
+// prep_kernel writes (no call has both; the forward pass of few tokens has neither).
 struct MxLayout {
     size_t w, codes, scales, mscales, total;
     int steps;
 };
-MxLayout mx_layout(size_t linear, long n, int hidden, int out) {
+MxLayout mx_layout(size_t linear, long n, int hidden, int out, bool backward) {
     MxLayout l;
     l.steps = (int)((mx_blocks(hidden) + 7) / 8);
     const size_t groups = (size_t)(n + 255) / 256 * 4, wide = (size_t)(out + 255) / 256 * 4;   // whole tiles
@@ -109,7 +109,7 @@ MxLayout mx_layout(size_t linear, long n, int hidden, int out) {
     l.scales = l.codes + up((size_t)n * mx_code_bytes(hidden));
     l.mscales = l.scales + up(groups * l.steps * 512);
     const size_t numbers = l.w + up(2 * (size_t)out * hidden), codes = l.mscales + up(wide * l.steps * 512);
-    l.total = numbers > codes ? numbers : codes;
+    l.total = !backward && n <= kRowsTokens ? linear : numbers > codes ? numbers : codes;
     return l;
 }
 
@@ -140,7 +140,7 @@ size_t lora_linear_mx_workspace_bytes(int num_tokens, int max_loras, int hidden,
     if (check_sizes(num_tokens, max_loras, hidden, slice_widths, num_slices, rank)) return 0;
     if (out_features < 8 || out_features % 8) return 0;
     const UPlan u = plan_u(num_tokens, max_loras, num_slices, rank, widest(slice_widths, num_slices));
-    return mx_layout(layout(num_tokens, max_loras, num_slices, rank, u, backward != 0).total, num_tokens, hidden, out_features).total;
+    return mx_layout(layout(num_tokens, max_loras, num_slices, rank, u, backward != 0).total, num_tokens, hidden, out_features, backward != 0).total;
 }
 
 int lora_linear_mx(const void *x, int64_t ldx, int num_tokens, int hidden, const void *codes, int64_t ldcodes,
@@ -156,7 +156,7 @@ int lora_linear_mx(const void *x, int64_t ldx, int num_tokens, int hidden, const
     if ((st = check_forward(x, num_tokens, w_bias, bias, num_slices, buf, y))) return st;
     const UPlan u = plan_u(num_tokens, meta->max_loras, num_slices, rank, widest(slice_widths, num_slices));
     const Layout l = layout(num_tokens, meta->max_loras, num_slices, rank, u, false);
-    const MxLayout m = mx_layout(l.total, num_tokens, hidden, out_features);
+    const MxLayout m = mx_layout(l.total, num_tokens, hidden, out_features, false);
     if (m.total > workspace_bytes) return LORA_ERR_BUFFER;
     if (num_tokens == 0) return LORA_OK;
     char *ws = static_cast<char *>(workspace);
@@ -224,7 +224,7 @@ int lora_linear_mx_backward(const void *dy, int64_t lddy, const void *x, int64_t
     if ((st = check_gradients(g, x, num_tokens, hidden, num_slices))) return st;
     const UPlan u = plan_u(num_tokens, meta->max_loras, num_slices, rank, widest(slice_widths, num_slices));
     const Layout l = layout(num_tokens, meta->max_loras, num_slices, rank, u, true);
-    const MxLayout m = mx_layout(l.total, num_tokens, hidden, out_features);
+    const MxLayout m = mx_layout(l.total, num_tokens, hidden, out_features, true);
     if (m.total > workspace_bytes) return LORA_ERR_BUFFER;
     char *ws = static_cast<char *>(workspace);
     const MxArgs turn = mx_args(ws + m.w, LORA_BF16, hidden, out_features, hidden, codes, ldcodes, scales, ldscales);
