@@ -317,7 +317,8 @@ int lora_prepare_meta_launches(int num_tokens, int max_loras);
  *     y[t] = w x[t] + w_bias                                   all out_features columns
  *     y[t] += lora_b[i][m] s_i[t] + bias[i][m]                 slice i's columns, m not -1
  *     s_i[t] = buf[i][t] = scale * lora_a[i][m] x[t]
- * accumulated in float32 and rounded to bfloat16 once; slice i's columns start
+ * accumulated in float32 and rounded to bfloat16 once (s_i[t] takes part as two
+ * bfloat16 numbers, together within 2^-16 of it, or as it is); slice i's columns start
  * at offset_start plus the widths before it, as for lora_expand.  Unlike
  * lora_expand every row and column of y is written (a token with id -1 gets
  * the shared projection alone); rows of buf of such tokens are not touched.
@@ -351,7 +352,8 @@ int lora_linear(const void *x, int64_t ldx, int num_tokens, int hidden, const vo
  *     da[i][m] = sum over tokens t of id m of u_i[t] x[t]^T    bf16 [max_loras][rank][hidden]
  *     db[i][m] = sum dy_i[t] s_i[t]^T                          bf16 [max_loras][width][rank]
  *     dbias[i][m] = sum dy_i[t]                                bf16 [max_loras][width]
- * Sums are float32, each result is rounded once.  Every id's gradients below
+ * Sums are float32, each result is rounded once; s_i[t] and u_i[t] take part in dx, da
+ * and db as two bfloat16 numbers, together within 2^-16 of them.  Every id's gradients below
  * max_loras are written: zeros for an id without tokens.  dx may be NULL (not
  * needed), dbias NULL or hold NULLs.  The shared projection is frozen: it has
  * no gradient.  Rows of dbuf of tokens with id -1 are not touched.  Results
@@ -456,8 +458,8 @@ int lora_mx_dequantize(const void *codes, int64_t ldcodes, const void *scales, i
  * 4 bits then); the adapters read x as it is in either case:
  *     y[t] = w q(x[t]) + w_bias + (slice i's columns) lora_b[i][m] s_i[t] + bias[i][m]
  *     s_i[t] = buf[i][t] = scale * lora_a[i][m] x[t]
- * Everything else is as for lora_linear; workspace_bytes is at least what
- * lora_linear_mx_workspace_bytes gives.  A block of w whose byte is 255 makes its
+ * Everything else is as for lora_linear (s_i[t] takes part as there); workspace_bytes
+ * is at least what lora_linear_mx_workspace_bytes gives.  A block of w whose byte is 255 makes its
  * column of y NaN; a block of x that is not finite, with quantize_x, its token's row.
  */
 int lora_linear_mx(const void *x, int64_t ldx, int num_tokens, int hidden, const void *codes, int64_t ldcodes,
@@ -491,7 +493,9 @@ size_t lora_linear_mx_workspace_bytes(int num_tokens, int max_loras, int hidden,
  * adapters (each is a training of its own) and groups is max_loras, or everything,
  * with groups 1.  For every group g, over all tensors:
  *     norms[g] = sqrt(sum of v^2)
- *     out      = v * min(1, max_norm / (norms[g] + 1e-6)),  rounded once
+ *     out      = v * min(1, max_norm / (norms[g] + 1e-6))
+ * The factor comes from the norm in double; it and its product with v are rounded to
+ * 24 bits each, bfloat16 results once more.
  *   grads, out  host arrays [num_tensors] of device pointers, contiguous; out[i] may be
  *           grads[i] (in place: what is not scaled is not touched); otherwise it
  *           overlaps no gradient, and no two results overlap (else LORA_ERR_BUFFER)
@@ -503,8 +507,12 @@ size_t lora_linear_mx_workspace_bytes(int num_tokens, int max_loras, int hidden,
  *   max_norm  above 0; infinity: nothing is scaled
  *   workspace  device memory, 256-byte aligned, of at least
  *           lora_clip_gradients_workspace_bytes; its contents are ignored
- * A group whose norm is not finite keeps its gradients as they are.  Squares and
- * sums are double, in a fixed order: deterministic.
+ * A group with an infinity or a NaN among its gradients keeps them as they are, bit
+ * for bit (multiplied by the factor, its finite ones would become zeros or NaN); its
+ * norm says so.  Whether a norm is finite is judged in double: a group of norm
+ * 2^128 or more is scaled, and norms[g] reads infinity.  Squares and sums are double,
+ * in a fixed order: deterministic.  norms and workspace share no memory with the
+ * gradients, the results or each other.
  */
 int lora_clip_gradients(const void *const *grads, void *const *out, const int64_t *sizes, const int *types,
                         int num_tensors, int groups, double max_norm, float *norms, void *workspace,

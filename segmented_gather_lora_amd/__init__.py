@@ -931,8 +931,8 @@ def lora_clip_gradients(grads, norms, max_norm: float, workspace, out: Optional[
     sequence of bf16 or float32 tensors, or a LoraGradients.  norms float32 [groups]
     is written: one norm over everything for groups 1, else norms[g] is that of the
     tensors' entries [g] (the gradients of adapter g: every tensor's first dimension
-    is groups).  max_norm infinity: the norms alone.  A group whose norm is not finite
-    keeps its gradients.  workspace uint8 of lora_clip_gradients_workspace_bytes."""
+    is groups).  max_norm infinity: the norms alone.  A group with an infinity or a NaN
+    in it keeps its gradients.  workspace uint8 of lora_clip_gradients_workspace_bytes."""
     import torch
     where = "lora_clip_gradients"
     _need(norms.dim() == 1 and norms.shape[0] >= 1, LORA_ERR_SHAPE, where, "norms must be [groups]")

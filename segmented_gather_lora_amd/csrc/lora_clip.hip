@@ -10,10 +10,13 @@
 // workgroup for itself: the same order, so the same bits) and scales the piece.
 // Both are bound by the bytes: read once for the norm, read and written once
 // for the scaling.  Where they are more than the last-level cache holds, the scaling
-// walks the pieces backwards, from what the first launch read last, and all else is read
-// and written past the cache: the gradients of 128 adapters of rank 128 (1.14 GB of
-// bfloat16) take 167 and 413 us, 6.8 and 5.5 TB/s; without either 227 and 425, with the
-// walk alone 209 and 418.
+// walks the pieces of a launch backwards, from what the norms' launch read last, and all
+// else is read and written past the cache: the gradients of 128 adapters of rank 128
+// (1.14 GB of bfloat16) take 167 and 411 us, 6.8 and 5.5 TB/s; without either 227 and 425,
+// with the walk alone 209 and 418.  More tensors than a launch describes (246, 164 with
+// results of their own) take several launches of either kind in the same order, and the
+// cache then holds the end of the last one: 448 tensors of 2 MB 489 us in place and 508
+// into results, one of as many bytes 491 and 474.
 //
 // Squares and sums are double: the square of a float32 may be beyond float32, and
 // the rate (a conversion and a multiply-add an element) is far from a bound.
@@ -31,12 +34,19 @@ namespace {
 constexpr int kThreads = 256;
 constexpr size_t kArgBytes = 4000;               // of a launch, for its tensors' descriptions
 constexpr long kMinPiece = 32 << 10, kMaxPiece = 256 << 10, kPieces = 4096;   // bytes; pieces that are enough
+// (bfloat16 of 1088 MB in pieces of 32, 64, 128, 256 and 512 KB: 561, 585, 568, 571, 580 us;
+// 32 MB: 22, 22, 23, 28, 44; 8 MB: 10, 13, 16, 23, 37.)
 // Partial sums of a group that every workgroup adds up by itself; more are added
-// once, by a launch of their own.
+// once, by a launch of their own: 1024 sums 9.2 us the one way and 9.6 the other, 2048
+// 19.4 and 18.7, 4096 37 and 31.
 constexpr int kSelfSums = 2048;
 constexpr int64_t kMaxUnits = 1 << 23;   // workgroups of a launch
 // Gradients of so many bytes do not stay in the 256 MB of last-level cache from one
-// launch to the next; the end that the first launch leaves there.
+// launch to the next; the end that the first launch leaves there.  us into the cache and
+// past it, with results of their own: 160 MB 87, 85; 192 MB 107, 100; 256 MB 155, 136;
+// in place, where half as much is touched, 192 MB 96, 105; 320 MB 165, 172; 512 MB 292,
+// 276 (the limit is that of results).  Kept, 320 MB in place: nothing 182, 64 MB 176, 128 MB
+// 173, 160 MB 168, 192 MB 166, 224 MB 163; 1088 MB 602, 595, 578, 581, 577, 580.
 constexpr int64_t kStreamBytes = 192 << 20, kKeptBytes = 160 << 20;
 
 // A factor as a float and a power of two: gradients near 2^128 and a small largest norm

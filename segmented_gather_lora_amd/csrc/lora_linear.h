@@ -457,6 +457,10 @@ struct LinearOp : PlainOp<T> {
 //       12: 39, 40; 20: 39, 44 (rank 16); 12: 61, 59; 20: 62, 75 (rank 64); 16: 198,
 //       233 (3 slices of rank 128); 20: 135, 120; 32: 144, 155 (256 tokens by 2048
 //       over 4096, rank 64)
+// W's codes beside bf16 activations (a lane then has 8 columns of two tokens), and codes on
+// both sides, whole calls of y with the products and with the steps, part at the same place:
+//       2: 22, 18; 4: 23, 21; 6: 23, 27; 8: 23, 28 (64 tokens by 1024 over 1024, rank 64);
+//       2: 49, 39; 4: 55, 49; 6: 57, 57; 8: 56, 58 (256 by 6144 over 4096, rank 64, both codes)
 template <bool BWD>
 constexpr int kDotSegs = BWD ? 20 : 4;
 template <class T, bool BWD>
@@ -1508,7 +1512,13 @@ struct LinearPlan {
 // Codes on both sides take 128 x 128 tiles where numbers take 256 x 256 (big false): a
 // walk has a quarter of the steps, so that a tile's start and end count, which two
 // workgroups a CU cover for each other: 8192 by 6144 over 4096 124 us, 8 adapters of
-// rank 64 154, 256 x 256 tiles 134 and 179; over 16384 458 and 404.
+// rank 64 154, 256 x 256 tiles 134 and 179.  (Over 16384 the larger ones were the faster,
+// 404 and 458: the rule does not look at K.)  Their limit to 64 x 64 tiles is the bf16
+// product's, and lies between few adapters and many for them too; whole calls over 4096,
+// 128 x 128 tiles and 64 x 64, one adapter of rank 16 first:
+//     160 tiles (256 by 10240): 35, 40;  32 adapters: 51, 45
+//     224 (256 by 14336): 36, 43;  52, 50;  224 (1024 by 3584): 39, 46;  45, 51
+//     240 (520 by 6144): 38, 45;  47, 49
 LinearPlan plan_linear(long n, long cols, bool big = true) {
     auto tiles = [&](long bm, long bn) { return ceil_div(cols, bm) * ceil_div(n, bn); };
     LinearPlan p;

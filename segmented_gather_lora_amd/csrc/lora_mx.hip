@@ -8,7 +8,8 @@ using namespace lora;
 namespace lora {
 namespace {
 
-// Bound by the bytes: 28672 rows of 4096 bf16 57 us (5.2 TB/s), back to bf16 50 us (5.9).
+// Bound by the bytes.  28672 rows of 4096: from bf16 53 to 65 us (57 at the least beside
+// other calls, 5.2 TB/s), back 50 (5.9); from float32 96 (5.5), back 122 (4.4).
 template <class F>
 __global__ __launch_bounds__(kMxThreads) void quantize_kernel(MxArgs a) {
     constexpr int kSpans = kMxThreads / kMxGroup;
@@ -194,7 +195,9 @@ int lora_linear_mx(const void *x, int64_t ldx, int num_tokens, int hidden, const
     // Where the bf16 projection takes 64 x 64 tiles, W's codes go into the product as they
     // are; larger tiles are bound by the MFMA or by x, and turn W into numbers first.  us of
     // the product from codes, and of both launches, over 4096 by 6144 columns, 32 adapters:
-    // 33 tokens 26, 45; 256: 31, 50; 512: 55, 66; (640: 63, 68; 1024: 90, 80)
+    // 33 tokens 26, 45; 256: 31, 50; 512: 55, 66; (640: 63, 68; 1024: 90, 80).  The limit is
+    // that of the bf16 product's tiles; few tokens by more columns stay faster from the codes
+    // beyond it: whole calls of 256 tokens by 14336 columns 69, 93
     // (that product's places in x are 32 bits)
     const bool near = (int64_t)num_tokens * ldx * 2 < ((int64_t)1 << 32);
     if (num_tokens <= kRowsTokens || (!quantize_x && near && plan_linear(num_tokens, out_features).tile == kSmall)) {
